@@ -15,7 +15,7 @@ A quantised pool holds one record per token slot, made of blocks of `hpc` kv hea
 of the number of kv heads that is at most 8).  A block is, per head, the D codes of K then the D codes of
 V (e4m3), followed by 16 bytes of scales: byte 2h is head h's K exponent and byte 2h + 1 its V exponent,
 both biased by 127 (the value is code x 2^(byte - 127)), the rest zero.  A record is padded to a multiple
-of 32 bytes.  The exponent of a row is the smallest e with max|x| <= 448 x 2^e, clamped to [-118, 120].
+of 32 bytes.  The exponent of a row is the smallest e with max|x| <= 448 x 2^e, clamped to [-118, 119].
 """
 import math
 
@@ -99,10 +99,10 @@ def slot_bytes(hkv, d):
 
 
 def row_exponents(x):
-    """Smallest e with max|x| <= 448 * 2^e over the last axis, clamped to [-118, 120] (fp32 rows)."""
+    """Smallest e with max|x| <= 448 * 2^e over the last axis, clamped to [-118, 119] (fp32 rows)."""
     m, ex = torch.frexp(x.abs().amax(-1))
     e = ex.to(torch.int32) - torch.where(m <= 0.875, 9, 8).to(torch.int32)
-    return torch.where(m == 0, -118, e).clamp(-118, 120)
+    return torch.where(m == 0, -118, e).clamp(-118, 119)
 
 
 def pow2(e):
@@ -411,7 +411,7 @@ def nearest_codes(x):
     e = torch.ceil(torch.log2(torch.where(top > 0, top, torch.ones_like(top)) / 448.0))
     e = torch.where(top > 448.0 * torch.exp2(e), e + 1, e)
     e = torch.where(top <= 448.0 * torch.exp2(e - 1), e - 1, e)
-    e = torch.where(top > 0, e, torch.full_like(e, -118)).clamp(-118, 120)
+    e = torch.where(top > 0, e, torch.full_like(e, -118)).clamp(-118, 119)
     y = x * torch.exp2(-e)
     step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
     return torch.round(y / step) * step * torch.exp2(e)
