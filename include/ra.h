@@ -63,6 +63,7 @@ typedef enum {
 #define RA_DEVERR_TABLE 0x2u   /* a req_pool_indices entry outside [0, table_rows) */
 #define RA_DEVERR_LENGTH 0x4u  /* a length outside its host-side bound, or a seq_len < 1 */
 #define RA_DEVERR_TIMEOUT 0x8u /* a bounded wait inside a kernel gave up (the kernel returned early) */
+#define RA_DEVERR_POSITION 0x10u /* a token position outside [0, max_position) (rotated as position 0) */
 
 /*
  * ra_kv_store -- write this step's new K/V rows into their pool slots.
@@ -249,6 +250,97 @@ ra_status ra_decode_attention_static(const void* k_pool, const void* v_pool, int
                                      const int32_t* group_level, int32_t max_group_prefix_len,
                                      int32_t max_group_size, int32_t max_group_levels, uint32_t* device_error,
                                      ra_stream_t stream);
+
+/*
+ * Quantised (e4m3) pools.  The serving pages measure bf16 caches only; this is an addition for callers
+ * whose decode is bound by the cache's bytes: a quantised pool holds twice the tokens and is read in half
+ * the time.  A pool is bytes [num_slots, slot_bytes] with slot_bytes = ra_kv8_slot_bytes(...), a slot's
+ * record holding one token's K and V for every kv head:
+ *   a record is made of blocks of hpc kv heads (hpc = the largest divisor of num_kv_heads that is <= 8);
+ *   a block is, per head, head_dim e4m3 codes of K, then head_dim codes of V, followed by 16 bytes of
+ *   exponents (byte 2h: K of the block's head h, byte 2h + 1: V; biased by 127; the rest zero);
+ *   a record is padded to a multiple of 32 bytes.
+ * A value is code * 2^(byte - 127).  A row's exponent is the smallest e with max|x| <= 448 * 2^e over its
+ * finite values, kept within [-118, 119]; a code is x * 2^-e rounded to nearest even.  Infinities and
+ * values beyond 448 * 2^119 are stored as +-448 * 2^e, NaN as NaN.
+ */
+
+/* Bytes of a slot's record (0 for unsupported head counts: head_dim 64 or 128, num_kv_heads 1 .. 1024). */
+size_t ra_kv8_slot_bytes(int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * ra_kv8_store -- ra_kv_store into a quantised pool: record out_cache_loc[i] = quantised rows i of
+ * k_new and v_new (bf16 [num_tokens, num_kv_heads, head_dim]), i < num_tokens.  Slots as in ra_kv_store
+ * (distinct but for the dummy slot 0; out-of-range slots are skipped and flagged RA_DEVERR_SLOT).
+ * The pool and the rows are 16-byte aligned.  num_tokens == 0 is a no-op.
+ */
+ra_status ra_kv8_store(void* kv8_pool, int64_t num_slots, int32_t num_kv_heads, int32_t head_dim, const void* k_new,
+                       const void* v_new, const int32_t* out_cache_loc, int64_t num_tokens, uint32_t* device_error,
+                       ra_stream_t stream);
+
+/*
+ * ra_kv8_load -- read records back: rows i of k_out and v_out (bf16 [num_tokens, num_kv_heads, head_dim])
+ * = the values of record slots[i], exact (a value has 4 significant bits).  slots may repeat; an
+ * out-of-range slot is read as slot 0 and flagged.  For ra_extend_attention over a quantised cache: load
+ * the cached prefix into a bf16 pool of the call and list its rows in the call's table.
+ */
+ra_status ra_kv8_load(const void* kv8_pool, int64_t num_slots, int32_t num_kv_heads, int32_t head_dim,
+                      const int32_t* slots, void* k_out, void* v_out, int64_t num_tokens, uint32_t* device_error,
+                      ra_stream_t stream);
+
+/*
+ * ra_kv8_decode_attention -- ra_decode_attention (without groups) over a quantised pool: the softmax
+ * attention of each request's query over the values its records stand for, accumulated in fp32, output
+ * bf16.  Arguments, checks, flags and the workspace (ra_decode_workspace_bytes with num_groups 0) are those
+ * of ra_decode_attention, with the one pool instead of two.
+ */
+ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_slots, int32_t num_kv_heads, int32_t head_dim,
+                                  const void* q, void* o, int32_t num_q_heads, float sm_scale,
+                                  const int32_t* req_to_token, int64_t table_stride, int64_t table_rows,
+                                  const int32_t* req_pool_indices, const int32_t* seq_lens, int32_t batch,
+                                  int32_t max_seq_len, void* workspace, size_t workspace_bytes,
+                                  uint32_t* device_error, ra_stream_t stream);
+
+/*
+ * ra_qk_norm_rope_store -- a layer's step between its qkv projection and attention, in one pass.  The
+ * attention calls take queries and keys that are normalised and rotated already; this call does both and
+ * the store:
+ *   y = x * rsqrt(mean(x^2) + eps) * w for each q and k head row x[0 .. head_dim) (w = q_weight or k_weight;
+ *       without weights y = x),
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin) for pair i < rotary_dim / 2 of the first rotary_dim
+ *       values, (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved = 1, with
+ *       cos = cos_sin[positions[t], i], sin = cos_sin[positions[t], rotary_dim / 2 + i],
+ *   q_out[t] = the q rows; pool slot out_cache_loc[t] = the k rows, and v's as they are.
+ * fp32 arithmetic, rounded once (nearest even) to bf16.
+ *   q, k, v:   bf16, head rows contiguous, token t at t * stride elements (slices of one projection's output
+ *              are fine); strides are multiples of 8.  q_out likewise; it may be q itself (same stride).
+ *   q_weight, k_weight: bf16 [head_dim], both or neither (NULL).
+ *   positions: int32 [num_tokens]; one outside [0, max_position) is flagged RA_DEVERR_POSITION and rotated
+ *              as position 0.
+ *   cos_sin:   fp32 [max_position, rotary_dim]; rotary_dim is a multiple of 16 in [16, head_dim].
+ *   k_pool, v_pool, out_cache_loc: as in ra_kv_store (a token whose slot is out of range is flagged and not
+ *              stored; its q rows are written).
+ * All buffers 16-byte aligned, index arrays 4-byte aligned.  num_tokens == 0 is a no-op.
+ */
+ra_status ra_qk_norm_rope_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                                const float* cos_sin, int64_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                void* q_out, int64_t q_out_stride, void* k_pool, void* v_pool, int64_t num_slots,
+                                const int32_t* out_cache_loc, int64_t num_tokens, uint32_t* device_error,
+                                ra_stream_t stream);
+
+/*
+ * ra_qk_norm_rope_kv8_store -- the same into a quantised pool: K is quantised from its fp32 values (one
+ * rounding), V from its bf16 values.
+ */
+ra_status ra_qk_norm_rope_kv8_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                                    const float* cos_sin, int64_t max_position, int32_t rotary_dim,
+                                    int32_t interleaved, void* q_out, int64_t q_out_stride, void* kv8_pool,
+                                    int64_t num_slots, const int32_t* out_cache_loc, int64_t num_tokens,
+                                    uint32_t* device_error, ra_stream_t stream);
 
 /*
  * ra_selftest_bounded_wait -- check, on the current device, that a wait inside a kernel that runs out

@@ -25,12 +25,16 @@ from . import _build
 __all__ = ["RAError", "ra_kv_store", "ra_extend_attention", "ra_extend_workspace_bytes", "ra_decode_attention",
            "ra_decode_workspace_bytes", "ra_decode_attention_store",
            "ra_decode_attention_static", "RA_DECODE_STATIC_SCRATCH_BYTES",
+           "ra_kv8_slot_bytes", "ra_kv8_store", "ra_kv8_load", "ra_kv8_decode_attention",
+           "ra_qk_norm_rope_store", "ra_qk_norm_rope_kv8_store",
            "ra_abi_version", "ra_selftest_bounded_wait", "library_path", "load", "DEVERR_SLOT", "DEVERR_TABLE", "DEVERR_LENGTH",
-           "DEVERR_TIMEOUT"]
+           "DEVERR_TIMEOUT", "DEVERR_POSITION"]
 
 RA_OK = 0
+RA_ERR_UNSUPPORTED = 2
 RA_DECODE_STATIC_SCRATCH_BYTES = 32 << 20  # size of the library's static decode scratch (include/ra.h)
 DEVERR_SLOT, DEVERR_TABLE, DEVERR_LENGTH, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEVERR_POSITION = 0x10
 _lib = None
 
 
@@ -70,9 +74,19 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.ra_decode_attention_static.restype = ctypes.c_int
     lib.ra_selftest_bounded_wait.argtypes = [i64, P, P]
     lib.ra_selftest_bounded_wait.restype = ctypes.c_int
+    lib.ra_kv8_slot_bytes.argtypes = [i32, i32]
+    lib.ra_kv8_slot_bytes.restype = sz
+    lib.ra_kv8_store.argtypes = [P, i64, i32, i32, P, P, P, i64, P, P]
+    lib.ra_kv8_load.argtypes = [P, i64, i32, i32, P, P, P, i64, P, P]
+    lib.ra_kv8_decode_attention.argtypes = [P, i64, i32, i32, P, P, i32, f32, P, i64, i64, P, P, i32, i32, P, sz, P, P]
+    norm_rope = [P, i64, P, i64, P, i64, i32, i32, i32, P, P, f32, P, P, i64, i32, i32, P, i64]
+    lib.ra_qk_norm_rope_store.argtypes = norm_rope + [P, P, i64, P, i64, P, P]
+    lib.ra_qk_norm_rope_kv8_store.argtypes = norm_rope + [P, i64, P, i64, P, P]
     lib.ra_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
     lib.ra_decode_workspace_bytes.restype = sz
-    for f in (lib.ra_kv_store, lib.ra_extend_attention, lib.ra_decode_attention, lib.ra_abi_version):
+    for f in (lib.ra_kv_store, lib.ra_extend_attention, lib.ra_decode_attention, lib.ra_abi_version, lib.ra_kv8_store,
+              lib.ra_kv8_load, lib.ra_kv8_decode_attention, lib.ra_qk_norm_rope_store,
+              lib.ra_qk_norm_rope_kv8_store):
         f.restype = ctypes.c_int
     lib.ra_status_string.argtypes = [ctypes.c_int]
     lib.ra_status_string.restype = ctypes.c_char_p
@@ -266,3 +280,149 @@ def ra_decode_attention_static(k_pool: torch.Tensor, v_pool: torch.Tensor, q: to
             _ptr(group_prefix_len, i32, "group_prefix_len", dev), _ptr(group_level, i32, "group_level", dev),
             int(max_group_prefix_len), int(max_group_size), int(max_group_levels),
             _ptr(device_error, i32, "device_error", dev), _stream(dev, stream)))
+
+
+def _launch(fn, device: torch.device, stream, *args) -> None:
+    """fn(*args, stream) with `device` current (the library asks for the current device's properties)."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device, stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device, stream)))
+
+
+def ra_kv8_slot_bytes(num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of a quantised pool's record per slot (the layout is in include/ra.h)."""
+    n = int(load().ra_kv8_slot_bytes(num_kv_heads, head_dim))
+    if n == 0:
+        raise RAError(RA_ERR_UNSUPPORTED, f"no quantised pool for {num_kv_heads} kv heads of {head_dim}")
+    return n
+
+
+def _kv8_pool(kv8_pool: torch.Tensor, num_kv_heads: int, head_dim: int):
+    """Pointer and slots of a quantised pool, uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)]."""
+    if kv8_pool.dim() != 2 or kv8_pool.shape[1] != ra_kv8_slot_bytes(num_kv_heads, head_dim):
+        raise ValueError(f"kv8_pool must be [num_slots, {ra_kv8_slot_bytes(num_kv_heads, head_dim)}]")
+    return _ptr(kv8_pool, torch.uint8, "kv8_pool", kv8_pool.device), kv8_pool.shape[0]
+
+
+def ra_kv8_store(kv8_pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, out_cache_loc: torch.Tensor,
+                 device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise new K/V rows ([num_tokens, Hkv, D] bf16) into the records of slots out_cache_loc."""
+    dev = kv8_pool.device
+    n, hkv, d = k_new.shape
+    if v_new.shape != k_new.shape or out_cache_loc.shape != (n,):
+        raise ValueError("k_new and v_new must be [num_tokens, Hkv, D] and out_cache_loc [num_tokens]")
+    pool, slots = _kv8_pool(kv8_pool, hkv, d)
+    bf, i32 = torch.bfloat16, torch.int32
+    _launch(load().ra_kv8_store, dev, stream, pool, slots, hkv, d, _ptr(k_new, bf, "k_new", dev),
+            _ptr(v_new, bf, "v_new", dev), _ptr(out_cache_loc, i32, "out_cache_loc", dev), n,
+            _ptr(device_error, i32, "device_error", dev))
+
+
+def ra_kv8_load(kv8_pool: torch.Tensor, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
+                device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Read the records of `slots` back into K/V rows ([num_tokens, Hkv, D] bf16), exactly."""
+    dev = kv8_pool.device
+    n, hkv, d = k_out.shape
+    if v_out.shape != k_out.shape or slots.shape != (n,):
+        raise ValueError("k_out and v_out must be [num_tokens, Hkv, D] and slots [num_tokens]")
+    pool, num_slots = _kv8_pool(kv8_pool, hkv, d)
+    bf, i32 = torch.bfloat16, torch.int32
+    _launch(load().ra_kv8_load, dev, stream, pool, num_slots, hkv, d, _ptr(slots, i32, "slots", dev),
+            _ptr(k_out, bf, "k_out", dev), _ptr(v_out, bf, "v_out", dev), n,
+            _ptr(device_error, i32, "device_error", dev))
+
+
+def ra_kv8_decode_attention(kv8_pool: torch.Tensor, q: torch.Tensor, o: torch.Tensor, req_to_token: torch.Tensor,
+                            req_pool_indices: torch.Tensor, seq_lens: torch.Tensor, *, num_kv_heads: int,
+                            max_seq_len: int, sm_scale: float, workspace: torch.Tensor,
+                            device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ra_decode_attention over a quantised pool (uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)]); q, o
+    [batch, Hq, D] bf16; workspace: uint8, ra_decode_workspace_bytes(batch, Hq, Hkv, D, max_seq_len)."""
+    dev = kv8_pool.device
+    batch, hq, d = q.shape
+    if o.shape != q.shape:
+        raise ValueError("q/o shape mismatch")
+    if req_pool_indices.shape != (batch,) or seq_lens.shape != (batch,) or req_to_token.dim() != 2:
+        raise ValueError("req_pool_indices and seq_lens must be [batch], req_to_token 2-D")
+    pool, num_slots = _kv8_pool(kv8_pool, num_kv_heads, d)
+    bf, i32 = torch.bfloat16, torch.int32
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
+    _launch(
+        load().ra_kv8_decode_attention, dev, stream, pool, num_slots, num_kv_heads, d, _ptr(q, bf, "q", dev), _ptr(o, bf, "o", dev), hq, float(sm_scale),
+        _ptr(req_to_token, i32, "req_to_token", dev), req_to_token.shape[1], req_to_token.shape[0],
+        _ptr(req_pool_indices, i32, "req_pool_indices", dev), _ptr(seq_lens, i32, "seq_lens", dev), batch,
+        int(max_seq_len), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+        _ptr(device_error, i32, "device_error", dev))
+
+
+def _head_rows(t: torch.Tensor, name: str, device: torch.device):
+    """Pointer and token stride (elements) of bf16 head rows [num_tokens, H, D]: a token's rows contiguous,
+    tokens at any stride (a slice of a fused projection's output)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    n, h, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{name}: a token's head rows must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), st if n > 1 else h * d
+
+
+def _norm_rope_args(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, eps, interleaved, dev):
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    if k.shape != (n, hkv, d) or v.shape != k.shape or q_out.shape != q.shape:
+        raise ValueError("q, q_out must be [num_tokens, Hq, D] and k, v [num_tokens, Hkv, D]")
+    if positions.shape != (n,) or cos_sin.dim() != 2:
+        raise ValueError("positions must be [num_tokens] and cos_sin [max_position, rotary_dim]")
+    for w in (q_weight, k_weight):
+        if w is not None and w.shape != (d,):
+            raise ValueError("weights must be [D]")
+    bf = torch.bfloat16
+    return (*_head_rows(q, "q", dev), *_head_rows(k, "k", dev), *_head_rows(v, "v", dev), hq, hkv, d,
+            _ptr(q_weight, bf, "q_weight", dev), _ptr(k_weight, bf, "k_weight", dev), float(eps),
+            _ptr(positions, torch.int32, "positions", dev), _ptr(cos_sin, torch.float32, "cos_sin", dev),
+            cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), *_head_rows(q_out, "q_out", dev))
+
+
+def ra_qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
+                          k_weight: Optional[torch.Tensor], positions: torch.Tensor, cos_sin: torch.Tensor,
+                          q_out: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                          out_cache_loc: torch.Tensor, *, eps: float = 1e-6, interleaved: bool = False,
+                          device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Per-head RMS norm of q and k, their rotation by cos_sin[positions] (fp32 [max_position, rotary_dim]:
+    cosines, then sines), q written to q_out, k and v to pool slots out_cache_loc.  q, k, v, q_out
+    [num_tokens, H, D] bf16, any token stride; weights [D] bf16, or None for no norm."""
+    dev = k_pool.device
+    args = _norm_rope_args(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, eps, interleaved, dev)
+    if k_pool.dim() != 3 or k_pool.shape[1:] != k.shape[1:] or v_pool.shape != k_pool.shape:
+        raise ValueError("pools must be [num_slots, Hkv, D]")
+    if out_cache_loc.shape != (q.shape[0],):
+        raise ValueError("out_cache_loc must be [num_tokens]")
+    bf, i32 = torch.bfloat16, torch.int32
+    _launch(
+        load().ra_qk_norm_rope_store, dev, stream, *args, _ptr(k_pool, bf, "k_pool", dev), _ptr(v_pool, bf, "v_pool", dev), k_pool.shape[0],
+        _ptr(out_cache_loc, i32, "out_cache_loc", dev), q.shape[0], _ptr(device_error, i32, "device_error", dev))
+
+
+def ra_qk_norm_rope_kv8_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
+                              k_weight: Optional[torch.Tensor], positions: torch.Tensor, cos_sin: torch.Tensor,
+                              q_out: torch.Tensor, kv8_pool: torch.Tensor, out_cache_loc: torch.Tensor, *,
+                              eps: float = 1e-6, interleaved: bool = False,
+                              device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ra_qk_norm_rope_store into a quantised pool (uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)])."""
+    dev = kv8_pool.device
+    args = _norm_rope_args(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, eps, interleaved, dev)
+    pool, num_slots = _kv8_pool(kv8_pool, k.shape[1], k.shape[2])
+    if out_cache_loc.shape != (q.shape[0],):
+        raise ValueError("out_cache_loc must be [num_tokens]")
+    i32 = torch.int32
+    _launch(
+        load().ra_qk_norm_rope_kv8_store, dev, stream, *args, pool, num_slots, _ptr(out_cache_loc, i32, "out_cache_loc", dev), q.shape[0],
+        _ptr(device_error, i32, "device_error", dev))

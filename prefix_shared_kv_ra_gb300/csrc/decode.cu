@@ -31,6 +31,7 @@
 
 #include "api_common.h"
 #include "decode_internal.h"
+#include "decode_item.cuh"
 #include "ra_ptx.cuh"
 
 namespace ra {
@@ -48,31 +49,6 @@ constexpr int kPlanThreads = 1024;  // one CTA plans the call
 constexpr int kRemBuckets = 64;     // size classes of the requests' last (short) items
 constexpr int kCombineWarps = 4;    // (request, q head) merges per combine CTA
 constexpr float kDecodeRescale = 8.0f;  // log2 units: the decode softmax's reference moves past this
-
-// One work item: keys [k0, k1) of request b for the kv heads of head group hg; d is its dense index
-// (request-major: the item's partial results live at d).
-struct Item {
-  int32_t b, split, hg, k0, k1, start, n_splits, row, d;
-};
-
-// Claim `idx` = (position in the plan's longest-first order) * n_hgroups + hg.  The plan (written by
-// decode_plan_kernel) lists only non-empty items of valid requests.  Plan arrays are read with plain
-// loads: they are written on the device by the kernel before this one.
-__device__ __forceinline__ void decode_item(const DecodeParams& p, int32_t idx, Item& it) {
-  it.hg = idx % p.n_hgroups;
-  it.d = p.order[idx / p.n_hgroups];
-  it.b = p.item_req[it.d];
-  const int32_t i0 = p.req_item0[it.b];
-  it.split = it.d - i0;
-  it.n_splits = p.req_item0[it.b + 1] - i0;
-  it.row = __ldg(p.rpi + it.b);
-  const int32_t L = min(__ldg(p.seq_lens + it.b), p.max_seq_len);
-  const int32_t start = p.key_start ? __ldg(p.key_start + it.b) : 0;
-  it.start = start < 0 ? 0 : (start > L ? L : start);
-  const int32_t chunk = p.plan[1];
-  it.k0 = it.start + it.split * chunk;
-  it.k1 = min(L, it.k0 + chunk);
-}
 
 // Persistent split-KV decode.  One CTA per SM pulls (request, split, head group) items from a
 // counter.  Warps hpc .. hpc+3 are producers: per 16-key slab, producer w copies a quarter of the
@@ -610,7 +586,7 @@ __device__ __forceinline__ void scatter_new_rows(const DecodeParams& p, int64_t 
 
 // The private-key work plan of one decode call, made on the device from the real lengths (the host only
 // knows bounds).  T = the batch's private keys (seq_len minus the cascade start, over valid requests);
-// chunk = max(kDecodeMinChunk, T / kDecodePlanItems rounded up to 16), so a call has at most
+// chunk = max(min_chunk, T / kDecodePlanItems rounded up to chunk_align), so a call has at most
 // kDecodePlanItems + batch items however long its contexts are.  Request b's items get the dense indices
 // req_item0[b] .. req_item0[b+1]-1 (where their partials live); the claim order lists every full-chunk
 // item first, then each request's shorter last item by decreasing size (longest processing time first),
@@ -666,7 +642,8 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
   const unsigned long long per_item = (s_total + kDecodePlanItems - 1) / kDecodePlanItems;
   // (the host bounds batch x max_seq_len by kDecodePlanItems x 2^30, so the chunk fits in 31 bits)
   const int32_t chunk = static_cast<int32_t>(
-      per_item <= kDecodeMinChunk ? kDecodeMinChunk : ((per_item + 15) / 16) * 16);
+      per_item <= static_cast<unsigned long long>(p.min_chunk) ? p.min_chunk
+                                                               : (per_item + p.chunk_align - 1) / p.chunk_align * p.chunk_align);
   // item counts (all, full-chunk) of this thread's requests, scanned over the block
   int32_t cnt = 0, full = 0;
   for (int32_t b = r0; b < r1; ++b) {
@@ -770,15 +747,39 @@ ra_status launch_decode(const DecodeParams& p, int grid, int smem, cudaStream_t 
   }
   if (ra_status st = launch_pdl("decode_kernel", kern, dim3(grid), dim3(32 * (p.hpc + kProducers + 1)), smem, stream, p))
     return st;
-  const int nwarps = p.batch * p.hq;
-  return launch_pdl("decode_combine_kernel", decode_combine_kernel<D>, dim3((nwarps + kCombineWarps - 1) / kCombineWarps),
-                    dim3(32 * kCombineWarps), 0, stream, p);
+  return launch_decode_combine(p, D, stream);
 }
 
 }  // namespace
 
+ra_status launch_decode_plan(const DecodeParams& p, int store_ctas, cudaStream_t stream) {
+  return launch_pdl("decode_plan_kernel", decode_plan_kernel, dim3(1 + store_ctas), dim3(kPlanThreads), 0, stream, p);
+}
+
+ra_status launch_decode_combine(const DecodeParams& p, int32_t head_dim, cudaStream_t stream) {
+  const int nwarps = p.batch * p.hq;
+  return launch_pdl("decode_combine_kernel", head_dim == 128 ? decode_combine_kernel<128> : decode_combine_kernel<64>,
+                    dim3((nwarps + kCombineWarps - 1) / kCombineWarps), dim3(32 * kCombineWarps), 0, stream, p);
+}
+
+void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.max_items = pl.max_items;
+  p.part_o = reinterpret_cast<float*>(ws + wl.part_o);
+  p.part_lse = reinterpret_cast<float*>(ws + wl.part_lse);
+  int32_t* ints = reinterpret_cast<int32_t*>(ws + wl.ints);
+  p.counter = ints + p.batch;
+  p.prefix_counter = ints + p.batch + 1;
+  p.prefix_done = ints + p.batch + 2;
+  p.plan = ints + p.batch + 3;
+  p.req_item0 = p.plan + 2;
+  p.item_req = p.req_item0 + p.batch + 1;
+  p.order = p.item_req + pl.max_items;
+  p.req_done = p.order + pl.max_items;
+}
+
 // kv heads per work item: the largest divisor of Hkv that is <= 8 (one consumer warp each).
-static int32_t heads_per_cta(int32_t num_kv_heads) {
+int32_t heads_per_cta(int32_t num_kv_heads) {
   for (int32_t h = kMaxHeadsPerCta; h > 1; --h)
     if (num_kv_heads % h == 0) return h;
   return 1;
@@ -965,10 +966,10 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
   p.seq_lens = seq_lens;
   p.batch = batch;
   p.max_seq_len = max_seq_len;
-  p.max_items = pl.max_items;
+  p.min_chunk = kDecodeMinChunk;
+  p.chunk_align = 16;
+  bind_decode_workspace(p, wl, pl, workspace);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part_o = reinterpret_cast<float*>(ws + wl.part_o);
-  p.part_lse = reinterpret_cast<float*>(ws + wl.part_lse);
   p.err = device_error;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // fused store: extra CTAs of the call's first kernel scatter the new rows (a few waves of 4 vectors
@@ -989,14 +990,6 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
   }
 
   int32_t* ints = reinterpret_cast<int32_t*>(ws + wl.ints);
-  p.counter = ints + batch;
-  p.prefix_counter = ints + batch + 1;
-  p.prefix_done = ints + batch + 2;
-  p.plan = ints + batch + 3;
-  p.req_item0 = p.plan + 2;
-  p.item_req = p.req_item0 + batch + 1;
-  p.order = p.item_req + pl.max_items;
-  p.req_done = p.order + pl.max_items;
   // Kernels rather than memsets, so that the launches of the call stay chained programmatically:
   // with groups, [set-up: counters, key starts, empty prefix partials] -> [prefix pass] -> [plan] ->
   // [decode] -> [combine]; without, [plan] -> [decode] -> [combine].
@@ -1021,9 +1014,7 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
     if (ra_status st = launch_cascade_prefix(p, ca, head_dim, s, &p.prefix_ctas)) return st;
   }
   // (with groups the set-up kernel did the fused store: the plan kernel runs behind the prefix pass)
-  if (ra_status st = launch_pdl("decode_plan_kernel", decode_plan_kernel, dim3(1 + (num_groups > 0 ? 0 : store_ctas)),
-                                dim3(kPlanThreads), 0, s, p))
-    return st;
+  if (ra_status st = launch_decode_plan(p, num_groups > 0 ? 0 : store_ctas, s)) return st;
   // persistent decode geometry
   p.hpc = heads_per_cta(num_kv_heads);
   p.n_hgroups = num_kv_heads / p.hpc;

@@ -37,6 +37,8 @@ struct DecodeParams {
   int32_t row_stride;        // bytes between keys in a ring stage (hpc * D * 2 + 16)
   int32_t stage_bytes;       // 2 * 16 * row_stride
   int32_t max_items;         // kDecodePlanItems + batch: bound of the plan's items
+  int32_t min_chunk;         // shortest full item of the plan (keys)
+  int32_t chunk_align;       // full items are a multiple of this many keys
   int32_t* counter;          // work-item counter (reset by the plan kernel)
   int32_t* prefix_counter;   // cascade prefix pass's work-item counter (zeroed with the key starts)
   int32_t* prefix_done;      // cascade prefix pass: CTAs that have written all their partials (zeroed likewise)
@@ -107,6 +109,13 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                        int32_t num_groups, int32_t max_group_prefix_len, int32_t max_group_size);
 DecodeWorkspace layout_decode_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                         int32_t head_dim, const DecodePlan& pl, int32_t cascade_levels);
+
+int32_t heads_per_cta(int32_t num_kv_heads);  // kv heads per work item: the largest divisor of Hkv that is <= 8
+// Point p's scratch members into a workspace of layout wl (p.batch set before).
+void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace);
+// The call's plan kernel (CTA 0) and combine kernel, around a decode kernel that counts its partials.
+ra_status launch_decode_plan(const DecodeParams& p, int store_ctas, cudaStream_t stream);
+ra_status launch_decode_combine(const DecodeParams& p, int32_t head_dim, cudaStream_t stream);
 
 // Tensor-core pass over each group's shared prefix: writes p.casc_o / p.casc_lse
 // for every member (defined with the tcgen05 attention kernel).

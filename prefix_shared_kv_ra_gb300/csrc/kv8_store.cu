@@ -1,0 +1,205 @@
+// kv8_store.cu -- ra_kv8_store and ra_kv8_load: rows into and out of a quantised pool.
+//
+// Both move each byte once and are HBM-bound (8 x 128 heads: 4096 bytes of bf16 and a 2080-byte record per
+// token).  A warp takes one block of one token: up to 16 rows (K and V of up to 8 heads) in steps of 32
+// lanes, D / 16 lanes per row, a lane holding 8 values of the row's first half and the 8 that lie D / 2
+// further (16-byte accesses of neighbouring lanes are contiguous on the bf16 side, 8-byte ones on the
+// record's side).  A lane issues all its steps' loads before the first use: 4 KB in flight per warp.
+// The store finds a row's largest magnitude with D / 16-lane shuffles and writes the block's 16 exponent
+// bytes as one vector, the padding with them, so that only whole sectors reach DRAM.
+#include "api_common.h"
+#include "kv8.cuh"
+
+namespace ra {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int D>
+struct Rows {
+  static constexpr int kLanes = D / 16;          // lanes per row
+  static constexpr int kPerStep = 32 / kLanes;   // rows per step
+  static constexpr int kSteps = 16 / kPerStep;   // a block has at most 16 rows
+};
+
+__device__ __forceinline__ uint2 quantise8(const uint4& v, float inv) {
+  return make_uint2(f32x4_to_e4m3x4(bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, bf16_lo(v.y) * inv, bf16_hi(v.y) * inv),
+                    f32x4_to_e4m3x4(bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, bf16_lo(v.w) * inv, bf16_hi(v.w) * inv));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv8_store_kernel(uint8_t* __restrict__ pool, int64_t num_slots, int32_t hkv,
+                                                             Kv8Shape sh, const uint4* __restrict__ k_new,
+                                                             const uint4* __restrict__ v_new,
+                                                             const int32_t* __restrict__ loc, int64_t units,
+                                                             uint32_t* __restrict__ err) {
+  using R = Rows<D>;
+  griddep_wait();  // earlier kernels may still read the records this store overwrites
+  griddep_launch();
+  const int lane = threadIdx.x & 31;
+  const int sub = lane % R::kLanes, row0 = lane / R::kLanes;
+  const int n_rows = 2 * sh.hpc;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+    const int64_t tok = u / sh.blocks;
+    const int32_t blk = static_cast<int32_t>(u - tok * sh.blocks);
+    const int32_t slot = __ldg(loc + tok);
+    uint4 a[R::kSteps], b[R::kSteps];
+#pragma unroll
+    for (int s = 0; s < R::kSteps; ++s) {
+      const int r = s * R::kPerStep + row0;
+      if (r < n_rows) {
+        const uint4* src = ((r & 1) ? v_new : k_new) + (tok * hkv + blk * sh.hpc + (r >> 1)) * (D / 8) + sub;
+        a[s] = __ldg(src);
+        b[s] = __ldg(src + D / 16);
+      } else {
+        a[s] = b[s] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    if (slot < 0 || slot >= num_slots) {  // warp-uniform
+      if (lane == 0 && blk == 0) flag_error(err, RA_DEVERR_SLOT);
+      continue;
+    }
+    uint8_t* rec = pool + static_cast<int64_t>(slot) * sh.slot_bytes + blk * sh.block_bytes;
+    uint32_t eb[R::kSteps];
+#pragma unroll
+    for (int s = 0; s < R::kSteps; ++s) {
+      uint32_t m = max(amax_bf16x8(a[s]), amax_bf16x8(b[s]));
+#pragma unroll
+      for (int off = 1; off < R::kLanes; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      const int32_t e = kv8_exponent(m);
+      eb[s] = static_cast<uint32_t>(e + 127);
+      const int r = s * R::kPerStep + row0;
+      if (r < n_rows) {
+        const float inv = pow2f(-e);
+        uint2* dst = reinterpret_cast<uint2*>(rec + r * D) + sub;
+        dst[0] = quantise8(a[s], inv);
+        dst[D / 16] = quantise8(b[s], inv);
+      }
+    }
+    const uint4 scales = gather_scale_bytes<R::kSteps, R::kPerStep, R::kLanes>(eb, n_rows);
+    uint4* tail = reinterpret_cast<uint4*>(rec + n_rows * D);
+    if (lane == 0) tail[0] = scales;
+    if (lane == 1 && blk == sh.blocks - 1 && sh.blocks * sh.block_bytes < sh.slot_bytes)
+      tail[1] = make_uint4(0, 0, 0, 0);  // the record's padding (16 bytes)
+  }
+}
+
+__device__ __forceinline__ uint4 restore8(const uint2& c, float s) {
+  const float2 p0 = f16x2_to_f32x2(e4m3x2_to_f16x2(c.x)), p1 = f16x2_to_f32x2(e4m3x2_hi_to_f16x2(c.x));
+  const float2 p2 = f16x2_to_f32x2(e4m3x2_to_f16x2(c.y)), p3 = f16x2_to_f32x2(e4m3x2_hi_to_f16x2(c.y));
+  return make_uint4(pack_bf16x2(p0.x * s, p0.y * s), pack_bf16x2(p1.x * s, p1.y * s),
+                    pack_bf16x2(p2.x * s, p2.y * s), pack_bf16x2(p3.x * s, p3.y * s));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv8_load_kernel(const uint8_t* __restrict__ pool, int64_t num_slots,
+                                                            int32_t hkv, Kv8Shape sh, const int32_t* __restrict__ slots,
+                                                            uint4* __restrict__ k_out, uint4* __restrict__ v_out,
+                                                            int64_t units, uint32_t* __restrict__ err) {
+  using R = Rows<D>;
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31;
+  const int sub = lane % R::kLanes, row0 = lane / R::kLanes;
+  const int n_rows = 2 * sh.hpc;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+    const int64_t tok = u / sh.blocks;
+    const int32_t blk = static_cast<int32_t>(u - tok * sh.blocks);
+    int32_t slot = __ldg(slots + tok);
+    if (slot < 0 || slot >= num_slots) {
+      if (lane == 0 && blk == 0) flag_error(err, RA_DEVERR_SLOT);
+      slot = 0;
+    }
+    const uint8_t* rec = pool + static_cast<int64_t>(slot) * sh.slot_bytes + blk * sh.block_bytes;
+    uint2 a[R::kSteps], b[R::kSteps];
+    uint32_t eb[R::kSteps];
+#pragma unroll
+    for (int s = 0; s < R::kSteps; ++s) {
+      const int r = s * R::kPerStep + row0;
+      if (r < n_rows) {
+        const uint2* src = reinterpret_cast<const uint2*>(rec + r * D) + sub;
+        a[s] = __ldg(src);
+        b[s] = __ldg(src + D / 16);
+        eb[s] = __ldg(rec + n_rows * D + r);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < R::kSteps; ++s) {
+      const int r = s * R::kPerStep + row0;
+      if (r < n_rows) {
+        const float scale = __uint_as_float(eb[s] << 23);
+        uint4* dst = ((r & 1) ? v_out : k_out) + (tok * hkv + blk * sh.hpc + (r >> 1)) * (D / 8) + sub;
+        dst[0] = restore8(a[s], scale);
+        dst[D / 16] = restore8(b[s], scale);
+      }
+    }
+  }
+}
+
+ra_status check_kv8(const void* pool, int64_t num_slots, int32_t num_kv_heads, int32_t head_dim, const void* k,
+                    const void* v, const int32_t* slots, int64_t n) {
+  RA_REQUIRE(n >= 0, "num_tokens must be >= 0 (got %lld)", (long long)n);
+  RA_REQUIRE(num_slots > 0, "num_slots must be > 0");
+  RA_REQUIRE(num_kv_heads > 0, "num_kv_heads must be > 0");
+  if (head_dim != 64 && head_dim != 128) return fail(RA_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", head_dim);
+  if (num_kv_heads > 1024) return fail(RA_ERR_UNSUPPORTED, "num_kv_heads %d (supported: up to 1024)", num_kv_heads);
+  if (n == 0) return RA_OK;
+  RA_REQUIRE(pool && k && v && slots, "null pointer argument");
+  RA_REQUIRE(aligned16(pool) && aligned16(k) && aligned16(v), "the pool and the rows must be 16-byte aligned");
+  RA_REQUIRE(aligned4(slots), "slot indices must be 4-byte aligned");
+  return RA_OK;
+}
+
+int grid_for(int64_t units, const DeviceInfo& dev) {
+  const int64_t want = (units + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t cap = static_cast<int64_t>(dev.num_sms) * 8;
+  return static_cast<int>(want < cap ? want : cap);
+}
+
+}  // namespace
+}  // namespace ra
+
+extern "C" size_t ra_kv8_slot_bytes(int32_t num_kv_heads, int32_t head_dim) {
+  if (num_kv_heads <= 0 || num_kv_heads > 1024 || (head_dim != 64 && head_dim != 128)) return 0;
+  return ra::kv8_shape(num_kv_heads, head_dim).slot_bytes;
+}
+
+extern "C" ra_status ra_kv8_store(void* kv8_pool, int64_t num_slots, int32_t num_kv_heads, int32_t head_dim,
+                                  const void* k_new, const void* v_new, const int32_t* out_cache_loc,
+                                  int64_t num_tokens, uint32_t* device_error, ra_stream_t stream) {
+  using namespace ra;
+  clear_error();
+  if (ra_status st = check_kv8(kv8_pool, num_slots, num_kv_heads, head_dim, k_new, v_new, out_cache_loc, num_tokens))
+    return st;
+  if (num_tokens == 0) return RA_OK;
+  DeviceInfo dev;
+  if (ra_status st = current_device(&dev)) return st;
+  const Kv8Shape sh = kv8_shape(num_kv_heads, head_dim);
+  const int64_t units = num_tokens * sh.blocks;
+  auto kern = head_dim == 128 ? kv8_store_kernel<128> : kv8_store_kernel<64>;
+  return launch_pdl("kv8_store_kernel", kern, dim3(grid_for(units, dev)), dim3(kThreads), 0,
+                    reinterpret_cast<cudaStream_t>(stream), static_cast<uint8_t*>(kv8_pool), num_slots, num_kv_heads,
+                    sh, static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), out_cache_loc, units,
+                    device_error);
+}
+
+extern "C" ra_status ra_kv8_load(const void* kv8_pool, int64_t num_slots, int32_t num_kv_heads, int32_t head_dim,
+                                 const int32_t* slots, void* k_out, void* v_out, int64_t num_tokens,
+                                 uint32_t* device_error, ra_stream_t stream) {
+  using namespace ra;
+  clear_error();
+  if (ra_status st = check_kv8(kv8_pool, num_slots, num_kv_heads, head_dim, k_out, v_out, slots, num_tokens)) return st;
+  if (num_tokens == 0) return RA_OK;
+  DeviceInfo dev;
+  if (ra_status st = current_device(&dev)) return st;
+  const Kv8Shape sh = kv8_shape(num_kv_heads, head_dim);
+  const int64_t units = num_tokens * sh.blocks;
+  auto kern = head_dim == 128 ? kv8_load_kernel<128> : kv8_load_kernel<64>;
+  return launch_pdl("kv8_load_kernel", kern, dim3(grid_for(units, dev)), dim3(kThreads), 0,
+                    reinterpret_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(kv8_pool), num_slots,
+                    num_kv_heads, sh, slots, static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), units,
+                    device_error);
+}
