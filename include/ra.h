@@ -343,6 +343,43 @@ ra_status ra_qk_norm_rope_kv8_store(const void* q, int64_t q_stride, const void*
                                     uint32_t* device_error, ra_stream_t stream);
 
 /*
+ * ra_tree_attention -- drafted tokens of a tree (speculative decoding) over a cached prefix.  The serving
+ * pages stop at one token per step; this is an addition for callers that verify several drafted tokens of a
+ * request in one call.  Request b (table row req_pool_indices[b]) has prefix_lens[b] cached tokens and
+ * draft_lens[b] drafted ones, whose K/V are stored already and listed at positions prefix_lens[b] ..
+ * prefix_lens[b] + draft_lens[b] - 1.  Drafted token i attends to all of the prefix and to the drafted
+ * tokens its mask names:
+ *   o[t, h, :] = sum_j softmax_j(sm_scale * <q[t, h], K[slot_j, h / G]>) V[slot_j, h / G],  t = qo_indptr[b] + i,
+ *   j < prefix_lens[b], and j = prefix_lens[b] + c for every c < draft_lens[b] with bit c % 32 of
+ *   tree_mask[t, c / 32] set (a token names itself if it is to see itself; any set is allowed, not only a
+ *   tree's ancestors).
+ * A row that sees nothing (no prefix, no bit set) gives 0.  Values of drafted tokens that a row's mask leaves
+ * out have no influence on it, whatever they are (also infinities and NaN).
+ *   q, o:      bf16 [total_q, num_q_heads, head_dim]; o must not alias q or the pools; rows outside every
+ *              request's range are left as they were.
+ *   qo_indptr: int32 [batch + 1], qo_indptr[b] the first row of request b; requests' rows must not overlap.
+ *   tree_mask: uint32 [total_q, mask_words], mask_words >= ceil(max_draft_len / 32).
+ *   max_draft_len (1 .. 1024), max_prefix_len: host-side bounds.  A request whose lengths are outside them or
+ *              the table, or whose rows are outside [0, total_q), is flagged RA_DEVERR_LENGTH and skipped; a
+ *              table row out of range RA_DEVERR_TABLE; a slot out of range is flagged RA_DEVERR_SLOT and read
+ *              as slot 0.
+ *   workspace: ra_tree_workspace_bytes(...) bytes, 16-byte aligned; calls that overlap on the GPU need
+ *              separate workspaces.
+ * The GQA group must divide 128.  batch == 0 or total_q == 0 is a no-op; draft_lens[b] == 0 writes nothing.
+ */
+ra_status ra_tree_attention(const void* k_pool, const void* v_pool, int64_t num_slots, int32_t num_kv_heads,
+                            int32_t head_dim, const void* q, void* o, int32_t num_q_heads, float sm_scale,
+                            const int32_t* req_to_token, int64_t table_stride, int64_t table_rows,
+                            const int32_t* req_pool_indices, const int32_t* prefix_lens, const int32_t* draft_lens,
+                            const int32_t* qo_indptr, const uint32_t* tree_mask, int32_t mask_words, int32_t batch,
+                            int64_t total_q, int32_t max_draft_len, int32_t max_prefix_len, void* workspace,
+                            size_t workspace_bytes, uint32_t* device_error, ra_stream_t stream);
+
+/* Workspace bytes ra_tree_attention needs (0 for invalid or unsupported sizes). */
+size_t ra_tree_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t max_draft_len);
+
+/*
  * ra_selftest_bounded_wait -- check, on the current device, that a wait inside a kernel that runs out
  * returns instead of hanging.  The pages have no counterpart: every wait in this library's kernels (on
  * an mbarrier or on a counter another CTA raises) is bounded by a clock deadline, after which the kernel

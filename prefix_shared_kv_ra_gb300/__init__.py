@@ -15,6 +15,7 @@ Functions keep the C names: ``ra_kv_store``, ``ra_extend_attention``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -26,7 +27,7 @@ __all__ = ["RAError", "ra_kv_store", "ra_extend_attention", "ra_extend_workspace
            "ra_decode_workspace_bytes", "ra_decode_attention_store",
            "ra_decode_attention_static", "RA_DECODE_STATIC_SCRATCH_BYTES",
            "ra_kv8_slot_bytes", "ra_kv8_store", "ra_kv8_load", "ra_kv8_decode_attention",
-           "ra_qk_norm_rope_store", "ra_qk_norm_rope_kv8_store",
+           "ra_qk_norm_rope_store", "ra_qk_norm_rope_kv8_store", "ra_tree_attention", "ra_tree_workspace_bytes",
            "ra_abi_version", "ra_selftest_bounded_wait", "library_path", "load", "DEVERR_SLOT", "DEVERR_TABLE", "DEVERR_LENGTH",
            "DEVERR_TIMEOUT", "DEVERR_POSITION"]
 
@@ -82,11 +83,15 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     norm_rope = [P, i64, P, i64, P, i64, i32, i32, i32, P, P, f32, P, P, i64, i32, i32, P, i64]
     lib.ra_qk_norm_rope_store.argtypes = norm_rope + [P, P, i64, P, i64, P, P]
     lib.ra_qk_norm_rope_kv8_store.argtypes = norm_rope + [P, i64, P, i64, P, P]
+    lib.ra_tree_attention.argtypes = [P, P, i64, i32, i32, P, P, i32, f32, P, i64, i64, P, P, P, P, P, i32, i32, i64,
+                                      i32, i32, P, sz, P, P]
+    lib.ra_tree_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32]
+    lib.ra_tree_workspace_bytes.restype = sz
     lib.ra_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
     lib.ra_decode_workspace_bytes.restype = sz
     for f in (lib.ra_kv_store, lib.ra_extend_attention, lib.ra_decode_attention, lib.ra_abi_version, lib.ra_kv8_store,
               lib.ra_kv8_load, lib.ra_kv8_decode_attention, lib.ra_qk_norm_rope_store,
-              lib.ra_qk_norm_rope_kv8_store):
+              lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention):
         f.restype = ctypes.c_int
     lib.ra_status_string.argtypes = [ctypes.c_int]
     lib.ra_status_string.restype = ctypes.c_char_p
@@ -105,18 +110,19 @@ def _check(status: int) -> None:
 def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, device: torch.device):
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(device: torch.device, stream) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(device: torch.device, stream) -> int:
+    # the raw handle of the current stream: torch.cuda.current_stream builds a Stream object around it, which
+    # costs more than the rest of a small call's checks
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def ra_selftest_bounded_wait(deadline_cycles: int, device_error: torch.Tensor, stream=None) -> None:
@@ -170,7 +176,7 @@ def ra_extend_attention(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Ten
         req_to_token.shape[1], req_to_token.shape[0], _ptr(req_pool_indices, i32, "req_pool_indices", dev),
         _ptr(prefix_lens, i32, "prefix_lens", dev), _ptr(extend_lens, i32, "extend_lens", dev),
         _ptr(qo_indptr, i32, "qo_indptr", dev), batch, total_q, int(max_extend_len), int(max_prefix_len),
-        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _ptr(device_error, i32, "device_error", dev),
+        workspace.data_ptr(), workspace.numel(), _ptr(device_error, i32, "device_error", dev),
         _stream(dev, stream)))
 
 
@@ -212,7 +218,7 @@ def ra_decode_attention(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Ten
         _ptr(group_indptr, i32, "group_indptr", dev), _ptr(group_reqs, i32, "group_reqs", dev),
         _ptr(group_prefix_start, i32, "group_prefix_start", dev), _ptr(group_prefix_len, i32, "group_prefix_len", dev),
         _ptr(group_level, i32, "group_level", dev), int(max_group_prefix_len), int(max_group_size),
-        int(max_group_levels), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+        int(max_group_levels), workspace.data_ptr(), workspace.numel(),
         _ptr(device_error, i32, "device_error", dev), _stream(dev, stream)))
 
 
@@ -247,7 +253,7 @@ def ra_decode_attention_store(k_pool: torch.Tensor, v_pool: torch.Tensor, k_new:
         _ptr(group_indptr, i32, "group_indptr", dev), _ptr(group_reqs, i32, "group_reqs", dev),
         _ptr(group_prefix_start, i32, "group_prefix_start", dev), _ptr(group_prefix_len, i32, "group_prefix_len", dev),
         _ptr(group_level, i32, "group_level", dev), int(max_group_prefix_len), int(max_group_size),
-        int(max_group_levels), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+        int(max_group_levels), workspace.data_ptr(), workspace.numel(),
         _ptr(device_error, i32, "device_error", dev), _stream(dev, stream)))
 
 
@@ -286,13 +292,16 @@ def _launch(fn, device: torch.device, stream, *args) -> None:
     """fn(*args, stream) with `device` current (the library asks for the current device's properties)."""
     if device.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {device}")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device, stream)))
+    if device.index == torch._C._cuda_getDevice():
+        status = fn(*args, _stream(device, stream))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(device, stream)))
+            status = fn(*args, _stream(device, stream))
+    if status != RA_OK:
+        _check(status)
 
 
+@functools.lru_cache(maxsize=None)
 def ra_kv8_slot_bytes(num_kv_heads: int, head_dim: int) -> int:
     """Bytes of a quantised pool's record per slot (the layout is in include/ra.h)."""
     n = int(load().ra_kv8_slot_bytes(num_kv_heads, head_dim))
@@ -303,9 +312,10 @@ def ra_kv8_slot_bytes(num_kv_heads: int, head_dim: int) -> int:
 
 def _kv8_pool(kv8_pool: torch.Tensor, num_kv_heads: int, head_dim: int):
     """Pointer and slots of a quantised pool, uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)]."""
-    if kv8_pool.dim() != 2 or kv8_pool.shape[1] != ra_kv8_slot_bytes(num_kv_heads, head_dim):
+    shape = kv8_pool.shape
+    if len(shape) != 2 or shape[1] != ra_kv8_slot_bytes(num_kv_heads, head_dim):
         raise ValueError(f"kv8_pool must be [num_slots, {ra_kv8_slot_bytes(num_kv_heads, head_dim)}]")
-    return _ptr(kv8_pool, torch.uint8, "kv8_pool", kv8_pool.device), kv8_pool.shape[0]
+    return _ptr(kv8_pool, torch.uint8, "kv8_pool", kv8_pool.device), shape[0]
 
 
 def ra_kv8_store(kv8_pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, out_cache_loc: torch.Tensor,
@@ -356,39 +366,43 @@ def ra_kv8_decode_attention(kv8_pool: torch.Tensor, q: torch.Tensor, o: torch.Te
         load().ra_kv8_decode_attention, dev, stream, pool, num_slots, num_kv_heads, d, _ptr(q, bf, "q", dev), _ptr(o, bf, "o", dev), hq, float(sm_scale),
         _ptr(req_to_token, i32, "req_to_token", dev), req_to_token.shape[1], req_to_token.shape[0],
         _ptr(req_pool_indices, i32, "req_pool_indices", dev), _ptr(seq_lens, i32, "seq_lens", dev), batch,
-        int(max_seq_len), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
+        int(max_seq_len), workspace.data_ptr(), workspace.numel(),
         _ptr(device_error, i32, "device_error", dev))
 
 
-def _head_rows(t: torch.Tensor, name: str, device: torch.device):
+def _head_rows(t: torch.Tensor, shape, name: str, device: torch.device):
     """Pointer and token stride (elements) of bf16 head rows [num_tokens, H, D]: a token's rows contiguous,
     tokens at any stride (a slice of a fused projection's output)."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    n, h, d = t.shape
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    n, h, d = shape
     st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: a token's head rows must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), st if n > 1 else h * d
+    return t.data_ptr(), st if n > 1 else h * d
 
 
 def _norm_rope_args(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, eps, interleaved, dev):
-    n, hq, d = q.shape
-    hkv = k.shape[1]
-    if k.shape != (n, hkv, d) or v.shape != k.shape or q_out.shape != q.shape:
-        raise ValueError("q, q_out must be [num_tokens, Hq, D] and k, v [num_tokens, Hkv, D]")
+    q_shape, k_shape = q.shape, k.shape
+    n, hq, d = q_shape
+    hkv = k_shape[1]
+    if k_shape[0] != n or k_shape[2] != d:
+        raise ValueError("q must be [num_tokens, Hq, D] and k, v [num_tokens, Hkv, D]")
     if positions.shape != (n,) or cos_sin.dim() != 2:
         raise ValueError("positions must be [num_tokens] and cos_sin [max_position, rotary_dim]")
     for w in (q_weight, k_weight):
         if w is not None and w.shape != (d,):
             raise ValueError("weights must be [D]")
     bf = torch.bfloat16
-    return (*_head_rows(q, "q", dev), *_head_rows(k, "k", dev), *_head_rows(v, "v", dev), hq, hkv, d,
-            _ptr(q_weight, bf, "q_weight", dev), _ptr(k_weight, bf, "k_weight", dev), float(eps),
+    max_position, rotary_dim = cos_sin.shape
+    return (*_head_rows(q, q_shape, "q", dev), *_head_rows(k, k_shape, "k", dev), *_head_rows(v, k_shape, "v", dev),
+            hq, hkv, d, _ptr(q_weight, bf, "q_weight", dev), _ptr(k_weight, bf, "k_weight", dev), float(eps),
             _ptr(positions, torch.int32, "positions", dev), _ptr(cos_sin, torch.float32, "cos_sin", dev),
-            cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), *_head_rows(q_out, "q_out", dev))
+            max_position, rotary_dim, 1 if interleaved else 0, *_head_rows(q_out, q_shape, "q_out", dev))
 
 
 def ra_qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -426,3 +440,40 @@ def ra_qk_norm_rope_kv8_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     _launch(
         load().ra_qk_norm_rope_kv8_store, dev, stream, *args, pool, num_slots, _ptr(out_cache_loc, i32, "out_cache_loc", dev), q.shape[0],
         _ptr(device_error, i32, "device_error", dev))
+
+
+def ra_tree_workspace_bytes(batch: int, total_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                            max_draft_len: int, max_prefix_len: int = 0) -> int:
+    """Workspace of ra_tree_attention for these bounds (it does not depend on max_prefix_len)."""
+    return int(load().ra_tree_workspace_bytes(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len))
+
+
+def ra_tree_attention(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Tensor, o: torch.Tensor,
+                      req_to_token: torch.Tensor, req_pool_indices: torch.Tensor, prefix_lens: torch.Tensor,
+                      draft_lens: torch.Tensor, qo_indptr: torch.Tensor, tree_mask: torch.Tensor, *,
+                      max_draft_len: int, max_prefix_len: int, sm_scale: float, workspace: torch.Tensor,
+                      device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Drafted tokens (q, o [total_q, Hq, D] bf16, request b's rows from qo_indptr[b]) over their request's
+    cached prefix and the drafted tokens named by their bit masks (tree_mask int32 [total_q, words], bit c % 32
+    of word c / 32 = drafted token c of the request is visible)."""
+    dev = k_pool.device
+    num_slots, hkv, d = k_pool.shape
+    total_q, hq, dq = q.shape
+    batch = req_pool_indices.shape[0]
+    if v_pool.shape != k_pool.shape or dq != d or o.shape != q.shape:
+        raise ValueError("pools must be [num_slots, Hkv, D] and q, o [total_q, Hq, D]")
+    if prefix_lens.shape != (batch,) or draft_lens.shape != (batch,) or qo_indptr.shape != (batch + 1,):
+        raise ValueError("req_pool_indices, prefix_lens and draft_lens must be [batch], qo_indptr [batch + 1]")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q or req_to_token.dim() != 2:
+        raise ValueError("tree_mask must be [total_q, words] and req_to_token 2-D")
+    bf, i32 = torch.bfloat16, torch.int32
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
+    _launch(
+        load().ra_tree_attention, dev, stream, _ptr(k_pool, bf, "k_pool", dev), _ptr(v_pool, bf, "v_pool", dev),
+        num_slots, hkv, d, _ptr(q, bf, "q", dev), _ptr(o, bf, "o", dev), hq, float(sm_scale),
+        _ptr(req_to_token, i32, "req_to_token", dev), req_to_token.shape[1], req_to_token.shape[0],
+        _ptr(req_pool_indices, i32, "req_pool_indices", dev), _ptr(prefix_lens, i32, "prefix_lens", dev),
+        _ptr(draft_lens, i32, "draft_lens", dev), _ptr(qo_indptr, i32, "qo_indptr", dev),
+        _ptr(tree_mask, i32, "tree_mask", dev), tree_mask.shape[1], batch, total_q, int(max_draft_len),
+        int(max_prefix_len), workspace.data_ptr(), workspace.numel(), _ptr(device_error, i32, "device_error", dev))

@@ -3,14 +3,17 @@
 // One CTA per SM runs a stream of work items.  An item is 256 query rows of one kv head -- two
 // 128-row tiles, each a GQA block of 128 / G tokens (or decode requests) x the G q heads of the kv
 // head -- against a range of keys gathered from the pool through a req_to_token row.  Every
-// gathered 128-key K/V tile feeds both query tiles, i.e. 256 rows of tensor-core work.  Two users:
+// gathered 128-key K/V tile feeds both query tiles, i.e. 256 rows of tensor-core work.  Three users:
 //
-//  * extend (EXTEND = true): rows are suffix tokens of one request; row (token i, head g) sees
+//  * extend (kExtendPass): rows are suffix tokens of one request; row (token i, head g) sees
 //    keys 0 .. P + i (cached prefix + causal suffix); the bf16 output is written directly.  Items
 //    come from a (request, query tile) list sorted longest first, times the kv heads.
-//  * cascade prefix pass (EXTEND = false): rows are the decode queries of the members of one
+//  * cascade prefix pass (kPrefixPass): rows are the decode queries of the members of one
 //    prefix group; all rows see the same range of the shared prefix, read once for the group;
 //    (output, log2-sum-exp) partials are written for the decode combine pass.
+//  * draft tree (kTreePass): rows are the drafted tokens of one request; all see the cached prefix,
+//    and of the drafted tokens the ones their bit mask names; an item is a (request, query tile, key
+//    split); an unsplit item writes bf16, a split one partials.
 //
 // Warp roles (512 threads):
 //  warps 0-3  softmax + epilogue of query tile 0, one thread per row = TMEM lane;
@@ -90,7 +93,17 @@ struct TcParams {
   int32_t max_csplits;
   float* casc_o;    // [casc_slots, batch, hq, D]
   float* casc_lse;  // [casc_slots, batch, hq]
+  // draft tree (rpi, prefix_lens, qo_indptr, o and the work list as for extend; extend_lens are the draft
+  // lengths; work_items are [4 * entries]: request, query tile, key split, partial slot or -1)
+  const uint32_t* tree_mask;  // [total_q, mask_words]
+  int32_t mask_words;
+  const int32_t* tree_chunk;  // keys per split (a multiple of 128)
+  int32_t part_rows;          // rows of a partial slot
+  float* part_o;              // [slots, hkv, part_rows, D]
+  float* part_lse;            // [slots, hkv, part_rows]
 };
+
+enum TcPass { kPrefixPass = 0, kExtendPass = 1, kTreePass = 2 };
 
 namespace tc {
 
@@ -140,17 +153,18 @@ struct Job {
   int32_t kbeg, kend, nt;  // keys [kbeg, kend) in nt 128-key tiles
   int32_t table_row;
   int32_t n_valid;   // valid tokens / members (of 2T)
-  int32_t causal0;   // extend: token t of the item sees keys < causal0 + t + 1
+  int32_t causal0;   // extend: token t of the item sees keys < causal0 + t + 1; tree: the prefix length
   int64_t q_tok0;    // extend: first q token
-  int32_t mem0;      // cascade: first member index into group_reqs
+  int32_t mem0;      // cascade: first member index into group_reqs; tree: the request's drafted tokens
   int32_t csplit;    // cascade: prefix split
-  int32_t slot;      // cascade: partial slot of the members (level x max_csplits + split)
+  int32_t slot;      // cascade: partial slot of the members (level x max_csplits + split); tree: partial
+                     // slot of the item, -1 for an unsplit one
   int32_t tiles;     // query tiles holding valid rows (1: tile 1 is empty; its MMAs and softmax are skipped,
                      // while every barrier still completes its phases as for two tiles)
 };
 
 // Item -> job; false for an empty or invalid item (reported once, when `report`).
-template <bool EXTEND>
+template <int PASS>
 __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, bool report) {
   const int T = kRows / p.group;
   j.kh = item % p.hkv;
@@ -160,7 +174,19 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
   j.mem0 = 0;
   j.csplit = 0;
   j.slot = 0;
-  if constexpr (EXTEND) {
+  if constexpr (PASS == kTreePass) {
+    // the list holds only non-empty items of requests whose indices and lengths were checked when it was built
+    const int4 e = __ldg(reinterpret_cast<const int4*>(p.work_items) + rest);
+    const int32_t draft = __ldg(p.extend_lens + e.x), P = __ldg(p.prefix_lens + e.x), chunk = __ldg(p.tree_chunk);
+    j.table_row = __ldg(p.rpi + e.x);
+    j.n_valid = min(kTiles * T, draft - e.y * kTiles * T);
+    j.causal0 = P;
+    j.mem0 = draft;
+    j.kbeg = e.z * chunk;
+    j.kend = min(P + draft, j.kbeg + chunk);
+    j.q_tok0 = __ldg(p.qo_indptr + e.x) + e.y * kTiles * T;
+    j.slot = e.w;
+  } else if constexpr (PASS == kExtendPass) {
     // entry `rest` of the work list: it holds only non-empty query tiles of requests whose lengths
     // were checked (and flagged) when it was built
     const int b = __ldg(p.work_items + 2 * rest);
@@ -224,12 +250,14 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
 
 }  // namespace tc
 
-template <int D, int KS, int VS, bool EXTEND>
+template <int D, int KS, int VS, int PASS>
 __global__ void __launch_bounds__(tc::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using namespace tc;
   using L = Layout<D, KS, VS>;
+  constexpr bool EXTEND = PASS != kPrefixPass;  // rows are tokens of one request, items come from a list
+  constexpr bool TREE = PASS == kTreePass;
   constexpr int HALVES = D / 64;  // 128-byte (64-element) column blocks of a row
   // K/V stage release: one barrier per key tile t (ring of KVF), committed after the last MMA reading
   // K_t and V_t (PV of query tile 1).  KVF > max(KS, VS): a producer waiting for tile t's release
@@ -324,7 +352,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           idx = -1;
           break;
         }
-        if (tc_job<EXTEND>(p, idx, cj, lane == 0)) break;
+        if (tc_job<PASS>(p, idx, cj, lane == 0)) break;
       }
       if (lane == 0) {
         s_item[n % kItemRing] = idx;
@@ -615,8 +643,9 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       if (__any_sync(0xffffffffu, ri < 0)) { ok = false; break; }
       if (ri == 0) break;
       const bool row_valid = tok < jb.n_valid;
-      int32_t lim;  // exclusive key limit of this row
-      if constexpr (EXTEND) lim = row_valid ? jb.causal0 + tok + 1 : jb.kend;
+      int32_t lim;  // exclusive key limit of this row (tree: of the keys every row sees)
+      if constexpr (TREE) lim = jb.causal0;
+      else if constexpr (EXTEND) lim = row_valid ? jb.causal0 + tok + 1 : jb.kend;
       else lim = jb.kend;
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < jb.nt; ++j) {
@@ -632,6 +661,27 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         const int32_t key0 = jb.kbeg + j * kKeys;
         const bool masked = key0 + kKeys > lim;
         const bool warp_masked = __any_sync(0xffffffffu, masked);
+        // tree: bit e of vis[c] = key key0 + 32 c + e is visible to this row
+        uint32_t vis[4];
+        if constexpr (TREE) {
+          vis[0] = vis[1] = vis[2] = vis[3] = 0xffffffffu;
+          if (warp_masked) {
+            const uint32_t* mrow = p.tree_mask + (jb.q_tok0 + (row_valid ? tok : 0)) * p.mask_words;
+            auto word = [&](int32_t i) -> uint32_t {  // drafted tokens 32 i .. of this row's mask
+              const int32_t left = jb.mem0 - 32 * i;
+              if (left <= 0 || !row_valid) return 0u;
+              const uint32_t w = __ldg(mrow + i);
+              return left >= 32 ? w : w & ((1u << left) - 1u);
+            };
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int32_t off = key0 + 32 * c - lim;  // the chunk's first drafted token
+              if (off >= 0) vis[c] = __funnelshift_r(word(off >> 5), word((off >> 5) + 1), off & 31);
+              else if (off > -32) vis[c] = (word(0) << -off) | ((1u << -off) - 1u);
+            }
+          }
+        }
+        (void)vis;
         // Every tile is exponentiated against a reference in a single pass: the current one, or on the
         // item's first tile the maximum of its first 32 columns.  The row sum bounds every probability
         // of the row (p <= sum), so a sum above kFastSumLimit, or one that is not finite, marks the
@@ -651,7 +701,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           auto max_chunk = [&](const uint32_t (&sr)[32], int c) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const float x = (masked && key0 + c * 32 + e >= lim) ? -INFINITY : __uint_as_float(sr[e]);
+              const bool hidden = TREE ? !(vis[c] >> e & 1u) : masked && key0 + c * 32 + e >= lim;
+              const float x = hidden ? -INFINITY : __uint_as_float(sr[e]);
               mx8[e & 7] = fmaxf(mx8[e & 7], x);
             }
           };
@@ -698,8 +749,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             for (int e = 0; e < 16; ++e) {
               float s0 = __uint_as_float(sr[2 * e]), s1 = __uint_as_float(sr[2 * e + 1]);
               if constexpr (decltype(mask_tag)::value) {
-                if (key0 + c * 32 + 2 * e >= lim) s0 = -INFINITY;
-                if (key0 + c * 32 + 2 * e + 1 >= lim) s1 = -INFINITY;
+                if (TREE ? !(vis[c] >> (2 * e) & 1u) : key0 + c * 32 + 2 * e >= lim) s0 = -INFINITY;
+                if (TREE ? !(vis[c] >> (2 * e + 1) & 1u) : key0 + c * 32 + 2 * e + 1 >= lim) s1 = -INFINITY;
               }
               float t0, t1;
               f2_unpack(f2_fma(f2_pack(s0, s1), scale2, neg_m2), t0, t1);
@@ -730,7 +781,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sum8[2 * e], sum8[2 * e + 1]);
           rowsum = ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
           if (exact) break;
-          const bool stale = !(rowsum <= kFastSumLimit);
+          // (a tree row may see no key of the first tile's chunk 0, or of any tile so far: no reference yet)
+          const bool stale = !(rowsum <= kFastSumLimit) || (TREE && m_ref == -INFINITY);
           if (!__any_sync(0xffffffffu, stale)) break;
           exact = true;
         }
@@ -762,8 +814,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       const bool late = !mbar_wait(smem_u32(&bar_o[ti]), n & 1);
       if (__any_sync(0xffffffffu, late)) { ok = false; break; }
       tc_fence_after();
-      const float inv_l = 1.f / l;
-      if constexpr (EXTEND) {
+      const float inv_l = TREE && l == 0.f ? 0.f : 1.f / l;  // a tree row that sees nothing gives 0
+      if (EXTEND && (!TREE || jb.slot < 0)) {
         __nv_bfloat16* dst = p.o + ((jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G)) * static_cast<int64_t>(D);
         uint32_t oa[D / 32][32];
 #pragma unroll
@@ -786,10 +838,17 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       } else {
         // fp32 partial rows, one per thread, at [slot][member][q head] (the G heads of a member contiguous),
         // written in whole 32-byte sectors
-        const int32_t member = __ldg(p.group_reqs + jb.mem0 + (row_valid ? tok : 0));
-        const bool write = row_valid && member >= 0 && member < p.batch;
-        const int64_t ps = (static_cast<int64_t>(jb.slot) * p.batch + (write ? member : 0)) * p.hq + jb.kh * G + (r % G);
-        float* dst = p.casc_o + ps * D;
+        // (tree: at [slot][kv head][row of the item])
+        bool write = row_valid;
+        int64_t ps;
+        if constexpr (TREE) {
+          ps = (static_cast<int64_t>(jb.slot) * p.hkv + jb.kh) * p.part_rows + (row_valid ? ti * kRows + r : 0);
+        } else {
+          const int32_t member = __ldg(p.group_reqs + jb.mem0 + (row_valid ? tok : 0));
+          write = row_valid && member >= 0 && member < p.batch;
+          ps = (static_cast<int64_t>(jb.slot) * p.batch + (write ? member : 0)) * p.hq + jb.kh * G + (r % G);
+        }
+        float* dst = (TREE ? p.part_o : p.casc_o) + ps * D;
         uint32_t oa[D / 32][32];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tmem_ld32(tmem + lane_addr + col_o + c * 32, oa[c]);
@@ -808,7 +867,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                            __uint_as_float(ov[8 * e + 7]) * inv_l);
           }
         }
-        if (write) p.casc_lse[ps] = m_used + __log2f(l);
+        if (write) (TREE ? p.part_lse : p.casc_lse)[ps] = m_used + __log2f(l);
       }
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_ofree[ti]));

@@ -10,12 +10,9 @@
 // Sources: SGLang paper summary, §3 (reuse the cached prefix KV, compute
 // only the suffix); yaopepe.com explainer, §04 (the matched prefix is
 // referenced, the unmatched suffix is prefilled against it).
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "api_common.h"
 #include "attn_tc.cuh"
+#include "attn_tc_host.h"
 #include "decode_internal.h"
 
 namespace ra {
@@ -146,68 +143,13 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int32_t
   }
 }
 
-// K ring / V ring depths: the tensor core waits on K first, so K gets the deeper ring.
-template <int D>
-constexpr int k_stages() { return D == 128 ? 3 : 4; }
-template <int D>
-constexpr int v_stages() { return D == 128 ? 2 : 4; }
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-// 2-D view [rows, head_dim] of a bf16 array whose rows are head_dim contiguous elements, read as
-// one 64-element (128-byte, 128B-swizzled) column block of 1 row: the box a TMA gather4 takes.
-ra_status row_gather_map(CUtensorMap* map, const void* base, int64_t rows, int32_t head_dim) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (!encode) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  if (rows <= 0 || rows > INT32_MAX) return fail(RA_ERR_UNSUPPORTED, "%lld rows exceed a TMA row coordinate", (long long)rows);
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim) * 2};
-  cuuint32_t box[2] = {64, 1};
-  cuuint32_t elem[2] = {1, 1};
-  CUresult cr = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, elem,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (cr != CUDA_SUCCESS) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled(rows) failed (%d)", static_cast<int>(cr));
-  return RA_OK;
-}
-
-// Opt the kernel into its dynamic shared memory and check that it was compiled to the per-thread
-// register count its setmaxnreg split is balanced against (a split above the block's launch
-// allocation would leave the softmax warps waiting for registers that never come).
-template <typename Kern>
-ra_status set_smem(Kern kern, int bytes, bool* configured, int device) {
-  if (configured[device]) return RA_OK;
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cudaFuncGetAttributes(attn_tc): %s", cudaGetErrorString(e));
-  if (fa.numRegs != tc::kLaunchRegs)
-    return fail(RA_ERR_UNSUPPORTED, "attn_tc kernel compiled to %d registers per thread, its register split needs %d",
-                fa.numRegs, tc::kLaunchRegs);
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cudaFuncSetAttribute(attn_tc): %s", cudaGetErrorString(e));
-  configured[device] = true;
-  return RA_OK;
-}
-
 template <int D>
 ra_status launch_extend(const TcParams& p, const CUtensorMap& qmap, int64_t entries, cudaStream_t s) {
   CUtensorMap kmap, vmap;
   if (ra_status st = row_gather_map(&kmap, p.k_pool, p.num_slots * p.hkv, D)) return st;
   if (ra_status st = row_gather_map(&vmap, p.v_pool, p.num_slots * p.hkv, D)) return st;
   using L = tc::Layout<D, k_stages<D>(), v_stages<D>()>;
-  auto kern = attn_tc_kernel<D, k_stages<D>(), v_stages<D>(), true>;
+  auto kern = attn_tc_kernel<D, k_stages<D>(), v_stages<D>(), kExtendPass>;
   static bool configured[64] = {};
   DeviceInfo dev;
   if (ra_status st = current_device(&dev)) return st;
@@ -223,7 +165,7 @@ ra_status launch_extend(const TcParams& p, const CUtensorMap& qmap, int64_t entr
 template <int D>
 ra_status launch_prefix(const TcParams& p, int grid_x, int num_groups, int32_t wave, cudaStream_t s, int32_t* ctas) {
   using L = tc::Layout<D, k_stages<D>(), v_stages<D>()>;
-  auto kern = attn_tc_kernel<D, k_stages<D>(), v_stages<D>(), false>;
+  auto kern = attn_tc_kernel<D, k_stages<D>(), v_stages<D>(), kPrefixPass>;
   static bool configured[64] = {};
   DeviceInfo dev;
   if (ra_status st = current_device(&dev)) return st;
@@ -333,21 +275,8 @@ extern "C" ra_status ra_extend_attention(const void* k_pool, const void* v_pool,
   RA_REQUIRE(aligned16(workspace), "workspace must be 16-byte aligned");
   RA_REQUIRE(ws.cap * num_kv_heads < (int64_t(1) << 31), "too many extend tiles for one grid");
 
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (!encode) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  // q viewed as [total_q][Hq][D]; one box = 128/G tokens x the G heads of a kv head x 64 dims
-  const int rows_per_tile = 128 / group;
   CUtensorMap qmap;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_q_heads),
-                        static_cast<cuuint64_t>(total_q)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
-                           static_cast<cuuint64_t>(num_q_heads) * head_dim * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(rows_per_tile)};
-  cuuint32_t elem[3] = {1, 1, 1};
-  CUresult cr = encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, elem,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (cr != CUDA_SUCCESS) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled(q) failed (%d)", static_cast<int>(cr));
+  if (ra_status st = query_tile_map(&qmap, q, total_q, num_q_heads, head_dim, group)) return st;
 
   TcParams p{};
   p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
