@@ -10,12 +10,13 @@ hand-written CUDA kernels.  There is no fallback: if the library is missing
 or fails to load, importing the binding raises.
 
 Functions keep the C names: ``ra_kv_store``, ``ra_extend_attention``,
-``ra_decode_attention``, ``ra_decode_workspace_bytes``.
+``ra_decode_attention``, ``ra_decode_workspace_bytes``, ... .
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 from typing import Optional
 
@@ -37,6 +38,7 @@ RA_DECODE_STATIC_SCRATCH_BYTES = 32 << 20  # size of the library's static decode
 DEVERR_SLOT, DEVERR_TABLE, DEVERR_LENGTH, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 DEVERR_POSITION = 0x10
 _lib = None
+_binding = None
 
 
 class RAError(RuntimeError):
@@ -288,17 +290,29 @@ def ra_decode_attention_static(k_pool: torch.Tensor, v_pool: torch.Tensor, q: to
             _ptr(device_error, i32, "device_error", dev), _stream(dev, stream)))
 
 
-def _launch(fn, device: torch.device, stream, *args) -> None:
-    """fn(*args, stream) with `device` current (the library asks for the current device's properties)."""
-    if device.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got {device}")
-    if device.index == torch._C._cuda_getDevice():
-        status = fn(*args, _stream(device, stream))
-    else:
+def _native():
+    """The C side of the calls below: the same checks and the call, without ctypes' cost per argument."""
+    global _binding
+    if _binding is None:
+        lib = load()
+        if not os.path.exists(_build.BINDING):
+            raise ImportError(f"{_build.BINDING} is not built; run prefix_shared_kv_ra_gb300._build.build()")
+        spec = importlib.util.spec_from_file_location("_ra_binding", _build.BINDING)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        fns = (lib.ra_kv8_store, lib.ra_kv8_load, lib.ra_kv8_slot_bytes, lib.ra_kv8_decode_attention,
+               lib.ra_qk_norm_rope_store, lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention)
+        mod.init(torch.bfloat16, torch.int32, torch.float32, torch.uint8, torch._C._cuda_getCurrentRawStream,
+                 torch._C._cuda_getDevice, *(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
+        _binding = mod
+    return _binding
+
+
+def _failed(status: int, fn, device: torch.device, *args) -> None:
+    if status == -1:  # another device is current: the library asks for the current device's properties
         with torch.cuda.device(device):
-            status = fn(*args, _stream(device, stream))
-    if status != RA_OK:
-        _check(status)
+            status = fn(*args)
+    _check(status)
 
 
 @functools.lru_cache(maxsize=None)
@@ -310,40 +324,22 @@ def ra_kv8_slot_bytes(num_kv_heads: int, head_dim: int) -> int:
     return n
 
 
-def _kv8_pool(kv8_pool: torch.Tensor, num_kv_heads: int, head_dim: int):
-    """Pointer and slots of a quantised pool, uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)]."""
-    shape = kv8_pool.shape
-    if len(shape) != 2 or shape[1] != ra_kv8_slot_bytes(num_kv_heads, head_dim):
-        raise ValueError(f"kv8_pool must be [num_slots, {ra_kv8_slot_bytes(num_kv_heads, head_dim)}]")
-    return _ptr(kv8_pool, torch.uint8, "kv8_pool", kv8_pool.device), shape[0]
-
-
 def ra_kv8_store(kv8_pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, out_cache_loc: torch.Tensor,
                  device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise new K/V rows ([num_tokens, Hkv, D] bf16) into the records of slots out_cache_loc."""
-    dev = kv8_pool.device
-    n, hkv, d = k_new.shape
-    if v_new.shape != k_new.shape or out_cache_loc.shape != (n,):
-        raise ValueError("k_new and v_new must be [num_tokens, Hkv, D] and out_cache_loc [num_tokens]")
-    pool, slots = _kv8_pool(kv8_pool, hkv, d)
-    bf, i32 = torch.bfloat16, torch.int32
-    _launch(load().ra_kv8_store, dev, stream, pool, slots, hkv, d, _ptr(k_new, bf, "k_new", dev),
-            _ptr(v_new, bf, "v_new", dev), _ptr(out_cache_loc, i32, "out_cache_loc", dev), n,
-            _ptr(device_error, i32, "device_error", dev))
+    args = (kv8_pool, k_new, v_new, out_cache_loc, device_error, stream)
+    status = _native().kv8_store(*args)
+    if status:
+        _failed(status, _native().kv8_store, kv8_pool.device, *args)
 
 
 def ra_kv8_load(kv8_pool: torch.Tensor, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
                 device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Read the records of `slots` back into K/V rows ([num_tokens, Hkv, D] bf16), exactly."""
-    dev = kv8_pool.device
-    n, hkv, d = k_out.shape
-    if v_out.shape != k_out.shape or slots.shape != (n,):
-        raise ValueError("k_out and v_out must be [num_tokens, Hkv, D] and slots [num_tokens]")
-    pool, num_slots = _kv8_pool(kv8_pool, hkv, d)
-    bf, i32 = torch.bfloat16, torch.int32
-    _launch(load().ra_kv8_load, dev, stream, pool, num_slots, hkv, d, _ptr(slots, i32, "slots", dev),
-            _ptr(k_out, bf, "k_out", dev), _ptr(v_out, bf, "v_out", dev), n,
-            _ptr(device_error, i32, "device_error", dev))
+    args = (kv8_pool, slots, k_out, v_out, device_error, stream)
+    status = _native().kv8_load(*args)
+    if status:
+        _failed(status, _native().kv8_load, kv8_pool.device, *args)
 
 
 def ra_kv8_decode_attention(kv8_pool: torch.Tensor, q: torch.Tensor, o: torch.Tensor, req_to_token: torch.Tensor,
@@ -352,57 +348,11 @@ def ra_kv8_decode_attention(kv8_pool: torch.Tensor, q: torch.Tensor, o: torch.Te
                             device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """ra_decode_attention over a quantised pool (uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)]); q, o
     [batch, Hq, D] bf16; workspace: uint8, ra_decode_workspace_bytes(batch, Hq, Hkv, D, max_seq_len)."""
-    dev = kv8_pool.device
-    batch, hq, d = q.shape
-    if o.shape != q.shape:
-        raise ValueError("q/o shape mismatch")
-    if req_pool_indices.shape != (batch,) or seq_lens.shape != (batch,) or req_to_token.dim() != 2:
-        raise ValueError("req_pool_indices and seq_lens must be [batch], req_to_token 2-D")
-    pool, num_slots = _kv8_pool(kv8_pool, num_kv_heads, d)
-    bf, i32 = torch.bfloat16, torch.int32
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
-    _launch(
-        load().ra_kv8_decode_attention, dev, stream, pool, num_slots, num_kv_heads, d, _ptr(q, bf, "q", dev), _ptr(o, bf, "o", dev), hq, float(sm_scale),
-        _ptr(req_to_token, i32, "req_to_token", dev), req_to_token.shape[1], req_to_token.shape[0],
-        _ptr(req_pool_indices, i32, "req_pool_indices", dev), _ptr(seq_lens, i32, "seq_lens", dev), batch,
-        int(max_seq_len), workspace.data_ptr(), workspace.numel(),
-        _ptr(device_error, i32, "device_error", dev))
-
-
-def _head_rows(t: torch.Tensor, shape, name: str, device: torch.device):
-    """Pointer and token stride (elements) of bf16 head rows [num_tokens, H, D]: a token's rows contiguous,
-    tokens at any stride (a slice of a fused projection's output)."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    n, h, d = shape
-    st, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and h > 1):
-        raise ValueError(f"{name}: a token's head rows must be contiguous")
-    return t.data_ptr(), st if n > 1 else h * d
-
-
-def _norm_rope_args(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, eps, interleaved, dev):
-    q_shape, k_shape = q.shape, k.shape
-    n, hq, d = q_shape
-    hkv = k_shape[1]
-    if k_shape[0] != n or k_shape[2] != d:
-        raise ValueError("q must be [num_tokens, Hq, D] and k, v [num_tokens, Hkv, D]")
-    if positions.shape != (n,) or cos_sin.dim() != 2:
-        raise ValueError("positions must be [num_tokens] and cos_sin [max_position, rotary_dim]")
-    for w in (q_weight, k_weight):
-        if w is not None and w.shape != (d,):
-            raise ValueError("weights must be [D]")
-    bf = torch.bfloat16
-    max_position, rotary_dim = cos_sin.shape
-    return (*_head_rows(q, q_shape, "q", dev), *_head_rows(k, k_shape, "k", dev), *_head_rows(v, k_shape, "v", dev),
-            hq, hkv, d, _ptr(q_weight, bf, "q_weight", dev), _ptr(k_weight, bf, "k_weight", dev), float(eps),
-            _ptr(positions, torch.int32, "positions", dev), _ptr(cos_sin, torch.float32, "cos_sin", dev),
-            max_position, rotary_dim, 1 if interleaved else 0, *_head_rows(q_out, q_shape, "q_out", dev))
+    args = (kv8_pool, q, o, req_to_token, req_pool_indices, seq_lens, num_kv_heads, max_seq_len, sm_scale, workspace,
+            device_error, stream)
+    status = _native().kv8_decode(*args)
+    if status:
+        _failed(status, _native().kv8_decode, kv8_pool.device, *args)
 
 
 def ra_qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -413,16 +363,11 @@ def ra_qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
     """Per-head RMS norm of q and k, their rotation by cos_sin[positions] (fp32 [max_position, rotary_dim]:
     cosines, then sines), q written to q_out, k and v to pool slots out_cache_loc.  q, k, v, q_out
     [num_tokens, H, D] bf16, any token stride; weights [D] bf16, or None for no norm."""
-    dev = k_pool.device
-    args = _norm_rope_args(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, eps, interleaved, dev)
-    if k_pool.dim() != 3 or k_pool.shape[1:] != k.shape[1:] or v_pool.shape != k_pool.shape:
-        raise ValueError("pools must be [num_slots, Hkv, D]")
-    if out_cache_loc.shape != (q.shape[0],):
-        raise ValueError("out_cache_loc must be [num_tokens]")
-    bf, i32 = torch.bfloat16, torch.int32
-    _launch(
-        load().ra_qk_norm_rope_store, dev, stream, *args, _ptr(k_pool, bf, "k_pool", dev), _ptr(v_pool, bf, "v_pool", dev), k_pool.shape[0],
-        _ptr(out_cache_loc, i32, "out_cache_loc", dev), q.shape[0], _ptr(device_error, i32, "device_error", dev))
+    args = (q, k, v, q_weight, k_weight, positions, cos_sin, q_out, k_pool, v_pool, out_cache_loc, eps, interleaved,
+            device_error, stream)
+    status = _native().norm_rope_store(*args)
+    if status:
+        _failed(status, _native().norm_rope_store, k_pool.device, *args)
 
 
 def ra_qk_norm_rope_kv8_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -431,15 +376,11 @@ def ra_qk_norm_rope_kv8_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                               eps: float = 1e-6, interleaved: bool = False,
                               device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """ra_qk_norm_rope_store into a quantised pool (uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)])."""
-    dev = kv8_pool.device
-    args = _norm_rope_args(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, eps, interleaved, dev)
-    pool, num_slots = _kv8_pool(kv8_pool, k.shape[1], k.shape[2])
-    if out_cache_loc.shape != (q.shape[0],):
-        raise ValueError("out_cache_loc must be [num_tokens]")
-    i32 = torch.int32
-    _launch(
-        load().ra_qk_norm_rope_kv8_store, dev, stream, *args, pool, num_slots, _ptr(out_cache_loc, i32, "out_cache_loc", dev), q.shape[0],
-        _ptr(device_error, i32, "device_error", dev))
+    args = (q, k, v, q_weight, k_weight, positions, cos_sin, q_out, kv8_pool, out_cache_loc, eps, interleaved,
+            device_error, stream)
+    status = _native().norm_rope_kv8_store(*args)
+    if status:
+        _failed(status, _native().norm_rope_kv8_store, kv8_pool.device, *args)
 
 
 def ra_tree_workspace_bytes(batch: int, total_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -456,24 +397,8 @@ def ra_tree_attention(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Tenso
     """Drafted tokens (q, o [total_q, Hq, D] bf16, request b's rows from qo_indptr[b]) over their request's
     cached prefix and the drafted tokens named by their bit masks (tree_mask int32 [total_q, words], bit c % 32
     of word c / 32 = drafted token c of the request is visible)."""
-    dev = k_pool.device
-    num_slots, hkv, d = k_pool.shape
-    total_q, hq, dq = q.shape
-    batch = req_pool_indices.shape[0]
-    if v_pool.shape != k_pool.shape or dq != d or o.shape != q.shape:
-        raise ValueError("pools must be [num_slots, Hkv, D] and q, o [total_q, Hq, D]")
-    if prefix_lens.shape != (batch,) or draft_lens.shape != (batch,) or qo_indptr.shape != (batch + 1,):
-        raise ValueError("req_pool_indices, prefix_lens and draft_lens must be [batch], qo_indptr [batch + 1]")
-    if tree_mask.dim() != 2 or tree_mask.shape[0] != total_q or req_to_token.dim() != 2:
-        raise ValueError("tree_mask must be [total_q, words] and req_to_token 2-D")
-    bf, i32 = torch.bfloat16, torch.int32
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
-    _launch(
-        load().ra_tree_attention, dev, stream, _ptr(k_pool, bf, "k_pool", dev), _ptr(v_pool, bf, "v_pool", dev),
-        num_slots, hkv, d, _ptr(q, bf, "q", dev), _ptr(o, bf, "o", dev), hq, float(sm_scale),
-        _ptr(req_to_token, i32, "req_to_token", dev), req_to_token.shape[1], req_to_token.shape[0],
-        _ptr(req_pool_indices, i32, "req_pool_indices", dev), _ptr(prefix_lens, i32, "prefix_lens", dev),
-        _ptr(draft_lens, i32, "draft_lens", dev), _ptr(qo_indptr, i32, "qo_indptr", dev),
-        _ptr(tree_mask, i32, "tree_mask", dev), tree_mask.shape[1], batch, total_q, int(max_draft_len),
-        int(max_prefix_len), workspace.data_ptr(), workspace.numel(), _ptr(device_error, i32, "device_error", dev))
+    args = (k_pool, v_pool, q, o, req_to_token, req_pool_indices, prefix_lens, draft_lens, qo_indptr, tree_mask,
+            max_draft_len, max_prefix_len, sm_scale, workspace, device_error, stream)
+    status = _native().tree(*args)
+    if status:
+        _failed(status, _native().tree, k_pool.device, *args)

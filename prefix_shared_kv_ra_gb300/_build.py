@@ -3,7 +3,8 @@
 Each translation unit is compiled in parallel to an object file under
 ``_build/``; they are linked into ``prefix_shared_kv_ra_gb300/libra.so``
 (static cudart, no libcuda link dependency: the driver entry points the
-library needs are resolved at run time).  A rebuild happens only when a
+library needs are resolved at run time).  ``_ra_binding.so`` beside it is the Python
+side of the small operators, plain C.  A rebuild happens only when a
 source or header is newer than the library.
 """
 from __future__ import annotations
@@ -13,12 +14,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libra.so")
+BINDING = os.path.join(PKG, "_ra_binding.so")  # argument checks of the small operators (CPython API, no CUDA)
 SOURCES = ["api_common.cu", "kv_store.cu", "decode.cu", "extend.cu", "decode_static.cu",
            "kv8_store.cu", "decode_kv8.cu", "qk_norm_rope.cu", "tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,7 +48,21 @@ def _stale(target: str) -> bool:
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
+def build_binding(force: bool = False) -> str:
+    if not force and not _stale(BINDING):
+        return BINDING
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I",
+                        sysconfig.get_paths()["include"], os.path.join(CSRC, "py_binding.c"), "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for py_binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    build_binding(force)
     if not force and not _stale(LIB):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
