@@ -23,7 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libra.so")
 BINDING = os.path.join(PKG, "_ra_binding.so")  # argument checks of the small operators (CPython API, no CUDA)
 SOURCES = ["api_common.cu", "kv_store.cu", "decode.cu", "extend.cu", "decode_static.cu",
-           "kv8_store.cu", "decode_kv8.cu", "qk_norm_rope.cu", "tree.cu"]
+           "kv8_store.cu", "decode_kv8.cu", "qk_norm_rope.cu", "tree.cu", "tree_narrow.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]

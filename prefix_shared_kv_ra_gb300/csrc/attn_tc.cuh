@@ -94,7 +94,8 @@ struct TcParams {
   float* casc_o;    // [casc_slots, batch, hq, D]
   float* casc_lse;  // [casc_slots, batch, hq]
   // draft tree (rpi, prefix_lens, qo_indptr, o and the work list as for extend; extend_lens are the draft
-  // lengths; work_items are [4 * entries]: request, query tile, key split, partial slot or -1)
+  // lengths; work_items are [8 * entries]: request, query tile, key split, partial slot or -1; prefix length,
+  // drafted tokens, table row, first query row)
   const uint32_t* tree_mask;  // [total_q, mask_words]
   int32_t mask_words;
   const int32_t* tree_chunk;  // keys per split (a multiple of 128)
@@ -176,15 +177,16 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
   j.slot = 0;
   if constexpr (PASS == kTreePass) {
     // the list holds only non-empty items of requests whose indices and lengths were checked when it was built
-    const int4 e = __ldg(reinterpret_cast<const int4*>(p.work_items) + rest);
-    const int32_t draft = __ldg(p.extend_lens + e.x), P = __ldg(p.prefix_lens + e.x), chunk = __ldg(p.tree_chunk);
-    j.table_row = __ldg(p.rpi + e.x);
-    j.n_valid = min(kTiles * T, draft - e.y * kTiles * T);
-    j.causal0 = P;
-    j.mem0 = draft;
+    const int4 e = __ldg(reinterpret_cast<const int4*>(p.work_items) + 2 * rest);
+    const int4 f = __ldg(reinterpret_cast<const int4*>(p.work_items) + 2 * rest + 1);
+    const int32_t chunk = __ldg(p.tree_chunk);
+    j.table_row = f.z;
+    j.n_valid = min(kTiles * T, f.y - e.y * kTiles * T);
+    j.causal0 = f.x;
+    j.mem0 = f.y;
     j.kbeg = e.z * chunk;
-    j.kend = min(P + draft, j.kbeg + chunk);
-    j.q_tok0 = __ldg(p.qo_indptr + e.x) + e.y * kTiles * T;
+    j.kend = min(f.x + f.y, j.kbeg + chunk);
+    j.q_tok0 = f.w + e.y * kTiles * T;
     j.slot = e.w;
   } else if constexpr (PASS == kExtendPass) {
     // entry `rest` of the work list: it holds only non-empty query tiles of requests whose lengths

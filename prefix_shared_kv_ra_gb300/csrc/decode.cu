@@ -747,19 +747,15 @@ ra_status launch_decode(const DecodeParams& p, int grid, int smem, cudaStream_t 
   }
   if (ra_status st = launch_pdl("decode_kernel", kern, dim3(grid), dim3(32 * (p.hpc + kProducers + 1)), smem, stream, p))
     return st;
-  return launch_decode_combine(p, D, stream);
+  const int nwarps = p.batch * p.hq;
+  return launch_pdl("decode_combine_kernel", decode_combine_kernel<D>, dim3((nwarps + kCombineWarps - 1) / kCombineWarps),
+                    dim3(32 * kCombineWarps), 0, stream, p);
 }
 
 }  // namespace
 
 ra_status launch_decode_plan(const DecodeParams& p, int store_ctas, cudaStream_t stream) {
   return launch_pdl("decode_plan_kernel", decode_plan_kernel, dim3(1 + store_ctas), dim3(kPlanThreads), 0, stream, p);
-}
-
-ra_status launch_decode_combine(const DecodeParams& p, int32_t head_dim, cudaStream_t stream) {
-  const int nwarps = p.batch * p.hq;
-  return launch_pdl("decode_combine_kernel", head_dim == 128 ? decode_combine_kernel<128> : decode_combine_kernel<64>,
-                    dim3((nwarps + kCombineWarps - 1) / kCombineWarps), dim3(32 * kCombineWarps), 0, stream, p);
 }
 
 void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace) {

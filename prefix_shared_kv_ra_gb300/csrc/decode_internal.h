@@ -113,9 +113,8 @@ DecodeWorkspace layout_decode_workspace(int32_t batch, int32_t num_q_heads, int3
 int32_t heads_per_cta(int32_t num_kv_heads);  // kv heads per work item: the largest divisor of Hkv that is <= 8
 // Point p's scratch members into a workspace of layout wl (p.batch set before).
 void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace);
-// The call's plan kernel (CTA 0) and combine kernel, around a decode kernel that counts its partials.
+// The call's plan kernel: CTA 0 plans, `store_ctas` more run the fused store.
 ra_status launch_decode_plan(const DecodeParams& p, int store_ctas, cudaStream_t stream);
-ra_status launch_decode_combine(const DecodeParams& p, int32_t head_dim, cudaStream_t stream);
 
 // Tensor-core pass over each group's shared prefix: writes p.casc_o / p.casc_lse
 // for every member (defined with the tcgen05 attention kernel).

@@ -30,18 +30,13 @@
 #include "decode_item.cuh"
 #include "kv8.cuh"
 #include "ra_ptx.cuh"
+#include "slab_ring.cuh"
 
 namespace ra {
 
 namespace {
 
 constexpr int kSlab = 32;          // keys per ring stage
-constexpr int kMaxStages = 8;
-constexpr int kItemRing = 16;      // published items; the leader runs at most nstage + 1 items ahead
-constexpr int kProducers = 4;      // warps issuing a slab's bulk copies, kSlab / kProducers records each
-constexpr int kRowsPerProducer = kSlab / kProducers;
-constexpr int kHdrBytes = 640;     // full/empty barriers, item ring, abort flag, item / done / free barriers
-constexpr int kSmemLimit = 227 * 1024;
 constexpr float kRescale = 8.0f;   // log2 units: a reference moves when a score exceeds it by more
 constexpr int kQExp = 14;          // q's largest value in f16
 
@@ -50,6 +45,28 @@ struct Kv8DecodeParams {
   const uint8_t* pool;
   int64_t slot_bytes;
   int32_t block_bytes;
+};
+
+// The producers' view: one bulk copy per key, the head group's block of the slot's record.
+struct Kv8Source {
+  const Kv8DecodeParams& pp;
+  int32_t* counter;
+  int64_t num_slots;
+  uint32_t* err;
+  __device__ __forceinline__ explicit Kv8Source(const Kv8DecodeParams& q)
+      : pp(q), counter(q.d.counter), num_slots(q.d.num_slots), err(q.d.err) {}
+  __device__ __forceinline__ int32_t claims() const { return pp.d.plan[0] * pp.d.n_hgroups; }
+  __device__ __forceinline__ void item(int32_t idx, SlabKeys& k) const {
+    Item it;
+    decode_item(pp.d, idx, it);
+    k = SlabKeys{pp.d.table + static_cast<int64_t>(it.row) * pp.d.table_stride, it.k0, it.k1, it.hg};
+  }
+  __device__ __forceinline__ uint32_t key_bytes() const { return pp.block_bytes; }
+  __device__ __forceinline__ void copy(uint32_t stage, int key, int32_t slot, int32_t group, uint32_t bar) const {
+    bulk_g2s(stage + key * pp.block_bytes,
+             pp.pool + static_cast<int64_t>(slot) * pp.slot_bytes + static_cast<int64_t>(group) * pp.block_bytes,
+             pp.block_bytes, bar);
+  }
 };
 
 // D[16x8] += A[16x16] (row) * B[16x8] (col), f16 inputs, fp32 accumulate.
@@ -86,10 +103,10 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   return v;
 }
 
-// Warp roles as in the bf16 decode kernel: hpc consumer warps (one kv head each), kProducers copy warps, of
-// which the first claims the items, and a signal warp that counts each request's finished partials.
+// Warp roles: hpc consumer warps (one kv head each), the ring's copy warps, and a signal warp that counts each
+// request's finished partials for the combine and frees the item entries.
 template <int D>
-__global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1)
+__global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1)
     kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams pp) {
   const DecodeParams& p = pp.d;
   constexpr int KW = D / 16;  // words of a K row per lane = MMA k steps of the scores
@@ -99,151 +116,28 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nc = p.hpc;
-  const int ns = p.nstage;
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t full0 = sbase;        // ns mbarriers (kProducers arrivals + bytes)
-  const uint32_t empty0 = sbase + 64;  // ns mbarriers (nc consumer arrivals)
-  volatile int32_t* s_items = reinterpret_cast<volatile int32_t*>(smem + 128);
-  volatile int32_t* s_abort = reinterpret_cast<volatile int32_t*>(smem + 192);
-  const uint32_t item0 = sbase + 256;  // kItemRing mbarriers: entry published
-  const uint32_t done0 = sbase + 384;  // kItemRing mbarriers: every consumer warp is done with the entry
-  const uint32_t free0 = sbase + 512;  // kItemRing mbarriers: the signal warp has read the entry (slot free)
-  const uint32_t stage0 = sbase + kHdrBytes;
   const int RS = p.row_stride;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < ns; ++s) {
-      mbar_init(full0 + 8 * s, kProducers);
-      mbar_init(empty0 + 8 * s, nc);
-    }
-    for (int s = 0; s < kItemRing; ++s) {
-      mbar_init(item0 + 8 * s, 1);
-      mbar_init(done0 + 8 * s, nc);
-      mbar_init(free0 + 8 * s, 1);
-    }
-    *s_abort = 0;
-    fence_mbar_init();
-  }
+  const SlabRing rg(smem, p.nstage, p.stage_bytes);
+  if (threadIdx.x == 0) rg.init(nc, 1);
   __syncthreads();
   griddep_wait();  // the plan, its reset counters and everything before them are complete
   griddep_launch();  // the combine may launch: it waits per request for the partials it merges
 
-  if (warp >= nc && warp < nc + kProducers) {
-    // ================================================================ producers
-    const int pw = warp - nc;
-    const bool leader = pw == 0;
-    const int key_in_slab = pw * kRowsPerProducer + lane;  // this lane's record of a slab (lane < kRowsPerProducer)
-    const uint32_t row_off = key_in_slab * RS;
-    int32_t n_claims = 0;
-    auto claim = [&]() -> int32_t {  // warp-collective
-      int32_t idx = 0;
-      if (lane == 0) idx = atomicAdd(p.counter, 1);
-      idx = __shfl_sync(0xffffffffu, idx, 0);
-      return idx < n_claims ? idx : -1;
-    };
-    // entry n reuses the ring slot of entry n - kItemRing: the signal warp, the last reader, must have read it
-    auto publish = [&](int32_t n, int32_t idx) -> bool {
-      if (n >= kItemRing && !mbar_wait(free0 + 8 * (n % kItemRing), ((n / kItemRing) - 1) & 1)) return false;
-      if (lane == 0) {
-        s_items[n % kItemRing] = idx;
-        mbar_arrive(item0 + 8 * (n % kItemRing));
-      }
-      return true;
-    };
-    // 1: item n in `it`; 0: end of work; -1: a bounded wait ran out
-    auto next_item = [&](int32_t n, Item& it) -> int {
-      if (!mbar_wait(item0 + 8 * (n % kItemRing), (n / kItemRing) & 1)) return -1;
-      const int32_t idx = s_items[n % kItemRing];
-      if (idx < 0) return 0;
-      decode_item(p, idx, it);
-      return 1;
-    };
-    auto load_slot = [&](const Item& it, int32_t s) -> int32_t {  // records past the range repeat the last key
-      if (lane >= kRowsPerProducer) return 0;
-      const int32_t nk = it.k1 - it.k0;
-      int32_t key = s * kSlab + key_in_slab;
-      key = key < nk ? key : nk - 1;
-      return __ldg(p.table + static_cast<int64_t>(it.row) * p.table_stride + it.k0 + key);
-    };
-    n_claims = p.plan[0] * p.n_hgroups;
-    bool ok = true;
-    if (leader) ok = __all_sync(0xffffffffu, publish(0, claim()));
-    int32_t n = 0, c = 0, s = 0;
-    Item it;
-    int r = ok ? next_item(0, it) : -1;
-    ok = r >= 0;
-    int32_t slot = r > 0 ? load_slot(it, 0) : 0;
-    while (ok && r > 0) {
-      const int32_t n_slabs = (it.k1 - it.k0 + kSlab - 1) / kSlab;
-      // the leader claims the next item when this one has ns slabs left to issue (the claim overlaps them)
-      if (leader && s == (n_slabs > ns ? n_slabs - ns : 0) && !__all_sync(0xffffffffu, publish(n + 1, claim()))) {
-        ok = false;
-        break;
-      }
-      // one slab ahead: the next (item, slab) and its slot id
-      Item it2 = it;
-      int32_t s2 = s + 1, n2 = n;
-      int r2 = 1;
-      if (s2 == n_slabs) {
-        n2 = n + 1;
-        s2 = 0;
-        r2 = next_item(n2, it2);
-        if (r2 < 0) { ok = false; break; }
-      }
-      const int32_t slot2 = r2 > 0 ? load_slot(it2, s2) : 0;
-      // slab s of item n into stage c % ns
-      const int st = c % ns;
-      if (c >= ns && !mbar_wait(empty0 + 8 * st, ((c / ns) + 1) & 1)) { ok = false; break; }
-      if (*s_abort) { ok = false; break; }
-      if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * st, kRowsPerProducer * pp.block_bytes);
-      __syncwarp();
-      if (lane < kRowsPerProducer) {
-        int32_t sl = slot;
-        if (sl < 0 || sl >= p.num_slots) {
-          flag_error(p.err, RA_DEVERR_SLOT);
-          sl = 0;
-        }
-        bulk_g2s(stage0 + st * p.stage_bytes + row_off,
-                 pp.pool + static_cast<int64_t>(sl) * pp.slot_bytes + it.hg * pp.block_bytes, pp.block_bytes,
-                 full0 + 8 * st);
-      }
-      ++c;
-      it = it2;
-      s = s2;
-      n = n2;
-      r = r2;
-      slot = slot2;
-    }
-    if (ok) {
-      // end of work (entry n holds -1): every producer arrives on the next stage, the consumers read
-      // the marker from it
-      const int st = c % ns;
-      if (c >= ns && !mbar_wait(empty0 + 8 * st, ((c / ns) + 1) & 1)) ok = false;
-      if (ok && lane == 0) mbar_arrive(full0 + 8 * st);
-    }
-    if (!ok) {
-      if (lane == 0) {
-        *s_abort = 1;
-        flag_error(p.err, RA_DEVERR_TIMEOUT);
-      }
-      // copies this warp issued must land before the CTA leaves
-      for (int32_t j = (c > ns ? c - ns : 0); j < c; ++j) mbar_wait(full0 + 8 * (j % ns), (j / ns) & 1);
-    }
+  if (warp >= nc && warp < nc + kRingProducers) {
+    slab_producer<kSlab>(rg, Kv8Source(pp), warp - nc);
     return;
   }
-  if (warp == nc + kProducers) {
+  if (warp == nc + kRingProducers) {
     // ================================================================ signaller
     for (int32_t n = 0;; ++n) {
-      const int e = n % kItemRing;
-      if (!mbar_wait(done0 + 8 * e, (n / kItemRing) & 1)) {
-        if (lane == 0) {
-          *s_abort = 1;
-          flag_error(p.err, RA_DEVERR_TIMEOUT);
-        }
+      const int e = n % kRingEntries;
+      if (!mbar_wait(rg.done0 + 8 * e, (n / kRingEntries) & 1)) {
+        if (lane == 0) rg.give_up(p.err);
         break;
       }
-      const int32_t idx = s_items[e];
+      const int32_t idx = rg.items[e];
       __syncwarp();
-      if (lane == 0) mbar_arrive(free0 + 8 * e);
+      if (lane == 0) mbar_arrive(rg.free0 + 8 * e);
       if (idx < 0) break;
       if (lane == 0) {
         Item it;
@@ -257,7 +151,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1)
     }
     return;
   }
-  if (warp > nc + kProducers) return;
+  if (warp > nc + kRingProducers) return;
 
   // ================================================================ consumers
   const int g = lane >> 2;
@@ -268,13 +162,11 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1)
   int32_t n = 0, c = 0;
   bool clean = false;  // left through the end marker
   for (;; ++n) {
-    int st = c % ns;
-    if (!mbar_wait(full0 + 8 * st, (c / ns) & 1) || *s_abort) break;
-    const int32_t idx = s_items[n % kItemRing];
+    const int32_t idx = rg.entry(n);
     if (idx < 0) {
-      clean = true;
+      clean = idx == -1;
       __syncwarp();
-      if (lane == 0) mbar_arrive(done0 + 8 * (n % kItemRing));  // the signal warp reads the end marker
+      if (clean && lane == 0) mbar_arrive(rg.done0 + 8 * (n % kRingEntries));  // the signal warp reads the end marker
       break;
     }
     Item it;
@@ -316,9 +208,9 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1)
     const int32_t n_slabs = (it.k1 - it.k0 + kSlab - 1) / kSlab;
     bool ok = true;
     for (int32_t s = 0; s < n_slabs; ++s, ++c) {
-      st = c % ns;
-      if (s > 0 && !mbar_wait(full0 + 8 * st, (c / ns) & 1)) { ok = false; break; }
-      const uint32_t stage = stage0 + st * p.stage_bytes;
+      const int st = c % rg.nstage;
+      if (!mbar_wait(rg.full0 + 8 * st, (c / rg.nstage) & 1)) { ok = false; break; }
+      const uint32_t stage = rg.stage0 + st * rg.stage_bytes;
       // S^T[16 keys x 8 heads] = K Q^T for the slab's halves
       float x[kSlab / 16][4], y[kSlab / 16][4];
 #pragma unroll
@@ -408,7 +300,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * st);
+      if (lane == 0) mbar_arrive(rg.empty0 + 8 * st);
     }
     if (!ok) break;
 #pragma unroll
@@ -451,13 +343,79 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1)
     }
     // this warp's part of the entry is written (__syncwarp orders the lanes' stores before lane 0's release)
     __syncwarp();
-    if (lane == 0) mbar_arrive(done0 + 8 * (n % kItemRing));
+    if (lane == 0) mbar_arrive(rg.done0 + 8 * (n % kRingEntries));
   }
-  if (!clean && lane == 0) {
-    // a bounded wait ran out: stop the producers as well
-    *s_abort = 1;
-    flag_error(p.err, RA_DEVERR_TIMEOUT);
+  if (!clean && lane == 0) rg.give_up(p.err);  // a bounded wait ran out: stop the producers as well
+}
+
+// Merge the partials of every split request, `per_row` warps per (request, q head) row, each a share of the
+// partials.  Launched while the decode kernel runs: a row waits only for its own request's count of finished
+// (item, head group) partials, so early requests merge while others are read.  One warp per row serves large
+// batches; few rows with many splits would wait on one warp's chain of loads (32 rows of 108 partials: 18 us
+// with one warp each, 5 us with eight).
+constexpr int kCombineWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_kernel(const __grid_constant__ DecodeParams p,
+                                                                         int per_row) {
+  constexpr int V = D / 32;
+  constexpr int kAhead = 8;
+  __shared__ float s_acc[kCombineWarps][32 * V], s_m[kCombineWarps], s_w[kCombineWarps];
+  griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = warp % per_row;
+  const int64_t bh = static_cast<int64_t>(blockIdx.x) * (kCombineWarps / per_row) + warp / per_row;
+  const bool in = bh < static_cast<int64_t>(p.batch) * p.hq;
+  const int32_t b = in ? static_cast<int32_t>(bh / p.hq) : 0;
+  const int32_t h = in ? static_cast<int32_t>(bh - static_cast<int64_t>(b) * p.hq) : 0;
+  // the plan completed before the decode kernel let this one launch
+  const int32_t L = __ldg(p.seq_lens + b), row = __ldg(p.rpi + b);
+  const int32_t i0 = __ldcg(p.req_item0 + b), n = __ldcg(p.req_item0 + b + 1) - i0;
+  bool merge = in && n > 1 && L >= 1 && row >= 0 && row < p.table_rows;  // the others: written directly, or invalid
+  if (merge) {
+    bool ready = true;
+    if (lane == 0 && !(ready = wait_count(p.req_done + b, n * p.n_hgroups))) flag_error(p.err, RA_DEVERR_TIMEOUT);
+    merge = __shfl_sync(0xffffffffu, ready, 0);
+    // every lane reads the count itself: with the fence its loads of the partials follow an acquire
+    (void)ld_relaxed_gpu(p.req_done + b);
+    fence_acq_rel_gpu();
   }
+  float acc[V], m = -INFINITY, wsum = 0.f;
+  merge_partials<V, kAhead>(
+      merge ? n : 0, share, per_row,
+      [&](int s) { return __ldcg(p.part_lse + static_cast<int64_t>(i0 + s) * p.hq + h); },
+      [&](int s, float(&x)[V]) {
+        load_row_cg<V>(p.part_o + (static_cast<int64_t>(i0 + s) * p.hq + h) * D + lane * V, x);
+      },
+      acc, m, wsum);
+  if (per_row > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
+    if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
+    __syncthreads();
+    if (share == 0) {
+      float top = m;
+      for (int k = 1; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = 0.f;
+      wsum = 0.f;
+      for (int k = 0; k < per_row; ++k) {
+        const float f = ex2(s_m[warp + k] - ref);
+        wsum = fmaf(f, s_w[warp + k], wsum);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(f, s_acc[warp + k][lane * V + v], acc[v]);
+      }
+    }
+  }
+  if (merge && share == 0) {
+    const float inv = 1.f / wsum;
+    __nv_bfloat16* dst = p.o + bh * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+  }
+  griddep_wait();  // this grid's completion implies the decode kernel's
 }
 
 template <int D>
@@ -465,11 +423,11 @@ ra_status launch(const Kv8DecodeParams& pp, int grid, int smem, const DeviceInfo
   auto kern = kv8_decode_kernel<D>;
   static bool configured[64] = {};
   if (!configured[dev.device]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmemLimit);
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cudaFuncSetAttribute(kv8 decode): %s", cudaGetErrorString(e));
     configured[dev.device] = true;
   }
-  return launch_pdl("kv8_decode_kernel", kern, dim3(grid), dim3(32 * (pp.d.hpc + kProducers + 1)), smem, stream, pp);
+  return launch_pdl("kv8_decode_kernel", kern, dim3(grid), dim3(32 * (pp.d.hpc + kRingProducers + 1)), smem, stream, pp);
 }
 
 }  // namespace
@@ -534,7 +492,7 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   p.seq_lens = seq_lens;
   p.batch = batch;
   p.max_seq_len = max_seq_len;
-  p.min_chunk = kDecodeMinChunk;
+  p.min_chunk = 2 * kSlab;
   p.chunk_align = kSlab;
   p.err = device_error;
   bind_decode_workspace(p, wl, pl, workspace);
@@ -542,14 +500,20 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   p.n_hgroups = sh.blocks;
   p.row_stride = sh.block_bytes;
   p.stage_bytes = kSlab * p.row_stride;
-  p.nstage = (kSmemLimit - kHdrBytes) / p.stage_bytes;
-  if (p.nstage > kMaxStages) p.nstage = kMaxStages;
-  const int smem = kHdrBytes + p.nstage * p.stage_bytes;
+  p.nstage = (kRingSmemLimit - kRingHdrBytes) / p.stage_bytes;
+  if (p.nstage > kRingMaxStages) p.nstage = kRingMaxStages;
+  const int smem = kRingHdrBytes + p.nstage * p.stage_bytes;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (ra_status st = launch_decode_plan(p, 0, s)) return st;
   const int64_t n_items = static_cast<int64_t>(pl.max_items) * p.n_hgroups;  // bound of the claims
   const int grid = static_cast<int>(n_items < dev.num_sms ? n_items : dev.num_sms);
   if (ra_status st = head_dim == 128 ? launch<128>(pp, grid, smem, dev, s) : launch<64>(pp, grid, smem, dev, s))
     return st;
-  return launch_decode_combine(p, head_dim, s);
+  // as many warps per row as the SMs hold at once (8 CTAs of 8 warps each would be their limit; half of it)
+  const int64_t rows = static_cast<int64_t>(batch) * num_q_heads;
+  int per_row = 1;
+  while (per_row < kCombineWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 4 * kCombineWarps) per_row *= 2;
+  const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
+  return launch_pdl("kv8_combine_kernel", head_dim == 128 ? kv8_combine_kernel<128> : kv8_combine_kernel<64>,
+                    dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row);
 }

@@ -3,10 +3,14 @@
 // Each request has T drafted tokens whose K/V sit in the pool behind its P cached ones; drafted token i
 // attends to all of the prefix and to the drafted tokens its bit mask names:
 //   o_i = sum_j softmax_j(scale <q_i, k_j>) v_j   over j < P and over P + t with bit t of mask_i.
-// One pass of the tcgen05 attention kernel (attn_tc.cuh, kTreePass) does both parts: rows are (token, head
-// of the GQA group), up to 256 per item, each gathered 128-key tile feeding all of them, and only the tiles
-// that hold drafted tokens look at the masks.  T * G rows share every key, so wide trees are bound by the
-// tensor cores and the softmax's issue slots like extend, small ones by latency and the gathers:
+// One pass does both parts; rows are (token, head of the GQA group), and only the keys of drafted tokens look
+// at the masks.  T * G rows share every key of a kv head:
+//  * up to 64 rows the call is bound by HBM (2 flop per byte and row), and the items of tree_narrow.cu stream
+//    whole slot rows of several heads with few large copies;
+//  * more rows are bound by the tensor cores and the softmax's issue slots, like extend: the tcgen05 attention
+//    kernel (attn_tc.cuh, kTreePass), up to 256 rows per item, each gathered 128-key tile feeding all of them.
+//    (Its 128-byte gathers take ~16 bytes per clock and SM: with 32 rows it ran at 62% of HBM at most.)
+// Around it:
 //  * the work list (one CTA, on the device, from the real lengths) splits the key ranges only as far as the
 //    SMs need it, since an unsplit item writes its bf16 rows directly while a split one costs fp32 partials
 //    (4 * D + 4 bytes per row and split, written and read again) and a merge;
@@ -21,99 +25,21 @@
 #include "api_common.h"
 #include "attn_tc.cuh"
 #include "attn_tc_host.h"
-#include "decode_internal.h"
+#include "slab_ring.cuh"
+#include "tree_internal.h"
 
 namespace ra {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kBins = 1024;        // key tiles of an item, longest first; longer ones share the first bin
-constexpr int kPlanSms = 152;      // GB300; a constant, so that the workspace does not depend on the device
-constexpr int kWaves = 2;          // a batch with at least this many unsplit items per SM is only balanced
+constexpr int kPlanThreads = 256;  // one SM runs the list: its issue slots are what a larger block would share
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanCached = 1024;  // requests whose lengths the list kernel keeps in shared memory
+constexpr int kBins = kPlanThreads;  // size classes of the items, longest first
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = kMergeThreads / 32;  // rows per merge unit, one warp each
+constexpr int kMergeWarps = kMergeThreads / 32;
 
-struct TreeWorkspace {
-  int32_t* header;     // [8]: listed items, claim counter, keys per split, merges
-  int32_t* items;      // [4 * cap]
-  int32_t* merges;     // [4 * cap_merge]: request, query tile, first partial slot, splits
-  int32_t* bad;        // [batch * hkv]: a drafted token's V holds a value that is not finite
-  float* part_o;
-  float* part_lse;
-  int64_t cap, cap_parts;
-  int32_t part_rows;
-  size_t total;
-};
-
-// Items: one per (request, query tile) plus the extra ones of split ranges.  A range is split only if it is
-// longer than the chunk, and the chunk is at least total / (kWaves * kPlanSms) (all ranges times the kv heads):
-// the split ranges' pieces number at most sum ceil(n / c) <= sum 2 n / c <= 2 * kWaves * kPlanSms / hkv.
-TreeWorkspace layout_tree(int32_t batch, int64_t total_q, int32_t hq, int32_t hkv, int32_t d, int32_t max_draft,
-                          void* base) {
-  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const int32_t group = hq / hkv;
-  const int32_t tokens = tc::kTiles * (128 / group);
-  TreeWorkspace w{};
-  w.cap_parts = 2 * kWaves * kPlanSms / hkv;
-  w.cap = (total_q + tokens - 1) / tokens + batch + w.cap_parts;
-  const int64_t rows = static_cast<int64_t>(max_draft) * group;
-  w.part_rows = static_cast<int32_t>(rows < 256 ? rows : 256);
-  uint8_t* b = static_cast<uint8_t*>(base);
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    uint8_t* at = b ? b + off : nullptr;
-    off += up(bytes);
-    return at;
-  };
-  w.header = reinterpret_cast<int32_t*>(take(32));
-  w.items = reinterpret_cast<int32_t*>(take(static_cast<size_t>(w.cap) * 16));
-  w.merges = reinterpret_cast<int32_t*>(take(static_cast<size_t>(w.cap_parts) * 16));
-  w.bad = reinterpret_cast<int32_t*>(take(static_cast<size_t>(batch) * hkv * 4));
-  const size_t part = static_cast<size_t>(w.cap_parts) * hkv * w.part_rows;
-  w.part_lse = reinterpret_cast<float*>(take(part * 4));
-  w.part_o = reinterpret_cast<float*>(take(part * d * 4));
-  w.total = off;
-  return w;
-}
-
-struct TreeParams {
-  const __nv_bfloat16 *k_pool, *v_pool, *q;
-  __nv_bfloat16* o;
-  int64_t num_slots, table_stride, table_rows, total_q;
-  int32_t hq, hkv, group;
-  float scale_log2;
-  const int32_t *table, *rpi, *prefix_lens, *draft_lens, *qo_indptr;
-  const uint32_t* mask;
-  int32_t mask_words, batch, max_draft, max_prefix;
-  int32_t tokens_per_item;
-  TreeWorkspace ws;
-  uint32_t* err;
-};
-
-// Request b's lengths and first row; false (reported once) if they, its table row or its rows of q are out of
-// bounds: such a request writes nothing.
-__device__ __forceinline__ bool tree_request(const TreeParams& p, int32_t b, int32_t& P, int32_t& T, bool report) {
-  P = __ldg(p.prefix_lens + b);
-  T = __ldg(p.draft_lens + b);
-  const int64_t q0 = __ldg(p.qo_indptr + b);
-  const int32_t row = __ldg(p.rpi + b);
-  if (P < 0 || P > p.max_prefix || T < 0 || T > p.max_draft || static_cast<int64_t>(P) + T > p.table_stride ||
-      q0 < 0 || q0 + T > p.total_q) {
-    if (report) flag_error(p.err, RA_DEVERR_LENGTH);
-    return false;
-  }
-  if (row < 0 || row >= p.table_rows) {
-    if (report) flag_error(p.err, RA_DEVERR_TABLE);
-    return false;
-  }
-  return T > 0;
-}
-
-__device__ __forceinline__ int32_t tiles_of(int32_t keys) { return (keys + tc::kKeys - 1) / tc::kKeys; }
-__device__ __forceinline__ int32_t bin_of(int32_t tiles) { return kBins - 1 - min(tiles, kBins - 1); }
-
-// CTA 0 lists the items, longest first; CTAs 1.. scan the drafted tokens' V rows, one request at a time.
+// CTA 0 lists the items, longest first; CTAs 1 .. scan the drafted tokens' V rows, one request at a time.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_constant__ TreeParams p, int32_t head_dim) {
   griddep_wait();  // the call's inputs; the workspace may still be read by the call before
   griddep_launch();
@@ -141,68 +67,96 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     return;
   }
   __shared__ int32_t s_bin[kBins];
-  __shared__ int32_t s_warp[kPlanThreads / 32];
-  __shared__ unsigned long long s_work, s_entries, s_best;
-  __shared__ int32_t s_longest, s_parts, s_merges;
+  __shared__ int32_t s_warp[kPlanWarps], s_long[kPlanWarps], s_entries[kPlanWarps], s_chunk[kPlanWarps];
+  __shared__ float s_cost[kPlanWarps];
+  __shared__ unsigned long long s_work[kPlanWarps];
+  __shared__ int32_t s_parts, s_merges;
+  __shared__ int4 s_req[kPlanCached];  // P, T (0 where nothing is computed), units, query tiles
   s_bin[t] = 0;
-  if (t == 0) {
-    s_work = s_entries = 0;
-    s_best = ~0ull;
-    s_longest = 1;
-    s_parts = s_merges = 0;
-  }
-  __syncthreads();
-  const int32_t per_item = p.tokens_per_item;
-  unsigned long long work = 0, entries = 0;
-  int32_t longest = 0;
+  if (t == 0) s_parts = s_merges = 0;
+  const int32_t per_item = p.sh.tokens_per_item, heads = p.sh.heads, unit = p.sh.unit;
+  const int32_t slots = p.sh.waves * kTreeSms;  // items that fill the SMs `waves` times
+  auto request = [&](int32_t b, bool first) -> int4 {
+    if (!first && b < kPlanCached) return s_req[b];
+    int4 q;
+    if (!tree_request(p, b, q.x, q.y, first)) return make_int4(0, 0, 0, 0);
+    q.z = (q.x + q.y + unit - 1) / unit;
+    q.w = (q.y + per_item - 1) / per_item;
+    return q;
+  };
+  unsigned long long work = 0;
+  int32_t entries = 0, longest = 1;
   for (int32_t b = t; b < p.batch; b += kPlanThreads) {
-    int32_t P, T;
-    if (!tree_request(p, b, P, T, true)) continue;
-    const int32_t q_tiles = (T + per_item - 1) / per_item, nt = tiles_of(P + T);
-    work += static_cast<unsigned long long>(q_tiles) * nt;
-    entries += q_tiles;
-    longest = max(longest, nt);
+    const int4 q = request(b, true);
+    if (b < kPlanCached) s_req[b] = q;
+    work += static_cast<unsigned long long>(q.w) * q.z;
+    entries += q.w;
+    longest = max(longest, q.z);
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    work += __shfl_xor_sync(0xffffffffu, work, off);
-    entries += __shfl_xor_sync(0xffffffffu, entries, off);
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, off));
-  }
-  if (lane == 0) {
-    atomicAdd(&s_work, work);
-    atomicAdd(&s_entries, entries);
-    atomicMax(&s_longest, longest);
-  }
+  for (int off = 16; off > 0; off >>= 1) work += __shfl_xor_sync(0xffffffffu, work, off);
+  entries = __reduce_add_sync(0xffffffffu, entries);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) s_work[warp] = work, s_entries[warp] = entries, s_long[warp] = longest;
   __syncthreads();
-  // Key tiles per split.  The least is total / (kWaves * kPlanSms), which bounds the partials.  With that
-  // many unsplit items it also balances the SMs; with fewer, the split of the longest range into 1 .. 1024
-  // pieces that gives the shortest schedule, waves * (tiles + 3) (a CTA fills and drains in ~3 tiles' time).
-  const unsigned long long all = s_work * p.hkv;
-  const unsigned long long per_sm = (all + kWaves * kPlanSms - 1) / (kWaves * kPlanSms);
-  const int32_t least = static_cast<int32_t>(min(per_sm, static_cast<unsigned long long>(s_longest)));
-  int32_t chunk = max(least, 1);
-  if (s_entries * p.hkv < kWaves * kPlanSms) {
-    const int32_t c = max((s_longest + t) / (t + 1), chunk);
-    unsigned long long items = 0;
-    for (int32_t b = 0; b < p.batch; ++b) {
-      int32_t P, T;
-      if (!tree_request(p, b, P, T, false)) continue;
-      items += static_cast<unsigned long long>((T + per_item - 1) / per_item) * ((tiles_of(P + T) + c - 1) / c);
-    }
-    const unsigned long long waves = (items * p.hkv + kPlanSms - 1) / kPlanSms;
-    atomicMin(&s_best, (waves * (c + 3)) << 32 | static_cast<unsigned long long>(c));
-    __syncthreads();
-    chunk = static_cast<int32_t>(s_best & 0xffffffffull);
+  work = 0, entries = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) {
+    work += s_work[w];
+    entries += s_entries[w];
+    longest = max(longest, s_long[w]);
   }
-  // counting sort of the items by key tiles, longest first
+  // Units per split.  The least is total / (waves * SMs), which bounds the partials.  With that many unsplit
+  // items it also balances the SMs; with fewer, the longest range is cut into the number of pieces (at most
+  // two per SM and head) whose schedule is shortest: a piece alone, or the mean load of an SM and a quarter
+  // of a piece for the uneven end of a longest-first list.  64 numbers of pieces are weighed, four threads
+  // each; the estimate may round (only the choice depends on it).
+  const unsigned long long all = work * heads;
+  const unsigned long long per_slot =
+      all >> 31 ? (all + slots - 1) / slots : (static_cast<uint32_t>(all) + slots - 1) / static_cast<uint32_t>(slots);
+  const int32_t least = max(1, static_cast<int32_t>(min(per_slot, static_cast<unsigned long long>(longest))));
+  int32_t chunk = least;
+  if (static_cast<int64_t>(entries) * heads < slots) {
+    const int32_t most = max(1, min(longest, 2 * kTreeSms / heads));
+    const int32_t cand = t >> 2;
+    const int32_t k = cand < 32 ? min(cand + 1, most) : min(most, 32 + (cand - 31) * max(most - 32, 0) / 32);
+    const int32_t c = max((longest + k - 1) / k, least);
+    const float per = 1.f / static_cast<float>(c);
+    int32_t fixed = 0;
+    for (int32_t b = t & 3; b < p.batch; b += 4) {
+      const int4 q = request(b, false);
+      const int32_t pieces = static_cast<int32_t>(ceilf(static_cast<float>(q.z) * per - 1e-3f));
+      fixed += q.w * pieces * (pieces > 1 ? p.sh.split_overhead : p.sh.overhead);
+    }
+    fixed += __shfl_xor_sync(0xffffffffu, fixed, 1);
+    fixed += __shfl_xor_sync(0xffffffffu, fixed, 2);
+    const float mean = (static_cast<float>(all) + static_cast<float>(fixed) * heads) * (1.f / kTreeSms);
+    float cost = fmaxf(static_cast<float>(c + (c < longest ? p.sh.split_overhead : p.sh.overhead)), mean + 0.25f * c);
+    int32_t mine = c;
+#pragma unroll
+    for (int off = 16; off >= 4; off >>= 1) {
+      const float oc = __shfl_xor_sync(0xffffffffu, cost, off);
+      const int32_t om = __shfl_xor_sync(0xffffffffu, mine, off);
+      if (oc < cost || (oc == cost && om > mine)) cost = oc, mine = om;  // on a tie the longer piece
+    }
+    if (lane == 0) s_cost[warp] = cost, s_chunk[warp] = mine;
+    __syncthreads();
+    chunk = s_chunk[0], cost = s_cost[0];
+#pragma unroll
+    for (int w = 1; w < kPlanWarps; ++w)
+      if (s_cost[w] < cost || (s_cost[w] == cost && s_chunk[w] > chunk)) cost = s_cost[w], chunk = s_chunk[w];
+  }
+  // counting sort of the items by size, longest first
+  const float scale = (kBins - 1) / static_cast<float>(min(chunk, longest));
+  auto bin_of = [&](int32_t units) {
+    return kBins - 1 - min(kBins - 1, static_cast<int32_t>(static_cast<float>(units) * scale));
+  };
+  const int32_t full_bin = bin_of(chunk);
   for (int32_t b = t; b < p.batch; b += kPlanThreads) {
-    int32_t P, T;
-    if (!tree_request(p, b, P, T, false)) continue;
-    const int32_t q_tiles = (T + per_item - 1) / per_item, nt = tiles_of(P + T);
-    const int32_t full = nt / chunk, rem = nt % chunk;
-    if (full > 0) atomicAdd(&s_bin[bin_of(chunk)], full * q_tiles);
-    if (rem > 0) atomicAdd(&s_bin[bin_of(rem)], q_tiles);
+    const int4 q = request(b, false);
+    const int32_t full = q.z / chunk, rem = q.z - full * chunk;
+    if (full > 0) atomicAdd(&s_bin[full_bin], full * q.w);
+    if (rem > 0) atomicAdd(&s_bin[bin_of(rem)], q.w);
   }
   __syncthreads();
   const int32_t mine = s_bin[t];
@@ -214,35 +168,51 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   }
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    int32_t w = s_warp[lane];
+  int32_t before = 0, total = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, w, off);
-      if (lane >= off) w += y;
-    }
-    s_warp[lane] = w;
+  for (int w = 0; w < kPlanWarps; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
   }
+  s_bin[t] = before + incl - mine;
   __syncthreads();
-  s_bin[t] = (warp > 0 ? s_warp[warp - 1] : 0) + incl - mine;
-  const int32_t total = s_warp[kPlanThreads / 32 - 1];
-  __syncthreads();
+  // The items of a request are its full pieces, then its shorter last one, of each query tile.  Every lane
+  // takes the places of a request of its own (requests strided over the warps), then the warp writes the
+  // items of its lanes' requests together.
   int4* items = reinterpret_cast<int4*>(p.ws.items);
-  for (int32_t b = t; b < p.batch; b += kPlanThreads) {
-    int32_t P, T;
-    if (!tree_request(p, b, P, T, false)) continue;
-    const int32_t q_tiles = (T + per_item - 1) / per_item, nt = tiles_of(P + T);
-    const int32_t splits = (nt + chunk - 1) / chunk;
-    for (int32_t i = 0; i < q_tiles; ++i) {
-      int32_t part = -1;
+  for (int32_t b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+    const int32_t b = b0 + lane * kPlanWarps + warp;
+    const bool in = b < p.batch;
+    const int4 q = in ? request(b, false) : make_int4(0, 0, 0, 0);
+    const int32_t full = q.z / chunk, rem = q.z - full * chunk, splits = full + (rem > 0 ? 1 : 0);
+    int32_t at_full = 0, at_rem = 0, part0 = 0, merge0 = 0, row = 0, q0 = 0;
+    if (q.y > 0) {
+      row = __ldg(p.rpi + b);
+      q0 = __ldg(p.qo_indptr + b);
+      if (full > 0) at_full = atomicAdd(&s_bin[full_bin], full * q.w);
+      if (rem > 0) at_rem = atomicAdd(&s_bin[bin_of(rem)], q.w);
       if (splits > 1) {
-        part = atomicAdd(&s_parts, splits);
-        reinterpret_cast<int4*>(p.ws.merges)[atomicAdd(&s_merges, 1)] = make_int4(b, i, part, splits);
+        part0 = atomicAdd(&s_parts, splits * q.w);
+        merge0 = atomicAdd(&s_merges, q.w);
       }
-      for (int32_t s = 0; s < splits; ++s) {
-        const int32_t pos = atomicAdd(&s_bin[bin_of(min(chunk, nt - s * chunk))], 1);
-        if (pos < p.ws.cap) items[pos] = make_int4(b, i, s, part < 0 ? -1 : part + s);
-        else flag_error(p.err, RA_DEVERR_LENGTH);  // draft lengths sum above total_q
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, q.y > 0); left != 0; left &= left - 1) {
+      const int src = __ffs(left) - 1;
+      auto of = [&](int32_t x) { return __shfl_sync(0xffffffffu, x, src); };
+      const int32_t n = of(splits), nf = of(full), n_tiles = of(q.w), pf = of(at_full), pr = of(at_rem), part = of(part0),
+                    mg = of(merge0), bb = of(b);
+      const int4 about = make_int4(of(q.x), of(q.y), of(row), of(q0));
+      for (int32_t i = lane; i < n_tiles * n; i += 32) {
+        const int32_t tile = i / n, s = i - tile * n;
+        const int32_t pos = s < nf ? pf + tile * nf + s : pr + tile;
+        if (n > 1 && s == 0)
+          reinterpret_cast<int4*>(p.ws.merges)[mg + tile] = make_int4(bb, tile, part + tile * n, n);
+        if (pos < p.ws.cap) {
+          items[2 * pos] = make_int4(bb, tile, s, n > 1 ? part + tile * n + s : -1);
+          items[2 * pos + 1] = about;
+        } else {
+          flag_error(p.err, RA_DEVERR_LENGTH);  // draft lengths sum above total_q
+        }
       }
     }
   }
@@ -250,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   if (t == 0) {
     p.ws.header[0] = static_cast<int32_t>(total < p.ws.cap ? total : p.ws.cap);
     p.ws.header[1] = 0;
-    p.ws.header[2] = chunk * tc::kKeys;
+    p.ws.header[2] = chunk * unit;
     p.ws.header[3] = s_merges;
   }
 }
@@ -292,82 +262,79 @@ __device__ void recompute_row(const TreeParams& p, int32_t b, int32_t P, int32_t
   for (int e = 0; e < V; ++e) p.o[(row * p.hq + h) * D + lane * V + e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
-// Join the splits (o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M), a warp per row), and recompute the marked
-// (request, kv head) pairs' rows.  Persistent: units of kMergeRows rows of a split query tile and kv head.
+// Join the splits (o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M)), and recompute the marked (request, kv
+// head) pairs' rows.  Persistent: a unit is kMergeWarps / `per_row` rows of a split query tile and kv head,
+// `per_row` warps each taking a share of a row's partials (the shares are joined through shared memory), so
+// that few rows with many splits do not wait on one warp's loads.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p, int per_row) {
   constexpr int V = D / 32;
   constexpr int kAhead = 8;  // partial rows in flight per warp
-  griddep_wait();
+  __shared__ float s_acc[kMergeWarps][32 * V], s_m[kMergeWarps], s_w[kMergeWarps];
+  // The attention kernel waited for the plan before it let this one launch: the plan's lists may be read at
+  // once.  The partials may be read, and o written, once the attention kernel is complete.
   griddep_launch();
+  bool waited = false;
+  auto wait_partials = [&]() {
+    if (!waited) griddep_wait();
+    waited = true;
+  };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t chunks = (p.ws.part_rows + kMergeRows - 1) / kMergeRows;
-  const int64_t units = static_cast<int64_t>(p.ws.header[3]) * p.hkv * chunks;
+  const int rows_per_unit = kMergeWarps / per_row;
+  const int share = warp % per_row;
+  const int32_t chunks = (p.ws.part_rows + rows_per_unit - 1) / rows_per_unit;
+  const int64_t pairs = static_cast<int64_t>(p.batch) * p.hkv;
+  const int64_t first_pair = static_cast<int64_t>(blockIdx.x) * kMergeThreads;
+  const int32_t mark = first_pair + threadIdx.x < pairs ? __ldcg(p.ws.bad + first_pair + threadIdx.x) : 0;
+  const int64_t units = static_cast<int64_t>(__ldcg(p.ws.header + 3)) * p.hkv * chunks;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int32_t r = static_cast<int32_t>(u % chunks) * kMergeRows + warp;
+    const int32_t r = static_cast<int32_t>(u % chunks) * rows_per_unit + warp / per_row;
     const int64_t rest = u / chunks;
     const int32_t kh = static_cast<int32_t>(rest % p.hkv);
-    const int4 e = reinterpret_cast<const int4*>(p.ws.merges)[rest / p.hkv];
-    const int32_t tok = e.y * p.tokens_per_item + r / p.group;
-    if (r >= p.ws.part_rows || tok >= __ldg(p.draft_lens + e.x) || p.ws.bad[e.x * p.hkv + kh]) continue;
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(p.ws.merges) + rest / p.hkv);
+    const int32_t tok = e.y * p.sh.tokens_per_item + r / p.group;
+    const bool live = r < p.ws.part_rows && tok < __ldg(p.draft_lens + e.x) && !__ldcg(p.ws.bad + e.x * p.hkv + kh);
     const int64_t slot_rows = static_cast<int64_t>(p.hkv) * p.ws.part_rows;  // rows between partial slots
     const int64_t row0 = (static_cast<int64_t>(e.z) * p.hkv + kh) * p.ws.part_rows + r;
-    float acc[V], mrun = -INFINITY, wsum = 0.f;
+    const int64_t row = __ldg(p.qo_indptr + e.x) + tok;
+    wait_partials();
+    float acc[V], m = -INFINITY, wsum = 0.f;
+    merge_partials<V, kAhead>(
+        live ? e.w : 0, share, per_row, [&](int s) { return __ldcg(p.ws.part_lse + row0 + s * slot_rows); },
+        [&](int s, float(&x)[V]) { load_row_cg<V>(p.ws.part_o + (row0 + s * slot_rows) * D + lane * V, x); }, acc, m,
+        wsum);
+    if (per_row > 1) {
+      __syncthreads();  // the unit before has been read
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int base = 0; base < e.w; base += 32) {
-      const int cnt = min(32, e.w - base);
-      const float ls = lane < cnt ? __ldcg(p.ws.part_lse + row0 + (base + lane) * slot_rows) : -INFINITY;
-      float mc = ls;
+      for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
+      if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
+      __syncthreads();
+      if (share != 0) continue;
+      float top = m;
+      for (int k = 1; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
+      const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, off));
-      const float mnew = fmaxf(mrun, mc), mref = mnew == -INFINITY ? 0.f : mnew;
-      const float sc = ex2(mrun - mref);
-      wsum *= sc;
+      for (int v = 0; v < V; ++v) acc[v] = 0.f;
+      wsum = 0.f;
+      for (int k = 0; k < per_row; ++k) {
+        const float f = ex2(s_m[warp + k] - ref);
+        wsum = fmaf(f, s_w[warp + k], wsum);
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] *= sc;
-      mrun = mnew;
-      const float wl = ex2(ls - mref);  // 0 for a split in which the row sees nothing
-      wsum += wl;
-      for (int k0 = 0; k0 < cnt; k0 += kAhead) {
-        float x[kAhead][V];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (k0 + k < cnt) {
-            const float* src = p.ws.part_o + (row0 + (base + k0 + k) * slot_rows) * D + lane * V;
-            if constexpr (V == 4) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-              x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
-            } else {
-              const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-              x[k][0] = y.x, x[k][1] = y.y;
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const float w = __shfl_sync(0xffffffffu, wl, (k0 + k) & 31);
-          if (k0 + k < cnt) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[k][v], acc[v]);
-          }
-        }
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(f, s_acc[warp + k][lane * V + v], acc[v]);
       }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
+    if (!live) continue;
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    const int64_t row = __ldg(p.qo_indptr + e.x) + tok;
     __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D + lane * V;
 #pragma unroll
     for (int v = 0; v < V; v += 2)
       *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
   }
-  const int64_t pairs = static_cast<int64_t>(p.batch) * p.hkv;
+  wait_partials();
   const int64_t threads = static_cast<int64_t>(gridDim.x) * kMergeThreads;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kMergeThreads; i0 < pairs; i0 += threads) {
+  for (int64_t i0 = first_pair; i0 < pairs; i0 += threads) {
     const int64_t mine = i0 + threadIdx.x;
-    const bool marked = mine < pairs && p.ws.bad[mine] != 0;
+    const bool marked = i0 == first_pair ? mark != 0 : mine < pairs && p.ws.bad[mine] != 0;
     if (!__syncthreads_or(marked)) continue;
     for (int64_t pair = i0; pair < i0 + kMergeThreads && pair < pairs; ++pair) {
       const int32_t b = static_cast<int32_t>(pair / p.hkv), kh = static_cast<int32_t>(pair % p.hkv);
@@ -380,9 +347,9 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 }
 
 template <int D>
-ra_status launch_tree(const TcParams& tp, const TreeParams& p, const CUtensorMap& qmap, const DeviceInfo& dev,
-                      cudaStream_t s) {
-  CUtensorMap kmap, vmap;
+ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev) {
+  CUtensorMap qmap, kmap, vmap;
+  if (ra_status st = query_tile_map(&qmap, p.q, p.total_q, p.hq, D, p.group)) return st;
   if (ra_status st = row_gather_map(&kmap, p.k_pool, p.num_slots * p.hkv, D)) return st;
   if (ra_status st = row_gather_map(&vmap, p.v_pool, p.num_slots * p.hkv, D)) return st;
   using L = tc::Layout<D, k_stages<D>(), v_stages<D>()>;
@@ -391,23 +358,61 @@ ra_status launch_tree(const TcParams& tp, const TreeParams& p, const CUtensorMap
   if (L::kDynSmem > dev.max_smem_optin)
     return fail(RA_ERR_UNSUPPORTED, "tree kernel needs %d bytes of shared memory", L::kDynSmem);
   if (ra_status st = set_smem(kern, L::kDynSmem, configured, dev.device)) return st;
-  // the list kernel: one CTA for the list, one per request (at most the other SMs) for the scan of V
-  const int scan = p.batch < dev.num_sms - 1 ? p.batch : dev.num_sms - 1;
-  if (ra_status st = launch_pdl("tree_plan_kernel", tree_plan_kernel, dim3(1 + scan), dim3(kPlanThreads), 0, s, p, D))
-    return st;
+  TcParams tp{};
+  tp.k_pool = p.k_pool;
+  tp.v_pool = p.v_pool;
+  tp.num_slots = p.num_slots;
+  tp.hkv = p.hkv;
+  tp.q = p.q;
+  tp.hq = p.hq;
+  tp.group = p.group;
+  tp.scale_log2 = p.scale_log2;
+  tp.table = p.table;
+  tp.table_stride = p.table_stride;
+  tp.table_rows = p.table_rows;
+  tp.err = p.err;
+  tp.total_q = p.total_q;
+  tp.o = p.o;
+  tp.work_count = p.ws.header;
+  tp.work_counter = p.ws.header + 1;
+  tp.work_items = p.ws.items;
+  tp.tree_chunk = p.ws.header + 2;
+  tp.tree_mask = p.mask;
+  tp.mask_words = p.mask_words;
+  tp.part_rows = p.ws.part_rows;
+  tp.part_o = p.ws.part_o;
+  tp.part_lse = p.ws.part_lse;
   const int64_t items = p.ws.cap * p.hkv;
   const int grid = static_cast<int>(items < dev.num_sms ? items : dev.num_sms);
-  if (ra_status st = launch_pdl("attn_tc_kernel<tree>", kern, dim3(grid), dim3(tc::kThreads), L::kDynSmem, s, tp, qmap,
-                                kmap, vmap))
-    return st;
-  // Persistent.  At most cap_parts / 2 query tiles are split (each into two or more).
-  const int64_t chunks = (p.ws.part_rows + kMergeRows - 1) / kMergeRows;
-  const int64_t want = std::max<int64_t>(1, p.ws.cap_parts / 2 * p.hkv * chunks), most = dev.num_sms * 4;
-  return launch_pdl("tree_merge_kernel", tree_merge_kernel<D>, dim3(static_cast<unsigned>(want < most ? want : most)),
-                    dim3(kMergeThreads), 0, s, p);
+  return launch_pdl("attn_tc_kernel<tree>", kern, dim3(grid), dim3(tc::kThreads), L::kDynSmem, s, tp, qmap, kmap, vmap);
 }
 
-bool tree_shape_ok(int32_t batch, int64_t total_q, int32_t hq, int32_t hkv, int32_t d, int32_t max_draft) {
+ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& dev, cudaStream_t s) {
+  // the list kernel: one CTA for the list, one per request (at most the other SMs) for the scan of V
+  const int scan = p.batch < dev.num_sms - 1 ? p.batch : dev.num_sms - 1;
+  if (ra_status st = launch_pdl("tree_plan_kernel", tree_plan_kernel, dim3(1 + scan), dim3(kPlanThreads), 0, s, p,
+                                head_dim))
+    return st;
+  if (ra_status st = p.sh.narrow       ? launch_tree_narrow(p, head_dim, dev, s)
+                     : head_dim == 128 ? launch_wide<128>(p, s, dev)
+                                       : launch_wide<64>(p, s, dev))
+    return st;
+  // Persistent.  At most cap_parts / 2 query tiles are split (each into two or more).  With many splits per tile
+  // (their number is bounded, so few tiles) several warps share a row: as many as leave each unit's rows enough
+  // for the SMs' CTAs.
+  const int64_t tiles = std::min<int64_t>(p.ws.cap_parts / 2, static_cast<int64_t>(p.batch) *
+                                          ((p.max_draft + p.sh.tokens_per_item - 1) / p.sh.tokens_per_item));
+  const int64_t rows = std::max<int64_t>(1, tiles) * p.hkv * p.ws.part_rows;
+  const int64_t most = static_cast<int64_t>(dev.num_sms) * 16;
+  int per_row = 1;
+  while (per_row < kMergeWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 4 * kMergeWarps) per_row *= 2;
+  const int64_t want = (rows * per_row + kMergeWarps - 1) / kMergeWarps;
+  auto kern = head_dim == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
+  return launch_pdl("tree_merge_kernel", kern, dim3(static_cast<unsigned>(want < most ? want : most)),
+                    dim3(kMergeThreads), 0, s, p, per_row);
+}
+
+bool tree_args_ok(int32_t batch, int64_t total_q, int32_t hq, int32_t hkv, int32_t d, int32_t max_draft) {
   return batch >= 0 && batch <= 65535 && total_q >= 0 && total_q < (int64_t(1) << 31) && hkv > 0 && hq > 0 &&
          hq % hkv == 0 && 128 % (hq / hkv) == 0 && (d == 64 || d == 128) && max_draft >= 1 && max_draft <= 1024;
 }
@@ -417,7 +422,7 @@ bool tree_shape_ok(int32_t batch, int64_t total_q, int32_t hq, int32_t hkv, int3
 
 extern "C" size_t ra_tree_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
                                           int32_t head_dim, int32_t max_draft_len) {
-  if (!ra::tree_shape_ok(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len)) return 0;
+  if (!ra::tree_args_ok(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len)) return 0;
   return ra::layout_tree(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len, nullptr).total;
 }
 
@@ -468,9 +473,6 @@ extern "C" ra_status ra_tree_attention(const void* k_pool, const void* v_pool, i
   RA_REQUIRE(static_cast<int64_t>(batch) * num_kv_heads < (int64_t(1) << 31), "batch x num_kv_heads too large");
   DeviceInfo dev;
   if (ra_status st = current_device(&dev)) return st;
-  CUtensorMap qmap;
-  if (ra_status st = query_tile_map(&qmap, q, total_q, num_q_heads, head_dim, group)) return st;
-
   p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
   p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -493,36 +495,7 @@ extern "C" ra_status ra_tree_attention(const void* k_pool, const void* v_pool, i
   p.batch = batch;
   p.max_draft = max_draft_len;
   p.max_prefix = max_prefix_len;
-  p.tokens_per_item = tc::kTiles * (128 / group);
+  p.sh = tree_shape(num_q_heads, num_kv_heads, max_draft_len);
   p.err = device_error;
-  TcParams tp{};
-  tp.k_pool = p.k_pool;
-  tp.v_pool = p.v_pool;
-  tp.num_slots = num_slots;
-  tp.hkv = num_kv_heads;
-  tp.q = p.q;
-  tp.hq = num_q_heads;
-  tp.group = group;
-  tp.scale_log2 = p.scale_log2;
-  tp.table = req_to_token;
-  tp.table_stride = table_stride;
-  tp.table_rows = table_rows;
-  tp.err = device_error;
-  tp.rpi = req_pool_indices;
-  tp.prefix_lens = prefix_lens;
-  tp.extend_lens = draft_lens;
-  tp.qo_indptr = qo_indptr;
-  tp.total_q = total_q;
-  tp.o = p.o;
-  tp.work_count = p.ws.header;
-  tp.work_counter = p.ws.header + 1;
-  tp.work_items = p.ws.items;
-  tp.tree_chunk = p.ws.header + 2;
-  tp.tree_mask = tree_mask;
-  tp.mask_words = mask_words;
-  tp.part_rows = p.ws.part_rows;
-  tp.part_o = p.ws.part_o;
-  tp.part_lse = p.ws.part_lse;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return head_dim == 128 ? launch_tree<128>(tp, p, qmap, dev, s) : launch_tree<64>(tp, p, qmap, dev, s);
+  return launch_tree(p, head_dim, dev, reinterpret_cast<cudaStream_t>(stream));
 }
