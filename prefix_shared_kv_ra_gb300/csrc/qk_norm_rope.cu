@@ -12,7 +12,7 @@
 // angles add rot * 4).  A row is D / 16 lanes wide, a lane holding 8 values of its first half and the 8 that
 // lie D / 2 further: with rot = D and half-split pairs both members of a pair are in one lane and the
 // rotation needs no exchange; other forms fetch the partner with shuffles.  A warp takes a unit of one
-// token: kQSteps steps of 32 * 16 / D q rows, or the 2 * hpc rows of one K/V block (hpc <= 8 heads); all
+// token: one or more steps of 512 / D q rows, or the 2 * hpc rows of one K/V block (hpc <= 8 heads); all
 // loads of a unit are issued before the first use, and the angles and weights are loaded once per unit.
 #include <cmath>
 
@@ -164,9 +164,9 @@ __device__ __forceinline__ void norm_rope_row(float (&x)[2][8], bool norm, const
   }
 }
 
-template <int D, int ROPE, bool KV8, int QSTEPS>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int kLanes = D / 16, kPerStep = 32 / kLanes, kKvSteps = 16 / kPerStep;
+template <int D, int ROPE, bool KV8, int QSTEPS, int KVSTEPS>
+__global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int kLanes = D / 16, kPerStep = 32 / kLanes, kKvSteps = KVSTEPS;
   griddep_wait();  // q, k and v come from the kernel before; earlier kernels may still read the slots
   griddep_launch();
   const int lane = threadIdx.x & 31;
@@ -299,12 +299,20 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
   }
 }
 
-template <int D, bool KV8, int QSTEPS>
+template <int D, bool KV8, int QSTEPS, int KVSTEPS>
 ra_status launch(const NormRopeParams& p, bool interleaved, int grid, cudaStream_t s) {
-  auto kern = interleaved    ? qk_norm_rope_kernel<D, kAdjacent, KV8, QSTEPS>
-              : p.rot == D   ? qk_norm_rope_kernel<D, kHalfFull, KV8, QSTEPS>
-                             : qk_norm_rope_kernel<D, kHalfPart, KV8, QSTEPS>;
+  auto kern = interleaved    ? qk_norm_rope_kernel<D, kAdjacent, KV8, QSTEPS, KVSTEPS>
+              : p.rot == D   ? qk_norm_rope_kernel<D, kHalfFull, KV8, QSTEPS, KVSTEPS>
+                             : qk_norm_rope_kernel<D, kHalfPart, KV8, QSTEPS, KVSTEPS>;
   return launch_pdl("qk_norm_rope_kernel", kern, dim3(grid), dim3(kThreads), 0, s, p);
+}
+
+template <int D, bool KV8>
+ra_status launch_steps(const NormRopeParams& p, bool interleaved, bool wide, bool deep, int grid, ra_stream_t stream) {
+  constexpr int kMost = 16 / (32 / (D / 16));  // steps of 16 rows
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (wide) return deep ? launch<D, KV8, kMost, kMost>(p, interleaved, grid, s) : launch<D, KV8, kMost, 1>(p, interleaved, grid, s);
+  return deep ? launch<D, KV8, 1, kMost>(p, interleaved, grid, s) : launch<D, KV8, 1, 1>(p, interleaved, grid, s);
 }
 
 ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t num_tokens, int32_t interleaved,
@@ -337,23 +345,24 @@ ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t n
   DeviceInfo dev;
   if (ra_status st = current_device(&dev)) return st;
   p.sh = kv8_shape(p.hkv, head_dim);
+  // q rows per unit: 16 (4 KB of loads in flight per warp), or one step where that fills the SMs' warps badly: few
+  // tokens (a decode step of 64 has 1.6 warps per SM sub-partition with one step), or more than a quarter of
+  // the rows of the last unit missing.  Measured, 4777 tokens: 8/2 heads of 64 7.4 us with 16 rows, 5.4 with
+  // one step; 12/3 heads of 128 14.7 and 19.3.
   const int32_t per_step = 32 / (head_dim / 16);
-  // q rows per unit: 16 (the loads of 4 KB in flight per warp) once that fills the SMs' warps, else one step
-  // (the shortest chain; a decode step of 64 tokens has 1.6 warps per SM sub-partition with one)
   const int64_t big = num_tokens * ((p.hq + 15) / 16 + p.sh.blocks);
-  const bool wide = big >= static_cast<int64_t>(dev.num_sms) * 16;
+  const bool wide = 4 * p.hq >= 48 * ((p.hq + 15) / 16) && big >= static_cast<int64_t>(dev.num_sms) * 16;
+  const bool deep = 2 * p.sh.hpc > per_step;  // a K/V block takes more than one step
   const int32_t q_rows = wide ? 16 : per_step;
   p.q_units = (p.hq + q_rows - 1) / q_rows;
   p.units_per_token = p.q_units + p.sh.blocks;
   p.units = num_tokens * p.units_per_token;
   const int64_t want = (p.units + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(dev.num_sms) * 8;
   const int grid = static_cast<int>(want < cap ? want : cap);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (head_dim == 128)
-    return kv8 ? (wide ? launch<128, true, 4>(p, interleaved, grid, s) : launch<128, true, 1>(p, interleaved, grid, s))
-               : (wide ? launch<128, false, 4>(p, interleaved, grid, s) : launch<128, false, 1>(p, interleaved, grid, s));
-  return kv8 ? (wide ? launch<64, true, 2>(p, interleaved, grid, s) : launch<64, true, 1>(p, interleaved, grid, s))
-             : (wide ? launch<64, false, 2>(p, interleaved, grid, s) : launch<64, false, 1>(p, interleaved, grid, s));
+  return head_dim == 128 ? (kv8 ? launch_steps<128, true>(p, interleaved, wide, deep, grid, stream)
+                                : launch_steps<128, false>(p, interleaved, wide, deep, grid, stream))
+                         : (kv8 ? launch_steps<64, true>(p, interleaved, wide, deep, grid, stream)
+                                : launch_steps<64, false>(p, interleaved, wide, deep, grid, stream));
 }
 
 NormRopeParams common_params(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
