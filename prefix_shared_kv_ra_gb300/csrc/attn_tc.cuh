@@ -273,8 +273,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
-  griddep_wait();  // the previous kernel (the work-list pass / the key-start scatter) has completed
-  griddep_launch();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = p.group;
@@ -309,6 +307,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_wait();  // the previous kernel (the work-list pass / the key-start scatter) has completed; the set-up
+  griddep_launch();  // above overlaps it
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
   auto give_up = [&]() {

@@ -32,7 +32,8 @@ namespace ra {
 
 namespace {
 
-constexpr int kPlanThreads = 256;  // one SM runs the list: its issue slots are what a larger block would share
+constexpr int kScanThreads = 1024;  // the list kernel's block: the scan's loads in flight
+constexpr int kPlanThreads = 256;   // of which this many build the list: one SM's issue slots bound it
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanCached = 1024;  // requests whose lengths the list kernel keeps in shared memory
 constexpr int kBins = kPlanThreads;  // size classes of the items, longest first
@@ -40,19 +41,19 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 
 // CTA 0 lists the items, longest first; CTAs 1 .. scan the drafted tokens' V rows, one request at a time.
-__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_constant__ TreeParams p, int32_t head_dim) {
+__global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_constant__ TreeParams p, int32_t head_dim) {
   griddep_wait();  // the call's inputs; the workspace may still be read by the call before
   griddep_launch();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (blockIdx.x > 0) {
     for (int32_t b = blockIdx.x - 1; b < p.batch; b += gridDim.x - 1) {
-      for (int32_t h = t; h < p.hkv; h += kPlanThreads) p.ws.bad[b * p.hkv + h] = 0;
+      for (int32_t h = t; h < p.hkv; h += kScanThreads) p.ws.bad[b * p.hkv + h] = 0;
       __syncthreads();
       int32_t P, T;
       if (!tree_request(p, b, P, T, false)) continue;
       const int32_t* slots = p.table + static_cast<int64_t>(__ldg(p.rpi + b)) * p.table_stride + P;
       const int32_t vecs = p.hkv * head_dim / 8, per_head = head_dim / 8;
-      for (int32_t j = warp; j < T; j += kPlanThreads / 32) {
+      for (int32_t j = warp; j < T; j += kScanThreads / 32) {
         int32_t slot = __ldg(slots + j);
         if (slot < 0 || slot >= p.num_slots) slot = 0;  // (as the attention kernel reads it, which flags it)
         const uint4* v = reinterpret_cast<const uint4*>(p.v_pool) + static_cast<int64_t>(slot) * vecs;
@@ -66,6 +67,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     }
     return;
   }
+  if (t >= kPlanThreads) return;
+  auto list_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kPlanThreads) : "memory"); };  // (the list's threads)
   __shared__ int32_t s_bin[kBins];
   __shared__ int32_t s_warp[kPlanWarps], s_long[kPlanWarps], s_entries[kPlanWarps], s_chunk[kPlanWarps];
   __shared__ float s_cost[kPlanWarps];
@@ -98,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
   entries = __reduce_add_sync(0xffffffffu, entries);
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0) s_work[warp] = work, s_entries[warp] = entries, s_long[warp] = longest;
-  __syncthreads();
+  list_sync();
   work = 0, entries = 0;
 #pragma unroll
   for (int w = 0; w < kPlanWarps; ++w) {
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       if (oc < cost || (oc == cost && om > mine)) cost = oc, mine = om;  // on a tie the longer piece
     }
     if (lane == 0) s_cost[warp] = cost, s_chunk[warp] = mine;
-    __syncthreads();
+    list_sync();
     chunk = s_chunk[0], cost = s_cost[0];
 #pragma unroll
     for (int w = 1; w < kPlanWarps; ++w)
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     if (full > 0) atomicAdd(&s_bin[full_bin], full * q.w);
     if (rem > 0) atomicAdd(&s_bin[bin_of(rem)], q.w);
   }
-  __syncthreads();
+  list_sync();
   const int32_t mine = s_bin[t];
   int32_t incl = mine;
 #pragma unroll
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     if (lane >= off) incl += y;
   }
   if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
+  list_sync();
   int32_t before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kPlanWarps; ++w) {
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
     total += s_warp[w];
   }
   s_bin[t] = before + incl - mine;
-  __syncthreads();
+  list_sync();
   // The items of a request are its full pieces, then its shorter last one, of each query tile.  Every lane
   // takes the places of a request of its own (requests strided over the warps), then the warp writes the
   // items of its lanes' requests together.
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const __grid_co
       }
     }
   }
-  __syncthreads();
+  list_sync();
   if (t == 0) {
     p.ws.header[0] = static_cast<int32_t>(total < p.ws.cap ? total : p.ws.cap);
     p.ws.header[1] = 0;
@@ -390,7 +393,7 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
 ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& dev, cudaStream_t s) {
   // the list kernel: one CTA for the list, one per request (at most the other SMs) for the scan of V
   const int scan = p.batch < dev.num_sms - 1 ? p.batch : dev.num_sms - 1;
-  if (ra_status st = launch_pdl("tree_plan_kernel", tree_plan_kernel, dim3(1 + scan), dim3(kPlanThreads), 0, s, p,
+  if (ra_status st = launch_pdl("tree_plan_kernel", tree_plan_kernel, dim3(1 + scan), dim3(kScanThreads), 0, s, p,
                                 head_dim))
     return st;
   if (ra_status st = p.sh.narrow       ? launch_tree_narrow(p, head_dim, dev, s)
@@ -403,7 +406,7 @@ ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& d
   const int64_t tiles = std::min<int64_t>(p.ws.cap_parts / 2, static_cast<int64_t>(p.batch) *
                                           ((p.max_draft + p.sh.tokens_per_item - 1) / p.sh.tokens_per_item));
   const int64_t rows = std::max<int64_t>(1, tiles) * p.hkv * p.ws.part_rows;
-  const int64_t most = static_cast<int64_t>(dev.num_sms) * 16;
+  const int64_t most = static_cast<int64_t>(dev.num_sms) * 8;
   int per_row = 1;
   while (per_row < kMergeWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 4 * kMergeWarps) per_row *= 2;
   const int64_t want = (rows * per_row + kMergeWarps - 1) / kMergeWarps;
