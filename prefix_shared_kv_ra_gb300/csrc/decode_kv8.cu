@@ -129,23 +129,27 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
   }
   if (warp == nc + kRingProducers) {
     // ================================================================ signaller
+    // (the item's request is looked up while the item is at work: the signal that follows its last store is on
+    // the way of the merge)
     for (int32_t n = 0;; ++n) {
       const int e = n % kRingEntries;
-      if (!mbar_wait(rg.done0 + 8 * e, (n / kRingEntries) & 1)) {
+      const int32_t idx = rg.entry(n);
+      int32_t* count = nullptr;  // the request's count, if its partials are merged by the combine
+      if (idx >= 0 && lane == 0) {
+        Item it;
+        decode_item(p, idx, it);
+        if (it.n_splits > 1) count = p.req_done + it.b;
+      }
+      if (idx < -1 || !mbar_wait(rg.done0 + 8 * e, (n / kRingEntries) & 1)) {
         if (lane == 0) rg.give_up(p.err);
         break;
       }
-      const int32_t idx = rg.items[e];
       __syncwarp();
       if (lane == 0) mbar_arrive(rg.free0 + 8 * e);
       if (idx < 0) break;
-      if (lane == 0) {
-        Item it;
-        decode_item(p, idx, it);
-        if (it.n_splits > 1) {  // partials, merged by the combine
-          __threadfence();      // the consumers' partials (ordered before this by the done barrier) first
-          atomicAdd(p.req_done + it.b, 1);
-        }
+      if (count) {
+        __threadfence();  // the consumers' partials (ordered before this by the done barrier) first
+        atomicAdd(count, 1);
       }
       __syncwarp();
     }
@@ -348,69 +352,84 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
   if (!clean && lane == 0) rg.give_up(p.err);  // a bounded wait ran out: stop the producers as well
 }
 
-// Merge the partials of every split request, `per_row` warps per (request, q head) row, each a share of the
-// partials.  Launched while the decode kernel runs: a row waits only for its own request's count of finished
-// (item, head group) partials, so early requests merge while others are read.  One warp per row serves large
-// batches; few rows with many splits would wait on one warp's chain of loads (32 rows of 108 partials: 18 us
-// with one warp each, 5 us with eight).
+// Merge the partials of every split request.  Launched while the decode kernel runs: a row (request, q head)
+// waits only for its own request's count of finished (item, head group) partials.  Two forms:
+//  * many rows: 8 lanes per row, a warp's four rows at once (224 requests of 64 heads: the call ends 12 us after
+//    its last item with a row per warp, one after the other);
+//  * few rows: `per_row` warps share one, each a part of its partials (32 rows of 108 partials: 18 us with
+//    one warp each, 5 us with eight).
 constexpr int kCombineWarps = 8;
+constexpr int kRowLanes = 8;
+constexpr int kRowsPerWarp = 32 / kRowLanes;
+
+// The request's partials, once they are written (a warp's lanes may ask for different requests): their first
+// index and number, 0 if its rows were written directly or it is invalid.
+__device__ __forceinline__ int32_t wait_partials(const DecodeParams& p, int32_t b, bool in, int32_t& i0) {
+  // the plan completed before the decode kernel let this one launch
+  const int32_t L = __ldg(p.seq_lens + b), row = __ldg(p.rpi + b);
+  i0 = __ldcg(p.req_item0 + b);
+  int32_t n = __ldcg(p.req_item0 + b + 1) - i0;
+  if (!in || n <= 1 || L < 1 || row < 0 || row >= p.table_rows) n = 0;
+  // every lane reads the count itself: with the fence its loads of the partials follow an acquire
+  if (n > 0 && !wait_count(p.req_done + b, n * p.n_hgroups)) {
+    flag_error(p.err, RA_DEVERR_TIMEOUT);
+    n = 0;
+  }
+  fence_acq_rel_gpu();
+  return n;
+}
 
 template <int D>
-__global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_kernel(const __grid_constant__ DecodeParams p,
-                                                                         int per_row) {
+__global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int V = D / kRowLanes;
+  griddep_launch();
+  const int sub = (threadIdx.x & 31) % kRowLanes;
+  const int32_t bh = static_cast<int32_t>(blockIdx.x * (32 * kCombineWarps / kRowLanes) + threadIdx.x / kRowLanes);
+  const bool in = bh < p.batch * p.hq;
+  const int32_t b = in ? bh / p.hq : 0, h = in ? bh - b * p.hq : 0;
+  int32_t i0;
+  const int32_t n = wait_partials(p, b, in, i0);
+  __syncwarp();
+  float acc[V], wsum;
+  merge_rows<kRowLanes, V, 256 / D>(
+      n, [&](int s) { return __ldcg(p.part_lse + static_cast<int64_t>(i0 + s) * p.hq + h); },
+      [&](int s, float(&x)[V]) {
+        load_row_part<kRowLanes, V>(p.part_o + (static_cast<int64_t>(i0 + s) * p.hq + h) * D, sub, x);
+      },
+      acc, wsum);
+  if (n > 0) store_row_part<kRowLanes, V>(p.o + static_cast<int64_t>(bh) * D, sub, acc, 1.f / wsum);
+  griddep_wait();  // this grid's completion implies the decode kernel's
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(const __grid_constant__ DecodeParams p,
+                                                                             int per_row) {
   constexpr int V = D / 32;
-  constexpr int kAhead = 8;
   __shared__ float s_acc[kCombineWarps][32 * V], s_m[kCombineWarps], s_w[kCombineWarps];
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = warp % per_row;
-  const int64_t bh = static_cast<int64_t>(blockIdx.x) * (kCombineWarps / per_row) + warp / per_row;
-  const bool in = bh < static_cast<int64_t>(p.batch) * p.hq;
-  const int32_t b = in ? static_cast<int32_t>(bh / p.hq) : 0;
-  const int32_t h = in ? static_cast<int32_t>(bh - static_cast<int64_t>(b) * p.hq) : 0;
-  // the plan completed before the decode kernel let this one launch
-  const int32_t L = __ldg(p.seq_lens + b), row = __ldg(p.rpi + b);
-  const int32_t i0 = __ldcg(p.req_item0 + b), n = __ldcg(p.req_item0 + b + 1) - i0;
-  bool merge = in && n > 1 && L >= 1 && row >= 0 && row < p.table_rows;  // the others: written directly, or invalid
-  if (merge) {
-    bool ready = true;
-    if (lane == 0 && !(ready = wait_count(p.req_done + b, n * p.n_hgroups))) flag_error(p.err, RA_DEVERR_TIMEOUT);
-    merge = __shfl_sync(0xffffffffu, ready, 0);
-    // every lane reads the count itself: with the fence its loads of the partials follow an acquire
-    (void)ld_relaxed_gpu(p.req_done + b);
-    fence_acq_rel_gpu();
-  }
-  float acc[V], m = -INFINITY, wsum = 0.f;
-  merge_partials<V, kAhead>(
-      merge ? n : 0, share, per_row,
-      [&](int s) { return __ldcg(p.part_lse + static_cast<int64_t>(i0 + s) * p.hq + h); },
+  const int32_t bh = static_cast<int32_t>(blockIdx.x) * (kCombineWarps / per_row) + warp / per_row;
+  const bool in = bh < p.batch * p.hq;
+  const int32_t b = in ? bh / p.hq : 0, h = in ? bh - b * p.hq : 0;
+  int32_t i0;
+  const int32_t n = wait_partials(p, b, in, i0);
+  __syncwarp();
+  float acc[V], m, wsum;
+  merge_partials<V, 8>(
+      n, share, per_row, [&](int s) { return __ldcg(p.part_lse + static_cast<int64_t>(i0 + s) * p.hq + h); },
       [&](int s, float(&x)[V]) {
         load_row_cg<V>(p.part_o + (static_cast<int64_t>(i0 + s) * p.hq + h) * D + lane * V, x);
       },
       acc, m, wsum);
-  if (per_row > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
-    if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
-    __syncthreads();
-    if (share == 0) {
-      float top = m;
-      for (int k = 1; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
-      const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = 0.f;
-      wsum = 0.f;
-      for (int k = 0; k < per_row; ++k) {
-        const float f = ex2(s_m[warp + k] - ref);
-        wsum = fmaf(f, s_w[warp + k], wsum);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(f, s_acc[warp + k][lane * V + v], acc[v]);
-      }
-    }
-  }
-  if (merge && share == 0) {
+  for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
+  if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
+  __syncthreads();
+  if (n > 0 && share == 0) {
+    join_shares<V>(per_row, warp, s_acc, s_m, s_w, acc, wsum);
     const float inv = 1.f / wsum;
-    __nv_bfloat16* dst = p.o + bh * D + lane * V;
+    __nv_bfloat16* dst = p.o + static_cast<int64_t>(bh) * D + lane * V;
 #pragma unroll
     for (int v = 0; v < V; v += 2)
       *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
@@ -464,6 +483,7 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   // the device plan's item length must fit in 31 bits (it is at most batch x max_seq_len / kDecodePlanItems)
   RA_REQUIRE(static_cast<int64_t>(batch) * max_seq_len <= static_cast<int64_t>(kDecodePlanItems) << 30,
              "batch x max_seq_len too large");
+  RA_REQUIRE(static_cast<int64_t>(batch) * num_q_heads < (int64_t(1) << 30), "batch x num_q_heads too large");
   const DecodePlan pl = plan_decode(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len, 0, 0, 0);
   const DecodeWorkspace wl = layout_decode_workspace(batch, num_q_heads, num_kv_heads, head_dim, pl, 0);
   if (workspace_bytes < wl.total)
@@ -509,11 +529,16 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   const int grid = static_cast<int>(n_items < dev.num_sms ? n_items : dev.num_sms);
   if (ra_status st = head_dim == 128 ? launch<128>(pp, grid, smem, dev, s) : launch<64>(pp, grid, smem, dev, s))
     return st;
-  // as many warps per row as the SMs hold at once (8 CTAs of 8 warps each would be their limit; half of it)
-  const int64_t rows = static_cast<int64_t>(batch) * num_q_heads;
+  // few rows: as many warps per row as three CTAs per SM hold
+  const int64_t rows = static_cast<int64_t>(batch) * num_q_heads, warps = static_cast<int64_t>(dev.num_sms) * 3 * kCombineWarps;
   int per_row = 1;
-  while (per_row < kCombineWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 4 * kCombineWarps) per_row *= 2;
-  const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
+  while (per_row < kCombineWarps && rows * per_row * 2 <= warps) per_row *= 2;
+  if (per_row > 1) {
+    const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
+    return launch_pdl("kv8_combine_few_kernel", head_dim == 128 ? kv8_combine_few_kernel<128> : kv8_combine_few_kernel<64>,
+                      dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row);
+  }
+  const int64_t per_cta = kCombineWarps * kRowsPerWarp;
   return launch_pdl("kv8_combine_kernel", head_dim == 128 ? kv8_combine_kernel<128> : kv8_combine_kernel<64>,
-                    dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row);
+                    dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta)), dim3(32 * kCombineWarps), 0, s, p);
 }

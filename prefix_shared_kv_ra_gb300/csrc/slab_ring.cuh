@@ -219,6 +219,93 @@ __device__ __forceinline__ void merge_partials(int n, int w, int warps, Lse lse_
   for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
 }
 
+// Join the shares of the `per_row` warps from `warp` on (their sums, references and weights in shared memory).
+template <int V>
+__device__ __forceinline__ void join_shares(int per_row, int warp, const float (*s_acc)[32 * V], const float* s_m,
+                                            const float* s_w, float (&acc)[V], float& wsum) {
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  for (int k = 0; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
+  const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  wsum = 0.f;
+  for (int k = 0; k < per_row; ++k) {
+    const float f = ex2(s_m[warp + k] - ref);
+    wsum = fmaf(f, s_w[warp + k], wsum);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(f, s_acc[warp + k][lane * V + v], acc[v]);
+  }
+}
+
+// The same for several rows per warp: LPR lanes per row, lane l of a row holding its floats 4 l .. + 4 of every
+// 4 * LPR (V = D / LPR of them).  n and the accessors may differ between a warp's rows; `n` 0 for none.  One
+// row per warp leaves a warp waiting for one row's loads at a time (~1.7 us a row at the end of a call, when
+// nothing else runs); four rows share that wait.
+template <int LPR, int V, int AHEAD, class Lse, class Row>
+__device__ __forceinline__ void merge_rows(int n, Lse lse_at, Row row_at, float (&acc)[V], float& wsum) {
+  const int sub = (threadIdx.x & 31) % LPR;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  float mrun = -INFINITY;
+  wsum = 0.f;
+  const int most = __reduce_max_sync(0xffffffffu, n);
+  for (int base = 0; base < most; base += LPR) {
+    const int cnt = min(LPR, n - base);  // (<= 0 for a row that is done)
+    const float ls = sub < cnt ? lse_at(base + sub) : -INFINITY;
+    float x[AHEAD][V];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (k < cnt) row_at(base + k, x[k]);
+    float mc = ls;
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, off));
+    const float mnew = fmaxf(mrun, mc), mref = mnew == -INFINITY ? 0.f : mnew;
+    const float sc = ex2(mrun - mref);
+    wsum *= sc;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= sc;
+    mrun = mnew;
+    const float wl = ex2(ls - mref);
+    wsum += wl;
+    const int round = min(LPR, most - base);
+    for (int k0 = 0; k0 < round; k0 += AHEAD) {
+      if (k0 > 0) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+          if (k0 + k < cnt) row_at(base + k0 + k, x[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, wl, (k0 + k) % LPR, LPR);
+        if (k0 + k < cnt) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = fmaf(wk, x[k][v], acc[v]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int off = LPR / 2; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
+}
+
+// Lane `sub`'s floats of a row (through L2), and its bf16 stores, in merge_rows' layout.
+template <int LPR, int V>
+__device__ __forceinline__ void load_row_part(const float* row, int sub, float (&x)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; v += 4) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(row + v * LPR) + sub);
+    x[v] = t.x, x[v + 1] = t.y, x[v + 2] = t.z, x[v + 3] = t.w;
+  }
+}
+template <int LPR, int V>
+__device__ __forceinline__ void store_row_part(__nv_bfloat16* row, int sub, const float (&x)[V], float f) {
+#pragma unroll
+  for (int v = 0; v < V; v += 4)
+    *(reinterpret_cast<uint2*>(row + v * LPR) + sub) =
+        make_uint2(pack_bf16x2(x[v] * f, x[v + 1] * f), pack_bf16x2(x[v + 2] * f, x[v + 3] * f));
+}
+
 template <int V>
 __device__ __forceinline__ void load_row_cg(const float* src, float (&x)[V]) {  // through L2
   if constexpr (V == 4) {

@@ -266,14 +266,14 @@ __device__ void recompute_row(const TreeParams& p, int32_t b, int32_t P, int32_t
 }
 
 // Join the splits (o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M)), and recompute the marked (request, kv
-// head) pairs' rows.  Persistent: a unit is kMergeWarps / `per_row` rows of a split query tile and kv head,
-// `per_row` warps each taking a share of a row's partials (the shares are joined through shared memory), so
+// head) pairs' rows.  Persistent: a unit is kMergeThreads / 8 rows of a split query tile (all kv heads), 8 lanes
+// per row, or (FEW) kMergeWarps / `per_row` rows, `per_row` warps each taking a share of a row's partials, so
 // that few rows with many splits do not wait on one warp's loads.
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p, int per_row) {
-  constexpr int V = D / 32;
-  constexpr int kAhead = 8;  // partial rows in flight per warp
-  __shared__ float s_acc[kMergeWarps][32 * V], s_m[kMergeWarps], s_w[kMergeWarps];
+  constexpr int LPR = FEW ? 32 : 8;
+  constexpr int V = D / LPR;
+  __shared__ float s_acc[FEW ? kMergeWarps : 1][32 * V], s_m[kMergeWarps], s_w[kMergeWarps];
   // The attention kernel waited for the plan before it let this one launch: the plan's lists may be read at
   // once.  The partials may be read, and o written, once the attention kernel is complete.
   griddep_launch();
@@ -282,56 +282,53 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     if (!waited) griddep_wait();
     waited = true;
   };
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows_per_unit = kMergeWarps / per_row;
-  const int share = warp % per_row;
-  const int32_t chunks = (p.ws.part_rows + rows_per_unit - 1) / rows_per_unit;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
+  const int rows_per_unit = FEW ? kMergeWarps / per_row : kMergeThreads / LPR;
+  const int share = FEW ? warp % per_row : 0;
+  const int mine = FEW ? warp / per_row : static_cast<int>(threadIdx.x) / LPR;
+  const int32_t tile_rows = p.hkv * p.ws.part_rows;  // rows of a query tile, all kv heads
+  const int32_t chunks = (tile_rows + rows_per_unit - 1) / rows_per_unit;
   const int64_t pairs = static_cast<int64_t>(p.batch) * p.hkv;
   const int64_t first_pair = static_cast<int64_t>(blockIdx.x) * kMergeThreads;
   const int32_t mark = first_pair + threadIdx.x < pairs ? __ldcg(p.ws.bad + first_pair + threadIdx.x) : 0;
-  const int64_t units = static_cast<int64_t>(__ldcg(p.ws.header + 3)) * p.hkv * chunks;
+  const int64_t units = static_cast<int64_t>(__ldcg(p.ws.header + 3)) * chunks;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int32_t r = static_cast<int32_t>(u % chunks) * rows_per_unit + warp / per_row;
-    const int64_t rest = u / chunks;
-    const int32_t kh = static_cast<int32_t>(rest % p.hkv);
-    const int4 e = __ldcg(reinterpret_cast<const int4*>(p.ws.merges) + rest / p.hkv);
+    const int64_t entry = u / chunks;
+    const int32_t flat = static_cast<int32_t>(u - entry * chunks) * rows_per_unit + mine;
+    const bool in = flat < tile_rows;
+    const int32_t kh = in ? flat / p.ws.part_rows : 0, r = in ? flat - kh * p.ws.part_rows : 0;
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(p.ws.merges) + entry);
     const int32_t tok = e.y * p.sh.tokens_per_item + r / p.group;
-    const bool live = r < p.ws.part_rows && tok < __ldg(p.draft_lens + e.x) && !__ldcg(p.ws.bad + e.x * p.hkv + kh);
+    const bool live = in && tok < __ldg(p.draft_lens + e.x) && !__ldcg(p.ws.bad + e.x * p.hkv + kh);
     const int64_t slot_rows = static_cast<int64_t>(p.hkv) * p.ws.part_rows;  // rows between partial slots
     const int64_t row0 = (static_cast<int64_t>(e.z) * p.hkv + kh) * p.ws.part_rows + r;
     const int64_t row = __ldg(p.qo_indptr + e.x) + tok;
+    __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D;
     wait_partials();
-    float acc[V], m = -INFINITY, wsum = 0.f;
-    merge_partials<V, kAhead>(
-        live ? e.w : 0, share, per_row, [&](int s) { return __ldcg(p.ws.part_lse + row0 + s * slot_rows); },
-        [&](int s, float(&x)[V]) { load_row_cg<V>(p.ws.part_o + (row0 + s * slot_rows) * D + lane * V, x); }, acc, m,
-        wsum);
-    if (per_row > 1) {
+    auto lse_at = [&](int s) { return __ldcg(p.ws.part_lse + row0 + s * slot_rows); };
+    auto row_at = [&](int s, float(&x)[V]) { load_row_part<LPR, V>(p.ws.part_o + (row0 + s * slot_rows) * D, sub, x); };
+    float acc[V], wsum;
+    if constexpr (FEW) {
+      float m;
+      merge_partials<V, 8>(
+          live ? e.w : 0, share, per_row, lse_at,
+          [&](int s, float(&x)[V]) { load_row_cg<V>(p.ws.part_o + (row0 + s * slot_rows) * D + lane * V, x); }, acc, m,
+          wsum);
       __syncthreads();  // the unit before has been read
 #pragma unroll
       for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
       if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
       __syncthreads();
-      if (share != 0) continue;
-      float top = m;
-      for (int k = 1; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
-      const float ref = top == -INFINITY ? 0.f : top;
+      if (share != 0 || !live) continue;
+      join_shares<V>(per_row, warp, s_acc, s_m, s_w, acc, wsum);
+      const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = 0.f;
-      wsum = 0.f;
-      for (int k = 0; k < per_row; ++k) {
-        const float f = ex2(s_m[warp + k] - ref);
-        wsum = fmaf(f, s_w[warp + k], wsum);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(f, s_acc[warp + k][lane * V + v], acc[v]);
-      }
+      for (int v = 0; v < V; v += 2)
+        *reinterpret_cast<__nv_bfloat162*>(dst + lane * V + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+    } else {
+      merge_rows<LPR, V, 256 / D>(live ? e.w : 0, lse_at, row_at, acc, wsum);
+      if (live) store_row_part<LPR, V>(dst, sub, acc, wsum == 0.f ? 0.f : 1.f / wsum);
     }
-    if (!live) continue;
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D + lane * V;
-#pragma unroll
-    for (int v = 0; v < V; v += 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
   }
   wait_partials();
   const int64_t threads = static_cast<int64_t>(gridDim.x) * kMergeThreads;
@@ -408,9 +405,11 @@ ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& d
   const int64_t rows = std::max<int64_t>(1, tiles) * p.hkv * p.ws.part_rows;
   const int64_t most = static_cast<int64_t>(dev.num_sms) * 8;
   int per_row = 1;
-  while (per_row < kMergeWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 4 * kMergeWarps) per_row *= 2;
-  const int64_t want = (rows * per_row + kMergeWarps - 1) / kMergeWarps;
-  auto kern = head_dim == 128 ? tree_merge_kernel<128> : tree_merge_kernel<64>;
+  while (per_row < kMergeWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 3 * kMergeWarps) per_row *= 2;
+  const int64_t per_cta = per_row > 1 ? kMergeWarps / per_row : kMergeThreads / 8;
+  const int64_t want = (rows + per_cta - 1) / per_cta;
+  auto kern = per_row > 1 ? (head_dim == 128 ? tree_merge_kernel<128, true> : tree_merge_kernel<64, true>)
+                          : (head_dim == 128 ? tree_merge_kernel<128, false> : tree_merge_kernel<64, false>);
   return launch_pdl("tree_merge_kernel", kern, dim3(static_cast<unsigned>(want < most ? want : most)),
                     dim3(kMergeThreads), 0, s, p, per_row);
 }
