@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
   }
   // Units per split.  The least is total / (waves * SMs), which bounds the partials.  With that many unsplit
   // items it also balances the SMs; with fewer, the longest range is cut into the number of pieces (at most
-  // two per SM and head) whose schedule is shortest: a piece alone, or the mean load of an SM and a quarter
-  // of a piece for the uneven end of a longest-first list.  64 numbers of pieces are weighed, four threads
-  // each; the estimate may round (only the choice depends on it).
+  // two per SM and head) whose longest-first schedule is shortest: the rounds of full pieces, and what the
+  // shorter last pieces take beyond the gaps of the last round.  64 numbers of pieces are weighed, four
+  // threads each; the estimate may round (only the choice depends on it).
   const unsigned long long all = work * heads;
   const unsigned long long per_slot =
       all >> 31 ? (all + slots - 1) / slots : (static_cast<uint32_t>(all) + slots - 1) / static_cast<uint32_t>(slots);
@@ -125,16 +125,26 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
     const int32_t k = cand < 32 ? min(cand + 1, most) : min(most, 32 + (cand - 31) * max(most - 32, 0) / 32);
     const int32_t c = max((longest + k - 1) / k, least);
     const float per = 1.f / static_cast<float>(c);
-    int32_t fixed = 0;
+    int32_t n_full = 0, n_rem = 0, rem_units = 0;
     for (int32_t b = t & 3; b < p.batch; b += 4) {
       const int4 q = request(b, false);
-      const int32_t pieces = static_cast<int32_t>(ceilf(static_cast<float>(q.z) * per - 1e-3f));
-      fixed += q.w * pieces * (pieces > 1 ? p.sh.split_overhead : p.sh.overhead);
+      const int32_t full = static_cast<int32_t>(static_cast<float>(q.z) * per + 1e-3f), rem = max(q.z - full * c, 0);
+      n_full += q.w * full;
+      n_rem += rem > 0 ? q.w : 0;
+      rem_units += q.w * rem;
     }
-    fixed += __shfl_xor_sync(0xffffffffu, fixed, 1);
-    fixed += __shfl_xor_sync(0xffffffffu, fixed, 2);
-    const float mean = (static_cast<float>(all) + static_cast<float>(fixed) * heads) * (1.f / kTreeSms);
-    float cost = fmaxf(static_cast<float>(c + (c < longest ? p.sh.split_overhead : p.sh.overhead)), mean + 0.25f * c);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      n_full += __shfl_xor_sync(0xffffffffu, n_full, off);
+      n_rem += __shfl_xor_sync(0xffffffffu, n_rem, off);
+      rem_units += __shfl_xor_sync(0xffffffffu, rem_units, off);
+    }
+    const float piece = static_cast<float>(c + (c < longest ? p.sh.split_overhead : p.sh.overhead));
+    const float fulls = static_cast<float>(n_full * heads);
+    const float rounds = fmaxf(ceilf(fulls * (1.f / kTreeSms)), 1.f);
+    const float rest = static_cast<float>(rem_units * heads) + static_cast<float>(n_rem * heads) * p.sh.split_overhead;
+    const float beyond = rest - 0.8f * (rounds * kTreeSms - fulls) * piece;
+    float cost = rounds * piece + (beyond > 0.f ? beyond * (1.f / kTreeSms) + 0.5f * static_cast<float>(c) : 0.f);
     int32_t mine = c;
 #pragma unroll
     for (int off = 16; off >= 4; off >>= 1) {
