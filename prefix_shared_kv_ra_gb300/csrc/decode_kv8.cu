@@ -520,13 +520,17 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   p.n_hgroups = sh.blocks;
   p.row_stride = sh.block_bytes;
   p.stage_bytes = kSlab * p.row_stride;
-  p.nstage = (kRingSmemLimit - kRingHdrBytes) / p.stage_bytes;
+  // A CTA of few heads waits on its own chain of slab, scores, softmax and product: two share an SM (their
+  // registers fit for up to 3 heads of 128, 4 of 64).
+  const int per_sm = sh.hpc <= (head_dim == 128 ? 3 : 4) ? 2 : 1;
+  p.nstage = (kRingSmemLimit / per_sm - 1024 - kRingHdrBytes) / p.stage_bytes;  // (1 KB per CTA is the system's)
   if (p.nstage > kRingMaxStages) p.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + p.nstage * p.stage_bytes;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (ra_status st = launch_decode_plan(p, 0, s)) return st;
   const int64_t n_items = static_cast<int64_t>(pl.max_items) * p.n_hgroups;  // bound of the claims
-  const int grid = static_cast<int>(n_items < dev.num_sms ? n_items : dev.num_sms);
+  const int64_t ctas = static_cast<int64_t>(dev.num_sms) * per_sm;
+  const int grid = static_cast<int>(n_items < ctas ? n_items : ctas);
   if (ra_status st = head_dim == 128 ? launch<128>(pp, grid, smem, dev, s) : launch<64>(pp, grid, smem, dev, s))
     return st;
   // few rows: as many warps per row as three CTAs per SM hold

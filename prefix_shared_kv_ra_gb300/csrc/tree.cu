@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
   if (t == 0) s_parts = s_merges = 0;
   const int32_t per_item = p.sh.tokens_per_item, heads = p.sh.heads, unit = p.sh.unit;
   const int32_t slots = p.sh.waves * kTreeSms;  // items that fill the SMs `waves` times
+  const int32_t ctas = p.sh.per_sm * kTreeSms;
   auto request = [&](int32_t b, bool first) -> int4 {
     if (!first && b < kPlanCached) return s_req[b];
     int4 q;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
   const int32_t least = max(1, static_cast<int32_t>(min(per_slot, static_cast<unsigned long long>(longest))));
   int32_t chunk = least;
   if (static_cast<int64_t>(entries) * heads < slots) {
-    const int32_t most = max(1, min(longest, 2 * kTreeSms / heads));
+    const int32_t most = max(1, min(longest, 2 * ctas / heads));
     const int32_t cand = t >> 2;
     const int32_t k = cand < 32 ? min(cand + 1, most) : min(most, 32 + (cand - 31) * max(most - 32, 0) / 32);
     const int32_t c = max((longest + k - 1) / k, least);
@@ -141,10 +142,10 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
     }
     const float piece = static_cast<float>(c + (c < longest ? p.sh.split_overhead : p.sh.overhead));
     const float fulls = static_cast<float>(n_full * heads);
-    const float rounds = fmaxf(ceilf(fulls * (1.f / kTreeSms)), 1.f);
+    const float sms = static_cast<float>(ctas), rounds = fmaxf(ceilf(fulls / sms), 1.f);
     const float rest = static_cast<float>(rem_units * heads) + static_cast<float>(n_rem * heads) * p.sh.split_overhead;
-    const float beyond = rest - 0.8f * (rounds * kTreeSms - fulls) * piece;
-    float cost = rounds * piece + (beyond > 0.f ? beyond * (1.f / kTreeSms) + 0.5f * static_cast<float>(c) : 0.f);
+    const float beyond = rest - 0.8f * (rounds * sms - fulls) * piece;
+    float cost = rounds * piece + (beyond > 0.f ? beyond / sms + 0.5f * static_cast<float>(c) : 0.f);
     int32_t mine = c;
 #pragma unroll
     for (int off = 16; off >= 4; off >>= 1) {
@@ -507,7 +508,7 @@ extern "C" ra_status ra_tree_attention(const void* k_pool, const void* v_pool, i
   p.batch = batch;
   p.max_draft = max_draft_len;
   p.max_prefix = max_prefix_len;
-  p.sh = tree_shape(num_q_heads, num_kv_heads, max_draft_len);
+  p.sh = tree_shape(num_q_heads, num_kv_heads, head_dim, max_draft_len);
   p.err = device_error;
   return launch_tree(p, head_dim, dev, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -20,6 +20,7 @@ struct TreeShape {
   bool narrow;
   int32_t row_blocks;       // narrow: 16-row blocks per kv head (1 or 2)
   int32_t hpc;              // narrow: kv heads per item
+  int32_t per_sm;           // CTAs of the attention kernel per SM
   int32_t heads;            // items per (request, query tile, split): kv heads, or head groups when narrow
   int32_t tokens_per_item;  // drafted tokens of a query tile
   int32_t unit;             // keys per unit of the plan (a key tile, or a slab pair)
@@ -28,14 +29,19 @@ struct TreeShape {
   int32_t split_overhead;   // that of a split item: its partials are written and read again
 };
 
-inline TreeShape tree_shape(int32_t hq, int32_t hkv, int32_t max_draft) {
+// Consumer warps of a narrow CTA: as many as their registers (accumulators of D values per row) allow.
+constexpr int tree_consumers(int32_t head_dim) { return head_dim == 128 ? 8 : 16; }
+
+inline TreeShape tree_shape(int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_draft) {
   TreeShape s{};
   const int32_t group = hq / hkv;
   const int64_t rows = static_cast<int64_t>(max_draft) * group;
   s.narrow = rows <= kTreeNarrowRows;
   if (s.narrow) {
     s.row_blocks = rows <= 16 ? 1 : 2;
-    for (s.hpc = 8 / s.row_blocks; hkv % s.hpc != 0;) --s.hpc;
+    for (s.hpc = tree_consumers(head_dim) / s.row_blocks; hkv % s.hpc != 0;) --s.hpc;
+    // a CTA of few consumer warps waits on its own chain of slab, scores, softmax and product: two share an SM
+    s.per_sm = s.hpc * s.row_blocks <= 2 ? 2 : 1;
     s.heads = hkv / s.hpc;
     s.tokens_per_item = max_draft;
     s.unit = 32;
@@ -44,6 +50,7 @@ inline TreeShape tree_shape(int32_t hq, int32_t hkv, int32_t max_draft) {
     s.split_overhead = 1 + s.row_blocks;  // a row's fp32 partial costs what 2 of a unit's 32 keys do
   } else {
     s.heads = hkv;
+    s.per_sm = 1;
     s.tokens_per_item = 2 * (128 / group);
     s.unit = 128;
     s.waves = 2;
@@ -72,7 +79,7 @@ inline TreeWorkspace layout_tree(int32_t batch, int64_t total_q, int32_t hq, int
                           void* base) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const int32_t group = hq / hkv;
-  const TreeShape sh = tree_shape(hq, hkv, max_draft);
+  const TreeShape sh = tree_shape(hq, hkv, d, max_draft);
   TreeWorkspace w{};
   w.cap_parts = 2 * sh.waves * kTreeSms / sh.heads;
   w.cap = (total_q + sh.tokens_per_item - 1) / sh.tokens_per_item + batch + w.cap_parts;

@@ -5,8 +5,8 @@
 // that is under the ~290 flop per byte at which GB300's tensor cores would bound it, and HBM is the bound.  So
 // the kernel is built like the decode one: copies of whole slot rows of a head group (hpc * D * 2 bytes, one
 // bulk copy for K and one for V of a key) into a ring, and consumer warps on mma.sync, which take 16 rows of one
-// head each: row_blocks warps share a head's keys in shared memory (8 warps in all: 8 heads of 16 rows, 4 of 32
-// or 2 of 64).  A tcgen05 tile would have 128 rows, and its swizzled operand layout would force 128-byte copies.
+// head each: row_blocks warps share a head's keys in shared memory (D = 128: up to 8 warps, 8 heads of 16 rows or
+// 4 of 32; D = 64: up to 16).  A tcgen05 tile would have 128 rows, and its swizzled operand layout would force 128-byte copies.
 //
 // Per warp: S = Q K^T with Q in registers (A) and K read by ldmatrix (B, keys as columns), online softmax with a
 // lazy reference per row (reduced over the 4 lanes of a row), P packed from the score fragments into A
@@ -20,8 +20,6 @@ namespace ra {
 
 namespace {
 
-constexpr int kConsumers = 8;
-constexpr int kThreads = 32 * (kConsumers + kRingProducers);
 constexpr float kRescale = 8.0f;  // log2 units: a row's reference moves when a score exceeds it by more
 
 struct NarrowParams {
@@ -73,7 +71,8 @@ struct NarrowSource {
 };
 
 template <int D, int SLAB>
-__global__ void __launch_bounds__(kThreads, 1) tree_narrow_kernel(const __grid_constant__ NarrowParams n) {
+__global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
+    tree_narrow_kernel(const __grid_constant__ NarrowParams n) {
   const TreeParams& p = n.t;
   constexpr int KT = D / 16;     // k steps of the scores
   constexpr int NB = SLAB / 8;   // 8-key blocks of a slab
@@ -278,7 +277,7 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
   n.row_bytes = p.sh.hpc * D * 2;
   n.row_stride = n.row_bytes + 16;
   n.stage_bytes = 2 * SLAB * n.row_stride;
-  n.nstage = (kRingSmemLimit - kRingHdrBytes) / n.stage_bytes;
+  n.nstage = (kRingSmemLimit / p.sh.per_sm - 1024 - kRingHdrBytes) / n.stage_bytes;  // (1 KB per CTA is the system's)
   if (n.nstage > kRingMaxStages) n.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + n.nstage * n.stage_bytes;
   auto kern = tree_narrow_kernel<D, SLAB>;
@@ -289,7 +288,8 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
     configured[dev.device] = true;
   }
   const int64_t items = p.ws.cap * p.sh.heads;
-  const int grid = static_cast<int>(items < dev.num_sms ? items : dev.num_sms);
+  const int64_t ctas = static_cast<int64_t>(dev.num_sms) * p.sh.per_sm;
+  const int grid = static_cast<int>(items < ctas ? items : ctas);
   return launch_pdl("tree_narrow_kernel", kern, dim3(grid),
                     dim3(32 * (p.sh.hpc * p.sh.row_blocks + kRingProducers)), smem, s, n);
 }
