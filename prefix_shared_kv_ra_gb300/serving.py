@@ -13,6 +13,8 @@ explainer, §04; anrans handbook "v0.2：不到四千行的调度核心跑出 3.
 * one decode token for every request past its prefill: a fresh slot each, then ra_kv_store +
   ra_decode_attention replayed from a CUDA graph captured per padded batch size (padding rows
   read and write the dummy slot 0, as the pages' CUDA-graph decode does);
+  with kv_dtype="e4m3" the cache is a quantised pool: ra_kv8_store and ra_kv8_decode_attention, and for the
+  extend call the admitted requests' contexts read back into bf16 rows of the step (ra_kv8_load);
 * completion: a finished turn is inserted into the tree (slots of positions another request
   inserted meanwhile are freed), unlocked, and its row released.
 
@@ -29,7 +31,7 @@ import numpy as np
 import torch
 
 from . import (ra_decode_attention, ra_decode_workspace_bytes, ra_extend_attention, ra_extend_workspace_bytes,
-               ra_kv_store)
+               ra_kv8_decode_attention, ra_kv8_load, ra_kv8_slot_bytes, ra_kv8_store, ra_kv_store)
 from .radix import RadixCache, SlotPool
 
 __all__ = ["ServingReplay", "Request", "multiturn_chat", "run_chat"]
@@ -50,15 +52,22 @@ class Request:
 class ServingReplay:
     def __init__(self, *, num_slots: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_len: int,
                  max_running: int, device, seed: int = 0, graph_sizes: Sequence[int] = (8, 16, 32, 64, 128, 256),
-                 use_graphs: bool = True):
+                 use_graphs: bool = True, kv_dtype: str = "bf16"):
+        if kv_dtype not in ("bf16", "e4m3"):
+            raise ValueError(f"kv_dtype must be 'bf16' or 'e4m3' (got {kv_dtype!r})")
         self.dev = torch.device(device)
         self.hq, self.hkv, self.d = num_q_heads, num_kv_heads, head_dim
         self.max_len, self.max_running = max_len, max_running
         self.pool = SlotPool(num_slots)
         self.cache = RadixCache(self.pool)
         bf = torch.bfloat16
-        self.k_pool = torch.zeros((num_slots, num_kv_heads, head_dim), dtype=bf, device=self.dev)
-        self.v_pool = torch.zeros_like(self.k_pool)
+        self.kv8_pool = None
+        if kv_dtype == "e4m3":
+            self.kv8_pool = torch.zeros((num_slots, ra_kv8_slot_bytes(num_kv_heads, head_dim)), dtype=torch.uint8,
+                                        device=self.dev)
+        else:
+            self.k_pool = torch.zeros((num_slots, num_kv_heads, head_dim), dtype=bf, device=self.dev)
+            self.v_pool = torch.zeros_like(self.k_pool)
         # rows 0 .. max_running-1 for requests; the last row is the padding row (slot 0 everywhere)
         self.table = torch.zeros((max_running + 1, max_len), dtype=torch.int32, device=self.dev)
         self.pad_row = max_running
@@ -98,6 +107,25 @@ class ServingReplay:
     def _i32(self, a) -> torch.Tensor:
         return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(self.dev, non_blocking=True)
 
+    def _store(self, k_new, v_new, loc) -> None:
+        if self.kv8_pool is not None:
+            ra_kv8_store(self.kv8_pool, k_new, v_new, loc, device_error=self.err)
+        else:
+            ra_kv_store(self.k_pool, self.v_pool, k_new, v_new, loc, device_error=self.err)
+
+    def _extend_pool(self, admitted, rows):
+        """K and V pool, table and table rows of the extend call over the admitted requests."""
+        if self.kv8_pool is None:
+            return self.k_pool, self.v_pool, self.table, rows
+        # row i of the call's own pool holds the i-th position of the requests' contexts, one after the other
+        lens = np.array([r.slots.size for r in admitted])
+        starts = np.concatenate([[0], np.cumsum(lens)])
+        k = torch.empty((int(starts[-1]), self.hkv, self.d), dtype=torch.bfloat16, device=self.dev)
+        v = torch.empty_like(k)
+        ra_kv8_load(self.kv8_pool, self._i32(np.concatenate([r.slots for r in admitted])), k, v, device_error=self.err)
+        table = np.minimum(starts[:-1, None] + np.arange(lens.max())[None, :], starts[1:, None] - 1)
+        return k, v, self._i32(table), self._i32(np.arange(len(admitted)))
+
     # ------------------------------------------------------------------ decode graphs
     def _graph(self, bs: int):
         if bs in self._graphs:
@@ -114,10 +142,14 @@ class ServingReplay:
                                 dtype=torch.uint8, device=self.dev)
 
         def run():
-            ra_kv_store(self.k_pool, self.v_pool, buf["k_new"], buf["v_new"], buf["loc"], device_error=self.err)
-            ra_decode_attention(self.k_pool, self.v_pool, buf["q"], buf["o"], self.table, buf["rpi"], buf["lens"],
-                                max_seq_len=self.max_len, sm_scale=self.scale, workspace=buf["ws"],
-                                device_error=self.err)
+            self._store(buf["k_new"], buf["v_new"], buf["loc"])
+            args = dict(max_seq_len=self.max_len, sm_scale=self.scale, workspace=buf["ws"], device_error=self.err)
+            if self.kv8_pool is not None:
+                ra_kv8_decode_attention(self.kv8_pool, buf["q"], buf["o"], self.table, buf["rpi"], buf["lens"],
+                                        num_kv_heads=self.hkv, **args)
+            else:
+                ra_decode_attention(self.k_pool, self.v_pool, buf["q"], buf["o"], self.table, buf["rpi"], buf["lens"],
+                                    **args)
         g = None
         if self.use_graphs:
             run()  # first-call set-up outside the capture
@@ -182,12 +214,12 @@ class ServingReplay:
             total = int(ext.sum())
             loc = np.concatenate([r.slots[r.cached:] for r in admitted])
             q = self._randn((total, self.hq, self.d))
-            ra_kv_store(self.k_pool, self.v_pool, self._randn((total, self.hkv, self.d)),
-                        self._randn((total, self.hkv, self.d)), self._i32(loc), device_error=self.err)
+            self._store(self._randn((total, self.hkv, self.d)), self._randn((total, self.hkv, self.d)),
+                        self._i32(loc))
+            k_pool, v_pool, table, rows = self._extend_pool(admitted, self._i32([r.row for r in admitted]))
             ws = torch.empty(ra_extend_workspace_bytes(len(admitted), total, self.hq, self.hkv), dtype=torch.uint8,
                              device=self.dev)
-            ra_extend_attention(self.k_pool, self.v_pool, q, torch.empty_like(q), self.table,
-                                self._i32([r.row for r in admitted]), self._i32(pre), self._i32(ext),
+            ra_extend_attention(k_pool, v_pool, q, torch.empty_like(q), table, rows, self._i32(pre), self._i32(ext),
                                 self._i32(np.concatenate([[0], np.cumsum(ext)])), max_extend_len=int(ext.max()),
                                 max_prefix_len=int(pre.max()), sm_scale=self.scale, workspace=ws,
                                 device_error=self.err)

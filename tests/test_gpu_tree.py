@@ -120,7 +120,8 @@ CASES = [
     ([640], [100], 16, 16, 128, "tree"), ([45, 700], [31, 32], 5, 5, 64, "tree"), ([200], [17], 12, 3, 128, "chain"),
     ([260, 10], [40, 96], 32, 8, 128, "any"), ([0, 0, 64], [40, 33, 9], 32, 8, 128, "any"),
     ([0, 130], [70, 70], 8, 2, 64, "none"), ([4000], [4], 8, 1, 128, "tree"), ([250], [12], 16, 1, 128, "tree"),
-    ([20, 400], [1024, 700], 4, 1, 64, "tree"),
+    ([20, 400], [1024, 700], 4, 1, 64, "tree"), ([70, 0], [1, 3], 32, 1, 128, "tree"), ([300], [5], 128, 1, 64, "tree"),
+    ([150, 31], [2, 1], 64, 4, 128, "tree"), ([97], [6], 40, 20, 64, "any"), ([33, 500, 64], [32, 17, 1], 11, 11, 64, "tree"),
 ]
 
 
