@@ -291,7 +291,7 @@ def ra_decode_attention_static(k_pool: torch.Tensor, v_pool: torch.Tensor, q: to
 
 
 def _native():
-    """The C side of the calls below: the same checks and the call, without ctypes' cost per argument."""
+    """The C++ side of the calls below: the same checks and the call, without ctypes' cost per argument."""
     global _binding
     if _binding is None:
         lib = load()
@@ -302,17 +302,9 @@ def _native():
         spec.loader.exec_module(mod)
         fns = (lib.ra_kv8_store, lib.ra_kv8_load, lib.ra_kv8_slot_bytes, lib.ra_kv8_decode_attention,
                lib.ra_qk_norm_rope_store, lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention)
-        mod.init(torch.bfloat16, torch.int32, torch.float32, torch.uint8, torch._C._cuda_getCurrentRawStream,
-                 torch._C._cuda_getDevice, *(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
+        mod.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
         _binding = mod
     return _binding
-
-
-def _failed(status: int, fn, device: torch.device, *args) -> None:
-    if status == -1:  # another device is current: the library asks for the current device's properties
-        with torch.cuda.device(device):
-            status = fn(*args)
-    _check(status)
 
 
 @functools.lru_cache(maxsize=None)
@@ -327,19 +319,17 @@ def ra_kv8_slot_bytes(num_kv_heads: int, head_dim: int) -> int:
 def ra_kv8_store(kv8_pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, out_cache_loc: torch.Tensor,
                  device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise new K/V rows ([num_tokens, Hkv, D] bf16) into the records of slots out_cache_loc."""
-    args = (kv8_pool, k_new, v_new, out_cache_loc, device_error, stream)
-    status = _native().kv8_store(*args)
+    status = (_binding or _native()).kv8_store(kv8_pool, k_new, v_new, out_cache_loc, device_error, stream)
     if status:
-        _failed(status, _native().kv8_store, kv8_pool.device, *args)
+        _check(status)
 
 
 def ra_kv8_load(kv8_pool: torch.Tensor, slots: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
                 device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Read the records of `slots` back into K/V rows ([num_tokens, Hkv, D] bf16), exactly."""
-    args = (kv8_pool, slots, k_out, v_out, device_error, stream)
-    status = _native().kv8_load(*args)
+    status = (_binding or _native()).kv8_load(kv8_pool, slots, k_out, v_out, device_error, stream)
     if status:
-        _failed(status, _native().kv8_load, kv8_pool.device, *args)
+        _check(status)
 
 
 def ra_kv8_decode_attention(kv8_pool: torch.Tensor, q: torch.Tensor, o: torch.Tensor, req_to_token: torch.Tensor,
@@ -348,11 +338,10 @@ def ra_kv8_decode_attention(kv8_pool: torch.Tensor, q: torch.Tensor, o: torch.Te
                             device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """ra_decode_attention over a quantised pool (uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)]); q, o
     [batch, Hq, D] bf16; workspace: uint8, ra_decode_workspace_bytes(batch, Hq, Hkv, D, max_seq_len)."""
-    args = (kv8_pool, q, o, req_to_token, req_pool_indices, seq_lens, num_kv_heads, max_seq_len, sm_scale, workspace,
-            device_error, stream)
-    status = _native().kv8_decode(*args)
+    status = (_binding or _native()).kv8_decode(kv8_pool, q, o, req_to_token, req_pool_indices, seq_lens, num_kv_heads,
+                                                max_seq_len, sm_scale, workspace, device_error, stream)
     if status:
-        _failed(status, _native().kv8_decode, kv8_pool.device, *args)
+        _check(status)
 
 
 def ra_qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -363,11 +352,10 @@ def ra_qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
     """Per-head RMS norm of q and k, their rotation by cos_sin[positions] (fp32 [max_position, rotary_dim]:
     cosines, then sines), q written to q_out, k and v to pool slots out_cache_loc.  q, k, v, q_out
     [num_tokens, H, D] bf16, any token stride; weights [D] bf16, or None for no norm."""
-    args = (q, k, v, q_weight, k_weight, positions, cos_sin, q_out, k_pool, v_pool, out_cache_loc, eps, interleaved,
-            device_error, stream)
-    status = _native().norm_rope_store(*args)
+    status = (_binding or _native()).norm_rope_store(q, k, v, q_weight, k_weight, positions, cos_sin, q_out, k_pool,
+                                                     v_pool, out_cache_loc, eps, interleaved, device_error, stream)
     if status:
-        _failed(status, _native().norm_rope_store, k_pool.device, *args)
+        _check(status)
 
 
 def ra_qk_norm_rope_kv8_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -376,11 +364,10 @@ def ra_qk_norm_rope_kv8_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                               eps: float = 1e-6, interleaved: bool = False,
                               device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """ra_qk_norm_rope_store into a quantised pool (uint8 [num_slots, ra_kv8_slot_bytes(Hkv, D)])."""
-    args = (q, k, v, q_weight, k_weight, positions, cos_sin, q_out, kv8_pool, out_cache_loc, eps, interleaved,
-            device_error, stream)
-    status = _native().norm_rope_kv8_store(*args)
+    status = (_binding or _native()).norm_rope_kv8_store(q, k, v, q_weight, k_weight, positions, cos_sin, q_out,
+                                                         kv8_pool, out_cache_loc, eps, interleaved, device_error, stream)
     if status:
-        _failed(status, _native().norm_rope_kv8_store, kv8_pool.device, *args)
+        _check(status)
 
 
 def ra_tree_workspace_bytes(batch: int, total_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -397,8 +384,8 @@ def ra_tree_attention(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Tenso
     """Drafted tokens (q, o [total_q, Hq, D] bf16, request b's rows from qo_indptr[b]) over their request's
     cached prefix and the drafted tokens named by their bit masks (tree_mask int32 [total_q, words], bit c % 32
     of word c / 32 = drafted token c of the request is visible)."""
-    args = (k_pool, v_pool, q, o, req_to_token, req_pool_indices, prefix_lens, draft_lens, qo_indptr, tree_mask,
-            max_draft_len, max_prefix_len, sm_scale, workspace, device_error, stream)
-    status = _native().tree(*args)
+    status = (_binding or _native()).tree(k_pool, v_pool, q, o, req_to_token, req_pool_indices, prefix_lens, draft_lens,
+                                          qo_indptr, tree_mask, max_draft_len, max_prefix_len, sm_scale, workspace,
+                                          device_error, stream)
     if status:
-        _failed(status, _native().tree, k_pool.device, *args)
+        _check(status)

@@ -4,14 +4,16 @@ Each translation unit is compiled in parallel to an object file under
 ``_build/``; they are linked into ``prefix_shared_kv_ra_gb300/libra.so``
 (static cudart, no libcuda link dependency: the driver entry points the
 library needs are resolved at run time).  ``_ra_binding.so`` beside it is the Python
-side of the small operators, plain C.  A rebuild happens only when a
+side of the small operators, C++.  A rebuild happens only when a
 source or header is newer than the library.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -21,7 +23,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libra.so")
-BINDING = os.path.join(PKG, "_ra_binding.so")  # argument checks of the small operators (CPython API, no CUDA)
+BINDING = os.path.join(PKG, "_ra_binding.so")  # argument checks of the small operators (CPython API and torch's C++ tensors)
 SOURCES = ["api_common.cu", "kv_store.cu", "decode.cu", "extend.cu", "decode_static.cu",
            "kv8_store.cu", "decode_kv8.cu", "qk_norm_rope.cu", "tree.cu", "tree_narrow.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,19 +53,23 @@ def _stale(target: str) -> bool:
 def build_binding(force: bool = False) -> str:
     if not force and not _stale(BINDING):
         return BINDING
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_lib = os.path.join(torch_dir, "lib")
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(shutil.which(_nvcc()) or _nvcc())), "include")
     tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I",
-                        sysconfig.get_paths()["include"], os.path.join(CSRC, "py_binding.c"), "-o", tmp],
-                       capture_output=True, text=True)
+    r = subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-Wno-missing-field-initializers", "-shared",
+                        "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"), "-I",
+                        cuda_include, os.path.join(CSRC, "py_binding.cpp"), "-o", tmp, "-L", torch_lib, "-ltorch_python",
+                        "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{torch_lib}"], capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for py_binding.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for py_binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    build_binding(force)
     if not force and not _stale(LIB):
+        build_binding()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -80,8 +86,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

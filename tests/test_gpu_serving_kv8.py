@@ -38,8 +38,3 @@ def test_chat_replay_over_a_quantised_pool():
         bound = R.attention_bound(ref, a, x, 128, R.EPS_F16) + lens[b] * 2.0 ** -24 * np.abs(v).max()
         assert (np.abs(o - ref) <= bound).all()
 
-
-def test_unknown_kv_dtype_is_refused():
-    with pytest.raises(ValueError):
-        ServingReplay(num_slots=64, num_q_heads=2, num_kv_heads=1, head_dim=64, max_len=8, max_running=1,
-                      device="cuda:0", kv_dtype="int8")

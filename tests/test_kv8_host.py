@@ -160,3 +160,18 @@ def test_bindings_check_before_the_call():
         ra.ra_qk_norm_rope_kv8_store(q, k, k, w, w, idx, cs.double(), q, pool, idx)
     with pytest.raises(ValueError):
         ra.ra_qk_norm_rope_kv8_store(q, k, k, w[:32], w, idx, cs, q, pool, idx)
+
+
+def test_replay_refuses_an_unknown_cache_type():
+    from prefix_shared_kv_ra_gb300.serving import ServingReplay
+    with pytest.raises(ValueError):
+        ServingReplay(num_slots=64, num_q_heads=2, num_kv_heads=1, head_dim=64, max_len=8, max_running=1,
+                      device="cuda:0", kv_dtype="int8")
+
+
+def test_bindings_take_tensors_only():
+    t = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    pool = torch.zeros(16, ra.ra_kv8_slot_bytes(2, 64), dtype=torch.uint8)
+    for bad in (None, 3, [1, 2], np.zeros(3, np.int32)):
+        with pytest.raises(TypeError):
+            ra.ra_kv8_store(pool, t, t, bad)
