@@ -31,6 +31,7 @@
 #include "kv8.cuh"
 #include "ra_ptx.cuh"
 #include "slab_ring.cuh"
+#include "small_plan.cuh"
 
 namespace ra {
 
@@ -45,20 +46,64 @@ struct Kv8DecodeParams {
   const uint8_t* pool;
   int64_t slot_bytes;
   int32_t block_bytes;
+  int32_t ctas;  // small call: the grid
+};
+constexpr int kSmallLeast = 2;  // units of a small call's shortest piece
+
+// The items of a call: the plan kernel's list, or (SMALL) this warp's own plan.
+template <bool SMALL>
+struct Kv8Items {
+  const DecodeParams& p;
+  SmallPlan plan;
+  int32_t len, row;  // SMALL: of this lane's request
+
+  __device__ __forceinline__ Kv8Items(const DecodeParams& q, int32_t ctas, bool report) : p(q), len(0), row(0) {
+    if constexpr (SMALL) {
+      const int lane = threadIdx.x & 31;
+      if (lane < p.batch) {
+        row = __ldg(p.rpi + lane);
+        len = __ldg(p.seq_lens + lane);
+        const bool bad_row = row < 0 || row >= p.table_rows, bad_len = len < 1 || len > p.max_seq_len;
+        if (report && bad_row) flag_error(p.err, RA_DEVERR_TABLE);
+        else if (report && bad_len) flag_error(p.err, RA_DEVERR_LENGTH);
+        len = bad_row || len < 1 ? 0 : min(len, p.max_seq_len);
+      }
+      plan.make(len, p.n_hgroups, ctas, kSmallLeast);
+    }
+  }
+  __device__ __forceinline__ int32_t count() const { return (SMALL ? plan.n : p.plan[0]) * p.n_hgroups; }
+  // (SMALL: warp-collective)
+  __device__ __forceinline__ void item(int32_t idx, Item& it) const {
+    if constexpr (SMALL) {
+      it.hg = idx % p.n_hgroups;
+      it.d = idx / p.n_hgroups;
+      it.b = plan.request(it.d);
+      it.split = it.d - of_lane(plan.first, it.b);
+      it.n_splits = of_lane(plan.pieces, it.b);
+      it.row = of_lane(row, it.b);
+      it.start = 0;
+      it.k0 = it.split * plan.chunk;
+      it.k1 = min(of_lane(len, it.b), it.k0 + plan.chunk);
+    } else {
+      decode_item(p, idx, it);
+    }
+  }
 };
 
 // The producers' view: one bulk copy per key, the head group's block of the slot's record.
+template <bool SMALL>
 struct Kv8Source {
   const Kv8DecodeParams& pp;
+  const Kv8Items<SMALL>& items;
   int32_t* counter;
   int64_t num_slots;
   uint32_t* err;
-  __device__ __forceinline__ explicit Kv8Source(const Kv8DecodeParams& q)
-      : pp(q), counter(q.d.counter), num_slots(q.d.num_slots), err(q.d.err) {}
-  __device__ __forceinline__ int32_t claims() const { return pp.d.plan[0] * pp.d.n_hgroups; }
+  __device__ __forceinline__ Kv8Source(const Kv8DecodeParams& q, const Kv8Items<SMALL>& it)
+      : pp(q), items(it), counter(q.d.counter), num_slots(q.d.num_slots), err(q.d.err) {}
+  __device__ __forceinline__ int32_t claims() const { return items.count(); }
   __device__ __forceinline__ void item(int32_t idx, SlabKeys& k) const {
     Item it;
-    decode_item(pp.d, idx, it);
+    items.item(idx, it);
     k = SlabKeys{pp.d.table + static_cast<int64_t>(it.row) * pp.d.table_stride, it.k0, it.k1, it.hg};
   }
   __device__ __forceinline__ uint32_t key_bytes() const { return pp.block_bytes; }
@@ -105,7 +150,7 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
 
 // Warp roles: hpc consumer warps (one kv head each), the ring's copy warps, and a signal warp that counts each
 // request's finished partials for the combine and frees the item entries.
-template <int D>
+template <int D, bool SMALL>
 __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1)
     kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams pp) {
   const DecodeParams& p = pp.d;
@@ -123,40 +168,42 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
   griddep_wait();  // the plan, its reset counters and everything before them are complete
   griddep_launch();  // the combine may launch: it waits per request for the partials it merges
 
+  if (warp > nc + kRingProducers) return;
+  const Kv8Items<SMALL> items(p, pp.ctas, blockIdx.x == 0 && warp == 0);
   if (warp >= nc && warp < nc + kRingProducers) {
-    slab_producer<kSlab>(rg, Kv8Source(pp), warp - nc);
+    slab_producer<kSlab>(rg, Kv8Source<SMALL>(pp, items), warp - nc);
     return;
   }
   if (warp == nc + kRingProducers) {
-    // ================================================================ signaller
-    // (the item's request is looked up while the item is at work: the signal that follows its last store is on
-    // the way of the merge)
-    for (int32_t n = 0;; ++n) {
-      const int e = n % kRingEntries;
-      const int32_t idx = rg.entry(n);
-      int32_t* count = nullptr;  // the request's count, if its partials are merged by the combine
-      if (idx >= 0 && lane == 0) {
-        Item it;
-        decode_item(p, idx, it);
-        if (it.n_splits > 1) count = p.req_done + it.b;
+    if constexpr (!SMALL) {  // (a small call has one item per CTA, and its merge waits for the grid)
+      // ================================================================ signaller
+      // (the item's request is looked up while the item is at work: the signal that follows its last store is on
+      // the way of the merge)
+      for (int32_t n = 0;; ++n) {
+        const int e = n % kRingEntries;
+        const int32_t idx = rg.entry(n);
+        int32_t* count = nullptr;  // the request's count, if its partials are merged by the combine
+        if (idx >= 0 && lane == 0) {
+          Item it;
+          decode_item(p, idx, it);
+          if (it.n_splits > 1) count = p.req_done + it.b;
+        }
+        if (idx < -1 || !mbar_wait(rg.done0 + 8 * e, (n / kRingEntries) & 1)) {
+          if (lane == 0) rg.give_up(p.err);
+          break;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rg.free0 + 8 * e);
+        if (idx < 0) break;
+        if (count) {
+          __threadfence();  // the consumers' partials (ordered before this by the done barrier) first
+          atomicAdd(count, 1);
+        }
+        __syncwarp();
       }
-      if (idx < -1 || !mbar_wait(rg.done0 + 8 * e, (n / kRingEntries) & 1)) {
-        if (lane == 0) rg.give_up(p.err);
-        break;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(rg.free0 + 8 * e);
-      if (idx < 0) break;
-      if (count) {
-        __threadfence();  // the consumers' partials (ordered before this by the done barrier) first
-        atomicAdd(count, 1);
-      }
-      __syncwarp();
     }
     return;
   }
-  if (warp > nc + kRingProducers) return;
-
   // ================================================================ consumers
   const int g = lane >> 2;
   const int tq = lane & 3;
@@ -174,7 +221,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
       break;
     }
     Item it;
-    decode_item(p, idx, it);
+    items.item(idx, it);
     const int kh = it.hg * p.hpc + warp;
     // Q^T fragments (B operand): column g is q head kh*G + g, scaled to f16
     uint32_t qf[KW][2];
@@ -401,9 +448,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_kernel(const _
   griddep_wait();  // this grid's completion implies the decode kernel's
 }
 
-template <int D>
+template <int D, bool SMALL>
 __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(const __grid_constant__ DecodeParams p,
-                                                                             int per_row) {
+                                                                             int per_row, int32_t ctas) {
   constexpr int V = D / 32;
   __shared__ float s_acc[kCombineWarps][32 * V], s_m[kCombineWarps], s_w[kCombineWarps];
   griddep_launch();
@@ -412,9 +459,18 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(con
   const int32_t bh = static_cast<int32_t>(blockIdx.x) * (kCombineWarps / per_row) + warp / per_row;
   const bool in = bh < p.batch * p.hq;
   const int32_t b = in ? bh / p.hq : 0, h = in ? bh - b * p.hq : 0;
-  int32_t i0;
-  const int32_t n = wait_partials(p, b, in, i0);
-  __syncwarp();
+  int32_t i0, n;
+  if constexpr (SMALL) {
+    // (the lengths were complete before the decode kernel let this one launch)
+    const Kv8Items<true> items(p, ctas, false);
+    i0 = of_lane(items.plan.first, b);
+    n = of_lane(items.plan.pieces, b);
+    if (!in || n <= 1) n = 0;  // written directly, or invalid
+    griddep_wait();
+  } else {
+    n = wait_partials(p, b, in, i0);
+    __syncwarp();
+  }
   float acc[V], m, wsum;
   merge_partials<V, 8>(
       n, share, per_row, [&](int s) { return __ldcg(p.part_lse + static_cast<int64_t>(i0 + s) * p.hq + h); },
@@ -437,9 +493,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(con
   griddep_wait();  // this grid's completion implies the decode kernel's
 }
 
-template <int D>
-ra_status launch(const Kv8DecodeParams& pp, int grid, int smem, const DeviceInfo& dev, cudaStream_t stream) {
-  auto kern = kv8_decode_kernel<D>;
+template <int D, bool SMALL>
+ra_status launch_decode(const Kv8DecodeParams& pp, int grid, int smem, const DeviceInfo& dev, cudaStream_t stream) {
+  auto kern = kv8_decode_kernel<D, SMALL>;
   static bool configured[64] = {};
   if (!configured[dev.device]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmemLimit);
@@ -447,6 +503,34 @@ ra_status launch(const Kv8DecodeParams& pp, int grid, int smem, const DeviceInfo
     configured[dev.device] = true;
   }
   return launch_pdl("kv8_decode_kernel", kern, dim3(grid), dim3(32 * (pp.d.hpc + kRingProducers + 1)), smem, stream, pp);
+}
+
+template <int D>
+ra_status launch(Kv8DecodeParams& pp, int32_t per_sm, int smem, const DeviceInfo& dev, cudaStream_t s) {
+  DecodeParams& p = pp.d;
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.hq, warps = static_cast<int64_t>(dev.num_sms) * 3 * kCombineWarps;
+  const bool small = small_call(p.batch, p.max_seq_len, p.n_hgroups, per_sm);
+  if (small) {
+    pp.ctas = kSmallSms * per_sm;
+    if (ra_status st = launch_decode<D, true>(pp, pp.ctas, smem, dev, s)) return st;
+  } else {
+    if (ra_status st = launch_decode_plan(p, 0, s)) return st;
+    const int64_t n_items = static_cast<int64_t>(p.max_items) * p.n_hgroups;  // bound of the claims
+    const int64_t ctas = static_cast<int64_t>(dev.num_sms) * per_sm;
+    if (ra_status st = launch_decode<D, false>(pp, static_cast<int>(n_items < ctas ? n_items : ctas), smem, dev, s))
+      return st;
+  }
+  // few rows: as many warps per row as three CTAs per SM hold
+  int per_row = 1;
+  while (per_row < kCombineWarps && rows * per_row * 2 <= warps) per_row *= 2;
+  if (per_row > 1 || small) {
+    const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
+    return launch_pdl("kv8_combine_few_kernel", small ? kv8_combine_few_kernel<D, true> : kv8_combine_few_kernel<D, false>,
+                      dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row, pp.ctas);
+  }
+  const int64_t per_cta = kCombineWarps * kRowsPerWarp;
+  return launch_pdl("kv8_combine_kernel", kv8_combine_kernel<D>, dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta)),
+                    dim3(32 * kCombineWarps), 0, s, p);
 }
 
 }  // namespace
@@ -527,22 +611,5 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   if (p.nstage > kRingMaxStages) p.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + p.nstage * p.stage_bytes;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (ra_status st = launch_decode_plan(p, 0, s)) return st;
-  const int64_t n_items = static_cast<int64_t>(pl.max_items) * p.n_hgroups;  // bound of the claims
-  const int64_t ctas = static_cast<int64_t>(dev.num_sms) * per_sm;
-  const int grid = static_cast<int>(n_items < ctas ? n_items : ctas);
-  if (ra_status st = head_dim == 128 ? launch<128>(pp, grid, smem, dev, s) : launch<64>(pp, grid, smem, dev, s))
-    return st;
-  // few rows: as many warps per row as three CTAs per SM hold
-  const int64_t rows = static_cast<int64_t>(batch) * num_q_heads, warps = static_cast<int64_t>(dev.num_sms) * 3 * kCombineWarps;
-  int per_row = 1;
-  while (per_row < kCombineWarps && rows * per_row * 2 <= warps) per_row *= 2;
-  if (per_row > 1) {
-    const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
-    return launch_pdl("kv8_combine_few_kernel", head_dim == 128 ? kv8_combine_few_kernel<128> : kv8_combine_few_kernel<64>,
-                      dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row);
-  }
-  const int64_t per_cta = kCombineWarps * kRowsPerWarp;
-  return launch_pdl("kv8_combine_kernel", head_dim == 128 ? kv8_combine_kernel<128> : kv8_combine_kernel<64>,
-                    dim3(static_cast<unsigned>((rows + per_cta - 1) / per_cta)), dim3(32 * kCombineWarps), 0, s, p);
+  return head_dim == 128 ? launch<128>(pp, per_sm, smem, dev, s) : launch<64>(pp, per_sm, smem, dev, s);
 }

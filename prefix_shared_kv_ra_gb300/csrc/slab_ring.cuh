@@ -87,10 +87,11 @@ __device__ __forceinline__ void slab_producer(const SlabRing& rg, const Src& src
   const int key_in_slab = pw * kKeys + lane;  // this lane's key (lane < kKeys)
   const int ns = rg.nstage;
   const int32_t n_claims = src.claims();
-  // a CTA's first item is its block index; the counter hands out the items after the grid
+  // a CTA's first item is its block index; the counter hands out the items after the grid (if there are any)
   auto claim = [&](bool first) -> int32_t {  // warp-collective
     int32_t idx = static_cast<int32_t>(blockIdx.x);
     if (!first) {
+      if (n_claims <= static_cast<int32_t>(gridDim.x)) return -1;
       if (lane == 0) idx = static_cast<int32_t>(gridDim.x) + atomicAdd(src.counter, 1);
       idx = __shfl_sync(0xffffffffu, idx, 0);
     }

@@ -16,9 +16,10 @@
 //    (4 * D + 4 bytes per row and split, written and read again) and a merge;
 //  * a persistent merge kernel joins the splits; with nothing split it only looks at a count.
 // A value of V that is not finite must not reach rows whose mask leaves its token out, but a matrix product
-// multiplies it by their zero probability (0 * inf = NaN).  The list kernel's other CTAs therefore scan the
-// drafted tokens' V (at most a few MB) and mark the (request, kv head) pairs that hold one; the merge kernel
-// recomputes those rows key by key, skipping what is masked.  Prefix keys are seen by every row: there the
+// multiplies it by their zero probability (0 * inf = NaN).  The drafted tokens' V are therefore looked over (by
+// the narrow kernel in its slabs, for wide calls by the list kernel's other CTAs: at most a few MB) and the
+// (request, kv head) pairs that hold one marked; the merge kernel recomputes those rows key by key, skipping
+// what is masked.  Prefix keys are seen by every row: there the
 // product's NaN is the answer.
 #include <cmath>
 
@@ -40,7 +41,7 @@ constexpr int kBins = kPlanThreads;  // size classes of the items, longest first
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 
-// CTA 0 lists the items, longest first; CTAs 1 .. scan the drafted tokens' V rows, one request at a time.
+// CTA 0 lists the items, longest first; CTAs 1 .. (wide calls) scan the drafted tokens' V rows, one request at a time.
 __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_constant__ TreeParams p, int32_t head_dim) {
   griddep_wait();  // the call's inputs; the workspace may still be read by the call before
   griddep_launch();
@@ -67,6 +68,8 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
     }
     return;
   }
+  if (p.sh.narrow)  // the attention kernel finds the marks itself
+    for (int32_t i = t; i < p.batch * p.hkv; i += kScanThreads) p.ws.bad[i] = 0;
   if (t >= kPlanThreads) return;
   auto list_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kPlanThreads) : "memory"); };  // (the list's threads)
   __shared__ int32_t s_bin[kBins];
@@ -357,6 +360,59 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   }
 }
 
+// The merge of a small narrow call: a unit is kMergeWarps / `per_row` rows (request, kv head, row), of every
+// request, `per_row` warps each taking a share of a row's partials.  A row whose request is one piece was written
+// directly; a row of a marked (request, kv head) is recomputed by its first warp.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const __grid_constant__ TreeParams p,
+                                                                         int per_row) {
+  constexpr int V = D / 32;
+  __shared__ float s_acc[kMergeWarps][32 * V], s_m[kMergeWarps], s_w[kMergeWarps];
+  griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = warp % per_row;
+  const TreeSmall small(p, kTreeSms * p.sh.per_sm, false);  // (the inputs were complete before the attention kernel
+                                                            // let this one launch)
+  const int32_t rows = p.hkv * p.ws.part_rows;
+  const int32_t flat = static_cast<int32_t>(blockIdx.x) * (kMergeWarps / per_row) + warp / per_row;
+  const bool in = flat < p.batch * rows;
+  const int32_t b = in ? flat / rows : 0, kh = in ? (flat - b * rows) / p.ws.part_rows : 0;
+  const int32_t r = in ? flat - b * rows - kh * p.ws.part_rows : 0;
+  const int32_t P = of_lane(small.P, b), T = of_lane(small.T, b), q0 = of_lane(small.q0, b);
+  const int32_t n = of_lane(small.plan.pieces, b), first = of_lane(small.plan.first, b);
+  const int32_t tok = r / p.group;
+  const bool live = in && tok < T;
+  const int64_t row = static_cast<int64_t>(q0) + tok;
+  __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D;
+  const int64_t slot_rows = static_cast<int64_t>(p.hkv) * p.ws.part_rows;  // rows between partial slots
+  const int64_t row0 = (static_cast<int64_t>(first) * p.hkv + kh) * p.ws.part_rows + r;
+  griddep_wait();
+  // marks of the pieces that read drafted tokens: the ones from the prefix's end on
+  bool marked = false;
+  for (int32_t s = max(0, P / small.plan.chunk); live && s < n; ++s)
+    marked = marked || __ldcg(p.ws.bad + static_cast<int64_t>(first + s) * p.hkv + kh) != 0;
+  float acc[V], m, wsum;
+  merge_partials<V, 8>(
+      live && n > 1 ? n : 0, share, per_row, [&](int s) { return __ldcg(p.ws.part_lse + row0 + s * slot_rows); },
+      [&](int s, float(&x)[V]) { load_row_cg<V>(p.ws.part_o + (row0 + s * slot_rows) * D + lane * V, x); }, acc, m, wsum);
+  if (per_row > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
+    if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
+    __syncthreads();
+    if (share == 0) join_shares<V>(per_row, warp, s_acc, s_m, s_w, acc, wsum);
+  }
+  if (!live || share != 0) return;
+  if (marked) {
+    recompute_row<D>(p, b, P, T, tok, kh * p.group + r % p.group);
+  } else if (n > 1) {
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + lane * V + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+  }
+}
+
 template <int D>
 ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev) {
   CUtensorMap qmap, kmap, vmap;
@@ -399,12 +455,22 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
 }
 
 ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& dev, cudaStream_t s) {
-  // the list kernel: one CTA for the list, one per request (at most the other SMs) for the scan of V
-  const int scan = p.batch < dev.num_sms - 1 ? p.batch : dev.num_sms - 1;
+  if (p.sh.narrow &&
+      small_call(p.batch, static_cast<int64_t>(p.max_prefix) + p.max_draft, p.sh.heads, p.sh.per_sm)) {
+    if (ra_status st = launch_tree_narrow(p, head_dim, true, dev, s)) return st;
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.hkv * p.ws.part_rows;
+    int per_row = 1;
+    while (per_row < kMergeWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 3 * kMergeWarps) per_row *= 2;
+    const int64_t ctas = (rows * per_row + kMergeWarps - 1) / kMergeWarps;
+    return launch_pdl("tree_merge_small_kernel", head_dim == 128 ? tree_merge_small_kernel<128> : tree_merge_small_kernel<64>,
+                      dim3(static_cast<unsigned>(ctas)), dim3(kMergeThreads), 0, s, p, per_row);
+  }
+  // the list kernel: one CTA for the list, and (wide) one per request, at most the other SMs, for the scan of V
+  const int scan = p.sh.narrow ? 0 : p.batch < dev.num_sms - 1 ? p.batch : dev.num_sms - 1;
   if (ra_status st = launch_pdl("tree_plan_kernel", tree_plan_kernel, dim3(1 + scan), dim3(kScanThreads), 0, s, p,
                                 head_dim))
     return st;
-  if (ra_status st = p.sh.narrow       ? launch_tree_narrow(p, head_dim, dev, s)
+  if (ra_status st = p.sh.narrow       ? launch_tree_narrow(p, head_dim, false, dev, s)
                      : head_dim == 128 ? launch_wide<128>(p, s, dev)
                                        : launch_wide<64>(p, s, dev))
     return st;

@@ -8,10 +8,12 @@
 #include "../../include/ra.h"
 #include "api_common.h"
 #include "ra_ptx.cuh"
+#include "small_plan.cuh"
 
 namespace ra {
 
 constexpr int kTreeSms = 152;        // GB300; a constant, so that the workspace does not depend on the device
+constexpr int kTreeSmallLeast = 2;   // units of a small call's shortest piece
 constexpr int kTreeNarrowRows = 32;  // drafted tokens x GQA group up to which a call is narrow
 
 // How a call is cut: a narrow call (every request's rows of a kv head fit one mma.sync item) streams whole slot
@@ -64,7 +66,8 @@ struct TreeWorkspace {
   int32_t* header;     // [8]: listed items, claim counter, keys per split, merges
   int32_t* items;      // [8 * cap]: request, query tile, split, partial slot (-1: unsplit); P, T, table row, q row
   int32_t* merges;     // [4 * cap_merge]: request, query tile, first partial slot, splits
-  int32_t* bad;        // [batch * hkv]: a drafted token's V holds a value that is not finite
+  int32_t* bad;        // a drafted token's V holds a value that is not finite: [batch * hkv], or for a small
+                       // call [pieces * hkv] (of the keys the piece read)
   float* part_o;
   float* part_lse;
   int64_t cap, cap_parts;
@@ -95,7 +98,8 @@ inline TreeWorkspace layout_tree(int32_t batch, int64_t total_q, int32_t hq, int
   w.header = reinterpret_cast<int32_t*>(take(32));
   w.items = reinterpret_cast<int32_t*>(take(static_cast<size_t>(w.cap) * 32));
   w.merges = reinterpret_cast<int32_t*>(take(static_cast<size_t>(w.cap_parts) * 16));
-  w.bad = reinterpret_cast<int32_t*>(take(static_cast<size_t>(batch) * hkv * 4));
+  const int64_t marks = batch > w.cap_parts ? batch : w.cap_parts;  // (a small call has at most cap_parts pieces)
+  w.bad = reinterpret_cast<int32_t*>(take(static_cast<size_t>(marks) * hkv * 4));
   const size_t part = static_cast<size_t>(w.cap_parts) * hkv * w.part_rows;
   w.part_lse = reinterpret_cast<float*>(take(part * 4));
   w.part_o = reinterpret_cast<float*>(take(part * d * 4));
@@ -136,7 +140,24 @@ __device__ __forceinline__ bool tree_request(const TreeParams& p, int32_t b, int
   return T > 0;
 }
 
-// The narrow path's attention kernel, behind the plan kernel (tree_narrow.cu).
-ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, const DeviceInfo& dev, cudaStream_t stream);
+// A small narrow call's split, by this warp (its requests' lengths in the lanes).
+struct TreeSmall {
+  SmallPlan plan;
+  int32_t P, T, row, q0;  // of this lane's request
+
+  __device__ __forceinline__ TreeSmall(const TreeParams& p, int32_t ctas, bool report) : P(0), T(0), row(0), q0(0) {
+    const int lane = threadIdx.x & 31;
+    if (lane < p.batch) {
+      if (!tree_request(p, lane, P, T, report)) P = T = 0;
+      row = __ldg(p.rpi + lane);
+      q0 = __ldg(p.qo_indptr + lane);
+    }
+    plan.make(P + T, p.sh.heads, ctas, kTreeSmallLeast);
+  }
+};
+
+// The narrow path's attention kernel (tree_narrow.cu): behind the plan kernel, or a small call's.
+ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, bool small, const DeviceInfo& dev,
+                             cudaStream_t stream);
 
 }  // namespace ra

@@ -12,6 +12,8 @@
 // lazy reference per row (reduced over the 4 lanes of a row), P packed from the score fragments into A
 // fragments, O += P V with V read by transposing ldmatrix.  Ring rows are 16 bytes past a multiple of 128, so
 // ldmatrix is free of bank conflicts.
+#include <type_traits>
+
 #include "api_common.h"
 #include "slab_ring.cuh"
 #include "tree_internal.h"
@@ -32,33 +34,59 @@ struct NarrowParams {
 
 struct NarrowItem {
   int32_t k0, k1, slot, P, T, row, q0, hg;
+  int32_t mark;  // index of the item's marks / hkv: its request, or a small call's piece
 };
 
-__device__ __forceinline__ void narrow_item(const TreeParams& p, int32_t idx, NarrowItem& it) {
-  const int32_t rest = idx / p.sh.heads;
-  it.hg = idx - rest * p.sh.heads;
-  const int4 e = __ldg(reinterpret_cast<const int4*>(p.ws.items) + 2 * rest);
-  const int4 f = __ldg(reinterpret_cast<const int4*>(p.ws.items) + 2 * rest + 1);
-  const int32_t chunk = __ldg(p.ws.header + 2);
-  it.P = f.x, it.T = f.y, it.row = f.z, it.q0 = f.w;
-  it.slot = e.w;
-  it.k0 = e.z * chunk;
-  it.k1 = min(f.x + f.y, it.k0 + chunk);
-}
+// The items of a call: the plan kernel's list, or (SMALL) this warp's own plan.
+struct ListedItems {
+  const TreeParams& p;
+  __device__ __forceinline__ ListedItems(const TreeParams& q, bool) : p(q) {}
+  __device__ __forceinline__ int32_t count() const { return __ldg(p.ws.header) * p.sh.heads; }
+  __device__ __forceinline__ void item(int32_t idx, NarrowItem& it) const {
+    const int32_t rest = idx / p.sh.heads;
+    it.hg = idx - rest * p.sh.heads;
+    const int4 e = __ldg(reinterpret_cast<const int4*>(p.ws.items) + 2 * rest);
+    const int4 f = __ldg(reinterpret_cast<const int4*>(p.ws.items) + 2 * rest + 1);
+    const int32_t chunk = __ldg(p.ws.header + 2);
+    it.P = f.x, it.T = f.y, it.row = f.z, it.q0 = f.w;
+    it.slot = e.w;
+    it.mark = e.x;
+    it.k0 = e.z * chunk;
+    it.k1 = min(f.x + f.y, it.k0 + chunk);
+  }
+};
+struct SmallItems {
+  const TreeParams& p;
+  TreeSmall small;
+  __device__ __forceinline__ SmallItems(const TreeParams& q, bool report)
+      : p(q), small(q, kTreeSms * q.sh.per_sm, report) {}
+  __device__ __forceinline__ int32_t count() const { return small.plan.n * p.sh.heads; }
+  __device__ __forceinline__ void item(int32_t idx, NarrowItem& it) const {  // warp-collective
+    const int32_t d = idx / p.sh.heads;
+    it.hg = idx - d * p.sh.heads;
+    const int32_t b = small.plan.request(d), split = d - of_lane(small.plan.first, b);
+    it.P = of_lane(small.P, b), it.T = of_lane(small.T, b), it.row = of_lane(small.row, b), it.q0 = of_lane(small.q0, b);
+    it.slot = of_lane(small.plan.pieces, b) > 1 ? d : -1;
+    it.mark = d;
+    it.k0 = split * small.plan.chunk;
+    it.k1 = min(it.P + it.T, it.k0 + small.plan.chunk);
+  }
+};
 
 // The producers' view: K row and V row of a key for the item's head group.
-template <int SLAB>
+template <int SLAB, class Items>
 struct NarrowSource {
   const NarrowParams& n;
+  const Items& items;
   int32_t* counter;
   int64_t num_slots;
   uint32_t* err;
-  __device__ __forceinline__ explicit NarrowSource(const NarrowParams& q)
-      : n(q), counter(q.t.ws.header + 1), num_slots(q.t.num_slots), err(q.t.err) {}
-  __device__ __forceinline__ int32_t claims() const { return __ldg(n.t.ws.header) * n.t.sh.heads; }
+  __device__ __forceinline__ NarrowSource(const NarrowParams& q, const Items& i)
+      : n(q), items(i), counter(q.t.ws.header + 1), num_slots(q.t.num_slots), err(q.t.err) {}
+  __device__ __forceinline__ int32_t claims() const { return items.count(); }
   __device__ __forceinline__ void item(int32_t idx, SlabKeys& k) const {
     NarrowItem it;
-    narrow_item(n.t, idx, it);
+    items.item(idx, it);
     k = SlabKeys{n.t.table + static_cast<int64_t>(it.row) * n.t.table_stride, it.k0, it.k1, it.hg};
   }
   __device__ __forceinline__ uint32_t key_bytes() const { return 2 * n.row_bytes; }
@@ -70,7 +98,7 @@ struct NarrowSource {
   }
 };
 
-template <int D, int SLAB>
+template <int D, int SLAB, bool SMALL>
 __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
     tree_narrow_kernel(const __grid_constant__ NarrowParams n) {
   const TreeParams& p = n.t;
@@ -87,8 +115,10 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
   __syncthreads();
   griddep_wait();  // the plan and everything before it
   griddep_launch();
+  using Items = std::conditional_t<SMALL, SmallItems, ListedItems>;
+  const Items items(p, blockIdx.x == 0 && warp == 0);
   if (warp >= nc) {
-    if (warp < nc + kRingProducers) slab_producer<SLAB>(rg, NarrowSource<SLAB>(n), warp - nc);
+    if (warp < nc + kRingProducers) slab_producer<SLAB>(rg, NarrowSource<SLAB, Items>(n, items), warp - nc);
     return;
   }
   // ================================================================ consumers
@@ -107,7 +137,7 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
       break;
     }
     NarrowItem it;
-    narrow_item(p, idx, it);
+    items.item(idx, it);
     __syncwarp();
     if (lane == 0) mbar_arrive(rg.free0 + 8 * (i % kRingEntries));  // this warp has read the entry
     const int kh = it.hg * p.sh.hpc + hl;
@@ -136,6 +166,7 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
     for (int j = 0; j < OB; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
     const int32_t n_slabs = (it.k1 - it.k0 + SLAB - 1) / SLAB;
     bool ok = true;
+    uint32_t odd = 0;  // V values that are not finite, in slabs with drafted tokens
     for (int32_t s = 0; s < n_slabs; ++s, ++c) {
       const int st = c % rg.nstage;
       if (!mbar_wait(rg.full0 + 8 * st, (c / rg.nstage) & 1)) { ok = false; break; }
@@ -234,10 +265,27 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
           }
         }
       }
+      if (rb == 0 && it.k0 + (s + 1) * SLAB > it.P) {
+        // The head's V rows of a slab with drafted tokens: a value that is not finite would reach rows that do not
+        // see it through their zero probability; the merge kernel recomputes such a (request, kv head).
+        const uint32_t v_row = rg.stage0 + st * rg.stage_bytes + v_off;
+#pragma unroll
+        for (int e = 0; e < SLAB / 16 * (D / 16); ++e) {
+          uint32_t w[4];
+          ldsm_x4(v_row + (e / (D / 16)) * 16 * RS + (e % (D / 16)) * 32, w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) odd |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(rg.empty0 + 8 * st);
     }
     if (!ok) break;
+    if (rb == 0) {
+      // listed items add to marks the plan kernel cleared; a small call's piece writes its own
+      odd = __any_sync(0xffffffffu, odd);
+      if (lane == 0 && (SMALL || odd)) p.ws.bad[static_cast<int64_t>(it.mark) * p.hkv + kh] = odd;
+    }
     if (!busy) continue;
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
@@ -270,7 +318,7 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
   if (!clean && lane == 0) rg.give_up(p.err);  // a bounded wait ran out: stop the producers as well
 }
 
-template <int D, int SLAB>
+template <int D, int SLAB, bool SMALL>
 ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
   NarrowParams n{};
   n.t = p;
@@ -280,7 +328,7 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
   n.nstage = (kRingSmemLimit / p.sh.per_sm - 1024 - kRingHdrBytes) / n.stage_bytes;  // (1 KB per CTA is the system's)
   if (n.nstage > kRingMaxStages) n.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + n.nstage * n.stage_bytes;
-  auto kern = tree_narrow_kernel<D, SLAB>;
+  auto kern = tree_narrow_kernel<D, SLAB, SMALL>;
   static bool configured[64] = {};
   if (!configured[dev.device]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmemLimit);
@@ -288,8 +336,8 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
     configured[dev.device] = true;
   }
   const int64_t items = p.ws.cap * p.sh.heads;
-  const int64_t ctas = static_cast<int64_t>(dev.num_sms) * p.sh.per_sm;
-  const int grid = static_cast<int>(items < ctas ? items : ctas);
+  const int64_t ctas = static_cast<int64_t>(SMALL ? kTreeSms : dev.num_sms) * p.sh.per_sm;
+  const int grid = static_cast<int>(SMALL || items >= ctas ? ctas : items);
   return launch_pdl("tree_narrow_kernel", kern, dim3(grid),
                     dim3(32 * (p.sh.hpc * p.sh.row_blocks + kRingProducers)), smem, s, n);
 }
@@ -297,9 +345,10 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
 }  // namespace
 
 // 32-key slabs where three of them fit the ring, else 16 (8 heads of 128).
-ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, const DeviceInfo& dev, cudaStream_t s) {
-  if (head_dim == 128) return p.sh.hpc > 4 ? launch<128, 16>(p, dev, s) : launch<128, 32>(p, dev, s);
-  return launch<64, 32>(p, dev, s);
+ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, bool small, const DeviceInfo& dev, cudaStream_t s) {
+  if (head_dim == 64) return small ? launch<64, 32, true>(p, dev, s) : launch<64, 32, false>(p, dev, s);
+  if (p.sh.hpc > 4) return small ? launch<128, 16, true>(p, dev, s) : launch<128, 16, false>(p, dev, s);
+  return small ? launch<128, 32, true>(p, dev, s) : launch<128, 32, false>(p, dev, s);
 }
 
 }  // namespace ra
