@@ -12,12 +12,15 @@ namespace ra {
 
 constexpr int kSmallBatch = 32;
 constexpr int kSmallUnit = 32;    // keys per unit
-constexpr int kSmallRounds = 8;   // mean units per CTA, at the host's bounds, up to which a call is small
+constexpr int kSmallRounds = 48;  // mean units per CTA, at the host's bounds, up to which a call is small
 constexpr int kSmallSms = 152;    // GB300; a constant, so that host and device agree
 
 // Whether a call is small, from the host's bounds.  Its pieces have to fit: sum ceil(u / c) <= U / c + batch.  The
 // bound on the mean keeps the loss of the coarser schedule (up to a third: one piece per CTA, all as long as
-// the longest) below what the planning kernel costs.
+// the longest) below what the planning kernel costs.  Measured, planning kernel and small call, at their mean
+// units: quantised decode of 16 requests of 512..4096 keys (13) 25.9 and 20.6 us, of 1000..13700 (45) 50.9 and
+// 46.4, of 30 of 13000..13700 (85) 137.4 and 137.1; 16 x 4..8 drafted tokens over 512..4096 keys (27) 40.9 and
+// 36.5, 30 x 4..8 (51) 62.9 and 65.5.
 inline bool small_call(int64_t batch, int64_t max_keys, int64_t heads, int64_t per_sm) {
   const int64_t ctas = kSmallSms * per_sm;
   return batch <= kSmallBatch && 2 * batch * heads <= ctas &&

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   constexpr int V = D / LPR;
   __shared__ float s_acc[FEW ? kMergeWarps : 1][32 * V], s_m[kMergeWarps], s_w[kMergeWarps];
   // The attention kernel waited for the plan before it let this one launch: the plan's lists may be read at
-  // once.  The partials may be read, and o written, once the attention kernel is complete.
+  // once.  The partials and the marks may be read, and o written, once the attention kernel is complete.
   griddep_launch();
   bool waited = false;
   auto wait_partials = [&]() {
@@ -302,9 +302,6 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   const int mine = FEW ? warp / per_row : static_cast<int>(threadIdx.x) / LPR;
   const int32_t tile_rows = p.hkv * p.ws.part_rows;  // rows of a query tile, all kv heads
   const int32_t chunks = (tile_rows + rows_per_unit - 1) / rows_per_unit;
-  const int64_t pairs = static_cast<int64_t>(p.batch) * p.hkv;
-  const int64_t first_pair = static_cast<int64_t>(blockIdx.x) * kMergeThreads;
-  const int32_t mark = first_pair + threadIdx.x < pairs ? __ldcg(p.ws.bad + first_pair + threadIdx.x) : 0;
   const int64_t units = static_cast<int64_t>(__ldcg(p.ws.header + 3)) * chunks;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t entry = u / chunks;
@@ -313,12 +310,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     const int32_t kh = in ? flat / p.ws.part_rows : 0, r = in ? flat - kh * p.ws.part_rows : 0;
     const int4 e = __ldcg(reinterpret_cast<const int4*>(p.ws.merges) + entry);
     const int32_t tok = e.y * p.sh.tokens_per_item + r / p.group;
-    const bool live = in && tok < __ldg(p.draft_lens + e.x) && !__ldcg(p.ws.bad + e.x * p.hkv + kh);
+    const bool live = in && tok < __ldg(p.draft_lens + e.x);
     const int64_t slot_rows = static_cast<int64_t>(p.hkv) * p.ws.part_rows;  // rows between partial slots
     const int64_t row0 = (static_cast<int64_t>(e.z) * p.hkv + kh) * p.ws.part_rows + r;
     const int64_t row = __ldg(p.qo_indptr + e.x) + tok;
     __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D;
     wait_partials();
+    const bool mine_to_write = live && !__ldcg(p.ws.bad + e.x * p.hkv + kh);  // (the marked are recomputed below)
     auto lse_at = [&](int s) { return __ldcg(p.ws.part_lse + row0 + s * slot_rows); };
     auto row_at = [&](int s, float(&x)[V]) { load_row_part<LPR, V>(p.ws.part_o + (row0 + s * slot_rows) * D, sub, x); };
     float acc[V], wsum;
@@ -333,7 +331,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
       for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
       if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
       __syncthreads();
-      if (share != 0 || !live) continue;
+      if (share != 0 || !mine_to_write) continue;
       join_shares<V>(per_row, warp, s_acc, s_m, s_w, acc, wsum);
       const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
@@ -341,19 +339,20 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
         *reinterpret_cast<__nv_bfloat162*>(dst + lane * V + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
     } else {
       merge_rows<LPR, V, 256 / D>(live ? e.w : 0, lse_at, row_at, acc, wsum);
-      if (live) store_row_part<LPR, V>(dst, sub, acc, wsum == 0.f ? 0.f : 1.f / wsum);
+      if (mine_to_write) store_row_part<LPR, V>(dst, sub, acc, wsum == 0.f ? 0.f : 1.f / wsum);
     }
   }
   wait_partials();
+  const int64_t pairs = static_cast<int64_t>(p.batch) * p.hkv;
   const int64_t threads = static_cast<int64_t>(gridDim.x) * kMergeThreads;
-  for (int64_t i0 = first_pair; i0 < pairs; i0 += threads) {
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kMergeThreads; i0 < pairs; i0 += threads) {
     const int64_t mine = i0 + threadIdx.x;
-    const bool marked = i0 == first_pair ? mark != 0 : mine < pairs && p.ws.bad[mine] != 0;
+    const bool marked = mine < pairs && __ldcg(p.ws.bad + mine) != 0;
     if (!__syncthreads_or(marked)) continue;
     for (int64_t pair = i0; pair < i0 + kMergeThreads && pair < pairs; ++pair) {
       const int32_t b = static_cast<int32_t>(pair / p.hkv), kh = static_cast<int32_t>(pair % p.hkv);
       int32_t P, T;
-      if (!p.ws.bad[pair] || !tree_request(p, b, P, T, false)) continue;
+      if (!__ldcg(p.ws.bad + pair) || !tree_request(p, b, P, T, false)) continue;
       for (int32_t r = warp; r < T * p.group; r += kMergeThreads / 32)
         recompute_row<D>(p, b, P, T, r / p.group, kh * p.group + r % p.group);
     }

@@ -164,6 +164,27 @@ def test_decode_matches_64_bit_attention(lens, hq, hkv, d):
     check_decode(o, rec, table, rpi, lens, q, hkv, d ** -0.5)
 
 
+@pytest.mark.parametrize("batch,longest,bound", [(32, 300, None), (33, 300, None), (32, 1500, 1 << 20), (5, 2500, 1 << 20),
+                                                 (1, 6000, None), (100, 90, None)])
+@pytest.mark.parametrize("hq,hkv,d", [(16, 4, 128), (8, 2, 64)])
+def test_decode_planned_by_the_warps_and_by_the_kernel(batch, longest, bound, hq, hkv, d):
+    """Both sides of the small-call rule (32 requests; the bound of their keys), the same requests under a loose
+    bound, requests of one key among long ones."""
+    rng = np.random.default_rng(batch + longest)
+    lens = rng.integers(1, longest + 1, batch)
+    lens[-1] = 1
+    lens[0] = longest
+    rec, table, rpi, lens, q = decode_case(rng, lens, hq, hkv, d, spread=1)
+    if bound:
+        wide = np.full((table.shape[0], bound), -1, np.int32)
+        wide[:, :table.shape[1]] = table
+        table = wide
+    err = err_word()
+    o = decode(rec, table, rpi, lens, q, hkv, d ** -0.5, device_error=err)
+    assert int(err.item()) == 0
+    check_decode(o, rec, table, rpi, lens, q, hkv, d ** -0.5)
+
+
 def test_decode_shared_prefix_and_many_splits():
     rng = np.random.default_rng(9)
     rec, table, rpi, lens, q = decode_case(rng, rng.integers(400, 3000, 24), 32, 8, 128, spread=1, share=400)

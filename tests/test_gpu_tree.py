@@ -133,6 +133,22 @@ def test_tree_matches_64_bit_attention(prefix, draft, hq, hkv, d, kind):
     c.check(o)
 
 
+@pytest.mark.parametrize("batch,longest,bound", [(32, 200, None), (33, 200, None), (6, 900, 1 << 20), (1, 5000, None)])
+def test_tree_planned_by_the_warps_and_by_the_kernel(batch, longest, bound):
+    """Narrow requests on both sides of the small-call rule, and under a loose bound."""
+    rng = np.random.default_rng(batch + longest)
+    prefix, draft = rng.integers(0, longest + 1, batch), rng.integers(0, 9, batch)
+    prefix[0], draft[0] = longest, 8
+    c = Case(rng, prefix, draft, 32, 8, 128, gap=1)
+    if bound:
+        wide = np.full((c.table.shape[0], bound), -1, np.int32)
+        wide[:, :c.table.shape[1]] = c.table
+        c.table = wide
+    o = c.run(max_p=bound or longest)
+    assert int(c.err.item()) == 0
+    c.check(o)
+
+
 def test_tree_many_requests_unsplit():
     """Enough items that nothing is split (the direct bf16 rows), with rows between the requests left alone."""
     rng = np.random.default_rng(2)
@@ -174,12 +190,15 @@ def test_tree_rows_that_see_nothing_are_zero():
         assert not o.any()
 
 
-@pytest.mark.parametrize("prefix,n", [(0, 1), (300, 1), (2000, 1), (200, 60)])
+@pytest.mark.parametrize("prefix,n,hq", [(0, 1, 32), (300, 1, 32), (2000, 1, 32), (200, 60, 32), (0, 2, 8), (299, 1, 8),
+                                         (2000, 1, 8), (200, 60, 8), (999, 40, 8)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
-def test_values_behind_the_mask_do_not_matter(prefix, n, bad):
-    """A drafted token whose K and V are not finite changes only rows that see it (split and unsplit items)."""
+def test_values_behind_the_mask_do_not_matter(prefix, n, hq, bad):
+    """A drafted token whose K and V are not finite changes only rows that see it: wide (hq 32) and narrow (hq 8)
+    requests, split and unsplit, planned by the kernel and by the warps."""
     rng = np.random.default_rng(6)
-    c = Case(rng, [prefix] * n, [24] * n, 32, 8, 128, "none")
+    g = hq // 8
+    c = Case(rng, [prefix] * n, [24] * n, hq, 8, 128, "none")
     for s in c.seen:
         s[:] = np.eye(24, dtype=bool)
         s[:, 3] = False
@@ -199,7 +218,7 @@ def test_values_behind_the_mask_do_not_matter(prefix, n, bad):
     # for bit; the others within the bounds of the clean result (row 7's NaN score sends its warp through the
     # exact path, whose reference rounds other rows differently, and the bad V's head is recomputed in fp32)
     rest = np.setdiff1d(np.arange(c.total), np.arange(n) * 24 + 7)
-    other = np.setdiff1d(np.arange(32), np.arange(4, 12))
+    other = np.setdiff1d(np.arange(hq), np.arange(g, 3 * g))
     assert torch.equal(o[rest][:, other], clean[rest][:, other])
     for b in range(n):
         slots = c.table[c.rpi[b], :prefix + 24]
@@ -209,11 +228,11 @@ def test_values_behind_the_mask_do_not_matter(prefix, n, bad):
         off = np.abs(f64(o[q0:q0 + 24]) - ref) <= R.attention_bound(ref, a, x, c.d, R.EPS_BF16)
         assert np.delete(off, 7, 0).all()
     seeing = o[np.arange(n) * 24 + 7].float()
-    assert not torch.isfinite(seeing[:, 8:12, 5]).any()
-    assert torch.isnan(seeing[:, 4:8]).all()
+    assert not torch.isfinite(seeing[:, 2 * g:3 * g, 5]).any()
+    assert torch.isnan(seeing[:, g:2 * g]).all()
     if bad != bad:
-        assert torch.isnan(seeing[:, 8:12, 5]).all()
-    assert torch.isfinite(seeing[:, 12:]).all()
+        assert torch.isnan(seeing[:, 2 * g:3 * g, 5]).all()
+    assert torch.isfinite(seeing[:, 3 * g:]).all()
 
 
 def test_bad_requests_are_flagged_and_skipped():
