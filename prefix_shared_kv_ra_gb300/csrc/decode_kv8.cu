@@ -37,7 +37,10 @@ namespace ra {
 
 namespace {
 
-constexpr int kSlab = 32;          // keys per ring stage
+// Keys per ring stage.  A consumer warp's chain of loads, scores, softmax and product takes about as long for a
+// slab of either size, so heads of 64 get the longer one (150 requests of 1000..9000 keys, 8/8 heads: 170 us with
+// 32, 136 with 64).
+constexpr int slab_of(int head_dim) { return head_dim == 128 ? 32 : 64; }
 constexpr float kRescale = 8.0f;   // log2 units: a reference moves when a score exceeds it by more
 constexpr int kQExp = 14;          // q's largest value in f16
 
@@ -154,6 +157,7 @@ template <int D, bool SMALL>
 __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1)
     kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams pp) {
   const DecodeParams& p = pp.d;
+  constexpr int kSlab = slab_of(D);
   constexpr int KW = D / 16;  // words of a K row per lane = MMA k steps of the scores
   constexpr int VW = D / 32;  // words of a V row per lane
   constexpr int MT = D / 16;  // MMA m tiles of O^T
@@ -596,17 +600,17 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   p.seq_lens = seq_lens;
   p.batch = batch;
   p.max_seq_len = max_seq_len;
-  p.min_chunk = 2 * kSlab;
-  p.chunk_align = kSlab;
+  p.min_chunk = 64;
+  p.chunk_align = slab_of(head_dim);
   p.err = device_error;
   bind_decode_workspace(p, wl, pl, workspace);
   p.hpc = sh.hpc;
   p.n_hgroups = sh.blocks;
   p.row_stride = sh.block_bytes;
-  p.stage_bytes = kSlab * p.row_stride;
-  // A CTA of few heads waits on its own chain of slab, scores, softmax and product: two share an SM (their
-  // registers fit for up to 3 heads of 128, 4 of 64).
-  const int per_sm = sh.hpc <= (head_dim == 128 ? 3 : 4) ? 2 : 1;
+  p.stage_bytes = slab_of(head_dim) * p.row_stride;
+  // A CTA of few heads waits on its own chain of slab, scores, softmax and product: two share an SM where their
+  // registers fit (8 warps of 128 registers each).
+  const int per_sm = sh.hpc <= 3 ? 2 : 1;
   p.nstage = (kRingSmemLimit / per_sm - 1024 - kRingHdrBytes) / p.stage_bytes;  // (1 KB per CTA is the system's)
   if (p.nstage > kRingMaxStages) p.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + p.nstage * p.stage_bytes;
