@@ -5,15 +5,17 @@
 //   o_i = sum_j softmax_j(scale <q_i, k_j>) v_j   over j < P and over P + t with bit t of mask_i.
 // One pass does both parts; rows are (token, head of the GQA group), and only the keys of drafted tokens look
 // at the masks.  T * G rows share every key of a kv head:
-//  * up to 64 rows the call is bound by HBM (2 flop per byte and row), and the items of tree_narrow.cu stream
-//    whole slot rows of several heads with few large copies;
+//  * up to 32 rows the call is bound by HBM (2 flop per byte and row), and the items of tree_narrow.cu stream
+//    whole slot rows of several heads with few large copies (small calls of up to 128 rows take several such
+//    items per request: 8 x 20..40 tokens of 16/16 heads 44.6 us on the wide path, 29.0 on this);
 //  * more rows are bound by the tensor cores and the softmax's issue slots, like extend: the tcgen05 attention
 //    kernel (attn_tc.cuh, kTreePass), up to 256 rows per item, each gathered 128-key tile feeding all of them.
-//    (Its 128-byte gathers take ~16 bytes per clock and SM: with 32 rows it ran at 62% of HBM at most.)
+//    Its 128-byte gathers take ~16 bytes per clock and SM, 4.2 TB/s in all, whatever the rows: 64 requests x
+//    4..8 tokens over 512..4096 keys, 32/8 heads, took it 145 us and take the narrow path 118.
 // Around it:
-//  * the work list (one CTA, on the device, from the real lengths) splits the key ranges only as far as the
-//    SMs need it, since an unsplit item writes its bf16 rows directly while a split one costs fp32 partials
-//    (4 * D + 4 bytes per row and split, written and read again) and a merge;
+//  * the work list (one CTA, on the device, from the real lengths; small calls: every warp for itself) splits
+//    the key ranges only as far as the SMs need it, since an unsplit item writes its bf16 rows directly while
+//    a split one costs fp32 partials (4 * D + 4 bytes per row and split, written and read again) and a merge;
 //  * a persistent merge kernel joins the splits; with nothing split it only looks at a count.
 // A value of V that is not finite must not reach rows whose mask leaves its token out, but a matrix product
 // multiplies it by their zero probability (0 * inf = NaN).  The drafted tokens' V are therefore looked over (by
@@ -374,13 +376,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const _
                                                             // let this one launch)
   const int32_t rows = p.hkv * p.ws.part_rows;
   const int32_t flat = static_cast<int32_t>(blockIdx.x) * (kMergeWarps / per_row) + warp / per_row;
-  const bool in = flat < p.batch * rows;
-  const int32_t b = in ? flat / rows : 0, kh = in ? (flat - b * rows) / p.ws.part_rows : 0;
-  const int32_t r = in ? flat - b * rows - kh * p.ws.part_rows : 0;
-  const int32_t P = of_lane(small.P, b), T = of_lane(small.T, b), q0 = of_lane(small.q0, b);
-  const int32_t n = of_lane(small.plan.pieces, b), first = of_lane(small.plan.first, b);
+  const bool in = flat < p.batch * p.sh.q_tiles * rows;
+  const int32_t tile = in ? flat / rows : 0, kh = in ? (flat - tile * rows) / p.ws.part_rows : 0;  // of a request
+  const int32_t r = in ? flat - tile * rows - kh * p.ws.part_rows : 0;
+  const int32_t P = of_lane(small.P, tile), T = of_lane(small.T, tile), q0 = of_lane(small.q0, tile);
+  const int32_t n = of_lane(small.plan.pieces, tile), first = of_lane(small.plan.first, tile);
   const int32_t tok = r / p.group;
-  const bool live = in && tok < T;
+  const bool live = in && tok < of_lane(small.tokens, tile);
   const int64_t row = static_cast<int64_t>(q0) + tok;
   __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D;
   const int64_t slot_rows = static_cast<int64_t>(p.hkv) * p.ws.part_rows;  // rows between partial slots
@@ -403,7 +405,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const _
   }
   if (!live || share != 0) return;
   if (marked) {
-    recompute_row<D>(p, b, P, T, tok, kh * p.group + r % p.group);
+    const int32_t b = tile / p.sh.q_tiles;
+    recompute_row<D>(p, b, P, T, (tile - b * p.sh.q_tiles) * p.sh.tokens_per_item + tok, kh * p.group + r % p.group);
   } else if (n > 1) {
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
@@ -453,11 +456,15 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
   return launch_pdl("attn_tc_kernel<tree>", kern, dim3(grid), dim3(tc::kThreads), L::kDynSmem, s, tp, qmap, kmap, vmap);
 }
 
+bool tree_small(const TreeShape& sh, int32_t batch, int32_t max_prefix, int32_t max_draft) {
+  return sh.narrow && small_call(static_cast<int64_t>(batch) * sh.q_tiles, static_cast<int64_t>(max_prefix) + max_draft,
+                                 sh.heads, sh.per_sm);
+}
+
 ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& dev, cudaStream_t s) {
-  if (p.sh.narrow &&
-      small_call(p.batch, static_cast<int64_t>(p.max_prefix) + p.max_draft, p.sh.heads, p.sh.per_sm)) {
+  if (tree_small(p.sh, p.batch, p.max_prefix, p.max_draft)) {
     if (ra_status st = launch_tree_narrow(p, head_dim, true, dev, s)) return st;
-    const int64_t rows = static_cast<int64_t>(p.batch) * p.hkv * p.ws.part_rows;
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.sh.q_tiles * p.hkv * p.ws.part_rows;
     int per_row = 1;
     while (per_row < kMergeWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 3 * kMergeWarps) per_row *= 2;
     const int64_t ctas = (rows * per_row + kMergeWarps - 1) / kMergeWarps;
@@ -501,7 +508,13 @@ bool tree_args_ok(int32_t batch, int64_t total_q, int32_t hq, int32_t hkv, int32
 extern "C" size_t ra_tree_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
                                           int32_t head_dim, int32_t max_draft_len) {
   if (!ra::tree_args_ok(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len)) return 0;
-  return ra::layout_tree(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len, nullptr).total;
+  auto bytes = [&](bool tiled) {
+    return ra::layout_tree(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len,
+                           ra::tree_shape(num_q_heads, num_kv_heads, head_dim, max_draft_len, tiled), nullptr)
+        .total;
+  };
+  const size_t whole = bytes(false), tiled = ra::tree_tileable(num_q_heads, num_kv_heads, max_draft_len) ? bytes(true) : 0;
+  return whole > tiled ? whole : tiled;  // (a call's cut depends on max_prefix_len too)
 }
 
 extern "C" ra_status ra_tree_attention(const void* k_pool, const void* v_pool, int64_t num_slots, int32_t num_kv_heads,
@@ -543,9 +556,15 @@ extern "C" ra_status ra_tree_attention(const void* k_pool, const void* v_pool, i
                  aligned4(qo_indptr) && aligned4(tree_mask),
              "index arrays and masks must be 4-byte aligned");
   TreeParams p{};
-  p.ws = layout_tree(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len, workspace);
-  if (!workspace || workspace_bytes < p.ws.total)
-    return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace ? workspace_bytes : 0, p.ws.total);
+  const size_t need = ra_tree_workspace_bytes(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len);
+  if (!workspace || workspace_bytes < need)
+    return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace ? workspace_bytes : 0, need);
+  p.sh = tree_shape(num_q_heads, num_kv_heads, head_dim, max_draft_len, false);
+  if (tree_tileable(num_q_heads, num_kv_heads, max_draft_len)) {
+    const TreeShape tiled = tree_shape(num_q_heads, num_kv_heads, head_dim, max_draft_len, true);
+    if (tree_small(tiled, batch, max_prefix_len, max_draft_len)) p.sh = tiled;
+  }
+  p.ws = layout_tree(batch, total_q, num_q_heads, num_kv_heads, head_dim, max_draft_len, p.sh, workspace);
   RA_REQUIRE(aligned16(workspace), "workspace must be 16-byte aligned");
   RA_REQUIRE(p.ws.cap * num_kv_heads < (int64_t(1) << 31), "too many items for one grid");
   RA_REQUIRE(static_cast<int64_t>(batch) * num_kv_heads < (int64_t(1) << 31), "batch x num_kv_heads too large");
@@ -573,7 +592,6 @@ extern "C" ra_status ra_tree_attention(const void* k_pool, const void* v_pool, i
   p.batch = batch;
   p.max_draft = max_draft_len;
   p.max_prefix = max_prefix_len;
-  p.sh = tree_shape(num_q_heads, num_kv_heads, head_dim, max_draft_len);
   p.err = device_error;
   return launch_tree(p, head_dim, dev, reinterpret_cast<cudaStream_t>(stream));
 }

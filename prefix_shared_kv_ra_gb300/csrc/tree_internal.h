@@ -14,12 +14,15 @@ namespace ra {
 
 constexpr int kTreeSms = 152;        // GB300; a constant, so that the workspace does not depend on the device
 constexpr int kTreeSmallLeast = 2;   // units of a small call's shortest piece
-constexpr int kTreeNarrowRows = 32;  // drafted tokens x GQA group up to which a call is narrow
+constexpr int kTreeNarrowRows = 32;  // rows (drafted tokens x GQA group) of a narrow item
+constexpr int kTreeTiledRows = 128;  // rows per request up to which a small call takes several narrow items
 
-// How a call is cut: a narrow call (every request's rows of a kv head fit one mma.sync item) streams whole slot
-// rows of a head group per item, a wide one 256-row items of one kv head on the tcgen05 kernel.
+// How a call is cut: a narrow item (at most 32 rows of a kv head, on mma.sync) streams whole slot rows of a head
+// group, a wide one has up to 256 rows of one kv head on the tcgen05 kernel.  A call is narrow if its requests'
+// rows fit one item, and in several items per request (its keys read once per item) if it is small.
 struct TreeShape {
   bool narrow;
+  int32_t q_tiles;          // items that hold a request's drafted tokens, at the host's bound
   int32_t row_blocks;       // narrow: 16-row blocks per kv head (1 or 2)
   int32_t hpc;              // narrow: kv heads per item
   int32_t per_sm;           // CTAs of the attention kernel per SM
@@ -34,18 +37,24 @@ struct TreeShape {
 // Consumer warps of a narrow CTA: as many as their registers (accumulators of D values per row) allow.
 constexpr int tree_consumers(int32_t head_dim) { return head_dim == 128 ? 8 : 16; }
 
-inline TreeShape tree_shape(int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_draft) {
+// Whether requests of these bounds may be cut into several narrow items.
+inline bool tree_tileable(int32_t hq, int32_t hkv, int32_t max_draft) {
+  const int64_t group = hq / hkv, rows = max_draft * group;
+  return rows > kTreeNarrowRows && rows <= kTreeTiledRows && group <= kTreeNarrowRows;
+}
+
+inline TreeShape tree_shape(int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_draft, bool tiled) {
   TreeShape s{};
   const int32_t group = hq / hkv;
   const int64_t rows = static_cast<int64_t>(max_draft) * group;
-  s.narrow = rows <= kTreeNarrowRows;
+  s.narrow = rows <= kTreeNarrowRows || tiled;
   if (s.narrow) {
+    s.tokens_per_item = rows <= kTreeNarrowRows ? max_draft : kTreeNarrowRows / group;
     s.row_blocks = rows <= 16 ? 1 : 2;
     for (s.hpc = tree_consumers(head_dim) / s.row_blocks; hkv % s.hpc != 0;) --s.hpc;
     // a CTA of few consumer warps waits on its own chain of slab, scores, softmax and product: two share an SM
     s.per_sm = s.hpc * s.row_blocks <= 2 ? 2 : 1;
     s.heads = hkv / s.hpc;
-    s.tokens_per_item = max_draft;
     s.unit = 32;
     s.waves = 3;
     s.overhead = 1;
@@ -59,6 +68,7 @@ inline TreeShape tree_shape(int32_t hq, int32_t hkv, int32_t head_dim, int32_t m
     s.overhead = 3;
     s.split_overhead = 3 + static_cast<int32_t>((rows < 256 ? rows : 256) / 96);
   }
+  s.q_tiles = (max_draft + s.tokens_per_item - 1) / s.tokens_per_item;
   return s;
 }
 
@@ -79,15 +89,14 @@ struct TreeWorkspace {
 // longer than the chunk, and the chunk is at least total / (waves * kTreeSms) (all ranges times the heads):
 // the split ranges' pieces number at most sum ceil(n / c) <= sum 2 n / c <= 2 * waves * kTreeSms / heads.
 inline TreeWorkspace layout_tree(int32_t batch, int64_t total_q, int32_t hq, int32_t hkv, int32_t d, int32_t max_draft,
-                          void* base) {
+                                 const TreeShape& sh, void* base) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const int32_t group = hq / hkv;
-  const TreeShape sh = tree_shape(hq, hkv, d, max_draft);
   TreeWorkspace w{};
   w.cap_parts = 2 * sh.waves * kTreeSms / sh.heads;
   w.cap = (total_q + sh.tokens_per_item - 1) / sh.tokens_per_item + batch + w.cap_parts;
-  const int64_t rows = static_cast<int64_t>(max_draft) * group;
-  w.part_rows = static_cast<int32_t>(rows < 256 ? rows : 256);
+  const int64_t rows = static_cast<int64_t>(max_draft < sh.tokens_per_item ? max_draft : sh.tokens_per_item) * group;
+  w.part_rows = static_cast<int32_t>(rows);
   uint8_t* b = static_cast<uint8_t*>(base);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -140,19 +149,22 @@ __device__ __forceinline__ bool tree_request(const TreeParams& p, int32_t b, int
   return T > 0;
 }
 
-// A small narrow call's split, by this warp (its requests' lengths in the lanes).
+// A small narrow call's split, by this warp: lane b * q_tiles + i holds query tile i of request b.
 struct TreeSmall {
   SmallPlan plan;
-  int32_t P, T, row, q0;  // of this lane's request
+  int32_t P, T, row, q0, tokens;  // of this lane's request; its tile's first query row and tokens
 
-  __device__ __forceinline__ TreeSmall(const TreeParams& p, int32_t ctas, bool report) : P(0), T(0), row(0), q0(0) {
+  __device__ __forceinline__ TreeSmall(const TreeParams& p, int32_t ctas, bool report)
+      : P(0), T(0), row(0), q0(0), tokens(0) {
     const int lane = threadIdx.x & 31;
-    if (lane < p.batch) {
-      if (!tree_request(p, lane, P, T, report)) P = T = 0;
-      row = __ldg(p.rpi + lane);
-      q0 = __ldg(p.qo_indptr + lane);
+    const int32_t b = lane / p.sh.q_tiles, tile = lane - b * p.sh.q_tiles;
+    if (b < p.batch) {
+      if (!tree_request(p, b, P, T, report && tile == 0)) P = T = 0;
+      row = __ldg(p.rpi + b);
+      q0 = __ldg(p.qo_indptr + b) + tile * p.sh.tokens_per_item;
+      tokens = min(max(T - tile * p.sh.tokens_per_item, 0), p.sh.tokens_per_item);
     }
-    plan.make(P + T, p.sh.heads, ctas, kTreeSmallLeast);
+    plan.make(tokens > 0 ? P + T : 0, p.sh.heads, ctas, kTreeSmallLeast);
   }
 };
 

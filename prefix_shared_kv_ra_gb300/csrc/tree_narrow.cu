@@ -1,8 +1,8 @@
-// tree_narrow.cu -- the attention pass of ra_tree_attention for requests of at most 64 rows per kv head.
+// tree_narrow.cu -- the attention pass of ra_tree_attention on items of at most 32 rows per kv head.
 //
-// Rows are (drafted token, head of the GQA group); an item is a key range of one request for a group of hpc kv
-// heads, all their rows.  With R rows a key costs 4 * D bytes and 4 * D * R flop per kv head: up to 64 rows
-// that is under the ~290 flop per byte at which GB300's tensor cores would bound it, and HBM is the bound.  So
+// Rows are (drafted token, head of the GQA group); an item is a key range and a query tile of one request for a
+// group of hpc kv heads.  With R rows a key costs 4 * D bytes and 4 * D * R flop per kv head: up to 32 rows
+// that is far under the ~290 flop per byte at which GB300's tensor cores would bound it, and HBM is the bound.  So
 // the kernel is built like the decode one: copies of whole slot rows of a head group (hpc * D * 2 bytes, one
 // bulk copy for K and one for V of a key) into a ring, and consumer warps on mma.sync, which take 16 rows of one
 // head each: row_blocks warps share a head's keys in shared memory (D = 128: up to 8 warps, 8 heads of 16 rows or
@@ -33,7 +33,8 @@ struct NarrowParams {
 };
 
 struct NarrowItem {
-  int32_t k0, k1, slot, P, T, row, q0, hg;
+  int32_t k0, k1, slot, P, T, row, hg;
+  int32_t q0, tokens;  // the tile's first query row and tokens
   int32_t mark;  // index of the item's marks / hkv: its request, or a small call's piece
 };
 
@@ -48,7 +49,9 @@ struct ListedItems {
     const int4 e = __ldg(reinterpret_cast<const int4*>(p.ws.items) + 2 * rest);
     const int4 f = __ldg(reinterpret_cast<const int4*>(p.ws.items) + 2 * rest + 1);
     const int32_t chunk = __ldg(p.ws.header + 2);
-    it.P = f.x, it.T = f.y, it.row = f.z, it.q0 = f.w;
+    const int32_t t0 = e.y * p.sh.tokens_per_item;
+    it.P = f.x, it.T = f.y, it.row = f.z, it.q0 = f.w + t0;
+    it.tokens = min(p.sh.tokens_per_item, f.y - t0);
     it.slot = e.w;
     it.mark = e.x;
     it.k0 = e.z * chunk;
@@ -64,8 +67,9 @@ struct SmallItems {
   __device__ __forceinline__ void item(int32_t idx, NarrowItem& it) const {  // warp-collective
     const int32_t d = idx / p.sh.heads;
     it.hg = idx - d * p.sh.heads;
-    const int32_t b = small.plan.request(d), split = d - of_lane(small.plan.first, b);
-    it.P = of_lane(small.P, b), it.T = of_lane(small.T, b), it.row = of_lane(small.row, b), it.q0 = of_lane(small.q0, b);
+    const int32_t b = small.plan.request(d), split = d - of_lane(small.plan.first, b);  // (b: a request's tile)
+    it.P = of_lane(small.P, b), it.T = of_lane(small.T, b), it.row = of_lane(small.row, b);
+    it.q0 = of_lane(small.q0, b), it.tokens = of_lane(small.tokens, b);
     it.slot = of_lane(small.plan.pieces, b) > 1 ? d : -1;
     it.mark = d;
     it.k0 = split * small.plan.chunk;
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(rg.free0 + 8 * (i % kRingEntries));  // this warp has read the entry
     const int kh = it.hg * p.sh.hpc + hl;
-    const int32_t rows = it.T * p.group;
+    const int32_t rows = it.tokens * p.group;
     const bool live0 = r0 < rows, live1 = r1 < rows;
     const bool busy = rb * 16 < rows;  // a block past the request's rows only keeps the barriers' counts
     const int32_t t0 = r0 / p.group, t1 = r1 / p.group;
