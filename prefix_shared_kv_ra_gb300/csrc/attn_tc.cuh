@@ -104,7 +104,8 @@ struct TcParams {
   float* part_lse;            // [slots, hkv, part_rows]
 };
 
-enum TcPass { kPrefixPass = 0, kExtendPass = 1, kTreePass = 2 };
+// kTreeDualPass: the tree pass for calls whose items all have one live query tile.
+enum TcPass { kPrefixPass = 0, kExtendPass = 1, kTreePass = 2, kTreeDualPass = 3 };
 
 namespace tc {
 
@@ -160,6 +161,7 @@ struct Job {
   int32_t csplit;    // cascade: prefix split
   int32_t slot;      // cascade: partial slot of the members (level x max_csplits + split); tree: partial
                      // slot of the item, -1 for an unsplit one
+  int32_t dual;      // tree (dual pass): the item's one live query tile is in both tiles, which share out its key tiles
   int32_t tiles;     // query tiles holding valid rows (1: tile 1 is empty; its MMAs and softmax are skipped,
                      // while every barrier still completes its phases as for two tiles)
 };
@@ -175,7 +177,7 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
   j.mem0 = 0;
   j.csplit = 0;
   j.slot = 0;
-  if constexpr (PASS == kTreePass) {
+  if constexpr (PASS == kTreePass || PASS == kTreeDualPass) {
     // the list holds only non-empty items of requests whose indices and lengths were checked when it was built
     const int4 e = __ldg(reinterpret_cast<const int4*>(p.work_items) + 2 * rest);
     const int4 f = __ldg(reinterpret_cast<const int4*>(p.work_items) + 2 * rest + 1);
@@ -247,6 +249,7 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
   }
   j.nt = (j.kend - j.kbeg + kKeys - 1) / kKeys;
   j.tiles = j.n_valid > T ? 2 : 1;
+  j.dual = PASS == kTreeDualPass && j.tiles == 1 && j.nt > 1;
   return j.nt > 0;
 }
 
@@ -259,7 +262,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   using namespace tc;
   using L = Layout<D, KS, VS>;
   constexpr bool EXTEND = PASS != kPrefixPass;  // rows are tokens of one request, items come from a list
-  constexpr bool TREE = PASS == kTreePass;
+  constexpr bool DUAL = PASS == kTreeDualPass;
+  constexpr bool TREE = PASS == kTreePass || DUAL;
   constexpr int HALVES = D / 64;  // 128-byte (64-element) column blocks of a row
   // K/V stage release: one barrier per key tile t (ring of KVF), committed after the last MMA reading
   // K_t and V_t (PV of query tile 1).  KVF > max(KS, VS): a producer waiting for tile t's release
@@ -272,6 +276,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   __shared__ Job s_job[kItemRing];  // decoded by the claimer: no role reads the work list itself
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ __align__(8) uint64_t bar_join[2];  // tree, dual items: tile 1's sums are in s_join; its O has been read
+  __shared__ float2 s_join[DUAL ? kRows : 1];    // (reference, sum) of tile 1's rows
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -298,6 +304,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     }
     for (int s = 0; s < kItemRing; ++s) mbar_init(smem_u32(&bar_item[s]), 1);
     mbar_init(smem_u32(&bar_done), 1);
+    mbar_init(smem_u32(&bar_join[0]), 128);
+    mbar_init(smem_u32(&bar_join[1]), 128);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -321,6 +329,18 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     if (s_item[n % kItemRing] < 0) return 0;
     jb = s_job[n % kItemRing];
     return 1;
+  };
+
+  // Steps of an item (a QK and a PV on each query tile), the key tile of query tile i's step j counted from the
+  // item's first, and whether there is work in it.  Both tiles of an item work on the same key tile; of a dual
+  // item, whose rows fill one query tile only, tile i takes every other one: with one tile's chain of QK, softmax
+  // and PV at a time the tensor core would wait for most of it (64 requests x 8..16 drafted tokens over 512..4096
+  // keys, 64/8 heads: 148 us so, 131 with dual items, whose bound is the gathers).  A variant of its own: in
+  // the pass for 256-row items these lines cost 3%.
+  auto steps_of = [](const Job& b) -> int32_t { return DUAL && b.dual ? (b.nt + 1) >> 1 : b.nt; };
+  auto tile_at = [](const Job& b, int32_t j, int i) -> int32_t { return DUAL && b.dual ? 2 * j + i : j; };
+  auto live_at = [](const Job& b, int32_t j, int i) -> bool {
+    return DUAL && b.dual ? 2 * j + i < b.nt : i == 0 || b.tiles > 1;
   };
 
   if (warp >= kKWarp0 && warp < kMmaWarp) {
@@ -496,7 +516,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             asm volatile(
                 "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(sQ(i) + h * (kRows * 128)),
-                "l"(&qmap), "r"(h * 64), "r"(jb.kh * G), "r"(static_cast<int32_t>(jb.q_tok0 + i * T)), "r"(bq)
+                "l"(&qmap), "r"(h * 64), "r"(jb.kh * G),
+                "r"(static_cast<int32_t>(jb.q_tok0 + (DUAL && jb.dual ? 0 : i * T))), "r"(bq)
                 : "memory");
           }
         }
@@ -508,7 +529,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity));
     };
     bool ok = true;
-    int32_t n = 0, g = 0;  // items done, key tiles done (all items)
+    int32_t n = 0, g = 0;  // items done, steps done (all items)
+    int32_t kt0 = 0;       // key tiles of the items done
     Job jb{}, jn{};
     int r = wait_item(0, jb);
     if (!__all_sync(0xffffffffu, r >= 0)) ok = false;
@@ -524,11 +546,12 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       load_q(jb, 0);
       load_q(jb, 1);
     }
-    // S_i = Q_i K_gg^T; for an empty query tile (live false) only the commit, which keeps bar_s's phases
-    auto qk = [&](int i, int gg, bool live) -> bool {
-      const int st = gg % KS;
-      if (i == 0) {
-        if (!wait_all(bar_kf[st], (gg / KS) & 1)) return false;
+    // S_i = Q_i K_kt^T; for an empty query tile (live false) only the commit, which keeps bar_s's phases.  The
+    // tiles share a key tile (tile 0 waits for it) unless the item is dual.
+    auto qk = [&](int i, int kt, bool live, bool dual) -> bool {
+      const int st = kt % KS;
+      if (i == 0 || (DUAL && dual && live)) {
+        if (!wait_all(bar_kf[st], (kt / KS) & 1)) return false;
         tc_fence_after();
       }
       if (lane == 0) {
@@ -543,10 +566,12 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       __syncwarp();
       return true;
     };
-    // O_i += P_i V_gg; j = key tile within the item.  After the last P of the item, query tile i is
+    // O_i += P_i V of the tile's step j (step gg of all items).  After the last P of the item, query tile i is
     // free (the softmax saw S_i, so its QK has completed): the next item's tile is loaded then.
     auto pv = [&](int i, int gg, int j) -> bool {
-      const int st = gg % VS;
+      const int kt = kt0 + tile_at(jb, j, i);
+      const int st = kt % VS;
+      const bool live = live_at(jb, j, i);  // an empty query tile issues no PV (its O is never read)
       if (!wait_all(bar_p[i], gg & 1)) return false;
       tc_fence_after();
       if (j == 0 && n > 0) {
@@ -554,12 +579,11 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         if (!wait_all(bar_ofree[i], (n - 1) & 1)) return false;
         tc_fence_after();
       }
-      if (i == 0) {
-        if (!wait_all(bar_vf[st], (gg / VS) & 1)) return false;
+      if (i == 0 || (DUAL && jb.dual && live)) {
+        if (!wait_all(bar_vf[st], (kt / VS) & 1)) return false;
         tc_fence_after();
       }
       if (lane == 0) {
-        const bool live = i < jb.tiles;  // an empty query tile issues no PV (its O is never read)
         const uint64_t vd = desc_v0 + st * kTile16;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16 && live; ++kk) {
@@ -568,8 +592,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         }
         // Each commit stalls the tensor pipe briefly, so there are three per key tile: S_0, S_1 and the
         // K/V release here.  O_i needs none until the item's last tile: S_i's commit also covers PV_i.
-        if (i == kTiles - 1) tc_commit(smem_u32(&bar_kvfree[gg % KVF]));
-        if (j == jb.nt - 1) tc_commit(smem_u32(&bar_o[i]));
+        if (DUAL && jb.dual ? live : i == kTiles - 1) tc_commit(smem_u32(&bar_kvfree[kt % KVF]));
+        if (j == steps_of(jb) - 1) tc_commit(smem_u32(&bar_o[i]));
       }
       __syncwarp();
       return true;
@@ -591,34 +615,38 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       ok = wait_all(bar_q[0], 0) && wait_all(bar_q[1], 0);
       if (ok) {
         tc_fence_after();
-        ok = qk(0, 0, true) && qk(1, 0, jb.tiles > 1);
+        ok = qk(0, 0, true, jb.dual) && qk(1, tile_at(jb, 0, 1), live_at(jb, 0, 1), jb.dual);
       }
     }
     while (ok && r > 0) {
       // (no per-tile look at the abort flag: after a failure elsewhere this warp leaves through the
       // deadline of its next wait; the check on the loop's back edge measured ~1% of the kernel)
-      for (int j = 0; ok && j < jb.nt; ++j) {
+      for (int j = 0; ok && j < steps_of(jb); ++j) {
         const int gg = g + j;
-        const bool last = j + 1 == jb.nt;
+        const bool last = j + 1 == steps_of(jb);
         // The QK on tile i after this key tile's PV: this item's next key tile, or after its last the next
         // item's first, once that item's query tile has landed.  One call site per query tile: the loop
         // body exists once (a copy for an item's last tile measured 6-8% slower: the MMA warp's code
         // shares an instruction cache with the softmax warps of its sub-partition).
         auto qk_after = [&](int i) -> bool {
-          bool live = i == 0 || jb.tiles > 1;
+          bool live = live_at(jb, j + 1, i), dual = DUAL && jb.dual;
+          int kt = kt0 + tile_at(jb, j + 1, i);
           if (last) {
             if (next == 0) return true;
             if (!wait_all(bar_q[i], (n + 1) & 1)) return false;
             tc_fence_after();
-            live = i < jn.tiles;
+            live = live_at(jn, 0, i);
+            dual = DUAL && jn.dual;
+            kt = kt0 + jb.nt + tile_at(jn, 0, i);
           }
-          return qk(i, gg + 1, live);
+          return qk(i, kt, live, dual);
         };
         ok = (!last || reload_q(0, gg)) && pv(0, gg, j) && (!last || reload_q(1, gg)) && qk_after(0) &&
              pv(1, gg, j) && qk_after(1);
       }
       if (!ok) break;
-      g += jb.nt;
+      g += steps_of(jb);
+      kt0 += jb.nt;
       ++n;
       r = next;
       jb = jn;
@@ -636,31 +664,33 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t col_s = ti * kKeys;
     const uint32_t col_o = kColO + ti * 128;
-    const int tok = ti * T + r / G;         // token / member of the item
+    const int tile_tok = ti * T + r / G;    // token / member of the item
     bool ok = true;
-    int32_t n = 0, g = 0;
+    int32_t n = 0, g = 0, join = 0;  // (join: dual items done)
+    (void)join;
     for (;; ++n) {
       Job jb;
       const int ri = wait_item(n, jb);
       if (__any_sync(0xffffffffu, ri < 0)) { ok = false; break; }
       if (ri == 0) break;
+      const int tok = DUAL && jb.dual ? r / G : tile_tok;
       const bool row_valid = tok < jb.n_valid;
       int32_t lim;  // exclusive key limit of this row (tree: of the keys every row sees)
       if constexpr (TREE) lim = jb.causal0;
       else if constexpr (EXTEND) lim = row_valid ? jb.causal0 + tok + 1 : jb.kend;
       else lim = jb.kend;
       float m_used = -INFINITY, l = 0.f;
-      for (int j = 0; j < jb.nt; ++j) {
+      for (int j = 0; j < steps_of(jb); ++j) {
         const int gg = g + j;
         // (as in the MMA warp, no per-tile look at the abort flag: the wait's deadline ends a failed CTA)
         const bool fail_here = !mbar_wait(smem_u32(&bar_s[ti]), gg & 1);
         if (__any_sync(0xffffffffu, fail_here)) { ok = false; break; }  // warp-uniform: tcgen05.ld/st are collective
-        if (ti >= jb.tiles) {  // an empty query tile: no S was computed; keep bar_p's phase
+        if (!live_at(jb, j, ti)) {  // an empty query tile: no S was computed; keep bar_p's phase
           mbar_arrive(smem_u32(&bar_p[ti]));
           continue;
         }
         tc_fence_after();
-        const int32_t key0 = jb.kbeg + j * kKeys;
+        const int32_t key0 = jb.kbeg + tile_at(jb, j, ti) * kKeys;
         const bool masked = key0 + kKeys > lim;
         const bool warp_masked = __any_sync(0xffffffffu, masked);
         // tree: bit e of vis[c] = key key0 + 32 c + e is visible to this row
@@ -811,19 +841,65 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         mbar_arrive(smem_u32(&bar_p[ti]));
       }
       if (!ok) break;
-      g += jb.nt;
+      g += steps_of(jb);
       // ---- epilogue: O / l, then O_i is released to the next item's first PV
       const bool late = !mbar_wait(smem_u32(&bar_o[ti]), n & 1);
       if (__any_sync(0xffffffffu, late)) { ok = false; break; }
       tc_fence_after();
+      float own = 1.f, other = 0.f;  // a dual item's factors of this tile's O and of tile 1's
+      (void)own, (void)other;
+      if constexpr (DUAL) {
+        if (jb.dual && ti == 1) {
+          // tile 0's threads read this tile's sums and O of the same rows
+          s_join[r] = make_float2(m_used, l);
+          tc_fence_before();
+          mbar_arrive(smem_u32(&bar_join[0]));
+          const bool stuck = !mbar_wait(smem_u32(&bar_join[1]), join & 1);
+          ++join;
+          if (__any_sync(0xffffffffu, stuck)) { ok = false; break; }
+          tc_fence_before();
+          mbar_arrive(smem_u32(&bar_ofree[ti]));
+          continue;
+        }
+        if (jb.dual) {
+          const bool stuck = !mbar_wait(smem_u32(&bar_join[0]), join & 1) || !mbar_wait(smem_u32(&bar_o[1]), n & 1);
+          ++join;
+          if (__any_sync(0xffffffffu, stuck)) { ok = false; break; }
+          tc_fence_after();
+          const float2 b = s_join[r];
+          const float top = fmaxf(m_used, b.x), ref = top == -INFINITY ? 0.f : top;
+          own = ex2(m_used - ref), other = ex2(b.x - ref);
+          m_used = top;
+          l = l * own + b.y * other;
+        }
+      }
       const float inv_l = TREE && l == 0.f ? 0.f : 1.f / l;  // a tree row that sees nothing gives 0
-      if (EXTEND && (!TREE || jb.slot < 0)) {
-        __nv_bfloat16* dst = p.o + ((jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G)) * static_cast<int64_t>(D);
-        uint32_t oa[D / 32][32];
+      // O of this thread's row, all columns, as the epilogues write it (a dual item's two halves joined)
+      auto load_o = [&](uint32_t (&oa)[D / 32][32]) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tmem_ld32(tmem + lane_addr + col_o + c * 32, oa[c]);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tc_wait_ld_regs(oa[c]);  // ties each array to the wait (one real wait)
+        if constexpr (DUAL) {
+          if (jb.dual) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ob[32];
+              tmem_ld32(tmem + lane_addr + col_o + 128 + c * 32, ob);
+              tc_wait_ld_regs(ob);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                oa[c][e] = __float_as_uint(__uint_as_float(oa[c][e]) * own + __uint_as_float(ob[e]) * other);
+            }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&bar_join[1]));
+          }
+        }
+      };
+      if (EXTEND && (!TREE || jb.slot < 0)) {
+        __nv_bfloat16* dst = p.o + ((jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G)) * static_cast<int64_t>(D);
+        uint32_t oa[D / 32][32];
+        load_o(oa);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t (&ov)[32] = oa[c];
@@ -852,10 +928,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         }
         float* dst = (TREE ? p.part_o : p.casc_o) + ps * D;
         uint32_t oa[D / 32][32];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) tmem_ld32(tmem + lane_addr + col_o + c * 32, oa[c]);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) tc_wait_ld_regs(oa[c]);  // ties each array to the wait (one real wait)
+        load_o(oa);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t (&ov)[32] = oa[c];

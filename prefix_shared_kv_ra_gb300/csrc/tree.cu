@@ -415,14 +415,14 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const _
   }
 }
 
-template <int D>
+template <int D, int PASS>
 ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev) {
   CUtensorMap qmap, kmap, vmap;
   if (ra_status st = query_tile_map(&qmap, p.q, p.total_q, p.hq, D, p.group)) return st;
   if (ra_status st = row_gather_map(&kmap, p.k_pool, p.num_slots * p.hkv, D)) return st;
   if (ra_status st = row_gather_map(&vmap, p.v_pool, p.num_slots * p.hkv, D)) return st;
   using L = tc::Layout<D, k_stages<D>(), v_stages<D>()>;
-  auto kern = attn_tc_kernel<D, k_stages<D>(), v_stages<D>(), kTreePass>;
+  auto kern = attn_tc_kernel<D, k_stages<D>(), v_stages<D>(), PASS>;
   static bool configured[64] = {};
   if (L::kDynSmem > dev.max_smem_optin)
     return fail(RA_ERR_UNSUPPORTED, "tree kernel needs %d bytes of shared memory", L::kDynSmem);
@@ -476,10 +476,14 @@ ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& d
   if (ra_status st = launch_pdl("tree_plan_kernel", tree_plan_kernel, dim3(1 + scan), dim3(kScanThreads), 0, s, p,
                                 head_dim))
     return st;
-  if (ra_status st = p.sh.narrow       ? launch_tree_narrow(p, head_dim, false, dev, s)
-                     : head_dim == 128 ? launch_wide<128>(p, s, dev)
-                                       : launch_wide<64>(p, s, dev))
-    return st;
+  if (p.sh.narrow) {
+    if (ra_status st = launch_tree_narrow(p, head_dim, false, dev, s)) return st;
+  } else {
+    const bool one_tile = p.max_draft * p.group <= tc::kRows;  // every item's rows fit one query tile
+    if (ra_status st = head_dim == 128 ? (one_tile ? launch_wide<128, kTreeDualPass>(p, s, dev) : launch_wide<128, kTreePass>(p, s, dev))
+                                       : (one_tile ? launch_wide<64, kTreeDualPass>(p, s, dev) : launch_wide<64, kTreePass>(p, s, dev)))
+      return st;
+  }
   // Persistent.  At most cap_parts / 2 query tiles are split (each into two or more).  With many splits per tile
   // (their number is bounded, so few tiles) several warps share a row: as many as leave each unit's rows enough
   // for the SMs' CTAs.

@@ -149,6 +149,24 @@ def test_tree_planned_by_the_warps_and_by_the_kernel(batch, longest, bound):
     c.check(o)
 
 
+@pytest.mark.parametrize("hq,hkv,d,draft", [(32, 8, 128, 16), (8, 8, 64, 70), (8, 1, 128, 8), (16, 2, 64, 13)])
+def test_tree_one_query_tile_on_the_wide_path(hq, hkv, d, draft):
+    """Requests of 33..128 rows per kv head in calls that are not small: both query tiles of an item share out its
+    key tiles (even and odd numbers of them, a single one), split (few kv heads) and unsplit."""
+    rng = np.random.default_rng(hq + draft)
+    prefix, drafts = rng.integers(0, 1100, 40), rng.integers(0, draft + 1, 40)
+    prefix[:6], drafts[:6] = [0, 1, 127, 128, 129, 1500], [draft, 1, 1, draft, 1, draft]
+    c = Case(rng, prefix, drafts, hq, hkv, d, gap=1)
+    o = c.run(max_p=1 << 20 if hq == 32 else 1500, table=i32(np.pad(c.table, ((0, 0), (0, 1 << 20 if hq == 32 else 0)))))
+    assert int(c.err.item()) == 0
+    c.check(o)
+    c = Case(rng, prefix[:34], np.minimum(drafts[:34], 9), hq, hkv, d, "chain", grow=3.0)
+    c.max_t = draft
+    c.words = -(-draft // 32)
+    c.mask = np.pad(c.mask, ((0, 0), (0, c.words - c.mask.shape[1])))
+    c.check(c.run())
+
+
 def test_tree_many_requests_unsplit():
     """Enough items that nothing is split (the direct bf16 rows), with rows between the requests left alone."""
     rng = np.random.default_rng(2)
