@@ -292,7 +292,8 @@ ra_status ra_kv8_load(const void* kv8_pool, int64_t num_slots, int32_t num_kv_he
  * ra_kv8_decode_attention -- ra_decode_attention (without groups) over a quantised pool: the softmax
  * attention of each request's query over the values its records stand for, accumulated in fp32, output
  * bf16.  Arguments, checks, flags and the workspace (ra_decode_workspace_bytes with num_groups 0) are those
- * of ra_decode_attention, with the one pool instead of two.
+ * of ra_decode_attention, with the one pool instead of two.  Calls that overlap on the GPU need separate
+ * workspaces.
  */
 ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_slots, int32_t num_kv_heads, int32_t head_dim,
                                   const void* q, void* o, int32_t num_q_heads, float sm_scale,
