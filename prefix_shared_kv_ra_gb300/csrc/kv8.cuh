@@ -98,15 +98,16 @@ __device__ __forceinline__ uint32_t amax_bf16x8(const uint4& v) {
 }
 
 // A warp's up-to-16 exponent bytes: row r (K and V of the block's heads interleaved, as in the record) was
-// handled in step r / kRowsPerStep by the lanes from (r % kRowsPerStep) * kLanesPerRow.  Every lane calls;
-// rows past n_rows give 0.
+// handled in step r / kRowsPerStep by the lanes from (base + r % kRowsPerStep) * kLanesPerRow (base: the block's
+// first row of the step, where several blocks share one).  Every lane calls; rows past n_rows give 0.
 template <int kSteps, int kRowsPerStep, int kLanesPerRow>
-__device__ __forceinline__ uint4 gather_scale_bytes(const uint32_t (&eb)[kSteps], int n_rows) {
+__device__ __forceinline__ uint4 gather_scale_bytes(const uint32_t (&eb)[kSteps], int n_rows,
+                                                    int base = 0) {
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     if (r / kRowsPerStep < kSteps) {
-      const uint32_t b = __shfl_sync(0xffffffffu, eb[r / kRowsPerStep], (r % kRowsPerStep) * kLanesPerRow);
+      const uint32_t b = __shfl_sync(0xffffffffu, eb[r / kRowsPerStep], ((base + r % kRowsPerStep) * kLanesPerRow) & 31);
       if (r < n_rows) w[r >> 2] |= b << (8 * (r & 3));
     }
   }

@@ -13,7 +13,10 @@
 // lie D / 2 further: with rot = D and half-split pairs both members of a pair are in one lane and the
 // rotation needs no exchange; other forms fetch the partner with shuffles.  A warp takes a unit of one
 // token: one or more steps of 512 / D q rows, or the 2 * hpc rows of one K/V block (hpc <= 8 heads); all
-// loads of a unit are issued before the first use, and the angles and weights are loaded once per unit.
+// loads of a unit are issued before the first use, and the angles and weights are loaded once per unit.  Where
+// the heads of a token would leave such units part empty, units are flat: the next 512 / D q rows of all
+// tokens, or as many K/V blocks as fit a step, each row's lanes with their own token.
+#include <algorithm>
 #include <cmath>
 
 #include "api_common.h"
@@ -42,7 +45,9 @@ struct NormRopeParams {
   const int32_t* loc;
   int32_t hq, hkv;
   Kv8Shape sh;
-  int32_t q_units, units_per_token;
+  int32_t q_units, units_per_token;  // wide units: of a token
+  int64_t tokens, flat_q;            // flat units: the q units come first
+  int32_t bps;                       // flat units: K/V blocks per unit
   int64_t units;
   uint32_t* err;
 };
@@ -164,31 +169,59 @@ __device__ __forceinline__ void norm_rope_row(float (&x)[2][8], bool norm, const
   }
 }
 
+// QSTEPS: 512 / D q rows each in a unit; 0: flat units of one step
 template <int D, int ROPE, bool KV8, int QSTEPS, int KVSTEPS>
-__global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2) qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
+    qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = D / 16, kPerStep = 32 / kLanes, kKvSteps = KVSTEPS;
+  constexpr bool kFlat = QSTEPS == 0;
+  constexpr int kQSteps = kFlat ? 1 : QSTEPS;
   griddep_wait();  // q, k and v come from the kernel before; earlier kernels may still read the slots
   griddep_launch();
   const int lane = threadIdx.x & 31;
   const int sub = lane % kLanes, row0 = lane / kLanes;
   const bool norm = p.q_weight != nullptr;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  const int n_rows = 2 * p.sh.hpc;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < p.units; u += warps) {
-    const int64_t tok = u / p.units_per_token;
-    const int32_t part = static_cast<int32_t>(u - tok * p.units_per_token);
+    // this lane's token, and its q head (the unit's first) or its block of heads and row of the block
+    int64_t tok;
+    int32_t h0 = 0, blk = 0, base = 0;  // base: first row (of the warp's step) of the block
+    bool in = true, is_q;
+    if constexpr (kFlat) {
+      is_q = u < p.flat_q;
+      if (is_q) {
+        const uint32_t g = static_cast<uint32_t>(u) * kPerStep + row0, t = g / static_cast<uint32_t>(p.hq);
+        in = t < p.tokens;
+        tok = in ? t : 0;
+        h0 = in ? static_cast<int32_t>(g - t * p.hq) : p.hq;
+      } else {
+        const uint32_t i = kKvSteps == 1 ? row0 / n_rows : 0;
+        const uint32_t g = static_cast<uint32_t>(u - p.flat_q) * p.bps + i, t = g / static_cast<uint32_t>(p.sh.blocks);
+        in = i < static_cast<uint32_t>(p.bps) && t < p.tokens;
+        tok = in ? t : 0;
+        blk = in ? static_cast<int32_t>(g - t * p.sh.blocks) : 0;
+        base = i * n_rows;
+      }
+    } else {
+      tok = u / p.units_per_token;
+      const int32_t part = static_cast<int32_t>(u - tok * p.units_per_token);
+      is_q = part < p.q_units;
+      h0 = part * kQSteps * kPerStep + row0;
+      blk = part - p.q_units;
+    }
     int64_t pos = __ldg(p.positions + tok);
     if (pos < 0 || pos >= p.max_position) {
-      if (lane == 0 && part == 0) flag_error(p.err, RA_DEVERR_POSITION);
+      if (is_q && h0 == 0 && sub == 0) flag_error(p.err, RA_DEVERR_POSITION);  // (once per token)
       pos = 0;
     }
     const float* ang = p.cos_sin + pos * p.rot;
-    if (part < p.q_units) {  // q rows
+    if (is_q) {
       const __nv_bfloat16* src = p.q + tok * p.q_stride + 8 * sub;
       __nv_bfloat16* dst = p.q_out + tok * p.q_out_stride + 8 * sub;
-      const int32_t h0 = part * QSTEPS * kPerStep + row0;
-      uint4 a[QSTEPS], b[QSTEPS];
+      uint4 a[kQSteps], b[kQSteps];
 #pragma unroll
-      for (int s = 0; s < QSTEPS; ++s) {
+      for (int s = 0; s < kQSteps; ++s) {
         const int32_t h = h0 + s * kPerStep;
         a[s] = b[s] = make_uint4(0, 0, 0, 0);
         if (h < p.hq) {
@@ -204,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2)
       Angles<ROPE> an;
       load_angles<D, ROPE>(ang, p.rot, sub, an);
 #pragma unroll
-      for (int s = 0; s < QSTEPS; ++s) {
+      for (int s = 0; s < kQSteps; ++s) {
         const int32_t h = h0 + s * kPerStep;
         float x[2][8];
         unpack8(a[s], x[0]);
@@ -218,14 +251,12 @@ __global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2)
       continue;
     }
     // K and V rows of one block of heads, interleaved (row 2h: K of head h, 2h + 1: its V)
-    const int32_t blk = part - p.q_units;
-    const int n_rows = 2 * p.sh.hpc;
     uint4 a[kKvSteps], b[kKvSteps];
 #pragma unroll
     for (int s = 0; s < kKvSteps; ++s) {
-      const int r = s * kPerStep + row0;
+      const int r = s * kPerStep + row0 - base;
       a[s] = b[s] = make_uint4(0, 0, 0, 0);
-      if (r < n_rows) {
+      if (in && r < n_rows) {
         const __nv_bfloat16* src =
             ((r & 1) ? p.v + tok * p.v_stride : p.k + tok * p.k_stride) + (blk * p.sh.hpc + (r >> 1)) * D + 8 * sub;
         a[s] = __ldg(reinterpret_cast<const uint4*>(src));
@@ -240,17 +271,18 @@ __global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2)
     }
     Angles<ROPE> an;
     load_angles<D, ROPE>(ang, p.rot, sub, an);
-    if (slot < 0 || slot >= p.num_slots) {  // warp-uniform
-      if (lane == 0 && blk == 0) flag_error(p.err, RA_DEVERR_SLOT);
-      continue;
-    }
+    const bool stored = in && slot >= 0 && slot < p.num_slots;
+    if (in && !stored && sub == 0 && row0 == base && blk == 0) flag_error(p.err, RA_DEVERR_SLOT);
+    if (kFlat ? !__any_sync(0xffffffffu, stored) : !stored) continue;  // (warp-uniform)
     const bool is_v = row0 & 1;  // the same in every step: kPerStep is even
     uint8_t* rec = nullptr;
-    if constexpr (KV8) rec = p.kv8_pool + static_cast<int64_t>(slot) * p.sh.slot_bytes + blk * p.sh.block_bytes;
+    if constexpr (KV8) {
+      if (stored) rec = p.kv8_pool + static_cast<int64_t>(slot) * p.sh.slot_bytes + blk * p.sh.block_bytes;
+    }
     uint32_t eb[kKvSteps];
 #pragma unroll
     for (int s = 0; s < kKvSteps; ++s) {
-      const int r = s * kPerStep + row0;
+      const int r = s * kPerStep + row0 - base;
       float x[2][8], y[2][8];
       unpack8(a[s], x[0]);
       unpack8(b[s], x[1]);
@@ -258,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2)
       for (int j = 0; j < 8; ++j) y[0][j] = x[0][j], y[1][j] = x[1][j];
       norm_rope_row<D, ROPE>(y, norm, w, p.eps, p.rot, sub, an);  // (V's lanes compute it too and drop it)
       if constexpr (!KV8) {
-        if (r < n_rows) {
+        if (stored && r < n_rows) {
           __nv_bfloat16* dst = (is_v ? p.v_pool : p.k_pool) +
                                (static_cast<int64_t>(slot) * p.hkv + blk * p.sh.hpc + (r >> 1)) * D + 8 * sub;
           *reinterpret_cast<uint4*>(dst) = is_v ? a[s] : pack8(y[0]);
@@ -278,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2)
         for (int off = 1; off < kLanes; off <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
         const int32_t e = kv8_exponent(m);
         eb[s] = static_cast<uint32_t>(e + 127);
-        if (r < n_rows) {
+        if (stored && r < n_rows) {
           const float inv = pow2f(-e);
           uint2* dst = reinterpret_cast<uint2*>(rec + r * D) + sub;
 #pragma unroll
@@ -290,10 +322,10 @@ __global__ void __launch_bounds__(kThreads, QSTEPS == 1 && KVSTEPS == 1 ? 3 : 2)
       }
     }
     if constexpr (KV8) {
-      const uint4 scales = gather_scale_bytes<kKvSteps, kPerStep, kLanes>(eb, n_rows);
+      const uint4 scales = gather_scale_bytes<kKvSteps, kPerStep, kLanes>(eb, n_rows, base);
       uint4* tail = reinterpret_cast<uint4*>(rec + n_rows * D);
-      if (lane == 0) tail[0] = scales;
-      if (lane == 1 && blk == p.sh.blocks - 1 && p.sh.blocks * p.sh.block_bytes < p.sh.slot_bytes)
+      if (stored && row0 == base && sub == 0) tail[0] = scales;
+      if (stored && row0 == base && sub == 1 && blk == p.sh.blocks - 1 && p.sh.blocks * p.sh.block_bytes < p.sh.slot_bytes)
         tail[1] = make_uint4(0, 0, 0, 0);  // the record's padding (16 bytes)
     }
   }
@@ -307,12 +339,17 @@ ra_status launch(const NormRopeParams& p, bool interleaved, int grid, cudaStream
   return launch_pdl("qk_norm_rope_kernel", kern, dim3(grid), dim3(kThreads), 0, s, p);
 }
 
+enum Units { kWide, kOneStep, kFlatUnits };
+
 template <int D, bool KV8>
-ra_status launch_steps(const NormRopeParams& p, bool interleaved, bool wide, bool deep, int grid, ra_stream_t stream) {
+ra_status launch_steps(const NormRopeParams& p, bool interleaved, Units units, bool deep, int grid, ra_stream_t stream) {
   constexpr int kMost = 16 / (32 / (D / 16));  // steps of 16 rows
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (wide) return deep ? launch<D, KV8, kMost, kMost>(p, interleaved, grid, s) : launch<D, KV8, kMost, 1>(p, interleaved, grid, s);
-  return deep ? launch<D, KV8, 1, kMost>(p, interleaved, grid, s) : launch<D, KV8, 1, 1>(p, interleaved, grid, s);
+  if (units == kWide)
+    return deep ? launch<D, KV8, kMost, kMost>(p, interleaved, grid, s) : launch<D, KV8, kMost, 1>(p, interleaved, grid, s);
+  if (units == kOneStep)
+    return deep ? launch<D, KV8, 1, kMost>(p, interleaved, grid, s) : launch<D, KV8, 1, 1>(p, interleaved, grid, s);
+  return deep ? launch<D, KV8, 0, kMost>(p, interleaved, grid, s) : launch<D, KV8, 0, 1>(p, interleaved, grid, s);
 }
 
 ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t num_tokens, int32_t interleaved,
@@ -345,24 +382,36 @@ ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t n
   DeviceInfo dev;
   if (ra_status st = current_device(&dev)) return st;
   p.sh = kv8_shape(p.hkv, head_dim);
-  // q rows per unit: 16 (4 KB of loads in flight per warp), or one step where that fills the SMs' warps badly: few
-  // tokens (a decode step of 64 has 1.6 warps per SM sub-partition with one step), or more than a quarter of
-  // the rows of the last unit missing.  Measured, 4777 tokens: 8/2 heads of 64 7.4 us with 16 rows, 5.4 with
-  // one step; 12/3 heads of 128 14.7 and 19.3.
-  const int32_t per_step = 32 / (head_dim / 16);
-  const int64_t big = num_tokens * ((p.hq + 15) / 16 + p.sh.blocks);
-  const bool wide = 4 * p.hq >= 48 * ((p.hq + 15) / 16) && big >= static_cast<int64_t>(dev.num_sms) * 16;
-  const bool deep = 2 * p.sh.hpc > per_step;  // a K/V block takes more than one step
-  const int32_t q_rows = wide ? 16 : per_step;
-  p.q_units = (p.hq + q_rows - 1) / q_rows;
-  p.units_per_token = p.q_units + p.sh.blocks;
-  p.units = num_tokens * p.units_per_token;
+  // Wide units of 16 q rows (4 KB of loads in flight per warp); where more than a quarter of the rows of a
+  // token's last one were missing, flat units; and one step of one token for few tokens, where wide ones fill the
+  // SMs' warps badly (a decode step of 64 has 1.6 warps per SM sub-partition with one step) and latency counts
+  // (64 tokens, 32/8 heads of 128: 2.55 us, 2.9 with flat units).  Measured with 4777 tokens: 8/2 heads of 64
+  // 7.4 us wide, 5.4 in single steps, 4.5 flat; 28/4 heads of 128 20.7 us wide, 28.0 flat; 12/3 heads 14.7 and 17.4.
+  const int32_t per_step = 32 / (head_dim / 16), n_rows = 2 * p.sh.hpc;
+  const int64_t wide_units = num_tokens * ((p.hq + 15) / 16 + p.sh.blocks);
+  const bool few = wide_units < static_cast<int64_t>(dev.num_sms) * 16;
+  const bool filled = 4 * p.hq >= 48 * ((p.hq + 15) / 16);
+  // (flat units count rows in 32 bits)
+  const bool countable = num_tokens * std::max(p.hq, p.sh.blocks) < int64_t(1) << 31;
+  const Units units = few ? kOneStep : filled || !countable ? kWide : kFlatUnits;
+  const bool deep = n_rows > per_step;  // a K/V block takes more than one step
+  p.tokens = num_tokens;
+  if (units == kFlatUnits) {
+    p.bps = deep ? 1 : per_step / n_rows;
+    p.flat_q = (num_tokens * p.hq + per_step - 1) / per_step;
+    p.units = p.flat_q + (num_tokens * p.sh.blocks + p.bps - 1) / p.bps;
+  } else {
+    const int32_t q_rows = units == kWide ? 16 : per_step;
+    p.q_units = (p.hq + q_rows - 1) / q_rows;
+    p.units_per_token = p.q_units + p.sh.blocks;
+    p.units = num_tokens * p.units_per_token;
+  }
   const int64_t want = (p.units + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(dev.num_sms) * 8;
   const int grid = static_cast<int>(want < cap ? want : cap);
-  return head_dim == 128 ? (kv8 ? launch_steps<128, true>(p, interleaved, wide, deep, grid, stream)
-                                : launch_steps<128, false>(p, interleaved, wide, deep, grid, stream))
-                         : (kv8 ? launch_steps<64, true>(p, interleaved, wide, deep, grid, stream)
-                                : launch_steps<64, false>(p, interleaved, wide, deep, grid, stream));
+  return head_dim == 128 ? (kv8 ? launch_steps<128, true>(p, interleaved, units, deep, grid, stream)
+                                : launch_steps<128, false>(p, interleaved, units, deep, grid, stream))
+                         : (kv8 ? launch_steps<64, true>(p, interleaved, units, deep, grid, stream)
+                                : launch_steps<64, false>(p, interleaved, units, deep, grid, stream));
 }
 
 NormRopeParams common_params(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

@@ -50,6 +50,9 @@ CASES = [
     (5, 8, 2, 64, 64, False), (33, 8, 2, 64, 32, True), (1000, 8, 2, 64, 64, True), (17, 12, 3, 128, 64, False),
     (9, 5, 5, 64, 48, False), (9, 5, 5, 128, 96, False), (31, 16, 16, 128, 16, True), (31, 16, 16, 128, 128, True),
     (3, 20, 20, 64, 16, False), (2, 11, 11, 128, 112, True), (600, 40, 20, 64, 32, False), (50, 7, 1, 128, 32, False),
+    # many tokens of few heads: rows of several tokens and blocks share a warp
+    (1301, 8, 2, 64, 64, False), (1303, 5, 5, 64, 48, True), (1217, 3, 3, 128, 128, False), (1299, 7, 1, 64, 32, True),
+    (1217, 7, 1, 128, 64, False), (437, 5, 11, 64, 16, False), (1219, 9, 3, 64, 64, False), (2433, 1, 1, 128, 128, True),
 ]
 
 
@@ -153,6 +156,36 @@ def test_bad_positions_and_slots_are_flagged(kv8):
     pos = np.where((pos < 0) | (pos >= 300), 0, pos)
     check_rows(qo, q, w[0], 1e-6, cs.double().cpu().numpy()[pos], d, False)
     assert sorted(np.flatnonzero(written.cpu().numpy())) == sorted(loc[(loc >= 0) & (loc < S)])
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (5, 1, 64), (3, 3, 128), (5, 11, 64)])
+@pytest.mark.parametrize("kv8", [False, True])
+def test_bad_positions_and_slots_among_many_tokens(kv8, hq, hkv, d):
+    """Tokens that share a warp with a bad one are stored as alone; the bad ones' pool rows stay."""
+    n = 1217
+    rng, q, k, v, w, cs, pos, S, loc = setup(12, n, hq, hkv, d, d)
+    loc = loc.copy()
+    bad = rng.permutation(n)[:200]
+    bad.sort()
+    loc_bad = loc.copy()
+    loc_bad[bad] = np.where(np.arange(200) % 2, -1, S)
+    pools = []
+    for at in (loc, loc_bad):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        qo = torch.empty(n, hq, d, dtype=BF, device=DEV)
+        if kv8:
+            pool = torch.full((S, ra.ra_kv8_slot_bytes(hkv, d)), 0xAB, dtype=torch.uint8, device=DEV)
+            ra.ra_qk_norm_rope_kv8_store(q, k, v, *w, i32(pos), cs, qo, pool, i32(at), device_error=err)
+        else:
+            kp, vp = (torch.full((S, hkv, d), 9.0, dtype=BF, device=DEV) for _ in range(2))
+            ra.ra_qk_norm_rope_store(q, k, v, *w, i32(pos), cs, qo, kp, vp, i32(at), device_error=err)
+            pool = torch.cat([kp, vp], 1)
+        pools.append((pool, qo, int(err.item())))
+    assert pools[0][2] == 0 and pools[1][2] == ra.DEVERR_SLOT
+    assert torch.equal(pools[0][1], pools[1][1])
+    kept = np.setdiff1d(np.arange(S), loc[bad])
+    assert torch.equal(pools[0][0][kept], pools[1][0][kept])
+    assert (pools[1][0][loc[bad]] == (0xAB if kv8 else 9.0)).all()
 
 
 def test_layer_steps_together_over_a_quantised_pool():
