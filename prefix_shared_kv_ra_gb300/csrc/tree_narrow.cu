@@ -322,14 +322,17 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
   if (!clean && lane == 0) rg.give_up(p.err);  // a bounded wait ran out: stop the producers as well
 }
 
+int32_t stage_bytes(int32_t hpc, int32_t head_dim, int32_t slab) { return 2 * slab * (hpc * head_dim * 2 + 16); }
+int32_t ring_bytes(int32_t per_sm) { return kRingSmemLimit / per_sm - 1024 - kRingHdrBytes; }  // (1 KB per CTA is the system's)
+
 template <int D, int SLAB, bool SMALL>
 ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
   NarrowParams n{};
   n.t = p;
   n.row_bytes = p.sh.hpc * D * 2;
   n.row_stride = n.row_bytes + 16;
-  n.stage_bytes = 2 * SLAB * n.row_stride;
-  n.nstage = (kRingSmemLimit / p.sh.per_sm - 1024 - kRingHdrBytes) / n.stage_bytes;  // (1 KB per CTA is the system's)
+  n.stage_bytes = stage_bytes(p.sh.hpc, D, SLAB);
+  n.nstage = ring_bytes(p.sh.per_sm) / n.stage_bytes;
   if (n.nstage > kRingMaxStages) n.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + n.nstage * n.stage_bytes;
   auto kern = tree_narrow_kernel<D, SLAB, SMALL>;
@@ -348,11 +351,15 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
 
 }  // namespace
 
-// 32-key slabs where three of them fit the ring, else 16 (8 heads of 128).
+// 32-key slabs where two of them fit the ring, else 16-key ones (64 x 8 tokens over 512..4096 keys: 16/16 heads of
+// 64, where one fits, 118.6 and 106.5 us; 12/12, where two do, 84.6 and 87.3;
+// 5/5 heads of 128, two, 77.2 and 81.8).
 ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, bool small, const DeviceInfo& dev, cudaStream_t s) {
-  if (head_dim == 64) return small ? launch<64, 32, true>(p, dev, s) : launch<64, 32, false>(p, dev, s);
-  if (p.sh.hpc > 4) return small ? launch<128, 16, true>(p, dev, s) : launch<128, 16, false>(p, dev, s);
-  return small ? launch<128, 32, true>(p, dev, s) : launch<128, 32, false>(p, dev, s);
+  const bool wide = 2 * stage_bytes(p.sh.hpc, head_dim, 32) <= ring_bytes(p.sh.per_sm);
+  if (head_dim == 64 && wide) return small ? launch<64, 32, true>(p, dev, s) : launch<64, 32, false>(p, dev, s);
+  if (head_dim == 64) return small ? launch<64, 16, true>(p, dev, s) : launch<64, 16, false>(p, dev, s);
+  if (wide) return small ? launch<128, 32, true>(p, dev, s) : launch<128, 32, false>(p, dev, s);
+  return small ? launch<128, 16, true>(p, dev, s) : launch<128, 16, false>(p, dev, s);
 }
 
 }  // namespace ra

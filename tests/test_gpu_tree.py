@@ -122,6 +122,9 @@ CASES = [
     ([0, 130], [70, 70], 8, 2, 64, "none"), ([4000], [4], 8, 1, 128, "tree"), ([250], [12], 16, 1, 128, "tree"),
     ([20, 400], [1024, 700], 4, 1, 64, "tree"), ([70, 0], [1, 3], 32, 1, 128, "tree"), ([300], [5], 128, 1, 64, "tree"),
     ([150, 31], [2, 1], 64, 4, 128, "tree"), ([97], [6], 40, 20, 64, "any"), ([33, 500, 64], [32, 17, 1], 11, 11, 64, "tree"),
+    ([33, 500, 64, 7], [16, 9, 1, 16], 16, 16, 64, "tree"), ([300, 15, 1], [8, 7, 1], 28, 14, 64, "any"),
+    ([333, 17, 0], [9, 4, 6], 6, 6, 128, "tree"), ([333, 17, 0], [9, 4, 6], 7, 7, 128, "any"),
+    (list(range(3, 640, 15)), [1 + i % 8 for i in range(43)], 16, 16, 64, "any"),
 ]
 
 
