@@ -12,7 +12,8 @@
 // angles add rot * 4).  A row is D / 16 lanes wide, a lane holding 8 values of its first half and the 8 that
 // lie D / 2 further: with rot = D and half-split pairs both members of a pair are in one lane and the
 // rotation needs no exchange; other forms fetch the partner with shuffles.  A warp takes a unit of one
-// token: one or more steps of 512 / D q rows, or the 2 * hpc rows of one K/V block (hpc <= 8 heads); all
+// token: one or more steps of 512 / D q rows, or the 2 * hpc rows of one K/V block (hpc <= 8 heads), at once or
+// (single-step units) in a step each; all
 // loads of a unit are issued before the first use, and the angles and weights are loaded once per unit.  Where
 // the heads of a token would leave such units part empty, units are flat: the next 512 / D q rows of all
 // tokens, or as many K/V blocks as fit a step, each row's lanes with their own token.
@@ -48,16 +49,21 @@ struct NormRopeParams {
   int32_t q_units, units_per_token;  // wide units: of a token
   int64_t tokens, flat_q;            // flat units: the q units come first
   int32_t bps;                       // flat units: K/V blocks per unit
+  int32_t spb;                       // single-step units: units per K/V block
   int64_t units;
   uint32_t* err;
 };
 
-enum Rope { kHalfFull = 0, kHalfPart = 1, kAdjacent = 2 };
+// Half-split pairs with rot = D, rot <= D / 2 (a lane's second chunk is not turned, and both members of a pair lie in
+// first chunks: 8 exchanges a row where the general form makes 32; 2886 tokens, 12/3 heads, 64 of 128 values, e4m3:
+// 16.5 us -> 14.0) and between; adjacent pairs.
+enum Rope { kHalfFull, kHalfLow, kHalfPart, kAdjacent };
 
 // cosines and sines of a lane's two chunks of 8 values (first-half chunk, second-half chunk)
 template <int ROPE>
 struct Angles {
-  float c[ROPE == kHalfFull ? 1 : 2][8], s[ROPE == kHalfFull ? 1 : 2][8];
+  static constexpr int kChunks = ROPE == kHalfFull || ROPE == kHalfLow ? 1 : 2;
+  float c[kChunks][8], s[kChunks][8];
 };
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
@@ -73,12 +79,12 @@ __device__ __forceinline__ void load_angles(const float* row, int32_t rot, int s
     load8(row + half + 8 * sub, an.s[0]);
   } else {
 #pragma unroll
-    for (int ch = 0; ch < 2; ++ch) {
+    for (int ch = 0; ch < Angles<ROPE>::kChunks; ++ch) {
       const int e0 = ch * (D / 2) + 8 * sub;  // first value of the chunk
       if (e0 >= rot) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) an.c[ch][j] = 1.f, an.s[ch][j] = 0.f;
-      } else if constexpr (ROPE == kHalfPart) {
+      } else if constexpr (ROPE != kAdjacent) {
         const int f = e0 < half ? e0 : e0 - half;
         load8(row + f, an.c[ch]);
         load8(row + half + f, an.s[ch]);
@@ -132,6 +138,14 @@ __device__ __forceinline__ void norm_rope_row(float (&x)[2][8], bool norm, const
       x[0][j] = a * an.c[0][j] - b * an.s[0][j];
       x[1][j] = b * an.c[0][j] + a * an.s[0][j];
     }
+  } else if constexpr (ROPE == kHalfLow) {
+    const int hc = rot >> 4;  // chunks in half of the rotated part
+    const int partner = (threadIdx.x & 31) + (sub < hc ? hc : sub < 2 * hc ? -hc : 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float y = __shfl_sync(0xffffffffu, x[0][j], partner);
+      if (sub < 2 * hc) x[0][j] = x[0][j] * an.c[0][j] + y * an.s[0][j];
+    }
   } else if constexpr (ROPE == kHalfPart) {
     // the partner chunk of 8 lies rot / 2 values away, in the same or the other half, on some lane of the row
     const int hc = rot >> 4;  // chunks in half of the rotated part
@@ -175,7 +189,9 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
     qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = D / 16, kPerStep = 32 / kLanes, kKvSteps = KVSTEPS;
   constexpr bool kFlat = QSTEPS == 0;
+  constexpr bool kSingle = QSTEPS == 1;  // one step per unit
   constexpr int kQSteps = kFlat ? 1 : QSTEPS;
+  static_assert(!kSingle || KVSTEPS == 1, "single-step units");
   griddep_wait();  // q, k and v come from the kernel before; earlier kernels may still read the slots
   griddep_launch();
   const int lane = threadIdx.x & 31;
@@ -186,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < p.units; u += warps) {
     // this lane's token, and its q head (the unit's first) or its block of heads and row of the block
     int64_t tok;
-    int32_t h0 = 0, blk = 0, base = 0;  // base: first row (of the warp's step) of the block
+    int32_t h0 = 0, blk = 0, skip = 0;  // skip: what a lane's row of the block is less than its row of the warp
     bool in = true, is_q;
     if constexpr (kFlat) {
       is_q = u < p.flat_q;
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
         in = i < static_cast<uint32_t>(p.bps) && t < p.tokens;
         tok = in ? t : 0;
         blk = in ? static_cast<int32_t>(g - t * p.sh.blocks) : 0;
-        base = i * n_rows;
+        skip = i * n_rows;
       }
     } else {
       tok = u / p.units_per_token;
@@ -209,6 +225,13 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
       is_q = part < p.q_units;
       h0 = part * kQSteps * kPerStep + row0;
       blk = part - p.q_units;
+    }
+    if constexpr (kSingle) {
+      if (p.spb > 1 && !is_q) {
+        const int32_t step = blk % p.spb;
+        blk /= p.spb;
+        skip = -step * kPerStep;
+      }
     }
     int64_t pos = __ldg(p.positions + tok);
     if (pos < 0 || pos >= p.max_position) {
@@ -254,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
     uint4 a[kKvSteps], b[kKvSteps];
 #pragma unroll
     for (int s = 0; s < kKvSteps; ++s) {
-      const int r = s * kPerStep + row0 - base;
+      const int r = s * kPerStep + row0 - skip;
       a[s] = b[s] = make_uint4(0, 0, 0, 0);
       if (in && r < n_rows) {
         const __nv_bfloat16* src =
@@ -272,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
     Angles<ROPE> an;
     load_angles<D, ROPE>(ang, p.rot, sub, an);
     const bool stored = in && slot >= 0 && slot < p.num_slots;
-    if (in && !stored && sub == 0 && row0 == base && blk == 0) flag_error(p.err, RA_DEVERR_SLOT);
+    if (in && !stored && sub == 0 && row0 == skip && blk == 0) flag_error(p.err, RA_DEVERR_SLOT);
     if (kFlat ? !__any_sync(0xffffffffu, stored) : !stored) continue;  // (warp-uniform)
     const bool is_v = row0 & 1;  // the same in every step: kPerStep is even
     uint8_t* rec = nullptr;
@@ -282,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
     uint32_t eb[kKvSteps];
 #pragma unroll
     for (int s = 0; s < kKvSteps; ++s) {
-      const int r = s * kPerStep + row0 - base;
+      const int r = s * kPerStep + row0 - skip;
       float x[2][8], y[2][8];
       unpack8(a[s], x[0]);
       unpack8(b[s], x[1]);
@@ -322,19 +345,31 @@ __global__ void __launch_bounds__(kThreads, QSTEPS <= 1 && KVSTEPS == 1 ? 3 : 2)
       }
     }
     if constexpr (KV8) {
-      const uint4 scales = gather_scale_bytes<kKvSteps, kPerStep, kLanes>(eb, n_rows, base);
-      uint4* tail = reinterpret_cast<uint4*>(rec + n_rows * D);
-      if (stored && row0 == base && sub == 0) tail[0] = scales;
-      if (stored && row0 == base && sub == 1 && blk == p.sh.blocks - 1 && p.sh.blocks * p.sh.block_bytes < p.sh.slot_bytes)
-        tail[1] = make_uint4(0, 0, 0, 0);  // the record's padding (16 bytes)
+      // the block's 16 bytes of scales, zero past its rows, and behind the last block the record's padding
+      uint8_t* tail = rec + n_rows * D;
+      bool last;
+      if (kSingle && p.spb > 1) {  // the block's rows are in several units: each row's lanes write its byte, the
+        const int r = row0 - skip;  // last row's the rest
+        last = stored && r == n_rows - 1;
+        if (stored && sub == 0 && r < n_rows) tail[r] = static_cast<uint8_t>(eb[0]);
+        if (last)
+          for (int i = n_rows + sub; i < 16; i += kLanes) tail[i] = 0;
+      } else {
+        const uint4 scales = gather_scale_bytes<kKvSteps, kPerStep, kLanes>(eb, n_rows, skip);
+        last = stored && row0 == skip;
+        if (last && sub == 0) *reinterpret_cast<uint4*>(tail) = scales;
+      }
+      if (last && sub == 1 && blk == p.sh.blocks - 1 && p.sh.blocks * p.sh.block_bytes < p.sh.slot_bytes)
+        reinterpret_cast<uint4*>(tail)[1] = make_uint4(0, 0, 0, 0);
     }
   }
 }
 
 template <int D, bool KV8, int QSTEPS, int KVSTEPS>
 ra_status launch(const NormRopeParams& p, bool interleaved, int grid, cudaStream_t s) {
-  auto kern = interleaved    ? qk_norm_rope_kernel<D, kAdjacent, KV8, QSTEPS, KVSTEPS>
-              : p.rot == D   ? qk_norm_rope_kernel<D, kHalfFull, KV8, QSTEPS, KVSTEPS>
+  auto kern = interleaved      ? qk_norm_rope_kernel<D, kAdjacent, KV8, QSTEPS, KVSTEPS>
+              : p.rot == D     ? qk_norm_rope_kernel<D, kHalfFull, KV8, QSTEPS, KVSTEPS>
+              : 2 * p.rot <= D ? qk_norm_rope_kernel<D, kHalfLow, KV8, QSTEPS, KVSTEPS>
                              : qk_norm_rope_kernel<D, kHalfPart, KV8, QSTEPS, KVSTEPS>;
   return launch_pdl("qk_norm_rope_kernel", kern, dim3(grid), dim3(kThreads), 0, s, p);
 }
@@ -347,8 +382,7 @@ ra_status launch_steps(const NormRopeParams& p, bool interleaved, Units units, b
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (units == kWide)
     return deep ? launch<D, KV8, kMost, kMost>(p, interleaved, grid, s) : launch<D, KV8, kMost, 1>(p, interleaved, grid, s);
-  if (units == kOneStep)
-    return deep ? launch<D, KV8, 1, kMost>(p, interleaved, grid, s) : launch<D, KV8, 1, 1>(p, interleaved, grid, s);
+  if (units == kOneStep) return launch<D, KV8, 1, 1>(p, interleaved, grid, s);
   return deep ? launch<D, KV8, 0, kMost>(p, interleaved, grid, s) : launch<D, KV8, 0, 1>(p, interleaved, grid, s);
 }
 
@@ -385,8 +419,10 @@ ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t n
   // Wide units of 16 q rows (4 KB of loads in flight per warp); where more than a quarter of the rows of a
   // token's last one were missing, flat units; and one step of one token for few tokens, where wide ones fill the
   // SMs' warps badly (a decode step of 64 has 1.6 warps per SM sub-partition with one step) and latency counts
-  // (64 tokens, 32/8 heads of 128: 2.55 us, 2.9 with flat units).  Measured with 4777 tokens: 8/2 heads of 64
-  // 7.4 us wide, 5.4 in single steps, 4.5 flat; 28/4 heads of 128 20.7 us wide, 28.0 flat; 12/3 heads 14.7 and 17.4.
+  // (64 tokens, 32/8 heads of 128: 2.0 us, 2.9 with flat units; 300 tokens 2.7 us, 4.3 with a K/V block's four
+  // steps in one unit; 500 tokens of 64/8 heads, above the limit: 5.4, 6.1 in single steps).  Measured with 4777
+  // tokens: 8/2 heads of 64 7.4 us wide, 5.4 in single steps, 4.5 flat; 28/4 heads of 128 20.7 us wide, 28.0 flat;
+  // 12/3 heads 14.7 and 17.4.
   const int32_t per_step = 32 / (head_dim / 16), n_rows = 2 * p.sh.hpc;
   const int64_t wide_units = num_tokens * ((p.hq + 15) / 16 + p.sh.blocks);
   const bool few = wide_units < static_cast<int64_t>(dev.num_sms) * 16;
@@ -394,8 +430,9 @@ ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t n
   // (flat units count rows in 32 bits)
   const bool countable = num_tokens * std::max(p.hq, p.sh.blocks) < int64_t(1) << 31;
   const Units units = few ? kOneStep : filled || !countable ? kWide : kFlatUnits;
-  const bool deep = n_rows > per_step;  // a K/V block takes more than one step
+  const bool deep = n_rows > per_step;  // a K/V block takes more than one step (of a unit, or a unit each)
   p.tokens = num_tokens;
+  p.spb = units == kOneStep ? (n_rows + per_step - 1) / per_step : 1;
   if (units == kFlatUnits) {
     p.bps = deep ? 1 : per_step / n_rows;
     p.flat_q = (num_tokens * p.hq + per_step - 1) / per_step;
@@ -403,7 +440,7 @@ ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t n
   } else {
     const int32_t q_rows = units == kWide ? 16 : per_step;
     p.q_units = (p.hq + q_rows - 1) / q_rows;
-    p.units_per_token = p.q_units + p.sh.blocks;
+    p.units_per_token = p.q_units + p.sh.blocks * p.spb;
     p.units = num_tokens * p.units_per_token;
   }
   const int64_t want = (p.units + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(dev.num_sms) * 8;

@@ -351,9 +351,9 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
 
 }  // namespace
 
-// 32-key slabs where two of them fit the ring, else 16-key ones (64 x 8 tokens over 512..4096 keys: 16/16 heads of
-// 64, where one fits, 118.6 and 106.5 us; 12/12, where two do, 84.6 and 87.3;
-// 5/5 heads of 128, two, 77.2 and 81.8).
+// 32-key slabs where two of them fit the ring, else 16-key ones (64 x 8 tokens over 512..4096 keys, 32- and 16-key
+// slabs: 16/16 heads of 64, where one fits, 118.3 and 106.5 us; 12/12, where two do, 84.6 and 87.3; 5/5 heads of
+// 128, two, 77.2 and 81.8).
 ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, bool small, const DeviceInfo& dev, cudaStream_t s) {
   const bool wide = 2 * stage_bytes(p.sh.hpc, head_dim, 32) <= ring_bytes(p.sh.per_sm);
   if (head_dim == 64 && wide) return small ? launch<64, 32, true>(p, dev, s) : launch<64, 32, false>(p, dev, s);
