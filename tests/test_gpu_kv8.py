@@ -104,6 +104,40 @@ def test_bad_slots_are_flagged_and_skipped():
     assert np.array_equal(f64(k2)[[0, 2]], rk[[0, 0]]) and not f64(k2)[[1, 3]].any()
 
 
+@pytest.mark.parametrize("hkv,d", SHAPES + [(4, 128), (6, 128), (7, 64)])
+def test_many_tokens_with_special_values_and_bad_slots(hkv, d):
+    """Enough tokens that a warp takes whole blocks, or several of them, at once; the last ones leave it part empty."""
+    n = 2501
+    rng = np.random.default_rng(hkv + d)
+    k, v = rows(rng, n, hkv, d), rows(rng, n, hkv, d)
+    k[3, 0, :3] = torch.tensor([float("inf"), 1.0, float("nan")]).to(BF)
+    v[n - 1, hkv - 1, :2] = torch.tensor([float("-inf"), 0.25]).to(BF)
+    k[7], v[8, 0] = 0, float("inf")
+    S = n + 5
+    loc = rng.permutation(S)[:n]
+    bad = np.sort(rng.permutation(n)[:150])
+    at = loc.copy()
+    at[bad] = np.where(np.arange(150) % 2, -1, S)
+    good = np.setdiff1d(np.arange(n), bad)
+    pool = torch.full((S, ra.ra_kv8_slot_bytes(hkv, d)), 0xAB, dtype=torch.uint8, device=DEV)
+    err = err_word()
+    ra.ra_kv8_store(pool, k, v, i32(at), device_error=err)
+    assert int(err.item()) == ra.DEVERR_SLOT
+    got = pool.cpu().numpy()
+    exp = R.pack(f64(k), f64(v))
+    assert np.array_equal(got[loc[good]], exp[good])
+    assert np.all(got[np.setdiff1d(np.arange(S), loc[good])] == 0xAB)
+    pool = gpu(np.where(np.isin(np.arange(S), loc[good])[:, None], got, 0))
+    err.zero_()
+    k2, v2 = torch.full_like(k, 7), torch.full_like(v, 7)
+    ra.ra_kv8_load(pool, i32(loc[good]), k2[:len(good)], v2[:len(good)], device_error=err)
+    rk, rv = R.unpack(exp[good], hkv, d)
+    assert int(err.item()) == 0
+    assert np.array_equal(f64(k2)[:len(good)], rk, equal_nan=True)
+    assert np.array_equal(f64(v2)[:len(good)], rv, equal_nan=True)
+    assert (k2[len(good):] == 7).all() and (v2[len(good):] == 7).all()
+
+
 def decode_case(rng, lens, hq, hkv, d, spread=6, share=0):
     """A pool of quantised rows, a table over shuffled slots (the first `share` positions common to all
     requests), queries; records outside the contexts hold NaN codes."""
