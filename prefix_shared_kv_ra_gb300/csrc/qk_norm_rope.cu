@@ -420,12 +420,11 @@ ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t n
   // token's last one were missing, flat units; and one step of one token for few tokens, where wide ones fill the
   // SMs' warps badly (a decode step of 64 has 1.6 warps per SM sub-partition with one step) and latency counts
   // (64 tokens, 32/8 heads of 128: 2.0 us, 2.9 with flat units; 300 tokens 2.7 us, 4.3 with a K/V block's four
-  // steps in one unit; 500 tokens of 64/8 heads, above the limit: 5.4, 6.1 in single steps).  Measured with 4777
-  // tokens: 8/2 heads of 64 7.4 us wide, 5.4 in single steps, 4.5 flat; 28/4 heads of 128 20.7 us wide, 28.0 flat;
-  // 12/3 heads 14.7 and 17.4.
+  // steps in one unit; 806 tokens, above the limit, 3.8 us, 5.7 in single steps).  Measured with 9437 tokens: 12/3
+  // heads of 128 21.8 us wide, 27.8 flat; 8/1 heads 13.4 us flat, 16.4 in single steps.
   const int32_t per_step = 32 / (head_dim / 16), n_rows = 2 * p.sh.hpc;
   const int64_t wide_units = num_tokens * ((p.hq + 15) / 16 + p.sh.blocks);
-  const bool few = wide_units < static_cast<int64_t>(dev.num_sms) * 16;
+  const bool few = wide_units < static_cast<int64_t>(dev.num_sms) * 8;
   const bool filled = 4 * p.hq >= 48 * ((p.hq + 15) / 16);
   // (flat units count rows in 32 bits)
   const bool countable = num_tokens * std::max(p.hq, p.sh.blocks) < int64_t(1) << 31;
@@ -443,7 +442,10 @@ ra_status norm_rope_call(NormRopeParams p, bool kv8, int32_t head_dim, int64_t n
     p.units_per_token = p.q_units + p.sh.blocks * p.spb;
     p.units = num_tokens * p.units_per_token;
   }
-  const int64_t want = (p.units + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(dev.num_sms) * 8;
+  // Loops of as many CTAs as are resident (9437 tokens, 64/8 heads: 61.5 us, 62.9 with a second, partial wave,
+  // 71.5 with a unit per warp); single steps run in waves of CTAs (300 tokens, 32/8 heads: 2.75 us, 3.7 with loops).
+  const int64_t want = (p.units + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t cap = static_cast<int64_t>(dev.num_sms) * (units == kOneStep ? 8 : units == kFlatUnits && !deep ? 3 : 2);
   const int grid = static_cast<int>(want < cap ? want : cap);
   return head_dim == 128 ? (kv8 ? launch_steps<128, true>(p, interleaved, units, deep, grid, stream)
                                 : launch_steps<128, false>(p, interleaved, units, deep, grid, stream))
