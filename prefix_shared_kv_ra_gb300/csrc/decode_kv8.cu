@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
 //  * many rows: 8 lanes per row, a warp's four rows at once (224 requests of 64 heads: the call ends 12 us after
 //    its last item with a row per warp, one after the other);
 //  * few rows: `per_row` warps share one, each a part of its partials (32 rows of 108 partials: 18 us with
-//    one warp each, 5 us with eight).
+//    one warp each, 5 us with eight; 73 requests of 64 heads, up to 43 partials a row: 41.5 us with 8 lanes per
+//    row, 36.9 with a warp).
 constexpr int kCombineWarps = 8;
 constexpr int kRowLanes = 8;
 constexpr int kRowsPerWarp = 32 / kRowLanes;
@@ -524,10 +525,10 @@ ra_status launch(Kv8DecodeParams& pp, int32_t per_sm, int smem, const DeviceInfo
     if (ra_status st = launch_decode<D, false>(pp, static_cast<int>(n_items < ctas ? n_items : ctas), smem, dev, s))
       return st;
   }
-  // few rows: as many warps per row as three CTAs per SM hold
+  // few rows: as many warps per row as three CTAs per SM hold, or one while four hold all rows
   int per_row = 1;
   while (per_row < kCombineWarps && rows * per_row * 2 <= warps) per_row *= 2;
-  if (per_row > 1 || small) {
+  if (per_row > 1 || small || rows <= static_cast<int64_t>(dev.num_sms) * 4 * kCombineWarps) {
     const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
     return launch_pdl("kv8_combine_few_kernel", small ? kv8_combine_few_kernel<D, true> : kv8_combine_few_kernel<D, false>,
                       dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row, pp.ctas);
