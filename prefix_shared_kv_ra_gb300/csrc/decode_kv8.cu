@@ -38,9 +38,14 @@ namespace ra {
 namespace {
 
 // Keys per ring stage.  A consumer warp's chain of loads, scores, softmax and product takes about as long for a
-// slab of either size, so heads of 64 get the longer one (150 requests of 1000..9000 keys, 8/8 heads: 170 us with
-// 32, 136 with 64).
-constexpr int slab_of(int head_dim) { return head_dim == 128 ? 32 : 64; }
+// slab of either size, so heads of 64 and groups of few heads get the longer one (150 requests of 1000..9000 keys:
+// 8/8 heads of 64 170 us with 32, 136 with 64; 16/4 heads of 128 166 and 136).  Heads of 128 need 160 registers
+// for it, so larger groups keep the short one, and so do the ones of which two CTAs share an SM.
+constexpr int kFewHeads = 4;
+constexpr int ctas_per_sm(int head_dim, int hpc) { return hpc <= (head_dim == 64 ? 3 : 2) ? 2 : 1; }
+constexpr int slab_of(int head_dim, int hpc) {
+  return head_dim == 64 || (hpc <= kFewHeads && ctas_per_sm(head_dim, hpc) == 1) ? 64 : 32;
+}
 constexpr float kRescale = 8.0f;   // log2 units: a reference moves when a score exceeds it by more
 constexpr int kQExp = 14;          // q's largest value in f16
 
@@ -153,11 +158,10 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
 
 // Warp roles: hpc consumer warps (one kv head each), the ring's copy warps, and a signal warp that counts each
 // request's finished partials for the combine and frees the item entries.
-template <int D, bool SMALL>
-__global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1)
+template <int D, int kSlab, bool SMALL>
+__global__ void __launch_bounds__(32 * ((D == 128 && kSlab == 64 ? kFewHeads : kMaxHeadsPerCta) + kRingProducers + 1), 1)
     kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams pp) {
   const DecodeParams& p = pp.d;
-  constexpr int kSlab = slab_of(D);
   constexpr int KW = D / 16;  // words of a K row per lane = MMA k steps of the scores
   constexpr int VW = D / 32;  // words of a V row per lane
   constexpr int MT = D / 16;  // MMA m tiles of O^T
@@ -498,9 +502,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(con
   griddep_wait();  // this grid's completion implies the decode kernel's
 }
 
-template <int D, bool SMALL>
+template <int D, int SLAB, bool SMALL>
 ra_status launch_decode(const Kv8DecodeParams& pp, int grid, int smem, const DeviceInfo& dev, cudaStream_t stream) {
-  auto kern = kv8_decode_kernel<D, SMALL>;
+  auto kern = kv8_decode_kernel<D, SLAB, SMALL>;
   static bool configured[64] = {};
   if (!configured[dev.device]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmemLimit);
@@ -510,25 +514,26 @@ ra_status launch_decode(const Kv8DecodeParams& pp, int grid, int smem, const Dev
   return launch_pdl("kv8_decode_kernel", kern, dim3(grid), dim3(32 * (pp.d.hpc + kRingProducers + 1)), smem, stream, pp);
 }
 
-template <int D>
+template <int D, int SLAB>
 ra_status launch(Kv8DecodeParams& pp, int32_t per_sm, int smem, const DeviceInfo& dev, cudaStream_t s) {
   DecodeParams& p = pp.d;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.hq, warps = static_cast<int64_t>(dev.num_sms) * 3 * kCombineWarps;
   const bool small = small_call(p.batch, p.max_seq_len, p.n_hgroups, per_sm);
   if (small) {
     pp.ctas = kSmallSms * per_sm;
-    if (ra_status st = launch_decode<D, true>(pp, pp.ctas, smem, dev, s)) return st;
+    if (ra_status st = launch_decode<D, SLAB, true>(pp, pp.ctas, smem, dev, s)) return st;
   } else {
     if (ra_status st = launch_decode_plan(p, 0, s)) return st;
     const int64_t n_items = static_cast<int64_t>(p.max_items) * p.n_hgroups;  // bound of the claims
     const int64_t ctas = static_cast<int64_t>(dev.num_sms) * per_sm;
-    if (ra_status st = launch_decode<D, false>(pp, static_cast<int>(n_items < ctas ? n_items : ctas), smem, dev, s))
+    if (ra_status st = launch_decode<D, SLAB, false>(pp, static_cast<int>(n_items < ctas ? n_items : ctas), smem, dev, s))
       return st;
   }
-  // few rows: as many warps per row as three CTAs per SM hold, or one while four hold all rows
+  // few rows: as many warps per row as three CTAs per SM hold, or one up to 32 rows per SM (101
+  // requests of 64 heads: 20.4 us with 8 lanes per row, 23.3 with a warp)
   int per_row = 1;
   while (per_row < kCombineWarps && rows * per_row * 2 <= warps) per_row *= 2;
-  if (per_row > 1 || small || rows <= static_cast<int64_t>(dev.num_sms) * 4 * kCombineWarps) {
+  if (per_row > 1 || small || rows <= static_cast<int64_t>(dev.num_sms) * 32) {
     const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
     return launch_pdl("kv8_combine_few_kernel", small ? kv8_combine_few_kernel<D, true> : kv8_combine_few_kernel<D, false>,
                       dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row, pp.ctas);
@@ -602,19 +607,22 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   p.batch = batch;
   p.max_seq_len = max_seq_len;
   p.min_chunk = 64;
-  p.chunk_align = slab_of(head_dim);
+  const int slab = slab_of(head_dim, sh.hpc);
+  p.chunk_align = slab;
   p.err = device_error;
   bind_decode_workspace(p, wl, pl, workspace);
   p.hpc = sh.hpc;
   p.n_hgroups = sh.blocks;
   p.row_stride = sh.block_bytes;
-  p.stage_bytes = slab_of(head_dim) * p.row_stride;
+  p.stage_bytes = slab * p.row_stride;
   // A CTA of few heads waits on its own chain of slab, scores, softmax and product: two share an SM where their
-  // registers fit (8 warps of 128 registers each).
-  const int per_sm = sh.hpc <= 3 ? 2 : 1;
+  // registers fit (8 warps of 128 registers each; 3 heads of 128 gain more from 64-key slabs: 150 requests of
+  // 1000..9000 keys, 12/3 heads 125 us as two CTAs, 116 as one; 1 head: 64 requests 47.8 and 53.6).
+  const int per_sm = ctas_per_sm(head_dim, sh.hpc);
   p.nstage = (kRingSmemLimit / per_sm - 1024 - kRingHdrBytes) / p.stage_bytes;  // (1 KB per CTA is the system's)
   if (p.nstage > kRingMaxStages) p.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + p.nstage * p.stage_bytes;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return head_dim == 128 ? launch<128>(pp, per_sm, smem, dev, s) : launch<64>(pp, per_sm, smem, dev, s);
+  if (head_dim == 64) return launch<64, 64>(pp, per_sm, smem, dev, s);
+  return slab == 64 ? launch<128, 64>(pp, per_sm, smem, dev, s) : launch<128, 32>(pp, per_sm, smem, dev, s);
 }

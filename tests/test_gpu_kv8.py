@@ -185,6 +185,8 @@ DECODE = [
     ([1], 8, 2, 64), ([1, 2, 3], 32, 8, 128), ([15, 16, 17, 31, 32, 33], 32, 8, 128), ([129, 128, 127], 64, 8, 128),
     ([1500], 32, 8, 128), ([700, 1, 2049, 64, 333], 16, 16, 128), ([513, 90], 12, 3, 128), ([260, 77], 5, 5, 64),
     ([100, 1000], 40, 20, 64), ([37, 512], 8, 1, 128), ([250], 11, 11, 64), ([640, 3], 24, 12, 128),
+    ([1, 63, 64, 65, 1000, 5], 12, 3, 128), ([127, 128, 129, 2500], 32, 4, 128), (list(range(5, 900, 20)), 12, 3, 128),
+    (list(range(1, 1300, 29)), 16, 4, 128), (list(range(5, 900, 20)), 4, 2, 128),
 ]
 
 
