@@ -57,25 +57,28 @@ struct Kv8DecodeParams {
   int32_t ctas;  // small call: the grid
 };
 constexpr int kSmallLeast = 2;  // units of a small call's shortest piece
+constexpr int kSmallMany = 32;  // small_call's bound for more than 32 requests
 
-// The items of a call: the plan kernel's list, or (SMALL) this warp's own plan.
-template <bool SMALL>
+// The items of a call: the plan kernel's list, or (SMALL = 1 or 2 requests per lane) this warp's own plan.
+template <int SMALL>
 struct Kv8Items {
   const DecodeParams& p;
-  SmallPlan plan;
-  int32_t len, row;  // SMALL: of this lane's request
+  SmallPlan<SMALL ? SMALL : 1> plan;
+  PerRequest<SMALL ? SMALL : 1> len, row;
 
-  __device__ __forceinline__ Kv8Items(const DecodeParams& q, int32_t ctas, bool report) : p(q), len(0), row(0) {
+  __device__ __forceinline__ Kv8Items(const DecodeParams& q, int32_t ctas, bool report) : p(q) {
     if constexpr (SMALL) {
-      const int lane = threadIdx.x & 31;
-      if (lane < p.batch) {
-        row = __ldg(p.rpi + lane);
-        len = __ldg(p.seq_lens + lane);
-        const bool bad_row = row < 0 || row >= p.table_rows, bad_len = len < 1 || len > p.max_seq_len;
+      auto request = [&](int32_t b, int32_t& l, int32_t& r) {
+        if (b >= p.batch) return;
+        r = __ldg(p.rpi + b);
+        l = __ldg(p.seq_lens + b);
+        const bool bad_row = r < 0 || r >= p.table_rows, bad_len = l < 1 || l > p.max_seq_len;
         if (report && bad_row) flag_error(p.err, RA_DEVERR_TABLE);
         else if (report && bad_len) flag_error(p.err, RA_DEVERR_LENGTH);
-        len = bad_row || len < 1 ? 0 : min(len, p.max_seq_len);
-      }
+        l = bad_row || l < 1 ? 0 : min(l, p.max_seq_len);
+      };
+#pragma unroll
+      for (int i = 0; i < SMALL; ++i) request(static_cast<int32_t>(threadIdx.x & 31) + 32 * i, len.v[i], row.v[i]);
       plan.make(len, p.n_hgroups, ctas, kSmallLeast);
     }
   }
@@ -86,12 +89,12 @@ struct Kv8Items {
       it.hg = idx % p.n_hgroups;
       it.d = idx / p.n_hgroups;
       it.b = plan.request(it.d);
-      it.split = it.d - of_lane(plan.first, it.b);
-      it.n_splits = of_lane(plan.pieces, it.b);
-      it.row = of_lane(row, it.b);
+      it.split = it.d - of_request(plan.first, it.b);
+      it.n_splits = of_request(plan.pieces, it.b);
+      it.row = of_request(row, it.b);
       it.start = 0;
       it.k0 = it.split * plan.chunk;
-      it.k1 = min(of_lane(len, it.b), it.k0 + plan.chunk);
+      it.k1 = min(of_request(len, it.b), it.k0 + plan.chunk);
     } else {
       decode_item(p, idx, it);
     }
@@ -99,7 +102,7 @@ struct Kv8Items {
 };
 
 // The producers' view: one bulk copy per key, the head group's block of the slot's record.
-template <bool SMALL>
+template <int SMALL>
 struct Kv8Source {
   const Kv8DecodeParams& pp;
   const Kv8Items<SMALL>& items;
@@ -158,7 +161,7 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
 
 // Warp roles: hpc consumer warps (one kv head each), the ring's copy warps, and a signal warp that counts each
 // request's finished partials for the combine and frees the item entries.
-template <int D, int kSlab, bool SMALL>
+template <int D, int kSlab, int SMALL>
 __global__ void __launch_bounds__(32 * ((D == 128 && kSlab == 64 ? kFewHeads : kMaxHeadsPerCta) + kRingProducers + 1), 1)
     kv8_decode_kernel(const __grid_constant__ Kv8DecodeParams pp) {
   const DecodeParams& p = pp.d;
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_kernel(const _
   griddep_wait();  // this grid's completion implies the decode kernel's
 }
 
-template <int D, bool SMALL>
+template <int D, int SMALL>
 __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(const __grid_constant__ DecodeParams p,
                                                                              int per_row, int32_t ctas) {
   constexpr int V = D / 32;
@@ -471,9 +474,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(con
   int32_t i0, n;
   if constexpr (SMALL) {
     // (the lengths were complete before the decode kernel let this one launch)
-    const Kv8Items<true> items(p, ctas, false);
-    i0 = of_lane(items.plan.first, b);
-    n = of_lane(items.plan.pieces, b);
+    const Kv8Items<SMALL> items(p, ctas, false);
+    i0 = of_request(items.plan.first, b);
+    n = of_request(items.plan.pieces, b);
     if (!in || n <= 1) n = 0;  // written directly, or invalid
     griddep_wait();
   } else {
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine_few_kernel(con
   griddep_wait();  // this grid's completion implies the decode kernel's
 }
 
-template <int D, int SLAB, bool SMALL>
+template <int D, int SLAB, int SMALL>
 ra_status launch_decode(const Kv8DecodeParams& pp, int grid, int smem, const DeviceInfo& dev, cudaStream_t stream) {
   auto kern = kv8_decode_kernel<D, SLAB, SMALL>;
   static bool configured[64] = {};
@@ -518,15 +521,17 @@ template <int D, int SLAB>
 ra_status launch(Kv8DecodeParams& pp, int32_t per_sm, int smem, const DeviceInfo& dev, cudaStream_t s) {
   DecodeParams& p = pp.d;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.hq, warps = static_cast<int64_t>(dev.num_sms) * 3 * kCombineWarps;
-  const bool small = small_call(p.batch, p.max_seq_len, p.n_hgroups, per_sm);
+  const bool small = small_call(p.batch, p.max_seq_len, p.n_hgroups, per_sm, kSmallMany), many = p.batch > 32;
   if (small) {
     pp.ctas = kSmallSms * per_sm;
-    if (ra_status st = launch_decode<D, SLAB, true>(pp, pp.ctas, smem, dev, s)) return st;
+    if (ra_status st = many ? launch_decode<D, SLAB, 2>(pp, pp.ctas, smem, dev, s)
+                            : launch_decode<D, SLAB, 1>(pp, pp.ctas, smem, dev, s))
+      return st;
   } else {
     if (ra_status st = launch_decode_plan(p, 0, s)) return st;
     const int64_t n_items = static_cast<int64_t>(p.max_items) * p.n_hgroups;  // bound of the claims
     const int64_t ctas = static_cast<int64_t>(dev.num_sms) * per_sm;
-    if (ra_status st = launch_decode<D, SLAB, false>(pp, static_cast<int>(n_items < ctas ? n_items : ctas), smem, dev, s))
+    if (ra_status st = launch_decode<D, SLAB, 0>(pp, static_cast<int>(n_items < ctas ? n_items : ctas), smem, dev, s))
       return st;
   }
   // few rows: as many warps per row as three CTAs per SM hold, or one up to 32 rows per SM (101
@@ -535,7 +540,8 @@ ra_status launch(Kv8DecodeParams& pp, int32_t per_sm, int smem, const DeviceInfo
   while (per_row < kCombineWarps && rows * per_row * 2 <= warps) per_row *= 2;
   if (per_row > 1 || small || rows <= static_cast<int64_t>(dev.num_sms) * 32) {
     const int64_t ctas = (rows * per_row + kCombineWarps - 1) / kCombineWarps;
-    return launch_pdl("kv8_combine_few_kernel", small ? kv8_combine_few_kernel<D, true> : kv8_combine_few_kernel<D, false>,
+    auto kern = !small ? kv8_combine_few_kernel<D, 0> : many ? kv8_combine_few_kernel<D, 2> : kv8_combine_few_kernel<D, 1>;
+    return launch_pdl("kv8_combine_few_kernel", kern,
                       dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps), 0, s, p, per_row, pp.ctas);
   }
   const int64_t per_cta = kCombineWarps * kRowsPerWarp;

@@ -1,7 +1,7 @@
 // small_plan.cuh -- the split of a small batch's key ranges, made by every warp for itself.
 //
 // A call of few requests and keys is over in a few microseconds, of which a planning kernel took three.  With at
-// most 32 requests a warp holds one per lane: it reads their lengths, finds the piece length for which all pieces
+// most 64 requests a warp holds one or two per lane: it reads their lengths, finds the piece length for which all pieces
 // of all head groups fit the grid at once (one per CTA: no claims, no counters), and looks items up by shuffles.
 // Every warp of the attention and merge kernels repeats this on the same inputs and gets the same split.
 #pragma once
@@ -10,7 +10,7 @@
 
 namespace ra {
 
-constexpr int kSmallBatch = 32;
+constexpr int kSmallBatch = 64;
 constexpr int kSmallUnit = 32;    // keys per unit
 constexpr int kSmallRounds = 48;  // mean units per CTA, at the host's bounds, up to which a call is small
 constexpr int kSmallSms = 152;    // GB300; a constant, so that host and device agree
@@ -20,46 +20,80 @@ constexpr int kSmallSms = 152;    // GB300; a constant, so that host and device 
 // the longest) below what the planning kernel costs.  Measured, planning kernel and small call, at their mean
 // units: quantised decode of 16 requests of 512..4096 keys (13) 25.9 and 20.6 us, of 1000..13700 (45) 50.9 and
 // 46.4, of 30 of 13000..13700 (85) 137.4 and 137.1; 16 x 4..8 drafted tokens over 512..4096 keys (27) 40.9 and
-// 36.5, 30 x 4..8 (51) 62.9 and 65.5.
-inline bool small_call(int64_t batch, int64_t max_keys, int64_t heads, int64_t per_sm) {
+// 36.5, 30 x 4..8 (51) 62.9 and 65.5.  With more than 32 requests the pieces are coarser and the bound, `many`, is
+// lower: quantised decode of 64 requests of 200..1000 keys (13) 25.9 and 22.5, of 500..2000 (27) 38.2 and 37.5, of
+// 500..3000 of 4 heads (40) 31.0 and 31.3; 64 x 4..7 drafted tokens over 100..1000 keys (13) 27.5 and 22.9, over
+// 1000..2000 (27) 43.4 and 44.2.
+inline bool small_call(int64_t batch, int64_t max_keys, int64_t heads, int64_t per_sm, int64_t many) {
   const int64_t ctas = kSmallSms * per_sm;
   return batch <= kSmallBatch && 2 * batch * heads <= ctas &&
-         batch * ((max_keys + kSmallUnit - 1) / kSmallUnit) * heads <= kSmallRounds * ctas;
+         batch * ((max_keys + kSmallUnit - 1) / kSmallUnit) * heads <= (batch <= 32 ? kSmallRounds : many) * ctas;
 }
 
-struct SmallPlan {
-  int32_t pieces;  // of this lane's request
-  int32_t first;   // its first piece
-  int32_t chunk;   // keys per piece
-  int32_t n;       // pieces of all requests
+// A lane's values of request `lane` (N = 1), or of `lane` and `lane` + 32 (N = 2: for 33 requests or more).
+template <int N>
+struct PerRequest {
+  int32_t v[N] = {};
+};
+// The value of request r (the same for the whole warp).
+template <int N>
+__device__ __forceinline__ int32_t of_request(const PerRequest<N>& x, int32_t r) {
+  return __shfl_sync(0xffffffffu, N == 1 || r < 32 ? x.v[0] : x.v[N - 1], r & 31);
+}
 
-  // keys: of this lane's request (0: none).  Warp-collective, as all members.
-  __device__ __forceinline__ void make(int32_t keys, int32_t heads, int32_t ctas, int32_t least) {
-    const int lane = threadIdx.x & 31;
-    const int32_t units = (keys + kSmallUnit - 1) / kSmallUnit;
-    const int32_t all = __reduce_add_sync(0xffffffffu, units) * heads;
+template <int N>
+struct SmallPlan {
+  PerRequest<N> pieces;
+  PerRequest<N> first;  // the request's first piece
+  int32_t chunk;     // keys per piece
+  int32_t n;         // pieces of all requests
+
+  // keys: of the requests (0: none).  Warp-collective, as all members.
+  __device__ __forceinline__ void make(const PerRequest<N>& keys, int32_t heads, int32_t ctas, int32_t least) {
+    PerRequest<N> units;
+    int32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      units.v[i] = (keys.v[i] + kSmallUnit - 1) / kSmallUnit;
+      all += units.v[i];
+    }
+    all = __reduce_add_sync(0xffffffffu, all) * heads;
     int32_t c = max(least, (all + ctas - 1) / ctas);
     for (;;) {
-      pieces = (units + c - 1) / c;
-      n = __reduce_add_sync(0xffffffffu, pieces);
+      n = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) n += pieces.v[i] = (units.v[i] + c - 1) / c;
+      n = __reduce_add_sync(0xffffffffu, n);
       if (n * heads <= ctas) break;  // (at the latest with one piece per request)
       c += max(1, c >> 4);
     }
     chunk = c * kSmallUnit;
-    first = pieces;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, first, off);
-      if (lane >= off) first += y;
-    }
-    first -= pieces;
+    first.v[0] = before(pieces.v[0]);
+    if constexpr (N == 2)
+      first.v[1] = before(pieces.v[1]) + __shfl_sync(0xffffffffu, first.v[0] + pieces.v[0], 31);
   }
   // The request of piece d < n.
   __device__ __forceinline__ int32_t request(int32_t d) const {
-    return 31 - __clz(__ballot_sync(0xffffffffu, pieces > 0 && first <= d));
+    const uint32_t lo = __ballot_sync(0xffffffffu, pieces.v[0] > 0 && first.v[0] <= d);
+    if constexpr (N == 2) {
+      const uint32_t hi = __ballot_sync(0xffffffffu, pieces.v[1] > 0 && first.v[1] <= d);
+      if (hi) return 63 - __clz(hi);
+    }
+    return 31 - __clz(lo);
+  }
+
+ private:
+  // Sum of x over the lanes below.
+  static __device__ __forceinline__ int32_t before(int32_t x) {
+    const int lane = threadIdx.x & 31;
+    int32_t sum = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += y;
+    }
+    return sum - x;
   }
 };
-
-__device__ __forceinline__ int32_t of_lane(int32_t x, int32_t lane) { return __shfl_sync(0xffffffffu, x, lane); }
 
 }  // namespace ra

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 // The merge of a small narrow call: a unit is kMergeWarps / `per_row` rows (request, kv head, row), of every
 // request, `per_row` warps each taking a share of a row's partials.  A row whose request is one piece was written
 // directly; a row of a marked (request, kv head) is recomputed by its first warp.
-template <int D>
+template <int D, int N>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const __grid_constant__ TreeParams p,
                                                                          int per_row) {
   constexpr int V = D / 32;
@@ -372,17 +372,17 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const _
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = warp % per_row;
-  const TreeSmall small(p, kTreeSms * p.sh.per_sm, false);  // (the inputs were complete before the attention kernel
+  const TreeSmall<N> small(p, kTreeSms * p.sh.per_sm, false);  // (the inputs were complete before the attention kernel
                                                             // let this one launch)
   const int32_t rows = p.hkv * p.ws.part_rows;
   const int32_t flat = static_cast<int32_t>(blockIdx.x) * (kMergeWarps / per_row) + warp / per_row;
   const bool in = flat < p.batch * p.sh.q_tiles * rows;
   const int32_t tile = in ? flat / rows : 0, kh = in ? (flat - tile * rows) / p.ws.part_rows : 0;  // of a request
   const int32_t r = in ? flat - tile * rows - kh * p.ws.part_rows : 0;
-  const int32_t P = of_lane(small.P, tile), T = of_lane(small.T, tile), q0 = of_lane(small.q0, tile);
-  const int32_t n = of_lane(small.plan.pieces, tile), first = of_lane(small.plan.first, tile);
+  const int32_t P = of_request(small.P, tile), T = of_request(small.T, tile), q0 = of_request(small.q0, tile);
+  const int32_t n = of_request(small.plan.pieces, tile), first = of_request(small.plan.first, tile);
   const int32_t tok = r / p.group;
-  const bool live = in && tok < of_lane(small.tokens, tile);
+  const bool live = in && tok < of_request(small.tokens, tile);
   const int64_t row = static_cast<int64_t>(q0) + tok;
   __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D;
   const int64_t slot_rows = static_cast<int64_t>(p.hkv) * p.ws.part_rows;  // rows between partial slots
@@ -456,20 +456,26 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
   return launch_pdl("attn_tc_kernel<tree>", kern, dim3(grid), dim3(tc::kThreads), L::kDynSmem, s, tp, qmap, kmap, vmap);
 }
 
-bool tree_small(const TreeShape& sh, int32_t batch, int32_t max_prefix, int32_t max_draft) {
-  return sh.narrow && small_call(static_cast<int64_t>(batch) * sh.q_tiles, static_cast<int64_t>(max_prefix) + max_draft,
-                                 sh.heads, sh.per_sm);
+// 0: the plan kernel's list; 1 or 2: a small call, of so many query tiles per lane.  (Requests in several narrow
+// items only up to 32 of these: 16 x 50..100 tokens of 8/8 heads of 64, 64 items 28.1 us, wide 16.2.)
+int tree_small(const TreeShape& sh, int32_t batch, int32_t max_prefix, int32_t max_draft) {
+  const int64_t tiles = static_cast<int64_t>(batch) * sh.q_tiles;
+  if (!sh.narrow || (sh.q_tiles > 1 && tiles > 32) ||
+      !small_call(tiles, static_cast<int64_t>(max_prefix) + max_draft, sh.heads, sh.per_sm, kTreeSmallMany))
+    return 0;
+  return tiles <= 32 ? 1 : 2;
 }
 
 ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& dev, cudaStream_t s) {
-  if (tree_small(p.sh, p.batch, p.max_prefix, p.max_draft)) {
-    if (ra_status st = launch_tree_narrow(p, head_dim, true, dev, s)) return st;
+  if (const int small = tree_small(p.sh, p.batch, p.max_prefix, p.max_draft)) {
+    if (ra_status st = launch_tree_narrow(p, head_dim, small, dev, s)) return st;
     const int64_t rows = static_cast<int64_t>(p.batch) * p.sh.q_tiles * p.hkv * p.ws.part_rows;
     int per_row = 1;
     while (per_row < kMergeWarps && rows * per_row * 2 <= static_cast<int64_t>(dev.num_sms) * 3 * kMergeWarps) per_row *= 2;
     const int64_t ctas = (rows * per_row + kMergeWarps - 1) / kMergeWarps;
-    return launch_pdl("tree_merge_small_kernel", head_dim == 128 ? tree_merge_small_kernel<128> : tree_merge_small_kernel<64>,
-                      dim3(static_cast<unsigned>(ctas)), dim3(kMergeThreads), 0, s, p, per_row);
+    auto kern = head_dim == 128 ? (small == 1 ? tree_merge_small_kernel<128, 1> : tree_merge_small_kernel<128, 2>)
+                                : (small == 1 ? tree_merge_small_kernel<64, 1> : tree_merge_small_kernel<64, 2>);
+    return launch_pdl("tree_merge_small_kernel", kern, dim3(static_cast<unsigned>(ctas)), dim3(kMergeThreads), 0, s, p, per_row);
   }
   // the list kernel: one CTA for the list, and (wide) one per request, at most the other SMs, for the scan of V
   const int scan = p.sh.narrow ? 0 : p.batch < dev.num_sms - 1 ? p.batch : dev.num_sms - 1;
@@ -477,7 +483,7 @@ ra_status launch_tree(const TreeParams& p, int32_t head_dim, const DeviceInfo& d
                                 head_dim))
     return st;
   if (p.sh.narrow) {
-    if (ra_status st = launch_tree_narrow(p, head_dim, false, dev, s)) return st;
+    if (ra_status st = launch_tree_narrow(p, head_dim, 0, dev, s)) return st;
   } else {
     const bool one_tile = p.max_draft * p.group <= tc::kRows;  // every item's rows fit one query tile
     if (ra_status st = head_dim == 128 ? (one_tile ? launch_wide<128, kTreeDualPass>(p, s, dev) : launch_wide<128, kTreePass>(p, s, dev))

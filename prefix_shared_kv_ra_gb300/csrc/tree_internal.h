@@ -14,6 +14,7 @@ namespace ra {
 
 constexpr int kTreeSms = 152;        // GB300; a constant, so that the workspace does not depend on the device
 constexpr int kTreeSmallLeast = 2;   // units of a small call's shortest piece
+constexpr int kTreeSmallMany = 16;   // small_call's bound for more than 32 requests
 constexpr int kTreeNarrowRows = 32;  // rows (drafted tokens x GQA group) of a narrow item
 constexpr int kTreeTiledRows = 128;  // rows per request up to which a small call takes several narrow items
 
@@ -149,27 +150,33 @@ __device__ __forceinline__ bool tree_request(const TreeParams& p, int32_t b, int
   return T > 0;
 }
 
-// A small narrow call's split, by this warp: lane b * q_tiles + i holds query tile i of request b.
+// A small narrow call's split, by this warp: its entry b * q_tiles + i is query tile i of request b.
+template <int N>
 struct TreeSmall {
-  SmallPlan plan;
-  int32_t P, T, row, q0, tokens;  // of this lane's request; its tile's first query row and tokens
+  SmallPlan<N> plan;
+  PerRequest<N> P, T, row, q0, tokens;  // of the request; the tile's first query row and tokens
 
-  __device__ __forceinline__ TreeSmall(const TreeParams& p, int32_t ctas, bool report)
-      : P(0), T(0), row(0), q0(0), tokens(0) {
-    const int lane = threadIdx.x & 31;
-    const int32_t b = lane / p.sh.q_tiles, tile = lane - b * p.sh.q_tiles;
-    if (b < p.batch) {
-      if (!tree_request(p, b, P, T, report && tile == 0)) P = T = 0;
-      row = __ldg(p.rpi + b);
-      q0 = __ldg(p.qo_indptr + b) + tile * p.sh.tokens_per_item;
-      tokens = min(max(T - tile * p.sh.tokens_per_item, 0), p.sh.tokens_per_item);
+  __device__ __forceinline__ TreeSmall(const TreeParams& p, int32_t ctas, bool report) {
+    PerRequest<N> keys;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int32_t entry = static_cast<int32_t>(threadIdx.x & 31) + 32 * i;
+      const int32_t b = entry / p.sh.q_tiles, tile = entry - b * p.sh.q_tiles;
+      if (b < p.batch) {
+        if (!tree_request(p, b, P.v[i], T.v[i], report && tile == 0)) P.v[i] = T.v[i] = 0;
+        row.v[i] = __ldg(p.rpi + b);
+        q0.v[i] = __ldg(p.qo_indptr + b) + tile * p.sh.tokens_per_item;
+        tokens.v[i] = min(max(T.v[i] - tile * p.sh.tokens_per_item, 0), p.sh.tokens_per_item);
+      }
+      keys.v[i] = tokens.v[i] > 0 ? P.v[i] + T.v[i] : 0;
     }
-    plan.make(tokens > 0 ? P + T : 0, p.sh.heads, ctas, kTreeSmallLeast);
+    plan.make(keys, p.sh.heads, ctas, kTreeSmallLeast);
   }
 };
 
-// The narrow path's attention kernel (tree_narrow.cu): behind the plan kernel, or a small call's.
-ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, bool small, const DeviceInfo& dev,
+// The narrow path's attention kernel (tree_narrow.cu): behind the plan kernel (small = 0), or a small call's (1 or
+// 2 query tiles per lane).
+ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, int small, const DeviceInfo& dev,
                              cudaStream_t stream);
 
 }  // namespace ra

@@ -38,7 +38,7 @@ struct NarrowItem {
   int32_t mark;  // index of the item's marks / hkv: its request, or a small call's piece
 };
 
-// The items of a call: the plan kernel's list, or (SMALL) this warp's own plan.
+// The items of a call: the plan kernel's list, or (SMALL = 1 or 2 query tiles per lane) this warp's own plan.
 struct ListedItems {
   const TreeParams& p;
   __device__ __forceinline__ ListedItems(const TreeParams& q, bool) : p(q) {}
@@ -58,19 +58,20 @@ struct ListedItems {
     it.k1 = min(f.x + f.y, it.k0 + chunk);
   }
 };
+template <int N>
 struct SmallItems {
   const TreeParams& p;
-  TreeSmall small;
+  TreeSmall<N> small;
   __device__ __forceinline__ SmallItems(const TreeParams& q, bool report)
       : p(q), small(q, kTreeSms * q.sh.per_sm, report) {}
   __device__ __forceinline__ int32_t count() const { return small.plan.n * p.sh.heads; }
   __device__ __forceinline__ void item(int32_t idx, NarrowItem& it) const {  // warp-collective
     const int32_t d = idx / p.sh.heads;
     it.hg = idx - d * p.sh.heads;
-    const int32_t b = small.plan.request(d), split = d - of_lane(small.plan.first, b);  // (b: a request's tile)
-    it.P = of_lane(small.P, b), it.T = of_lane(small.T, b), it.row = of_lane(small.row, b);
-    it.q0 = of_lane(small.q0, b), it.tokens = of_lane(small.tokens, b);
-    it.slot = of_lane(small.plan.pieces, b) > 1 ? d : -1;
+    const int32_t b = small.plan.request(d), split = d - of_request(small.plan.first, b);  // (b: a request's tile)
+    it.P = of_request(small.P, b), it.T = of_request(small.T, b), it.row = of_request(small.row, b);
+    it.q0 = of_request(small.q0, b), it.tokens = of_request(small.tokens, b);
+    it.slot = of_request(small.plan.pieces, b) > 1 ? d : -1;
     it.mark = d;
     it.k0 = split * small.plan.chunk;
     it.k1 = min(it.P + it.T, it.k0 + small.plan.chunk);
@@ -102,7 +103,7 @@ struct NarrowSource {
   }
 };
 
-template <int D, int SLAB, bool SMALL>
+template <int D, int SLAB, int SMALL>
 __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
     tree_narrow_kernel(const __grid_constant__ NarrowParams n) {
   const TreeParams& p = n.t;
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
   __syncthreads();
   griddep_wait();  // the plan and everything before it
   griddep_launch();
-  using Items = std::conditional_t<SMALL, SmallItems, ListedItems>;
+  using Items = std::conditional_t<SMALL != 0, SmallItems<SMALL ? SMALL : 1>, ListedItems>;
   const Items items(p, blockIdx.x == 0 && warp == 0);
   if (warp >= nc) {
     if (warp < nc + kRingProducers) slab_producer<SLAB>(rg, NarrowSource<SLAB, Items>(n, items), warp - nc);
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
 int32_t stage_bytes(int32_t hpc, int32_t head_dim, int32_t slab) { return 2 * slab * (hpc * head_dim * 2 + 16); }
 int32_t ring_bytes(int32_t per_sm) { return kRingSmemLimit / per_sm - 1024 - kRingHdrBytes; }  // (1 KB per CTA is the system's)
 
-template <int D, int SLAB, bool SMALL>
+template <int D, int SLAB, int SMALL>
 ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
   NarrowParams n{};
   n.t = p;
@@ -349,17 +350,20 @@ ra_status launch(const TreeParams& p, const DeviceInfo& dev, cudaStream_t s) {
                     dim3(32 * (p.sh.hpc * p.sh.row_blocks + kRingProducers)), smem, s, n);
 }
 
+template <int D, int SLAB>
+ra_status launch_items(const TreeParams& p, int small, const DeviceInfo& dev, cudaStream_t s) {
+  return small == 0 ? launch<D, SLAB, 0>(p, dev, s) : small == 1 ? launch<D, SLAB, 1>(p, dev, s) : launch<D, SLAB, 2>(p, dev, s);
+}
+
 }  // namespace
 
 // 32-key slabs where two of them fit the ring, else 16-key ones (64 x 8 tokens over 512..4096 keys, 32- and 16-key
 // slabs: 16/16 heads of 64, where one fits, 118.3 and 106.5 us; 12/12, where two do, 84.6 and 87.3; 5/5 heads of
 // 128, two, 77.2 and 81.8).
-ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, bool small, const DeviceInfo& dev, cudaStream_t s) {
+ra_status launch_tree_narrow(const TreeParams& p, int32_t head_dim, int small, const DeviceInfo& dev, cudaStream_t s) {
   const bool wide = 2 * stage_bytes(p.sh.hpc, head_dim, 32) <= ring_bytes(p.sh.per_sm);
-  if (head_dim == 64 && wide) return small ? launch<64, 32, true>(p, dev, s) : launch<64, 32, false>(p, dev, s);
-  if (head_dim == 64) return small ? launch<64, 16, true>(p, dev, s) : launch<64, 16, false>(p, dev, s);
-  if (wide) return small ? launch<128, 32, true>(p, dev, s) : launch<128, 32, false>(p, dev, s);
-  return small ? launch<128, 16, true>(p, dev, s) : launch<128, 16, false>(p, dev, s);
+  if (head_dim == 64) return wide ? launch_items<64, 32>(p, small, dev, s) : launch_items<64, 16>(p, small, dev, s);
+  return wide ? launch_items<128, 32>(p, small, dev, s) : launch_items<128, 16>(p, small, dev, s);
 }
 
 }  // namespace ra

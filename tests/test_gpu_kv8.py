@@ -221,6 +221,25 @@ def test_decode_planned_by_the_warps_and_by_the_kernel(batch, longest, bound, hq
     check_decode(o, rec, table, rpi, lens, q, hkv, d ** -0.5)
 
 
+@pytest.mark.parametrize("batch", [33, 50, 64, 65])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (12, 3, 128), (8, 2, 64), (16, 16, 64)])
+def test_decode_of_more_requests_than_lanes(batch, hq, hkv, d):
+    """33 to 64 requests (two per lane of a small call) and one more, two of them invalid, split and unsplit ones."""
+    rng = np.random.default_rng(batch + hq)
+    lens = rng.integers(1, 120, batch)
+    lens[[0, 31, 32, batch - 1]] = [500, 90, 431, 333]
+    rec, table, rpi, lens, q = decode_case(rng, lens, hq, hkv, d, spread=1)
+    r2, l2 = rpi.copy(), lens.copy()
+    r2[batch - 2], l2[3] = -1, 0
+    err = err_word()
+    o = decode(rec, table, r2, l2, q, hkv, d ** -0.5, device_error=err)
+    assert int(err.item()) == ra.DEVERR_TABLE | ra.DEVERR_LENGTH
+    assert (o[[3, batch - 2]] == 7.0).all()
+    ok = np.setdiff1d(np.arange(batch), [3, batch - 2])
+    check_decode(o[torch.from_numpy(ok).to(DEV)], rec, table, rpi[ok], lens[ok], q[torch.from_numpy(ok).to(DEV)], hkv,
+                 d ** -0.5)
+
+
 def test_decode_shared_prefix_and_many_splits():
     rng = np.random.default_rng(9)
     rec, table, rpi, lens, q = decode_case(rng, rng.integers(400, 3000, 24), 32, 8, 128, spread=1, share=400)

@@ -152,6 +152,40 @@ def test_tree_planned_by_the_warps_and_by_the_kernel(batch, longest, bound):
     c.check(o)
 
 
+@pytest.mark.parametrize("batch", [33, 50, 64, 65])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (5, 5, 64), (4, 1, 128)])
+def test_tree_of_more_requests_than_lanes(batch, hq, hkv, d):
+    """33 to 64 narrow requests (two per lane of a small call) and one more: empty and invalid ones, split and unsplit
+    ones, and a drafted token whose V is not finite."""
+    rng = np.random.default_rng(batch + hq)
+    prefix, draft = rng.integers(0, 90, batch), rng.integers(0, 9, batch)
+    prefix[[0, 31, 32, batch - 1]], draft[[0, 31, 32, batch - 1]] = [400, 60, 333, 250], [8, 1, 7, 5]
+    draft[5] = 0
+    c = Case(rng, prefix, draft, hq, hkv, d, gap=1)
+    P = c.P.copy()
+    P[batch - 2] = -1
+    slot = int(c.table[c.rpi[32], int(prefix[32]) + 2])
+    c.v[slot, 0, 7] = float("inf")
+    o = c.run(P=i32(P))
+    assert int(c.err.item()) == ra.DEVERR_LENGTH
+    at = int(c.qo[batch - 2])
+    assert (o[at:at + int(c.T[batch - 2])] == 7.0).all()
+    k, v = f64(c.k), f64(c.v)
+    for b in range(batch):
+        if b == batch - 2 or c.T[b] == 0:
+            continue
+        Pb, T, q0 = int(c.P[b]), int(c.T[b]), int(c.qo[b])
+        slots = c.table[c.rpi[b], :Pb + T]
+        seen = np.concatenate([np.ones((T, Pb), bool), c.seen[b]], 1)
+        vb = np.where(np.isfinite(v[slots]), v[slots], 0.0)
+        ref, a, x = R.attend(f64(c.q[q0:q0 + T]), k[slots], vb, c.scale, seen)
+        got = f64(o[q0:q0 + T])
+        blind = ~c.seen[b][:, 2] if b == 32 else np.ones(T, bool)      # rows without the infinite value
+        bad = np.abs(got - ref) > R.attention_bound(ref, a, x, d, R.EPS_BF16)
+        assert not bad[blind].any(), b
+        assert b != 32 or not np.isfinite(got[~blind][:, 0, 7]).any()
+
+
 @pytest.mark.parametrize("hq,hkv,d,draft", [(32, 8, 128, 16), (8, 8, 64, 70), (8, 1, 128, 8), (16, 2, 64, 13)])
 def test_tree_one_query_tile_on_the_wide_path(hq, hkv, d, draft):
     """Requests of 33..128 rows per kv head in calls that are not small: both query tiles of an item share out its
