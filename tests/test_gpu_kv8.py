@@ -204,7 +204,7 @@ def test_decode_matches_64_bit_attention(lens, hq, hkv, d):
                                                  (1, 6000, None), (100, 90, None)])
 @pytest.mark.parametrize("hq,hkv,d", [(16, 4, 128), (8, 2, 64)])
 def test_decode_planned_by_the_warps_and_by_the_kernel(batch, longest, bound, hq, hkv, d):
-    """Both sides of the small-call rule (32 requests; the bound of their keys), the same requests under a loose
+    """Both sides of the small-call rule (the number of requests; the bound of their keys), the same requests under a loose
     bound, requests of one key among long ones."""
     rng = np.random.default_rng(batch + longest)
     lens = rng.integers(1, longest + 1, batch)
