@@ -23,6 +23,7 @@ wall time; the attention values are synthetic (this drives the data path, not a 
 """
 from __future__ import annotations
 
+import gc
 import time
 from dataclasses import dataclass, field
 from typing import Dict, List, Optional, Sequence, Tuple
@@ -141,15 +142,22 @@ class ServingReplay:
         buf["ws"] = torch.empty(ra_decode_workspace_bytes(bs, self.hq, self.hkv, self.d, self.max_len),
                                 dtype=torch.uint8, device=self.dev)
 
-        def run():
-            self._store(buf["k_new"], buf["v_new"], buf["loc"])
-            args = dict(max_seq_len=self.max_len, sm_scale=self.scale, workspace=buf["ws"], device_error=self.err)
-            if self.kv8_pool is not None:
-                ra_kv8_decode_attention(self.kv8_pool, buf["q"], buf["o"], self.table, buf["rpi"], buf["lens"],
-                                        num_kv_heads=self.hkv, **args)
-            else:
-                ra_decode_attention(self.k_pool, self.v_pool, buf["q"], buf["o"], self.table, buf["rpi"], buf["lens"],
-                                    **args)
+        # `run` holds the tensors, not this object: a replay that goes out of use frees its graphs at once, and not
+        # when the garbage collector finds a cycle (destroying a graph invalidates a capture under way)
+        table, hkv = self.table, self.hkv
+        args = dict(max_seq_len=self.max_len, sm_scale=self.scale, workspace=buf["ws"], device_error=self.err)
+        if self.kv8_pool is not None:
+            pool = self.kv8_pool
+
+            def run():
+                ra_kv8_store(pool, buf["k_new"], buf["v_new"], buf["loc"], device_error=args["device_error"])
+                ra_kv8_decode_attention(pool, buf["q"], buf["o"], table, buf["rpi"], buf["lens"], num_kv_heads=hkv, **args)
+        else:
+            k_pool, v_pool = self.k_pool, self.v_pool
+
+            def run():
+                ra_kv_store(k_pool, v_pool, buf["k_new"], buf["v_new"], buf["loc"], device_error=args["device_error"])
+                ra_decode_attention(k_pool, v_pool, buf["q"], buf["o"], table, buf["rpi"], buf["lens"], **args)
         g = None
         if self.use_graphs:
             run()  # first-call set-up outside the capture
@@ -157,9 +165,15 @@ class ServingReplay:
             stream = torch.cuda.Stream(self.dev)
             stream.wait_stream(torch.cuda.current_stream(self.dev))
             g = torch.cuda.CUDAGraph()
-            with torch.cuda.stream(stream):
-                with torch.cuda.graph(g, stream=stream):
-                    run()
+            collects = gc.isenabled()
+            gc.disable()  # (other owners' graphs may be garbage in cycles)
+            try:
+                with torch.cuda.stream(stream):
+                    with torch.cuda.graph(g, stream=stream):
+                        run()
+            finally:
+                if collects:
+                    gc.enable()
             torch.cuda.current_stream(self.dev).wait_stream(stream)
             torch.cuda.synchronize(self.dev)
         self._graphs[bs] = (g, buf, run)

@@ -1,5 +1,8 @@
 """The serving replay over a quantised pool: the same chats admitted, prefilled, decoded from graphs and retired;
 slot accounting as over a bf16 pool, and one decode step against 64-bit attention over the records."""
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -38,3 +41,42 @@ def test_chat_replay_over_a_quantised_pool():
         bound = R.attention_bound(ref, a, x, 128, R.EPS_F16) + lens[b] * 2.0 ** -24 * np.abs(v).max()
         assert (np.abs(o - ref) <= bound).all()
 
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+def test_replay_and_its_graphs_are_freed_without_the_collector(kv_dtype):
+    """A graph destroyed while another is captured invalidates the capture: a replay is in no reference cycle, and
+    the collector does not run during its captures (a graph that is garbage in a cycle outlives them)."""
+    kw = dict(num_slots=1 << 10, num_q_heads=8, num_kv_heads=2, head_dim=64, max_len=256, max_running=8,
+              device="cuda:0", seed=3, graph_sizes=(2, 4, 8), kv_dtype=kv_dtype)
+    gc.collect()
+    gc.disable()
+    try:
+        rp = ServingReplay(**kw)
+        g = weakref.ref(rp._graph(2)[2])
+        whole = weakref.ref(rp)
+        del rp
+        assert whole() is None and g() is None
+    finally:
+        gc.enable()
+    rp = ServingReplay(**kw)
+    cycle = [torch.cuda.CUDAGraph()]
+    x = torch.zeros(8, device="cuda:0")
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream), torch.cuda.graph(cycle[0], stream=stream):
+        x.add_(1)
+    torch.cuda.synchronize()
+    cycle.append(cycle)
+    before = gc.get_threshold()
+    gc.disable()
+    try:
+        del cycle
+        gc.set_threshold(1, 1, 1)
+        gc.enable()
+        graph, buf, run = rp._graph(4)
+    finally:
+        gc.set_threshold(*before)
+        gc.collect()  # (not during a capture of a later test)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert gc.isenabled() and int(rp.err.item()) == 0
