@@ -11,7 +11,7 @@
 //  * more rows are bound by the tensor cores and the softmax's issue slots, like extend: the tcgen05 attention
 //    kernel (attn_tc.cuh, kTreePass), up to 256 rows per item, each gathered 128-key tile feeding all of them.
 //    Its 128-byte gathers take ~16 bytes per clock and SM, 4.2 TB/s in all, whatever the rows: 64 requests x
-//    4..8 tokens over 512..4096 keys, 32/8 heads, took it 145 us and take the narrow path 118.
+//    4..8 tokens over 512..4096 keys, 32/8 heads, took it 145 us and take the narrow path 111.
 // Around it:
 //  * the work list (one CTA, on the device, from the real lengths; small calls: every warp for itself) splits
 //    the key ranges only as far as the SMs need it, since an unsplit item writes its bf16 rows directly while
@@ -119,7 +119,10 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
   // items it also balances the SMs; with fewer, the longest range is cut into the number of pieces (at most
   // two per SM and head) whose longest-first schedule is shortest: the rounds of full pieces, and what the
   // shorter last pieces take beyond the gaps of the last round.  64 numbers of pieces are weighed, four
-  // threads each; the estimate may round (only the choice depends on it).
+  // threads each; the estimate may round (only the choice depends on it).  How much of the gaps is taken and
+  // what the last pieces stick out by is measured (64 x 4..8 tokens of 32/8 heads over 512..4096 keys with the wide
+  // path's factors 118.6 us, with their own 110.6; 8 x 32..64 tokens of 64/8 heads with the narrow path's 75.2,
+  // with their own 73.0).
   const unsigned long long all = work * heads;
   const unsigned long long per_slot =
       all >> 31 ? (all + slots - 1) / slots : (static_cast<uint32_t>(all) + slots - 1) / static_cast<uint32_t>(slots);
@@ -149,8 +152,8 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
     const float fulls = static_cast<float>(n_full * heads);
     const float sms = static_cast<float>(ctas), rounds = fmaxf(ceilf(fulls / sms), 1.f);
     const float rest = static_cast<float>(rem_units * heads) + static_cast<float>(n_rem * heads) * p.sh.split_overhead;
-    const float beyond = rest - 0.8f * (rounds * sms - fulls) * piece;
-    float cost = rounds * piece + (beyond > 0.f ? beyond / sms + 0.5f * static_cast<float>(c) : 0.f);
+    const float beyond = rest - (p.sh.narrow ? 1.f : 0.8f) * (rounds * sms - fulls) * piece;
+    float cost = rounds * piece + (beyond > 0.f ? beyond / sms + (p.sh.narrow ? 0.35f : 0.5f) * static_cast<float>(c) : 0.f);
     int32_t mine = c;
 #pragma unroll
     for (int off = 16; off >= 4; off >>= 1) {
