@@ -586,8 +586,8 @@ __device__ __forceinline__ void scatter_new_rows(const DecodeParams& p, int64_t 
 
 // The private-key work plan of one decode call, made on the device from the real lengths (the host only
 // knows bounds).  T = the batch's private keys (seq_len minus the cascade start, over valid requests);
-// chunk = max(min_chunk, T / kDecodePlanItems rounded up to chunk_align), so a call has at most
-// kDecodePlanItems + batch items however long its contexts are.  Request b's items get the dense indices
+// chunk = max(min_chunk, T / plan_items rounded up to chunk_align), so a call has at most
+// plan_items + batch items however long its contexts are.  Request b's items get the dense indices
 // req_item0[b] .. req_item0[b+1]-1 (where their partials live); the claim order lists every full-chunk
 // item first, then each request's shorter last item by decreasing size (longest processing time first),
 // so the CTAs that finish last finish on short items.  One CTA of kPlanThreads threads; each thread owns
@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
   for (int off = 16; off > 0; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
   if ((t & 31) == 0) atomicAdd(&s_total, tot);
   __syncthreads();
-  const unsigned long long per_item = (s_total + kDecodePlanItems - 1) / kDecodePlanItems;
-  // (the host bounds batch x max_seq_len by kDecodePlanItems x 2^30, so the chunk fits in 31 bits)
+  const unsigned long long per_item = (s_total + p.plan_items - 1) / p.plan_items;
+  // (the host bounds batch x max_seq_len by plan_items x 2^30, so the chunk fits in 31 bits)
   const int32_t chunk = static_cast<int32_t>(
       per_item <= static_cast<unsigned long long>(p.min_chunk) ? p.min_chunk
                                                                : (per_item + p.chunk_align - 1) / p.chunk_align * p.chunk_align);
@@ -962,6 +962,7 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
   p.seq_lens = seq_lens;
   p.batch = batch;
   p.max_seq_len = max_seq_len;
+  p.plan_items = kDecodePlanItems;
   p.min_chunk = kDecodeMinChunk;
   p.chunk_align = 16;
   bind_decode_workspace(p, wl, pl, workspace);

@@ -37,6 +37,7 @@ struct DecodeParams {
   int32_t row_stride;        // bytes between keys in a ring stage (hpc * D * 2 + 16)
   int32_t stage_bytes;       // 2 * 16 * row_stride
   int32_t max_items;         // kDecodePlanItems + batch: bound of the plan's items
+  int32_t plan_items;        // equal items that the plan cuts the call's keys into, at most kDecodePlanItems
   int32_t min_chunk;         // shortest full item of the plan (keys)
   int32_t chunk_align;       // full items are a multiple of this many keys
   int32_t* counter;          // work-item counter (reset by the plan kernel)

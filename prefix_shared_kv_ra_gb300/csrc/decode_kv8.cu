@@ -57,7 +57,6 @@ struct Kv8DecodeParams {
   int32_t ctas;  // small call: the grid
 };
 constexpr int kSmallLeast = 2;  // units of a small call's shortest piece
-constexpr int kSmallMany = 32;  // small_call's bound for more than 32 requests
 
 // The items of a call: the plan kernel's list, or (SMALL = 1 or 2 requests per lane) this warp's own plan.
 template <int SMALL>
@@ -521,7 +520,7 @@ template <int D, int SLAB>
 ra_status launch(Kv8DecodeParams& pp, int32_t per_sm, int smem, const DeviceInfo& dev, cudaStream_t s) {
   DecodeParams& p = pp.d;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.hq, warps = static_cast<int64_t>(dev.num_sms) * 3 * kCombineWarps;
-  const bool small = small_call(p.batch, p.max_seq_len, p.n_hgroups, per_sm, kSmallMany), many = p.batch > 32;
+  const bool small = small_call(p.batch, p.max_seq_len, p.n_hgroups, per_sm), many = p.batch > 32;
   if (small) {
     pp.ctas = kSmallSms * per_sm;
     if (ra_status st = many ? launch_decode<D, SLAB, 2>(pp, pp.ctas, smem, dev, s)
@@ -580,8 +579,8 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   RA_REQUIRE(aligned16(kv8_pool) && aligned16(q) && aligned16(o), "the pool, q and o must be 16-byte aligned");
   RA_REQUIRE(aligned4(req_to_token) && aligned4(req_pool_indices) && aligned4(seq_lens),
              "index arrays must be 4-byte aligned");
-  // the device plan's item length must fit in 31 bits (it is at most batch x max_seq_len / kDecodePlanItems)
-  RA_REQUIRE(static_cast<int64_t>(batch) * max_seq_len <= static_cast<int64_t>(kDecodePlanItems) << 30,
+  // the device plan's item length must fit in 31 bits (it is at most batch x max_seq_len / plan_items)
+  RA_REQUIRE(static_cast<int64_t>(batch) * max_seq_len <= static_cast<int64_t>(kSmallSms) << 30,
              "batch x max_seq_len too large");
   RA_REQUIRE(static_cast<int64_t>(batch) * num_q_heads < (int64_t(1) << 30), "batch x num_q_heads too large");
   const DecodePlan pl = plan_decode(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len, 0, 0, 0);
@@ -625,6 +624,12 @@ extern "C" ra_status ra_kv8_decode_attention(const void* kv8_pool, int64_t num_s
   // registers fit (8 warps of 128 registers each; 3 heads of 128 gain more from 64-key slabs: 150 requests of
   // 1000..9000 keys, 12/3 heads 125 us as two CTAs, 116 as one; 1 head: 64 requests 47.8 and 53.6).
   const int per_sm = ctas_per_sm(head_dim, sh.hpc);
+  // One full item per resident CTA, and the requests' shorter last ones, largest first, to even them out: 64 requests
+  // of 512..4096 keys, 32/8 heads 57.5 us, 59.5 with three per CTA (more partials), 104 of 267..8966, 64/8 heads
+  // 93.6 and 101, 200 of 1000..9000, 8/1 heads 103 and 127; the 224 of 65..13700, 64/8 heads, 190.1 with one and 189.4
+  // with two.
+  static_assert(2 * kSmallSms <= kDecodePlanItems, "the workspace holds the plan's items");
+  p.plan_items = kSmallSms * per_sm;
   p.nstage = (kRingSmemLimit / per_sm - 1024 - kRingHdrBytes) / p.stage_bytes;  // (1 KB per CTA is the system's)
   if (p.nstage > kRingMaxStages) p.nstage = kRingMaxStages;
   const int smem = kRingHdrBytes + p.nstage * p.stage_bytes;

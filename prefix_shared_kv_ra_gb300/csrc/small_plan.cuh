@@ -13,21 +13,22 @@ namespace ra {
 constexpr int kSmallBatch = 64;
 constexpr int kSmallUnit = 32;    // keys per unit
 constexpr int kSmallRounds = 48;  // mean units per CTA, at the host's bounds, up to which a call is small
+constexpr int kSmallRoundsMany = 16;  // the same for more than 32 requests
 constexpr int kSmallSms = 152;    // GB300; a constant, so that host and device agree
 
 // Whether a call is small, from the host's bounds.  Its pieces have to fit: sum ceil(u / c) <= U / c + batch.  The
 // bound on the mean keeps the loss of the coarser schedule (up to a third: one piece per CTA, all as long as
 // the longest) below what the planning kernel costs.  Measured, planning kernel and small call, at their mean
-// units: quantised decode of 16 requests of 512..4096 keys (13) 25.9 and 20.6 us, of 1000..13700 (45) 50.9 and
-// 46.4, of 30 of 13000..13700 (85) 137.4 and 137.1; 16 x 4..8 drafted tokens over 512..4096 keys (27) 40.9 and
-// 36.5, 30 x 4..8 (51) 62.9 and 65.5.  With more than 32 requests the pieces are coarser and the bound, `many`, is
-// lower: quantised decode of 64 requests of 200..1000 keys (13) 25.9 and 22.5, of 500..2000 (27) 38.2 and 37.5, of
-// 500..3000 of 4 heads (40) 31.0 and 31.3; 64 x 4..7 drafted tokens over 100..1000 keys (13) 27.5 and 22.9, over
-// 1000..2000 (27) 43.4 and 44.2.
-inline bool small_call(int64_t batch, int64_t max_keys, int64_t heads, int64_t per_sm, int64_t many) {
+// units: quantised decode of 16 requests of 512..4096 keys (13) 22.8 and 20.4 us, of 24 of 5000..8000 (39) 60.4 and
+// 59.2; 16 x 4..8 drafted tokens over 512..4096 keys (27) 40.9 and 36.5, 30 x 4..8 (51) 62.9 and 65.5.  With more
+// than 32 requests the pieces are coarser and the bound is lower: quantised decode of 64 requests of 200..1000 keys
+// (13) 24.1 and 22.2, of 500..1500 (20) 30.9 and 31.8; 64 x 4..7 drafted tokens over 100..1000 keys (13) 27.5 and
+// 22.9, over 1000..2000 (27) 43.4 and 44.2.
+inline bool small_call(int64_t batch, int64_t max_keys, int64_t heads, int64_t per_sm) {
   const int64_t ctas = kSmallSms * per_sm;
   return batch <= kSmallBatch && 2 * batch * heads <= ctas &&
-         batch * ((max_keys + kSmallUnit - 1) / kSmallUnit) * heads <= (batch <= 32 ? kSmallRounds : many) * ctas;
+         batch * ((max_keys + kSmallUnit - 1) / kSmallUnit) * heads <=
+             (batch <= 32 ? kSmallRounds : kSmallRoundsMany) * ctas;
 }
 
 // A lane's values of request `lane` (N = 1), or of `lane` and `lane` + 32 (N = 2: for 33 requests or more).

@@ -464,7 +464,7 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
 int tree_small(const TreeShape& sh, int32_t batch, int32_t max_prefix, int32_t max_draft) {
   const int64_t tiles = static_cast<int64_t>(batch) * sh.q_tiles;
   if (!sh.narrow || (sh.q_tiles > 1 && tiles > 32) ||
-      !small_call(tiles, static_cast<int64_t>(max_prefix) + max_draft, sh.heads, sh.per_sm, kTreeSmallMany))
+      !small_call(tiles, static_cast<int64_t>(max_prefix) + max_draft, sh.heads, sh.per_sm))
     return 0;
   return tiles <= 32 ? 1 : 2;
 }

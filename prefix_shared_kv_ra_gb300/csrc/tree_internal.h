@@ -14,7 +14,6 @@ namespace ra {
 
 constexpr int kTreeSms = 152;        // GB300; a constant, so that the workspace does not depend on the device
 constexpr int kTreeSmallLeast = 2;   // units of a small call's shortest piece
-constexpr int kTreeSmallMany = 16;   // small_call's bound for more than 32 requests
 constexpr int kTreeNarrowRows = 32;  // rows (drafted tokens x GQA group) of a narrow item
 constexpr int kTreeTiledRows = 128;  // rows per request up to which a small call takes several narrow items
 
