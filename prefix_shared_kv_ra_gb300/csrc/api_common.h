@@ -21,6 +21,13 @@ void clear_error();
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Partial rows are written in 32-byte stores, while a workspace is 16-byte aligned: its sections are laid out from the
+// next multiple of 32, and its size holds the bytes that this may skip.
+constexpr size_t kWorkspaceSlack = 16;
+inline uint8_t* workspace_base(void* workspace) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
+}
+
 struct DeviceInfo {
   int device = -1;
   int num_sms = 0;

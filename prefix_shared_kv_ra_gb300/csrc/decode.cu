@@ -759,11 +759,15 @@ ra_status launch_decode_plan(const DecodeParams& p, int store_ctas, cudaStream_t
 }
 
 void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace) {
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = workspace_base(workspace);
   p.max_items = pl.max_items;
   p.part_o = reinterpret_cast<float*>(ws + wl.part_o);
   p.part_lse = reinterpret_cast<float*>(ws + wl.part_lse);
   int32_t* ints = reinterpret_cast<int32_t*>(ws + wl.ints);
+  if (wl.casc_o != 0) {  // (behind the private partials, so never 0 with groups)
+    p.casc_o = reinterpret_cast<float*>(ws + wl.casc_o);
+    p.casc_lse = reinterpret_cast<float*>(ws + wl.casc_lse);
+  }
   p.counter = ints + p.batch;
   p.prefix_counter = ints + p.batch + 1;
   p.prefix_done = ints + p.batch + 2;
@@ -865,7 +869,7 @@ DecodeWorkspace layout_decode_workspace(int32_t batch, int32_t num_q_heads, int3
   w.zero_bytes = (static_cast<size_t>(batch) + 3) * sizeof(int32_t);
   w.ints_bytes = w.zero_bytes + (2 + static_cast<size_t>(batch) + 1 + 2 * static_cast<size_t>(pl.max_items) +
                                  static_cast<size_t>(batch)) * sizeof(int32_t);
-  off += up(w.ints_bytes);
+  off += up(w.ints_bytes + kWorkspaceSlack);
   w.total = off;
   return w;
 }
@@ -966,7 +970,6 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
   p.min_chunk = kDecodeMinChunk;
   p.chunk_align = 16;
   bind_decode_workspace(p, wl, pl, workspace);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.err = device_error;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // fused store: extra CTAs of the call's first kernel scatter the new rows (a few waves of 4 vectors
@@ -986,7 +989,6 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
     if (store_ctas < 1) store_ctas = 1;
   }
 
-  int32_t* ints = reinterpret_cast<int32_t*>(ws + wl.ints);
   // Kernels rather than memsets, so that the launches of the call stay chained programmatically:
   // with groups, [set-up: counters, key starts, empty prefix partials] -> [prefix pass] -> [plan] ->
   // [decode] -> [combine]; without, [plan] -> [decode] -> [combine].
@@ -996,8 +998,7 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
     p.prefix_wave = pl.prefix_wave;
     p.casc_slots = levels * pl.max_csplits;
     p.casc_one_level = (max_group_levels == 1 && group_prefix_start == nullptr) ? 1 : 0;
-    p.casc_o = reinterpret_cast<float*>(ws + wl.casc_o);
-    p.casc_lse = reinterpret_cast<float*>(ws + wl.casc_lse);
+    int32_t* ints = p.counter - batch;  // the block's start: the key starts
     p.key_start = ints;
     const int64_t n_lse = static_cast<int64_t>(batch) * num_q_heads * p.casc_slots;
     const int64_t lse_want = (n_lse + 256 * 8 - 1) / (256 * 8);  // ~8 values per thread

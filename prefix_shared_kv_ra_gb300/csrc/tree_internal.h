@@ -97,7 +97,7 @@ inline TreeWorkspace layout_tree(int32_t batch, int64_t total_q, int32_t hq, int
   w.cap = (total_q + sh.tokens_per_item - 1) / sh.tokens_per_item + batch + w.cap_parts;
   const int64_t rows = static_cast<int64_t>(max_draft < sh.tokens_per_item ? max_draft : sh.tokens_per_item) * group;
   w.part_rows = static_cast<int32_t>(rows);
-  uint8_t* b = static_cast<uint8_t*>(base);
+  uint8_t* b = workspace_base(base);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     uint8_t* at = b ? b + off : nullptr;
@@ -112,7 +112,7 @@ inline TreeWorkspace layout_tree(int32_t batch, int64_t total_q, int32_t hq, int
   const size_t part = static_cast<size_t>(w.cap_parts) * hkv * w.part_rows;
   w.part_lse = reinterpret_cast<float*>(take(part * 4));
   w.part_o = reinterpret_cast<float*>(take(part * d * 4));
-  w.total = off;
+  w.total = off + kWorkspaceSlack;
   return w;
 }
 
