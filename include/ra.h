@@ -355,7 +355,8 @@ ra_status ra_qk_norm_rope_kv8_store(const void* q, int64_t q_stride, const void*
  *   tree_mask[t, c / 32] set (a token names itself if it is to see itself; any set is allowed, not only a
  *   tree's ancestors).
  * A row that sees nothing (no prefix, no bit set) gives 0.  Values of drafted tokens that a row's mask leaves
- * out have no influence on it, whatever they are (also infinities and NaN).
+ * out have no influence on it, whatever they are (also infinities and NaN); an infinity or NaN in V of one that it
+ * sees makes that dimension of the row infinite or NaN.
  *   q, o:      bf16 [total_q, num_q_heads, head_dim]; o must not alias q or the pools; rows outside every
  *              request's range are left as they were.
  *   qo_indptr: int32 [batch + 1], qo_indptr[b] the first row of request b; requests' rows must not overlap.

@@ -99,6 +99,7 @@ struct TcParams {
   const uint32_t* tree_mask;  // [total_q, mask_words]
   int32_t mask_words;
   const int32_t* tree_chunk;  // keys per split (a multiple of 128)
+  const int32_t* tree_odd;    // [batch, hkv]: a drafted token's V holds a value that is not finite
   int32_t part_rows;          // rows of a partial slot
   float* part_o;              // [slots, hkv, part_rows, D]
   float* part_lse;            // [slots, hkv, part_rows]
@@ -162,6 +163,8 @@ struct Job {
   int32_t slot;      // cascade: partial slot of the members (level x max_csplits + split); tree: partial
                      // slot of the item, -1 for an unsplit one
   int32_t dual;      // tree (dual pass): the item's one live query tile is in both tiles, which share out its key tiles
+  int32_t kt0;       // tree: key tiles of the CTA's items before this one
+  int32_t odd;       // tree: drafted tokens' V of this kv head hold values that are not finite
   int32_t tiles;     // query tiles holding valid rows (1: tile 1 is empty; its MMAs and softmax are skipped,
                      // while every barrier still completes its phases as for two tiles)
 };
@@ -177,6 +180,8 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
   j.mem0 = 0;
   j.csplit = 0;
   j.slot = 0;
+  j.odd = 0;
+  j.kt0 = 0;
   if constexpr (PASS == kTreePass || PASS == kTreeDualPass) {
     // the list holds only non-empty items of requests whose indices and lengths were checked when it was built
     const int4 e = __ldg(reinterpret_cast<const int4*>(p.work_items) + 2 * rest);
@@ -190,6 +195,7 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
     j.kend = min(f.x + f.y, j.kbeg + chunk);
     j.q_tok0 = f.w + e.y * kTiles * T;
     j.slot = e.w;
+    j.odd = __ldg(p.tree_odd + static_cast<int64_t>(e.x) * p.hkv + j.kh);
   } else if constexpr (PASS == kExtendPass) {
     // entry `rest` of the work list: it holds only non-empty query tiles of requests whose lengths
     // were checked (and flagged) when it was built
@@ -360,6 +366,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     // claim the next non-empty item and publish it, decoded, as entry n of the ring (warp-collective).
     // Item blockIdx.x is this CTA's first without a claim; the counter hands out the items after the grid.
     bool own_first = true;
+    int32_t claimed_tiles = 0;
+    (void)claimed_tiles;
     auto claim_publish = [&](int32_t n) {
       int32_t idx;
       Job cj;
@@ -375,6 +383,10 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           break;
         }
         if (tc_job<PASS>(p, idx, cj, lane == 0)) break;
+      }
+      if constexpr (TREE) {
+        cj.kt0 = claimed_tiles;
+        claimed_tiles += cj.nt;
       }
       if (lane == 0) {
         s_item[n % kItemRing] = idx;
@@ -710,6 +722,21 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
               const int32_t off = key0 + 32 * c - lim;  // the chunk's first drafted token
               if (off >= 0) vis[c] = __funnelshift_r(word(off >> 5), word((off >> 5) + 1), off & 31);
               else if (off > -32) vis[c] = (word(0) << -off) | ((1u << -off) - 1u);
+            }
+            // Drafted tokens' V values that are not finite are set to 0 before the product, which would carry them,
+            // times a zero probability, to rows that do not see them (the merge kernel adds them to the rows that
+            // do).  Both query tiles of an item read the V tile, PV_1 behind PV_0, so tile 0's threads do it, a key row
+            // each (128 bytes per 64-column half, its 16-byte chunks swizzled).
+            if (s_job[n % kItemRing].odd && (ti == 0 || (DUAL && jb.dual))) {
+              const int32_t kt = s_job[n % kItemRing].kt0 + tile_at(jb, j, ti);
+              const bool fail_v = !mbar_wait(smem_u32(&bar_vf[kt % VS]), (kt / VS) & 1);
+              if (__any_sync(0xffffffffu, fail_v)) { ok = false; break; }
+              if (key0 + r >= lim) {
+#pragma unroll 1
+                for (int e = 0; e < D / 8; ++e)
+                  zero_not_finite_bf16x8(sV(kt % VS) + e / 8 * (kRows * 128) + r * 128 + e % 8 * 16);
+              }
+              fence_proxy_async_smem();
             }
           }
         }

@@ -138,6 +138,25 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ---------------------------------------------------------------- warp MMA (legacy path)
+// Set the values that are not finite of the 8 bf16 at a (16-byte aligned) shared address to 0; true if there were any.
+__device__ __forceinline__ bool zero_not_finite_bf16x8(uint32_t addr) {
+  uint32_t w[4];
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
+    w[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+    any = any || lo || hi;
+  }
+  if (any)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+  return any;
+}
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& a0, uint32_t& a1, uint32_t& a2, uint32_t& a3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)

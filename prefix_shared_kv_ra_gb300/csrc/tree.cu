@@ -19,10 +19,10 @@
 //  * a persistent merge kernel joins the splits; with nothing split it only looks at a count.
 // A value of V that is not finite must not reach rows whose mask leaves its token out, but a matrix product
 // multiplies it by their zero probability (0 * inf = NaN).  The drafted tokens' V are therefore looked over (by
-// the narrow kernel in its slabs, for wide calls by the list kernel's other CTAs: at most a few MB) and the
-// (request, kv head) pairs that hold one marked; the merge kernel recomputes those rows key by key, skipping
-// what is masked.  Prefix keys are seen by every row: there the
-// product's NaN is the answer.
+// the narrow kernel in its slabs, for wide calls by the list kernel's other CTAs: at most a few MB), the (request, kv
+// head) pairs that hold one marked, and such values set to 0 in shared memory before the product; the merge kernel
+// adds them to the rows that see them.  What that costs does not depend on the prefix.  Prefix
+// keys are seen by every row: there the product's NaN is the answer.
 #include <cmath>
 
 #include "api_common.h"
@@ -247,45 +247,93 @@ __global__ void __launch_bounds__(kScanThreads) tree_plan_kernel(const __grid_co
   }
 }
 
-// Row (token i of request b, q head h) key by key, one warp: D / 32 dims per lane, online softmax.
+// Add to row (token i of request b, q head h) of o the values that are not finite of the drafted tokens it sees, which
+// the attention kernels took as 0: one warp, D / 32 dims per lane, 4 tokens' rows in flight.  A weight is positive, so
+// such a value makes the row's dimension infinite, or NaN with an infinity of the other sign.  (The row was written
+// by this warp or by the kernel before.)
 template <int D>
-__device__ void recompute_row(const TreeParams& p, int32_t b, int32_t P, int32_t T, int32_t i, int32_t h) {
-  constexpr int V = D / 32;
+__device__ __forceinline__ void add_odd_values(const TreeParams& p, int32_t b, int32_t i, int32_t h) {
+  constexpr int V = D / 32, kAhead = 4;
   const int lane = threadIdx.x & 31;
+  int32_t P, T;
+  if (!tree_request(p, b, P, T, false)) return;
   const int64_t row = __ldg(p.qo_indptr + b) + i;
-  const int32_t* slots = p.table + static_cast<int64_t>(__ldg(p.rpi + b)) * p.table_stride;
+  const int32_t* slots = p.table + static_cast<int64_t>(__ldg(p.rpi + b)) * p.table_stride + P;
   const uint32_t* mrow = p.mask + row * p.mask_words;
-  float q[V], acc[V], m = -INFINITY, l = 0.f;
+  float add[V] = {};
+  for (int32_t j0 = 0; j0 < T; j0 += kAhead) {
+    const int32_t left = T - j0;
+    uint32_t seen = __ldg(mrow + (j0 >> 5)) >> (j0 & 31) & ((1u << kAhead) - 1u);
+    if (left < kAhead) seen &= (1u << left) - 1u;
+    if (seen == 0) continue;
+    uint32_t w[kAhead][V / 2];
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    q[e] = __bfloat162float(p.q[(row * p.hq + h) * D + lane * V + e]);
-    acc[e] = 0.f;
+    for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) w[k][e] = 0;
+      if (seen >> k & 1u) {
+        int32_t slot = __ldg(slots + j0 + k);
+        if (slot < 0 || slot >= p.num_slots) slot = 0;
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(
+            p.v_pool + (static_cast<int64_t>(slot) * p.hkv + h / p.group) * D + lane * V);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) w[k][e] = __ldg(v + e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        if ((w[k][e] & 0x7f80u) == 0x7f80u) add[2 * e] += __uint_as_float(w[k][e] << 16);
+        if ((w[k][e] & 0x7f800000u) == 0x7f800000u) add[2 * e + 1] += __uint_as_float(w[k][e] & 0xffff0000u);
+      }
   }
-  for (int32_t j = 0; j < P + T; ++j) {
-    if (j >= P && !(__ldg(mrow + ((j - P) >> 5)) >> ((j - P) & 31) & 1u)) continue;
-    int32_t slot = __ldg(slots + j);
-    if (slot < 0 || slot >= p.num_slots) slot = 0;
-    const int64_t at = (static_cast<int64_t>(slot) * p.hkv + h / p.group) * D + lane * V;
-    float s = 0.f;
+  __nv_bfloat16* dst = p.o + (row * p.hq + h) * D + lane * V;
 #pragma unroll
-    for (int e = 0; e < V; ++e) s = fmaf(q[e], __bfloat162float(p.k_pool[at + e]), s);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= p.scale_log2;
-    const float m_new = fmaxf(m, s);
-    const float alpha = m_new == m ? 1.f : ex2(m - m_new), w = s == -INFINITY ? 0.f : ex2(s - m_new);
-    m = m_new;
-    l = l * alpha + w;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = acc[e] * alpha + w * __bfloat162float(p.v_pool[at + e]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < V; ++e) p.o[(row * p.hq + h) * D + lane * V + e] = __float2bfloat16_rn(acc[e] * inv);
+  for (int e = 0; e < V; ++e)
+    if (add[e] != 0.f) dst[e] = __float2bfloat16_rn(__bfloat162float(dst[e]) + add[e]);  // (an infinity or NaN)
 }
 
-// Join the splits (o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M)), and recompute the marked (request, kv
-// head) pairs' rows.  Persistent: a unit is kMergeThreads / 8 rows of a split query tile (all kv heads), 8 lanes
+// The same for the rows of split query tiles that a warp of the merge kernel wrote: its units' once more.
+template <int D, bool FEW>
+__device__ __forceinline__ void add_to_split_rows(const TreeParams& p, int per_row) {
+  constexpr int kRows = FEW ? 1 : 4;  // of a warp and unit
+  const int warp = threadIdx.x >> 5;
+  if (FEW && warp % per_row != 0) return;
+  const int rows_per_unit = FEW ? kMergeWarps / per_row : kMergeWarps * kRows;
+  const int32_t tile_rows = p.hkv * p.ws.part_rows, chunks = (tile_rows + rows_per_unit - 1) / rows_per_unit;
+  const int64_t units = static_cast<int64_t>(__ldcg(p.ws.header + 3)) * chunks;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t entry = u / chunks;
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(p.ws.merges) + entry);
+    const int32_t flat0 = static_cast<int32_t>(u - entry * chunks) * rows_per_unit + (FEW ? warp / per_row : warp * kRows);
+    for (int32_t flat = flat0; flat < flat0 + kRows && flat < tile_rows; ++flat) {
+      const int32_t kh = flat / p.ws.part_rows, r = flat - kh * p.ws.part_rows;
+      const int32_t tok = e.y * p.sh.tokens_per_item + r / p.group;
+      if (tok < __ldg(p.draft_lens + e.x) && __ldcg(p.ws.bad + static_cast<int64_t>(e.x) * p.hkv + kh) != 0)
+        add_odd_values<D>(p, e.x, tok, kh * p.group + r % p.group);
+    }
+  }
+}
+
+// The same for query tile i (of all requests and kv heads) if it is of a marked pair and was not split (its keys fit
+// the chunk), by a CTA.
+template <int D>
+__device__ __forceinline__ void add_to_whole_rows(const TreeParams& p, int64_t i, int64_t tiles) {
+  const int64_t pair = i / p.sh.q_tiles;
+  if (i >= tiles || __ldcg(p.ws.bad + pair) == 0) return;
+  const int32_t b = static_cast<int32_t>(pair / p.hkv), kh = static_cast<int32_t>(pair % p.hkv);
+  const int32_t t0 = static_cast<int32_t>(i % p.sh.q_tiles) * p.sh.tokens_per_item;
+  int32_t P, T;
+  if (!tree_request(p, b, P, T, false) || P + T > __ldcg(p.ws.header + 2)) return;
+  const int32_t rows = min(T - t0, p.sh.tokens_per_item) * p.group;
+  for (int32_t r = threadIdx.x >> 5; r < rows; r += kMergeWarps)
+    add_odd_values<D>(p, b, t0 + r / p.group, kh * p.group + r % p.group);
+}
+
+// Join the splits (o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M)), and add the values that are not finite to the rows
+// of marked (request, kv head) pairs: to a split tile's row by the warp that wrote it, to the others at the end, by
+// (pair, query tile) over the grid.  Persistent: a unit is kMergeThreads / 8 rows of a split query tile (all kv heads), 8 lanes
 // per row, or (FEW) kMergeWarps / `per_row` rows, `per_row` warps each taking a share of a row's partials, so
 // that few rows with many splits do not wait on one warp's loads.
 template <int D, bool FEW>
@@ -296,9 +344,20 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   // The attention kernel waited for the plan before it let this one launch: the plan's lists may be read at
   // once.  The partials and the marks may be read, and o written, once the attention kernel is complete.
   griddep_launch();
+  // (With the wait comes the load of a mark for the query tiles that were not split, looked at in the end: of tile
+  // blockIdx.x + lookers * threadIdx.x, so that marked ones are spread over the CTAs of the first wave.)
+  const int32_t lookers = min(static_cast<int32_t>(gridDim.x), kTreeSms);
+  const int64_t tiles = static_cast<int64_t>(p.batch) * p.hkv * p.sh.q_tiles;
+  auto pair_of = [&](int64_t i) { return i < tiles ? static_cast<int32_t>(i / p.sh.q_tiles) : -1; };
+  auto mark_of = [&](int32_t pair) -> int32_t { return pair >= 0 ? __ldcg(p.ws.bad + pair) : 0; };
+  const int32_t first_pair = blockIdx.x < lookers ? pair_of(blockIdx.x + static_cast<int64_t>(threadIdx.x) * lookers) : -1;
+  int32_t mark = 0;
   bool waited = false;
   auto wait_partials = [&]() {
-    if (!waited) griddep_wait();
+    if (!waited) {
+      griddep_wait();
+      mark = mark_of(first_pair);
+    }
     waited = true;
   };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
@@ -308,6 +367,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   const int32_t tile_rows = p.hkv * p.ws.part_rows;  // rows of a query tile, all kv heads
   const int32_t chunks = (tile_rows + rows_per_unit - 1) / rows_per_unit;
   const int64_t units = static_cast<int64_t>(__ldcg(p.ws.header + 3)) * chunks;
+  bool marked = false;  // one of this thread's rows is of a marked pair
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t entry = u / chunks;
     const int32_t flat = static_cast<int32_t>(u - entry * chunks) * rows_per_unit + mine;
@@ -321,7 +381,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     const int64_t row = __ldg(p.qo_indptr + e.x) + tok;
     __nv_bfloat16* dst = p.o + (row * p.hq + kh * p.group + r % p.group) * D;
     wait_partials();
-    const bool mine_to_write = live && !__ldcg(p.ws.bad + e.x * p.hkv + kh);  // (the marked are recomputed below)
+    marked = marked || (live && __ldcg(p.ws.bad + static_cast<int64_t>(e.x) * p.hkv + kh) != 0);
     auto lse_at = [&](int s) { return __ldcg(p.ws.part_lse + row0 + s * slot_rows); };
     auto row_at = [&](int s, float(&x)[V]) { load_row_part<LPR, V>(p.ws.part_o + (row0 + s * slot_rows) * D, sub, x); };
     float acc[V], wsum;
@@ -336,7 +396,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
       for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
       if (lane == 0) s_m[warp] = m, s_w[warp] = wsum;
       __syncthreads();
-      if (share != 0 || !mine_to_write) continue;
+      if (share != 0 || !live) continue;
       join_shares<V>(per_row, warp, s_acc, s_m, s_w, acc, wsum);
       const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
@@ -344,29 +404,25 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
         *reinterpret_cast<__nv_bfloat162*>(dst + lane * V + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
     } else {
       merge_rows<LPR, V, 256 / D>(live ? e.w : 0, lse_at, row_at, acc, wsum);
-      if (mine_to_write) store_row_part<LPR, V>(dst, sub, acc, wsum == 0.f ? 0.f : 1.f / wsum);
+      if (live) store_row_part<LPR, V>(dst, sub, acc, wsum == 0.f ? 0.f : 1.f / wsum);
     }
   }
+  if (__any_sync(0xffffffffu, marked)) {
+    __syncwarp();
+    add_to_split_rows<D, FEW>(p, per_row);
+  }
   wait_partials();
-  const int64_t pairs = static_cast<int64_t>(p.batch) * p.hkv;
-  const int64_t threads = static_cast<int64_t>(gridDim.x) * kMergeThreads;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kMergeThreads; i0 < pairs; i0 += threads) {
-    const int64_t mine = i0 + threadIdx.x;
-    const bool marked = mine < pairs && __ldcg(p.ws.bad + mine) != 0;
-    if (!__syncthreads_or(marked)) continue;
-    for (int64_t pair = i0; pair < i0 + kMergeThreads && pair < pairs; ++pair) {
-      const int32_t b = static_cast<int32_t>(pair / p.hkv), kh = static_cast<int32_t>(pair % p.hkv);
-      int32_t P, T;
-      if (!__ldcg(p.ws.bad + pair) || !tree_request(p, b, P, T, false)) continue;
-      for (int32_t r = warp; r < T * p.group; r += kMergeThreads / 32)
-        recompute_row<D>(p, b, P, T, r / p.group, kh * p.group + r % p.group);
-    }
+  if (blockIdx.x >= lookers) return;
+  for (int64_t i0 = blockIdx.x; i0 < tiles; i0 += static_cast<int64_t>(lookers) * kMergeThreads) {
+    if (i0 != blockIdx.x) mark = mark_of(pair_of(i0 + static_cast<int64_t>(threadIdx.x) * lookers));
+    if (__syncthreads_or(mark != 0))
+      for (int32_t k = 0; k < kMergeThreads; ++k) add_to_whole_rows<D>(p, i0 + static_cast<int64_t>(k) * lookers, tiles);
   }
 }
 
 // The merge of a small narrow call: a unit is kMergeWarps / `per_row` rows (request, kv head, row), of every
 // request, `per_row` warps each taking a share of a row's partials.  A row whose request is one piece was written
-// directly; a row of a marked (request, kv head) is recomputed by its first warp.
+// directly; to a row of a marked (request, kv head) its first warp adds the values that are not finite.
 template <int D, int N>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const __grid_constant__ TreeParams p,
                                                                          int per_row) {
@@ -382,7 +438,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const _
   const bool in = flat < p.batch * p.sh.q_tiles * rows;
   const int32_t tile = in ? flat / rows : 0, kh = in ? (flat - tile * rows) / p.ws.part_rows : 0;  // of a request
   const int32_t r = in ? flat - tile * rows - kh * p.ws.part_rows : 0;
-  const int32_t P = of_request(small.P, tile), T = of_request(small.T, tile), q0 = of_request(small.q0, tile);
+  const int32_t P = of_request(small.P, tile), q0 = of_request(small.q0, tile);
   const int32_t n = of_request(small.plan.pieces, tile), first = of_request(small.plan.first, tile);
   const int32_t tok = r / p.group;
   const bool live = in && tok < of_request(small.tokens, tile);
@@ -407,14 +463,16 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_small_kernel(const _
     if (share == 0) join_shares<V>(per_row, warp, s_acc, s_m, s_w, acc, wsum);
   }
   if (!live || share != 0) return;
-  if (marked) {
-    const int32_t b = tile / p.sh.q_tiles;
-    recompute_row<D>(p, b, P, T, (tile - b * p.sh.q_tiles) * p.sh.tokens_per_item + tok, kh * p.group + r % p.group);
-  } else if (n > 1) {
+  if (n > 1) {
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
     for (int v = 0; v < V; v += 2)
       *reinterpret_cast<__nv_bfloat162*>(dst + lane * V + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+  }
+  if (marked) {
+    __syncwarp();
+    const int32_t b = tile / p.sh.q_tiles;
+    add_odd_values<D>(p, b, (tile - b * p.sh.q_tiles) * p.sh.tokens_per_item + tok, kh * p.group + r % p.group);
   }
 }
 
@@ -451,6 +509,7 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
   tp.tree_chunk = p.ws.header + 2;
   tp.tree_mask = p.mask;
   tp.mask_words = p.mask_words;
+  tp.tree_odd = p.ws.bad;
   tp.part_rows = p.ws.part_rows;
   tp.part_o = p.ws.part_o;
   tp.part_lse = p.ws.part_lse;

@@ -171,12 +171,38 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
     for (int j = 0; j < OB; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
     const int32_t n_slabs = (it.k1 - it.k0 + SLAB - 1) / SLAB;
     bool ok = true;
-    uint32_t odd = 0;  // V values that are not finite, in slabs with drafted tokens
+    bool odd = false;  // this warp cleared a drafted token's V value that was not finite
     for (int32_t s = 0; s < n_slabs; ++s, ++c) {
       const int st = c % rg.nstage;
       if (!mbar_wait(rg.full0 + 8 * st, (c / rg.nstage) & 1)) { ok = false; break; }
       if (busy) {
         const uint32_t stage = rg.stage0 + st * rg.stage_bytes;
+        const int32_t key0 = it.k0 + s * SLAB;
+        if (key0 + SLAB > it.P) {
+          // Drafted tokens' V values that are not finite would reach rows that do not see them through their zero
+          // probability: they are set to 0 here, and the merge kernel adds them to the rows that see them.  (Prefix
+          // tokens of the slab stay as they are.)  Both warps of a head do this, each before its own product: a
+          // value that one of them finds already cleared is cleared for both, and whichever found it marks it.
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < SLAB / 16 * (D / 16); ++e) {
+            uint32_t w[4];
+            ldsm_x4(stage + v_off + (e / (D / 16)) * 16 * RS + (e % (D / 16)) * 32, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
+          }
+          if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+            const uint32_t v0 = stage + SLAB * RS + hl * D * 2;
+            bool cleared = false;
+#pragma unroll 1
+            for (int e = lane; e < SLAB * (D / 8); e += 32)
+              if (key0 + e / (D / 8) >= it.P)
+                cleared = zero_not_finite_bf16x8(v0 + e / (D / 8) * RS + e % (D / 8) * 16) || cleared;
+            fence_proxy_async_smem();  // the stage's next copies come through the async proxy
+            __syncwarp();
+            odd = __any_sync(0xffffffffu, cleared) || odd;
+          }
+        }
         float x[NB][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b) x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
@@ -194,7 +220,6 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[b][e] *= p.scale_log2;
-        const int32_t key0 = it.k0 + s * SLAB;
         if (key0 + SLAB > it.P) {
           // a slab with drafted tokens (or past them): bit k of vis = key key0 + k is visible to the row
           auto visible = [&](int32_t tok, bool live) -> uint32_t {
@@ -270,26 +295,16 @@ __global__ void __launch_bounds__(32 * (tree_consumers(D) + kRingProducers), 1)
           }
         }
       }
-      if (rb == 0 && it.k0 + (s + 1) * SLAB > it.P) {
-        // The head's V rows of a slab with drafted tokens: a value that is not finite would reach rows that do not
-        // see it through their zero probability; the merge kernel recomputes such a (request, kv head).
-        const uint32_t v_row = rg.stage0 + st * rg.stage_bytes + v_off;
-#pragma unroll
-        for (int e = 0; e < SLAB / 16 * (D / 16); ++e) {
-          uint32_t w[4];
-          ldsm_x4(v_row + (e / (D / 16)) * 16 * RS + (e % (D / 16)) * 32, w[0], w[1], w[2], w[3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) odd |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
-        }
-      }
       __syncwarp();
       if (lane == 0) mbar_arrive(rg.empty0 + 8 * st);
     }
     if (!ok) break;
-    if (rb == 0) {
-      // listed items add to marks the plan kernel cleared; a small call's piece writes its own
-      odd = __any_sync(0xffffffffu, odd);
-      if (lane == 0 && (SMALL || odd)) p.ws.bad[static_cast<int64_t>(it.mark) * p.hkv + kh] = odd;
+    // listed items add to marks the plan kernel cleared; a small call's piece writes its own, each of a head's two warps
+    // a half of it
+    if (lane == 0 && (SMALL || odd)) {
+      int32_t* mark = p.ws.bad + static_cast<int64_t>(it.mark) * p.hkv + kh;
+      if (SMALL && p.sh.row_blocks == 2) reinterpret_cast<uint16_t*>(mark)[rb] = odd;
+      else *mark = odd;
     }
     if (!busy) continue;
 #pragma unroll
