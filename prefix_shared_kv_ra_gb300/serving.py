@@ -14,7 +14,8 @@ explainer, §04; anrans handbook "v0.2：不到四千行的调度核心跑出 3.
   ra_decode_attention replayed from a CUDA graph captured per padded batch size (padding rows
   read and write the dummy slot 0, as the pages' CUDA-graph decode does);
   with kv_dtype="e4m3" the cache is a quantised pool: ra_kv8_store and ra_kv8_decode_attention, and for the
-  extend call the admitted requests' contexts read back into bf16 rows of the step (ra_kv8_load);
+  extend call the slots of the admitted requests' contexts read back, each once, into bf16 rows of the step
+  (ra_kv8_load);
 * completion: a finished turn is inserted into the tree (slots of positions another request
   inserted meanwhile are freed), unlocked, and its row released.
 
@@ -118,13 +119,19 @@ class ServingReplay:
         """K and V pool, table and table rows of the extend call over the admitted requests."""
         if self.kv8_pool is None:
             return self.k_pool, self.v_pool, self.table, rows
-        # row i of the call's own pool holds the i-th position of the requests' contexts, one after the other
+        # the call's own pool holds each slot of the requests' contexts once (they share cached prefixes), in slot order
         lens = np.array([r.slots.size for r in admitted])
         starts = np.concatenate([[0], np.cumsum(lens)])
-        k = torch.empty((int(starts[-1]), self.hkv, self.d), dtype=torch.bfloat16, device=self.dev)
+        slots = np.concatenate([r.slots for r in admitted])
+        row_of = np.zeros(self.kv8_pool.shape[0], np.int32)
+        row_of[slots] = 1
+        distinct = np.flatnonzero(row_of)
+        row_of[distinct] = np.arange(distinct.size, dtype=np.int32)
+        k = torch.empty((distinct.size, self.hkv, self.d), dtype=torch.bfloat16, device=self.dev)
         v = torch.empty_like(k)
-        ra_kv8_load(self.kv8_pool, self._i32(np.concatenate([r.slots for r in admitted])), k, v, device_error=self.err)
-        table = np.minimum(starts[:-1, None] + np.arange(lens.max())[None, :], starts[1:, None] - 1)
+        ra_kv8_load(self.kv8_pool, self._i32(distinct), k, v, device_error=self.err)
+        # (entries past a context repeat its last one)
+        table = row_of[slots[np.minimum(starts[:-1, None] + np.arange(lens.max())[None, :], starts[1:, None] - 1)]]
         return k, v, self._i32(table), self._i32(np.arange(len(admitted)))
 
     # ------------------------------------------------------------------ decode graphs
