@@ -296,7 +296,8 @@ def _native():
     if _binding is None:
         lib = load()
         if not os.path.exists(_build.BINDING):
-            raise ImportError(f"{_build.BINDING} is not built; run prefix_shared_kv_ra_gb300._build.build()")
+            raise ImportError(f"{_build.BINDING}, the binding for this Python and torch, is not built; run "
+                              "prefix_shared_kv_ra_gb300._build.build()")
         spec = importlib.util.spec_from_file_location("_ra_binding", _build.BINDING)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)

@@ -3,8 +3,9 @@
 Each translation unit is compiled in parallel to an object file under
 ``_build/``; they are linked into ``prefix_shared_kv_ra_gb300/libra.so``
 (static cudart, no libcuda link dependency: the driver entry points the
-library needs are resolved at run time).  ``_ra_binding.so`` beside it is the Python
-side of the small operators, C++.  A rebuild happens only when a
+library needs are resolved at run time).  ``_ra_binding.*.so`` beside it is the Python
+side of the small operators, C++ on torch's tensors: it fits the Python and torch it was built
+with only, which its name gives.  A rebuild happens only when a
 source or header is newer than the library.
 """
 from __future__ import annotations
@@ -18,12 +19,15 @@ import subprocess
 import sys
 import sysconfig
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libra.so")
-BINDING = os.path.join(PKG, "_ra_binding.so")  # argument checks of the small operators (CPython API and torch's C++ tensors)
+# argument checks of the small operators (CPython API and torch's C++ tensors)
+BINDING = os.path.join(PKG, f"_ra_binding.{sysconfig.get_config_var('SOABI')}.torch{torch.__version__}.so")
 SOURCES = ["api_common.cu", "kv_store.cu", "decode.cu", "extend.cu", "decode_static.cu",
            "kv8_store.cu", "decode_kv8.cu", "qk_norm_rope.cu", "tree.cu", "tree_narrow.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
