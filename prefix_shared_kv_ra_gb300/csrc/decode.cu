@@ -779,7 +779,7 @@ void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const Dec
 }
 
 // kv heads per work item: the largest divisor of Hkv that is <= 8 (one consumer warp each).
-int32_t heads_per_cta(int32_t num_kv_heads) {
+static int32_t heads_per_cta(int32_t num_kv_heads) {
   for (int32_t h = kMaxHeadsPerCta; h > 1; --h)
     if (num_kv_heads % h == 0) return h;
   return 1;

@@ -111,7 +111,6 @@ DecodePlan plan_decode(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
 DecodeWorkspace layout_decode_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                         int32_t head_dim, const DecodePlan& pl, int32_t cascade_levels);
 
-int32_t heads_per_cta(int32_t num_kv_heads);  // kv heads per work item: the largest divisor of Hkv that is <= 8
 // Point p's scratch members into a workspace of layout wl (p.batch set before).
 void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace);
 // The call's plan kernel: CTA 0 plans, `store_ctas` more run the fused store.

@@ -1,12 +1,13 @@
 // slab_ring.cuh -- the producer side of the persistent split-KV kernels: items claimed from a counter, their
 // keys streamed slab by slab into a ring of shared-memory stages by bulk copies.
 //
-// One CTA per SM.  kRingProducers warps copy the records (or K and V rows) of a slab's keys, one lane per key,
+// One CTA per SM, or two for narrow head groups.  kRingProducers warps copy the records (or K and V rows) of a slab's keys, one lane per key,
 // each warp a part of the slab; the first of them also claims the items and publishes them through a ring of
 // entries with one mbarrier each, so that every producer looks one slab ahead across items for its slot ids.
 // Consumers take the items from the same entries (before the item's first slab has landed, so that they fetch
-// its queries meanwhile), wait on a stage's full barrier, arrive on its empty barrier after use and on the
-// entry's free barrier after their last look at it.  Every wait is bounded: a wait that
+// its queries meanwhile), wait on a stage's full barrier and arrive on its empty barrier after use; an entry's
+// free barrier takes the arrivals of its last readers (the consumers, or a warp that waits for them on its done
+// barrier).  Every wait is bounded: a wait that
 // runs out raises the CTA's abort flag and RA_DEVERR_TIMEOUT, and every role leaves.
 #pragma once
 
@@ -77,7 +78,7 @@ struct SlabKeys {
 };
 
 // Producer warp pw of kRingProducers (all lanes).  Src: claims() = items of the launch; item(idx, SlabKeys&);
-// copy(stage, key, slot, group, bar) issues one key's copies into row `key` of a stage; kKeyBytes() their bytes;
+// copy(stage, key, slot, group, bar) issues one key's copies into row `key` of a stage; key_bytes() their bytes;
 // counter, num_slots, err.  A slab's keys past the item's range repeat its last key (consumers mask them).
 template <int SLAB, class Src>
 __device__ __forceinline__ void slab_producer(const SlabRing& rg, const Src& src, int pw) {
