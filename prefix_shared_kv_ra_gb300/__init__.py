@@ -122,6 +122,8 @@ def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, device: torch
 
 
 def _stream(device: torch.device, stream) -> int:
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
     # the raw handle of the current stream: torch.cuda.current_stream builds a Stream object around it, which
     # costs more than the rest of a small call's checks
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
