@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   // item's first, and whether there is work in it.  Both tiles of an item work on the same key tile; of a dual
   // item, whose rows fill one query tile only, tile i takes every other one: with one tile's chain of QK, softmax
   // and PV at a time the tensor core would wait for most of it (64 requests x 8..16 drafted tokens over 512..4096
-  // keys, 64/8 heads: 148 us so, 131 with dual items, whose bound is the gathers).  A variant of its own: in
-  // the pass for 256-row items these lines cost 3%.
+  // keys, 64/8 heads: 148 us so, 134 with dual items).  A variant of its own: in the pass for 256-row items these
+  // lines cost 3%.
   auto steps_of = [](const Job& b) -> int32_t { return DUAL && b.dual ? (b.nt + 1) >> 1 : b.nt; };
   auto tile_at = [](const Job& b, int32_t j, int i) -> int32_t { return DUAL && b.dual ? 2 * j + i : j; };
   auto live_at = [](const Job& b, int32_t j, int i) -> bool {

@@ -8,10 +8,11 @@
 //  * up to 32 rows the call is bound by HBM (2 flop per byte and row), and the items of tree_narrow.cu stream
 //    whole slot rows of several heads with few large copies (small calls of up to 128 rows take several such
 //    items per request: 8 x 20..40 tokens of 16/16 heads 44.6 us on the wide path, 29.0 on this);
-//  * more rows are bound by the tensor cores and the softmax's issue slots, like extend: the tcgen05 attention
-//    kernel (attn_tc.cuh, kTreePass), up to 256 rows per item, each gathered 128-key tile feeding all of them.
-//    Its 128-byte gathers take ~16 bytes per clock and SM, 4.2 TB/s in all, whatever the rows: 64 requests x
-//    4..8 tokens over 512..4096 keys, 32/8 heads, took it 145 us and take the narrow path 111.
+//  * more rows go to the tcgen05 attention kernel (attn_tc.cuh, kTreePass), up to 256 rows per item, each gathered
+//    128-key tile feeding all of them.  It is bound by its chain of QK, softmax and PV per key tile more than by the
+//    gathers: with half of each K and V row gathered, 64 requests x 32..64 tokens over 512..4096 keys, 64/8 heads,
+//    take 261 us of 298, and x 8..16 tokens 128 of 134.  The chain's time does not shrink with the rows: x 4..8 tokens
+//    of 32/8 heads took it 145 us and take the narrow path 112.
 // Around it:
 //  * the work list (one CTA, on the device, from the real lengths; small calls: every warp for itself) splits
 //    the key ranges only as far as the SMs need it, since an unsplit item writes its bf16 rows directly while
