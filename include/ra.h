@@ -64,6 +64,8 @@ typedef enum {
 #define RA_DEVERR_LENGTH 0x4u  /* a length outside its host-side bound, or a seq_len < 1 */
 #define RA_DEVERR_TIMEOUT 0x8u /* a bounded wait inside a kernel gave up (the kernel returned early) */
 #define RA_DEVERR_POSITION 0x10u /* a token position outside [0, max_position) (rotated as position 0) */
+#define RA_DEVERR_FULL 0x20u   /* a free list without the pages a request needs, or without room for its slots */
+#define RA_DEVERR_VALUE 0x40u  /* a drafted token outside the vocabulary, or a row of it with nothing to choose from */
 
 /*
  * ra_kv_store -- write this step's new K/V rows into their pool slots.
@@ -380,6 +382,100 @@ ra_status ra_tree_attention(const void* k_pool, const void* v_pool, int64_t num_
 /* Workspace bytes ra_tree_attention needs (0 for invalid or unsupported sizes). */
 size_t ra_tree_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
                                int32_t head_dim, int32_t max_draft_len);
+
+/*
+ * ra_step_slots -- a step's slots, table entries, positions and row starts, made on the GPU from the requests' lengths.
+ * The serving pages do this on the host (each step's tokens get `out_cache_loc` slots, listed in `req_to_token`); this
+ * is an addition for callers whose lengths are on the GPU only, such as after ra_tree_verify.  Request b (table row
+ * req_pool_indices[b]) has seq_lens[b] tokens in the table and gets new_lens[b] more, at positions seq_lens[b] ..
+ * A page is page_size consecutive slots and holds page_size consecutive positions of a request: tokens in the
+ * request's last, partly filled page get the slots behind its last one, the others pages of the free list, taken from
+ * its end in the order of the requests and their positions (the n-th page taken is free_pages[free_count - 1 - n], with
+ * slots id * page_size ..).  Writes
+ *   out_cache_loc, positions: int32 [num_tokens]: slot and position of each new token, request by request; entries
+ *                behind the last new token get slot 0 (the dummy slot) and position 0;
+ *   req_to_token: each new token's slot at its position;
+ *   qo_indptr:   int32 [batch + 1]: the first token of each request;
+ *   seq_lens_out: int32 [batch]: seq_lens + new_lens (may be seq_lens itself);
+ *   free_count_out: int32 [1]: the pages left (may be free_count itself).
+ * Requests with new tokens must be in different table rows.  A request whose lengths are negative or beyond the table
+ * (RA_DEVERR_LENGTH), whose table row is out of range (RA_DEVERR_TABLE), whose tokens end behind num_tokens
+ * (RA_DEVERR_LENGTH) or whose pages the free list does not hold (RA_DEVERR_FULL; then no later request takes pages
+ * either) is flagged: its tokens keep their rows with slot 0, the table and its length stay as they are, and it takes no
+ * pages.  A page id or last slot that is negative or not a 32-bit slot is flagged RA_DEVERR_SLOT and read as slot 0; a
+ * free_count outside [0, free_capacity] is flagged RA_DEVERR_LENGTH and clamped.  page_size is 1 .. 2^20.
+ */
+ra_status ra_step_slots(int32_t* req_to_token, int64_t table_stride, int64_t table_rows,
+                        const int32_t* req_pool_indices, const int32_t* seq_lens, const int32_t* new_lens,
+                        int32_t batch, const int32_t* free_pages, int64_t free_capacity, const int32_t* free_count,
+                        int32_t* free_count_out, int32_t page_size, int32_t* out_cache_loc, int32_t* positions,
+                        int64_t num_tokens, int32_t* qo_indptr, int32_t* seq_lens_out, uint32_t* device_error,
+                        ra_stream_t stream);
+
+/*
+ * ra_tree_verify -- accept or refuse the drafted tokens of each request's tree against the target's probabilities, from
+ * given random numbers, such that the tokens that come out are distributed as the target's own.  Request b has
+ * draft_lens[b] nodes in rows qo_indptr[b] ..; node 0 is the token decided before (always accepted), node i > 0 a
+ * drafted token with parents[row] < i the index of its parent in the request.  Row `node` of the target's probabilities
+ * p (and of the drafts' q) is the distribution behind that node's token.  At a node, starting with node 0, its children
+ * are tried in index order, u the child's accept_uniforms entry and x its token:
+ *   drafts drawn from q (draft_probs given): with t = 0, S = 1 at the first child, accepted when
+ *       u q(x) S < max(p(x) - t q(x), 0);  on a refusal t <- t + S, S <- sum_v max(p(v) - t q(v), 0);
+ *   drafts taken as given (draft_probs NULL): with S = 1 and r = p, accepted when u S < r(x);  on a refusal
+ *       S <- S - r(x), r(x) <- 0.
+ * From the node where every child was refused (or that has none), next_tokens[b] is drawn from the residual
+ * r(v) = max(p(v) - t q(v), 0), or r: the smallest v with sum_{j <= v} r(j) > final_uniforms[b] sum_j r(j) (from p
+ * where nothing is left of r).  Rows of p and q are taken as normalised; negative values and NaN count as 0.  Sums
+ * and comparisons are held to about 2^-45.
+ *   target_probs, draft_probs: fp32 [total_q, vocab], rows at target_stride / draft_stride values (>= vocab).
+ *   accept_uniforms: fp32 [total_q]; final_uniforms: fp32 [batch]; in [0, 1).
+ *   path:        int32 [batch, max_draft_len]: the accepted nodes, ascending from node 0; -1 behind them.
+ *   accept_lens: int32 [batch]: their number (node 0 included); next_tokens: int32 [batch].
+ * draft_lens[b] == 0 gives no node and next token 0, as does a request whose length is outside [0, max_draft_len] or
+ * whose rows are outside [0, total_q) (flagged RA_DEVERR_LENGTH).  max_draft_len is 1 .. 1024.  A parent outside
+ * [0, i) makes node i unreachable.  A drafted token outside [0, vocab) is flagged RA_DEVERR_VALUE and has probability
+ * 0; so is a last row without a positive finite sum (next token 0).  batch == 0 is a no-op.
+ */
+ra_status ra_tree_verify(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                         int64_t draft_stride, int32_t vocab, const int32_t* draft_tokens, const int32_t* parents,
+                         const int32_t* draft_lens, const int32_t* qo_indptr, const float* accept_uniforms,
+                         const float* final_uniforms, int32_t batch, int64_t total_q, int32_t max_draft_len,
+                         int32_t* path, int32_t* accept_lens, int32_t* next_tokens, uint32_t* device_error,
+                         ra_stream_t stream);
+
+/*
+ * ra_tree_verify_greedy -- the same at temperature 0: a node's child is accepted when its token has the largest of the
+ * node's logits (the lowest such token; NaN counts as smaller than all), and next_tokens[b] is the last node's.  Only
+ * rows of accepted nodes are read.  target_logits: bf16 [total_q, vocab], or fp32 with logits_fp32 = 1, rows at
+ * logits_stride values.  Other arguments, outputs and flags are those of ra_tree_verify (RA_DEVERR_VALUE also for a
+ * row of NaN, whose next token is 0).
+ */
+ra_status ra_tree_verify_greedy(const void* target_logits, int32_t logits_fp32, int64_t logits_stride, int32_t vocab,
+                                const int32_t* draft_tokens, const int32_t* parents, const int32_t* draft_lens,
+                                const int32_t* qo_indptr, int32_t batch, int64_t total_q, int32_t max_draft_len,
+                                int32_t* path, int32_t* accept_lens, int32_t* next_tokens, uint32_t* device_error,
+                                ra_stream_t stream);
+
+/*
+ * ra_tree_commit -- after ra_tree_verify: the accepted tokens of each tree become the request's next tokens, and the
+ * slots of the refused ones return to the free list (of single slots: a token-granular pool).  out_cache_loc (int32
+ * [total_q]) are the drafted tokens' slots, path (int32 [batch, path_stride]) and accept_lens those of the
+ * verification.  For request b with P = prefix_lens[b], T = draft_lens[b], n = accept_lens[b]:
+ *   req_to_token[row, P + k] = out_cache_loc[qo_indptr[b] + path[b, k]], k < n;  entries P + n .. P + T - 1 are -1;
+ *   the slots of the T - n other nodes go to the end of free_list (entries free_count ..), request by request and in
+ *   the order of the nodes;  seq_lens_out[b] = P + n (may be prefix_lens itself);  free_count_out = free_count + all
+ *   that was returned (may be free_count itself).
+ * No K/V row moves.  A request whose lengths are negative, beyond the table or path_stride (1 .. 1024), or with n > T,
+ * or whose rows are outside [0, total_q), is flagged RA_DEVERR_LENGTH, one with a table row out of range
+ * RA_DEVERR_TABLE, and both are skipped (seq_lens_out[b] = P).  A path that does not ascend within the tree is flagged
+ * RA_DEVERR_LENGTH, slots that free_list (free_capacity entries) has no room for RA_DEVERR_FULL; they are lost.
+ */
+ra_status ra_tree_commit(int32_t* req_to_token, int64_t table_stride, int64_t table_rows,
+                         const int32_t* req_pool_indices, const int32_t* prefix_lens, const int32_t* draft_lens,
+                         const int32_t* qo_indptr, int32_t batch, const int32_t* out_cache_loc, int64_t total_q,
+                         const int32_t* path, int32_t path_stride, const int32_t* accept_lens, int32_t* seq_lens_out,
+                         int32_t* free_list, int64_t free_capacity, const int32_t* free_count, int32_t* free_count_out,
+                         uint32_t* device_error, ra_stream_t stream);
 
 /*
  * ra_selftest_bounded_wait -- check, on the current device, that a wait inside a kernel that runs out

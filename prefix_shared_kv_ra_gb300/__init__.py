@@ -29,14 +29,15 @@ __all__ = ["RAError", "ra_kv_store", "ra_extend_attention", "ra_extend_workspace
            "ra_decode_attention_static", "RA_DECODE_STATIC_SCRATCH_BYTES",
            "ra_kv8_slot_bytes", "ra_kv8_store", "ra_kv8_load", "ra_kv8_decode_attention",
            "ra_qk_norm_rope_store", "ra_qk_norm_rope_kv8_store", "ra_tree_attention", "ra_tree_workspace_bytes",
+           "ra_step_slots", "ra_tree_verify", "ra_tree_verify_greedy", "ra_tree_commit",
            "ra_abi_version", "ra_selftest_bounded_wait", "library_path", "load", "DEVERR_SLOT", "DEVERR_TABLE", "DEVERR_LENGTH",
-           "DEVERR_TIMEOUT", "DEVERR_POSITION"]
+           "DEVERR_TIMEOUT", "DEVERR_POSITION", "DEVERR_FULL", "DEVERR_VALUE"]
 
 RA_OK = 0
 RA_ERR_UNSUPPORTED = 2
 RA_DECODE_STATIC_SCRATCH_BYTES = 32 << 20  # size of the library's static decode scratch (include/ra.h)
 DEVERR_SLOT, DEVERR_TABLE, DEVERR_LENGTH, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
-DEVERR_POSITION = 0x10
+DEVERR_POSITION, DEVERR_FULL, DEVERR_VALUE = 0x10, 0x20, 0x40
 _lib = None
 _binding = None
 
@@ -87,13 +88,18 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.ra_qk_norm_rope_kv8_store.argtypes = norm_rope + [P, i64, P, i64, P, P]
     lib.ra_tree_attention.argtypes = [P, P, i64, i32, i32, P, P, i32, f32, P, i64, i64, P, P, P, P, P, i32, i32, i64,
                                       i32, i32, P, sz, P, P]
+    lib.ra_step_slots.argtypes = [P, i64, i64, P, P, P, i32, P, i64, P, P, i32, P, P, i64, P, P, P, P]
+    lib.ra_tree_verify.argtypes = [P, i64, P, i64, i32, P, P, P, P, P, P, i32, i64, i32, P, P, P, P, P]
+    lib.ra_tree_verify_greedy.argtypes = [P, i32, i64, i32, P, P, P, P, i32, i64, i32, P, P, P, P, P]
+    lib.ra_tree_commit.argtypes = [P, i64, i64, P, P, P, P, i32, P, i64, P, i32, P, P, P, i64, P, P, P, P]
     lib.ra_tree_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32]
     lib.ra_tree_workspace_bytes.restype = sz
     lib.ra_decode_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32]
     lib.ra_decode_workspace_bytes.restype = sz
     for f in (lib.ra_kv_store, lib.ra_extend_attention, lib.ra_decode_attention, lib.ra_abi_version, lib.ra_kv8_store,
               lib.ra_kv8_load, lib.ra_kv8_decode_attention, lib.ra_qk_norm_rope_store,
-              lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention):
+              lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention, lib.ra_step_slots, lib.ra_tree_verify,
+              lib.ra_tree_verify_greedy, lib.ra_tree_commit):
         f.restype = ctypes.c_int
     lib.ra_status_string.argtypes = [ctypes.c_int]
     lib.ra_status_string.restype = ctypes.c_char_p
@@ -304,7 +310,8 @@ def _native():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         fns = (lib.ra_kv8_store, lib.ra_kv8_load, lib.ra_kv8_slot_bytes, lib.ra_kv8_decode_attention,
-               lib.ra_qk_norm_rope_store, lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention)
+               lib.ra_qk_norm_rope_store, lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention, lib.ra_step_slots,
+               lib.ra_tree_verify, lib.ra_tree_verify_greedy, lib.ra_tree_commit)
         mod.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
         _binding = mod
     return _binding
@@ -390,5 +397,64 @@ def ra_tree_attention(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Tenso
     status = (_binding or _native()).tree(k_pool, v_pool, q, o, req_to_token, req_pool_indices, prefix_lens, draft_lens,
                                           qo_indptr, tree_mask, max_draft_len, max_prefix_len, sm_scale, workspace,
                                           device_error, stream)
+    if status:
+        _check(status)
+
+
+def ra_step_slots(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor, seq_lens: torch.Tensor,
+                  new_lens: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor,
+                  out_cache_loc: torch.Tensor, positions: torch.Tensor, qo_indptr: torch.Tensor,
+                  seq_lens_out: torch.Tensor, *, page_size: int = 1, free_count_out: Optional[torch.Tensor] = None,
+                  device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """new_lens[b] new tokens behind the seq_lens[b] of request b: their slots (pages taken from the end of
+    free_pages[:free_count]) into req_to_token and out_cache_loc, their positions, the requests' first rows
+    (qo_indptr) and new lengths.  All int32; free_count [1] (written in place unless free_count_out is given);
+    entries of out_cache_loc and positions [num_tokens] behind the last new token get 0."""
+    status = (_binding or _native()).step_slots(req_to_token, req_pool_indices, seq_lens, new_lens, free_pages, free_count,
+                                                out_cache_loc, positions, qo_indptr, seq_lens_out, page_size,
+                                                free_count_out, device_error, stream)
+    if status:
+        _check(status)
+
+
+def ra_tree_verify(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], draft_tokens: torch.Tensor,
+                   parents: torch.Tensor, draft_lens: torch.Tensor, qo_indptr: torch.Tensor,
+                   accept_uniforms: torch.Tensor, final_uniforms: torch.Tensor, path: torch.Tensor,
+                   accept_lens: torch.Tensor, next_tokens: torch.Tensor, *, max_draft_len: int,
+                   device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Accept or refuse drafted trees against the target's probabilities (fp32 [total_q, vocab], any row stride; row of
+    a node: the distribution behind its token) from given uniform numbers: path [batch, max_draft_len] (accepted
+    nodes, node 0 first, -1 behind), accept_lens and next_tokens [batch] (int32).  draft_probs: the distributions that
+    each node's children were drawn from, or None for drafts taken as given."""
+    status = (_binding or _native()).tree_verify(target_probs, draft_probs, draft_tokens, parents, draft_lens, qo_indptr,
+                                                 accept_uniforms, final_uniforms, path, accept_lens, next_tokens,
+                                                 max_draft_len, device_error, stream)
+    if status:
+        _check(status)
+
+
+def ra_tree_verify_greedy(target_logits: torch.Tensor, draft_tokens: torch.Tensor, parents: torch.Tensor,
+                          draft_lens: torch.Tensor, qo_indptr: torch.Tensor, path: torch.Tensor,
+                          accept_lens: torch.Tensor, next_tokens: torch.Tensor, *, max_draft_len: int,
+                          device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ra_tree_verify at temperature 0: a child is accepted when its token has the largest of its parent's logits
+    (bf16 or fp32 [total_q, vocab], any row stride; the lowest token of equal ones)."""
+    status = (_binding or _native()).tree_verify_greedy(target_logits, draft_tokens, parents, draft_lens, qo_indptr, path,
+                                                        accept_lens, next_tokens, max_draft_len, device_error, stream)
+    if status:
+        _check(status)
+
+
+def ra_tree_commit(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor, prefix_lens: torch.Tensor,
+                   draft_lens: torch.Tensor, qo_indptr: torch.Tensor, out_cache_loc: torch.Tensor, path: torch.Tensor,
+                   accept_lens: torch.Tensor, seq_lens_out: torch.Tensor, free_list: torch.Tensor,
+                   free_count: torch.Tensor, *, free_count_out: Optional[torch.Tensor] = None,
+                   device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The accepted path of each verified tree into req_to_token behind the prefix, the new lengths into seq_lens_out,
+    the refused tokens' slots to the end of free_list (free_count [1] written in place unless free_count_out is
+    given).  All int32."""
+    status = (_binding or _native()).tree_commit(req_to_token, req_pool_indices, prefix_lens, draft_lens, qo_indptr,
+                                                 out_cache_loc, path, accept_lens, seq_lens_out, free_list, free_count,
+                                                 free_count_out, device_error, stream)
     if status:
         _check(status)

@@ -28,6 +28,10 @@ decltype(&ra_kv8_decode_attention) p_kv8_decode;
 decltype(&ra_qk_norm_rope_store) p_norm_rope;
 decltype(&ra_qk_norm_rope_kv8_store) p_norm_rope_kv8;
 decltype(&ra_tree_attention) p_tree;
+decltype(&ra_step_slots) p_step_slots;
+decltype(&ra_tree_verify) p_tree_verify;
+decltype(&ra_tree_verify_greedy) p_tree_verify_greedy;
+decltype(&ra_tree_commit) p_tree_commit;
 
 PyObject* s_cuda_stream;
 
@@ -308,10 +312,150 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (table, rpi, seq_lens, new_lens, free_pages, free_count, out_cache_loc, positions, qo_indptr, seq_lens_out, page_size,
+//  free_count_out or None, err, stream)
+PyObject* step_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return method("ra_step_slots", n, 14, [&] {
+    const at::Tensor &table = tensor(a[0], "req_to_token", 2), &rpi = tensor(a[1], "req_pool_indices", 1),
+                     &lens = tensor(a[2], "seq_lens", 1), &news = tensor(a[3], "new_lens", 1),
+                     &pages = tensor(a[4], "free_pages", 1), &count = tensor(a[5], "free_count", 1),
+                     &loc = tensor(a[6], "out_cache_loc", 1), &positions = tensor(a[7], "positions", 1),
+                     &qo = tensor(a[8], "qo_indptr", 1), &out = tensor(a[9], "seq_lens_out", 1);
+    const at::Tensor& left = a[11] == Py_None ? count : tensor(a[11], "free_count_out", 1);
+    const at::Device device = table.device();
+    const int32_t batch = narrow(rpi.size(0), "batch");
+    length(lens, batch, "seq_lens", "[batch]");
+    length(news, batch, "new_lens", "[batch]");
+    length(out, batch, "seq_lens_out", "[batch]");
+    length(qo, static_cast<int64_t>(batch) + 1, "qo_indptr", "[batch + 1]");
+    length(positions, loc.size(0), "positions", "[num_tokens]");
+    length(count, 1, "free_count", "[1]");
+    length(left, 1, "free_count_out", "[1]");
+    const int32_t page = int_of(a[10], "page_size");
+    auto i32 = [&](const at::Tensor& t, const char* name) { return data<int32_t>(t, name, at::kInt, device); };
+    int32_t *tp = i32(table, "req_to_token"), *lp = i32(loc, "out_cache_loc"), *pp = i32(positions, "positions"),
+            *qp = i32(qo, "qo_indptr"), *op = i32(out, "seq_lens_out"), *fo = i32(left, "free_count_out");
+    const int32_t *rp = i32(rpi, "req_pool_indices"), *sp = i32(lens, "seq_lens"), *np = i32(news, "new_lens"),
+                  *fp = i32(pages, "free_pages"), *fc = i32(count, "free_count");
+    uint32_t* err = optional_data<uint32_t>(a[12], "device_error", at::kInt, device);
+    return launch(device, a[13], [&](ra_stream_t s) {
+      return p_step_slots(tp, table.size(1), table.size(0), rp, sp, np, batch, fp, pages.size(0), fc, fo, page, lp, pp,
+                          loc.size(0), qp, op, err, s);
+    });
+  });
+}
+
+// Rows [n, vocab] of one of two types, the values of a row contiguous, rows at any stride (>= vocab).
+const void* vocab_rows(const at::Tensor& t, const char* name, const at::Device& device, int64_t* stride) {
+  if (t.device() != device)
+    wrong(PyExc_ValueError, "%s: expected device %s, got %s", name, device.str().c_str(), t.device().str().c_str());
+  const int64_t n = t.size(0), vocab = t.size(1);
+  if (vocab > 1 && t.stride(1) != 1) wrong(PyExc_ValueError, "%s: a row's values must be contiguous", name);
+  *stride = n > 1 ? t.stride(0) : vocab;
+  if (*stride < vocab) wrong(PyExc_ValueError, "%s: rows must not overlap", name);
+  return t.data_ptr();
+}
+
+// target, [draft_probs], tokens, parents, draft_lens, qo_indptr, [accept_uniforms, final_uniforms], path, accept_lens,
+// next_tokens, max_draft_len, err, stream; in brackets: not for the greedy form
+PyObject* verify(PyObject* const* a, Py_ssize_t n, bool greedy) {
+  return method(greedy ? "ra_tree_verify_greedy" : "ra_tree_verify", n, greedy ? 11 : 14, [&] {
+    PyObject* const* tree = a + (greedy ? 1 : 2);
+    PyObject* const* out = tree + (greedy ? 4 : 6);
+    const at::Tensor &target = tensor(a[0], greedy ? "target_logits" : "target_probs", 2),
+                     &tokens = tensor(tree[0], "draft_tokens", 1), &parents = tensor(tree[1], "parents", 1),
+                     &drafts = tensor(tree[2], "draft_lens", 1), &qo = tensor(tree[3], "qo_indptr", 1),
+                     &path = tensor(out[0], "path", 2), &accepted = tensor(out[1], "accept_lens", 1),
+                     &next = tensor(out[2], "next_tokens", 1);
+    const at::Device device = target.device();
+    const int64_t total = target.size(0);
+    const int32_t batch = narrow(drafts.size(0), "batch"), vocab = narrow(target.size(1), "vocab");
+    const int32_t max_draft = int_of(out[3], "max_draft_len");
+    length(tokens, total, "draft_tokens", "[total_q]");
+    length(parents, total, "parents", "[total_q]");
+    length(qo, static_cast<int64_t>(batch) + 1, "qo_indptr", "[batch + 1]");
+    length(accepted, batch, "accept_lens", "[batch]");
+    length(next, batch, "next_tokens", "[batch]");
+    if (path.size(0) != batch || path.size(1) != max_draft)
+      wrong(PyExc_ValueError, "path: expected shape [batch, max_draft_len]");
+    int64_t stride, draft_stride = 0;
+    const void* tp = vocab_rows(target, greedy ? "target_logits" : "target_probs", device, &stride);
+    auto i32 = [&](const at::Tensor& t, const char* name) { return data<int32_t>(t, name, at::kInt, device); };
+    const int32_t *kp = i32(tokens, "draft_tokens"), *pp = i32(parents, "parents"), *dp = i32(drafts, "draft_lens"),
+                  *qp = i32(qo, "qo_indptr");
+    int32_t *wp = i32(path, "path"), *ap = i32(accepted, "accept_lens"), *np = i32(next, "next_tokens");
+    uint32_t* err = optional_data<uint32_t>(out[4], "device_error", at::kInt, device);
+    if (greedy) {
+      const bool fp32 = target.scalar_type() == at::kFloat;
+      if (!fp32) typed(target, "target_logits", at::kBFloat16, device);
+      return launch(device, out[5], [&](ra_stream_t s) {
+        return p_tree_verify_greedy(tp, fp32, stride, vocab, kp, pp, dp, qp, batch, total, max_draft, wp, ap, np, err, s);
+      });
+    }
+    typed(target, "target_probs", at::kFloat, device);
+    const void* draft = nullptr;
+    if (a[1] != Py_None) {
+      const at::Tensor& q = tensor(a[1], "draft_probs", 2);
+      typed(q, "draft_probs", at::kFloat, device);
+      same_shape(q, target, "draft_probs", "that of target_probs");
+      draft = vocab_rows(q, "draft_probs", device, &draft_stride);
+    }
+    const at::Tensor &ua = tensor(tree[4], "accept_uniforms", 1), &uf = tensor(tree[5], "final_uniforms", 1);
+    length(ua, total, "accept_uniforms", "[total_q]");
+    length(uf, batch, "final_uniforms", "[batch]");
+    const float *uap = data<float>(ua, "accept_uniforms", at::kFloat, device),
+                *ufp = data<float>(uf, "final_uniforms", at::kFloat, device);
+    return launch(device, out[5], [&](ra_stream_t s) {
+      return p_tree_verify(static_cast<const float*>(tp), stride, static_cast<const float*>(draft), draft_stride, vocab, kp,
+                           pp, dp, qp, uap, ufp, batch, total, max_draft, wp, ap, np, err, s);
+    });
+  });
+}
+
+PyObject* tree_verify(PyObject*, PyObject* const* a, Py_ssize_t n) { return verify(a, n, false); }
+PyObject* tree_verify_greedy(PyObject*, PyObject* const* a, Py_ssize_t n) { return verify(a, n, true); }
+
+// (table, rpi, prefix_lens, draft_lens, qo_indptr, out_cache_loc, path, accept_lens, seq_lens_out, free_list, free_count,
+//  free_count_out or None, err, stream)
+PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return method("ra_tree_commit", n, 14, [&] {
+    const at::Tensor &table = tensor(a[0], "req_to_token", 2), &rpi = tensor(a[1], "req_pool_indices", 1),
+                     &prefix = tensor(a[2], "prefix_lens", 1), &drafts = tensor(a[3], "draft_lens", 1),
+                     &qo = tensor(a[4], "qo_indptr", 1), &loc = tensor(a[5], "out_cache_loc", 1),
+                     &path = tensor(a[6], "path", 2), &accepted = tensor(a[7], "accept_lens", 1),
+                     &out = tensor(a[8], "seq_lens_out", 1), &list = tensor(a[9], "free_list", 1),
+                     &count = tensor(a[10], "free_count", 1);
+    const at::Tensor& left = a[11] == Py_None ? count : tensor(a[11], "free_count_out", 1);
+    const at::Device device = table.device();
+    const int32_t batch = narrow(rpi.size(0), "batch");
+    length(prefix, batch, "prefix_lens", "[batch]");
+    length(drafts, batch, "draft_lens", "[batch]");
+    length(qo, static_cast<int64_t>(batch) + 1, "qo_indptr", "[batch + 1]");
+    length(path, batch, "path", "[batch, max_draft_len]");
+    length(accepted, batch, "accept_lens", "[batch]");
+    length(out, batch, "seq_lens_out", "[batch]");
+    length(count, 1, "free_count", "[1]");
+    length(left, 1, "free_count_out", "[1]");
+    auto i32 = [&](const at::Tensor& t, const char* name) { return data<int32_t>(t, name, at::kInt, device); };
+    int32_t *tp = i32(table, "req_to_token"), *op = i32(out, "seq_lens_out"), *fp = i32(list, "free_list"),
+            *fo = i32(left, "free_count_out");
+    const int32_t *rp = i32(rpi, "req_pool_indices"), *pp = i32(prefix, "prefix_lens"), *dp = i32(drafts, "draft_lens"),
+                  *qp = i32(qo, "qo_indptr"), *lp = i32(loc, "out_cache_loc"), *wp = i32(path, "path"),
+                  *ap = i32(accepted, "accept_lens"), *fc = i32(count, "free_count");
+    const int32_t stride = narrow(path.size(1), "max_draft_len");
+    uint32_t* err = optional_data<uint32_t>(a[12], "device_error", at::kInt, device);
+    return launch(device, a[13], [&](ra_stream_t s) {
+      return p_tree_commit(tp, table.size(1), table.size(0), rp, pp, dp, qp, batch, lp, loc.size(0), wp, stride, ap, op, fp,
+                           list.size(0), fc, fo, err, s);
+    });
+  });
+}
+
 // init(addresses of the entry points in the order of the declarations above)
 PyObject* init(PyObject*, PyObject* args) {
-  unsigned long long a[7];
-  if (!PyArg_ParseTuple(args, "KKKKKKK", a, a + 1, a + 2, a + 3, a + 4, a + 5, a + 6)) return nullptr;
+  unsigned long long a[11];
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKKK", a, a + 1, a + 2, a + 3, a + 4, a + 5, a + 6, a + 7, a + 8, a + 9, a + 10))
+    return nullptr;
   p_kv8_store = reinterpret_cast<decltype(p_kv8_store)>(a[0]);
   p_kv8_load = reinterpret_cast<decltype(p_kv8_load)>(a[1]);
   p_kv8_slot_bytes = reinterpret_cast<decltype(p_kv8_slot_bytes)>(a[2]);
@@ -319,6 +463,10 @@ PyObject* init(PyObject*, PyObject* args) {
   p_norm_rope = reinterpret_cast<decltype(p_norm_rope)>(a[4]);
   p_norm_rope_kv8 = reinterpret_cast<decltype(p_norm_rope_kv8)>(a[5]);
   p_tree = reinterpret_cast<decltype(p_tree)>(a[6]);
+  p_step_slots = reinterpret_cast<decltype(p_step_slots)>(a[7]);
+  p_tree_verify = reinterpret_cast<decltype(p_tree_verify)>(a[8]);
+  p_tree_verify_greedy = reinterpret_cast<decltype(p_tree_verify_greedy)>(a[9]);
+  p_tree_commit = reinterpret_cast<decltype(p_tree_commit)>(a[10]);
   Py_RETURN_NONE;
 }
 
@@ -333,6 +481,10 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, "entry points of the libra
                          {"norm_rope_store", fast(norm_rope_store), METH_FASTCALL, nullptr},
                          {"norm_rope_kv8_store", fast(norm_rope_kv8_store), METH_FASTCALL, nullptr},
                          {"tree", fast(tree), METH_FASTCALL, nullptr},
+                         {"step_slots", fast(step_slots), METH_FASTCALL, nullptr},
+                         {"tree_verify", fast(tree_verify), METH_FASTCALL, nullptr},
+                         {"tree_verify_greedy", fast(tree_verify_greedy), METH_FASTCALL, nullptr},
+                         {"tree_commit", fast(tree_commit), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ra_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
