@@ -384,6 +384,46 @@ size_t ra_tree_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_hea
                                int32_t head_dim, int32_t max_draft_len);
 
 /*
+ * ra_extend_attention_mod, ra_decode_attention_mod -- ra_extend_attention and ra_decode_attention with changed scores and
+ * masks.  The serving pages' models need neither; this is an addition for models whose layers cap their scores, bias them
+ * by distance, or see a window, packed documents or a whole prefix.  For the row at position p of request b (extend: p =
+ * prefix_lens[b] + i; decode: p = seq_lens[b] - 1), the key at position j and q head h:
+ *   s = sm_scale * <q, K_j>;  with score_cap > 0: s <- score_cap * tanh(s / score_cap);
+ *   with slopes: s <- s - slopes[h] * |p - j|;
+ *   j is seen when j >= first and (j <= p or j < full), where first = max(first_key, p - window + 1, 0) (without the terms
+ *   that are not given) and full = min(full_lens[b], prefix_lens[b] + extend_lens[b]) (0 if not given).
+ * A row that sees no key gives 0.  What a row does not see has no influence on it, whatever it is (also infinities and
+ * NaN); an infinity or NaN in V of a key that it sees makes that dimension infinite or NaN.
+ *   score_cap:  0 (none), or 1e-6 .. 1e12.
+ *   window:     0 (none), or the number of keys up to its own that a row sees at most.
+ *   slopes:     fp32 [num_q_heads], or NULL.
+ *   first_key:  extend: int32 [total_q], decode: int32 [batch]; a position, e.g. of the row's document; or NULL.
+ *   full_lens:  int32 [batch], or NULL: positions below it are seen by every row of the request.
+ * Keys that no row of a tile sees are not read.  Everything else is as in ra_extend_attention and, without groups,
+ * ra_decode_attention: lengths, flags, and for decode the workspace (ra_decode_workspace_bytes with num_groups 0); for
+ * extend it is ra_extend_mod_workspace_bytes(...).  Calls that overlap on the GPU need separate workspaces.
+ */
+ra_status ra_extend_attention_mod(const void* k_pool, const void* v_pool, int64_t num_slots, int32_t num_kv_heads,
+                                  int32_t head_dim, const void* q, void* o, int32_t num_q_heads, float sm_scale,
+                                  float score_cap, int32_t window, const float* slopes, const int32_t* first_key,
+                                  const int32_t* full_lens, const int32_t* req_to_token, int64_t table_stride,
+                                  int64_t table_rows, const int32_t* req_pool_indices, const int32_t* prefix_lens,
+                                  const int32_t* extend_lens, const int32_t* qo_indptr, int32_t batch, int64_t total_q,
+                                  int32_t max_extend_len, int32_t max_prefix_len, void* workspace,
+                                  size_t workspace_bytes, uint32_t* device_error, ra_stream_t stream);
+
+/* Workspace bytes ra_extend_attention_mod needs (0 for invalid head counts). */
+size_t ra_extend_mod_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_heads, int32_t num_kv_heads);
+
+ra_status ra_decode_attention_mod(const void* k_pool, const void* v_pool, int64_t num_slots, int32_t num_kv_heads,
+                                  int32_t head_dim, const void* q, void* o, int32_t num_q_heads, float sm_scale,
+                                  float score_cap, int32_t window, const float* slopes, const int32_t* first_key,
+                                  const int32_t* req_to_token, int64_t table_stride, int64_t table_rows,
+                                  const int32_t* req_pool_indices, const int32_t* seq_lens, int32_t batch,
+                                  int32_t max_seq_len, void* workspace, size_t workspace_bytes, uint32_t* device_error,
+                                  ra_stream_t stream);
+
+/*
  * ra_step_slots -- a step's slots, table entries, positions and row starts, made on the GPU from the requests' lengths.
  * The serving pages do this on the host (each step's tokens get `out_cache_loc` slots, listed in `req_to_token`); this
  * is an addition for callers whose lengths are on the GPU only, such as after ra_tree_verify.  Request b (table row

@@ -29,6 +29,7 @@ __all__ = ["RAError", "ra_kv_store", "ra_extend_attention", "ra_extend_workspace
            "ra_decode_attention_static", "RA_DECODE_STATIC_SCRATCH_BYTES",
            "ra_kv8_slot_bytes", "ra_kv8_store", "ra_kv8_load", "ra_kv8_decode_attention",
            "ra_qk_norm_rope_store", "ra_qk_norm_rope_kv8_store", "ra_tree_attention", "ra_tree_workspace_bytes",
+           "ra_extend_attention_mod", "ra_extend_mod_workspace_bytes", "ra_decode_attention_mod",
            "ra_step_slots", "ra_tree_verify", "ra_tree_verify_greedy", "ra_tree_commit",
            "ra_abi_version", "ra_selftest_bounded_wait", "library_path", "load", "DEVERR_SLOT", "DEVERR_TABLE", "DEVERR_LENGTH",
            "DEVERR_TIMEOUT", "DEVERR_POSITION", "DEVERR_FULL", "DEVERR_VALUE"]
@@ -88,6 +89,11 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.ra_qk_norm_rope_kv8_store.argtypes = norm_rope + [P, i64, P, i64, P, P]
     lib.ra_tree_attention.argtypes = [P, P, i64, i32, i32, P, P, i32, f32, P, i64, i64, P, P, P, P, P, i32, i32, i64,
                                       i32, i32, P, sz, P, P]
+    changed = [P, P, i64, i32, i32, P, P, i32, f32, f32, i32, P, P]
+    lib.ra_extend_attention_mod.argtypes = changed + [P, P, i64, i64, P, P, P, P, i32, i64, i32, i32, P, sz, P, P]
+    lib.ra_decode_attention_mod.argtypes = changed + [P, i64, i64, P, P, i32, i32, P, sz, P, P]
+    lib.ra_extend_mod_workspace_bytes.argtypes = [i32, i64, i32, i32]
+    lib.ra_extend_mod_workspace_bytes.restype = sz
     lib.ra_step_slots.argtypes = [P, i64, i64, P, P, P, i32, P, i64, P, P, i32, P, P, i64, P, P, P, P]
     lib.ra_tree_verify.argtypes = [P, i64, P, i64, i32, P, P, P, P, P, P, i32, i64, i32, P, P, P, P, P]
     lib.ra_tree_verify_greedy.argtypes = [P, i32, i64, i32, P, P, P, P, i32, i64, i32, P, P, P, P, P]
@@ -99,7 +105,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     for f in (lib.ra_kv_store, lib.ra_extend_attention, lib.ra_decode_attention, lib.ra_abi_version, lib.ra_kv8_store,
               lib.ra_kv8_load, lib.ra_kv8_decode_attention, lib.ra_qk_norm_rope_store,
               lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention, lib.ra_step_slots, lib.ra_tree_verify,
-              lib.ra_tree_verify_greedy, lib.ra_tree_commit):
+              lib.ra_tree_verify_greedy, lib.ra_tree_commit, lib.ra_extend_attention_mod, lib.ra_decode_attention_mod):
         f.restype = ctypes.c_int
     lib.ra_status_string.argtypes = [ctypes.c_int]
     lib.ra_status_string.restype = ctypes.c_char_p
@@ -311,7 +317,8 @@ def _native():
         spec.loader.exec_module(mod)
         fns = (lib.ra_kv8_store, lib.ra_kv8_load, lib.ra_kv8_slot_bytes, lib.ra_kv8_decode_attention,
                lib.ra_qk_norm_rope_store, lib.ra_qk_norm_rope_kv8_store, lib.ra_tree_attention, lib.ra_step_slots,
-               lib.ra_tree_verify, lib.ra_tree_verify_greedy, lib.ra_tree_commit)
+               lib.ra_tree_verify, lib.ra_tree_verify_greedy, lib.ra_tree_commit, lib.ra_extend_attention_mod,
+               lib.ra_decode_attention_mod)
         mod.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
         _binding = mod
     return _binding
@@ -397,6 +404,43 @@ def ra_tree_attention(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Tenso
     status = (_binding or _native()).tree(k_pool, v_pool, q, o, req_to_token, req_pool_indices, prefix_lens, draft_lens,
                                           qo_indptr, tree_mask, max_draft_len, max_prefix_len, sm_scale, workspace,
                                           device_error, stream)
+    if status:
+        _check(status)
+
+
+def ra_extend_mod_workspace_bytes(batch: int, total_q: int, num_q_heads: int, num_kv_heads: int) -> int:
+    """Workspace of ra_extend_attention_mod."""
+    return int(load().ra_extend_mod_workspace_bytes(batch, total_q, num_q_heads, num_kv_heads))
+
+
+def ra_extend_attention_mod(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Tensor, o: torch.Tensor,
+                            req_to_token: torch.Tensor, req_pool_indices: torch.Tensor, prefix_lens: torch.Tensor,
+                            extend_lens: torch.Tensor, qo_indptr: torch.Tensor, *, max_extend_len: int,
+                            max_prefix_len: int, sm_scale: float, workspace: torch.Tensor, score_cap: float = 0.0,
+                            window: int = 0, slopes: Optional[torch.Tensor] = None,
+                            first_key: Optional[torch.Tensor] = None, full_lens: Optional[torch.Tensor] = None,
+                            device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ra_extend_attention with scores capped (score_cap tanh(s / score_cap)), biased by distance (slopes fp32 [Hq]:
+    - slopes[h] |p - j|), and rows that see positions max(first_key[row], p - window + 1) .. p and those below
+    full_lens[b] (int32 [total_q], [batch]).  Workspace: uint8, ra_extend_mod_workspace_bytes(batch, total_q, Hq, Hkv)."""
+    status = (_binding or _native()).extend_mod(k_pool, v_pool, q, o, req_to_token, req_pool_indices, prefix_lens,
+                                                extend_lens, qo_indptr, max_extend_len, max_prefix_len, sm_scale, workspace,
+                                                score_cap, window, slopes, first_key, full_lens, device_error, stream)
+    if status:
+        _check(status)
+
+
+def ra_decode_attention_mod(k_pool: torch.Tensor, v_pool: torch.Tensor, q: torch.Tensor, o: torch.Tensor,
+                            req_to_token: torch.Tensor, req_pool_indices: torch.Tensor, seq_lens: torch.Tensor, *,
+                            max_seq_len: int, sm_scale: float, workspace: torch.Tensor, score_cap: float = 0.0,
+                            window: int = 0, slopes: Optional[torch.Tensor] = None,
+                            first_key: Optional[torch.Tensor] = None, device_error: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """ra_decode_attention (without groups) with the changed scores and masks of ra_extend_attention_mod; first_key int32
+    [batch].  Workspace: uint8, ra_decode_workspace_bytes(batch, Hq, Hkv, D, max_seq_len)."""
+    status = (_binding or _native()).decode_mod(k_pool, v_pool, q, o, req_to_token, req_pool_indices, seq_lens, max_seq_len,
+                                                sm_scale, workspace, score_cap, window, slopes, first_key, device_error,
+                                                stream)
     if status:
         _check(status)
 

@@ -3,7 +3,7 @@
 // One CTA per SM runs a stream of work items.  An item is 256 query rows of one kv head -- two
 // 128-row tiles, each a GQA block of 128 / G tokens (or decode requests) x the G q heads of the kv
 // head -- against a range of keys gathered from the pool through a req_to_token row.  Every
-// gathered 128-key K/V tile feeds both query tiles, i.e. 256 rows of tensor-core work.  Three users:
+// gathered 128-key K/V tile feeds both query tiles, i.e. 256 rows of tensor-core work.  Four users:
 //
 //  * extend (kExtendPass): rows are suffix tokens of one request; row (token i, head g) sees
 //    keys 0 .. P + i (cached prefix + causal suffix); the bf16 output is written directly.  Items
@@ -14,6 +14,8 @@
 //  * draft tree (kTreePass): rows are the drafted tokens of one request; all see the cached prefix,
 //    and of the drafted tokens the ones their bit mask names; an item is a (request, query tile, key
 //    split); an unsplit item writes bf16, a split one partials.
+//  * extend with changed scores (kExtendModPass, kExtendCapPass): a row sees a range of keys with both ends its own
+//    (a window, documents, a prefix seen by all), its scores have a bias by distance and may be capped.
 //
 // Warp roles (512 threads):
 //  warps 0-3  softmax + epilogue of query tile 0, one thread per row = TMEM lane;
@@ -48,6 +50,7 @@
 #include <cuda_bf16.h>
 
 #include "ra_ptx.cuh"
+#include "score_mod.cuh"
 
 namespace ra {
 
@@ -103,10 +106,14 @@ struct TcParams {
   int32_t part_rows;          // rows of a partial slot
   float* part_o;              // [slots, hkv, part_rows, D]
   float* part_lse;            // [slots, hkv, part_rows]
+  // extend with changed scores (the extend arrays; work_items are [4 * entries]: request, query tile, first key of the
+  // tile's rows, end of their keys)
+  ScoreMod mod;
 };
 
 // kTreeDualPass: the tree pass for calls whose items all have one live query tile.
-enum TcPass { kPrefixPass = 0, kExtendPass = 1, kTreePass = 2, kTreeDualPass = 3 };
+// kExtendModPass, kExtendCapPass: extend with changed scores, without and with a cap.
+enum TcPass { kPrefixPass = 0, kExtendPass = 1, kTreePass = 2, kTreeDualPass = 3, kExtendModPass = 4, kExtendCapPass = 5 };
 
 namespace tc {
 
@@ -149,6 +156,10 @@ template <bool B>
 struct BoolTag {
   static constexpr bool value = B;
 };
+template <int K>
+struct KindTag {
+  static constexpr int value = K;
+};
 
 // One work item: key range, table row and query rows.
 struct Job {
@@ -158,7 +169,8 @@ struct Job {
   int32_t n_valid;   // valid tokens / members (of 2T)
   int32_t causal0;   // extend: token t of the item sees keys < causal0 + t + 1; tree: the prefix length
   int64_t q_tok0;    // extend: first q token
-  int32_t mem0;      // cascade: first member index into group_reqs; tree: the request's drafted tokens
+  int32_t mem0;      // cascade: first member index into group_reqs; tree: the request's drafted tokens; changed
+                     // scores: end of the keys that every row sees
   int32_t csplit;    // cascade: prefix split
   int32_t slot;      // cascade: partial slot of the members (level x max_csplits + split); tree: partial
                      // slot of the item, -1 for an unsplit one
@@ -196,6 +208,27 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
     j.q_tok0 = f.w + e.y * kTiles * T;
     j.slot = e.w;
     j.odd = __ldg(p.tree_odd + static_cast<int64_t>(e.x) * p.hkv + j.kh);
+  } else if constexpr (PASS == kExtendModPass || PASS == kExtendCapPass) {
+    // (as below; the list's builder found the tile's key range)
+    const int4 e = __ldg(reinterpret_cast<const int4*>(p.work_items) + rest);
+    const int32_t E = min(max(__ldg(p.extend_lens + e.x), 0), p.max_extend_len);
+    const int32_t P = __ldg(p.prefix_lens + e.x);
+    j.table_row = __ldg(p.rpi + e.x);
+    if (j.table_row < 0 || j.table_row >= p.table_rows) {
+      if (report && e.y == 0 && j.kh == 0) flag_error(p.err, RA_DEVERR_TABLE);
+      return false;
+    }
+    const int64_t q_first = __ldg(p.qo_indptr + e.x);
+    if (q_first < 0 || q_first + E > p.total_q) {
+      if (report && e.y == 0 && j.kh == 0) flag_error(p.err, RA_DEVERR_LENGTH);
+      return false;
+    }
+    j.n_valid = min(kTiles * T, E - e.y * kTiles * T);
+    j.causal0 = P + e.y * kTiles * T;
+    j.kbeg = e.z;
+    j.kend = e.w;
+    j.mem0 = p.mod.full_lens ? min(__ldg(p.mod.full_lens + e.x), P + E) : 0;
+    j.q_tok0 = q_first + e.y * kTiles * T;
   } else if constexpr (PASS == kExtendPass) {
     // entry `rest` of the work list: it holds only non-empty query tiles of requests whose lengths
     // were checked (and flagged) when it was built
@@ -259,6 +292,58 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
   return j.nt > 0;
 }
 
+// Attention of one row with changed scores, by a warp: a key per lane for the scores, D / 32 dimensions per lane for the
+// values.  For rows whose tensor-core result is not finite although values that are not finite may lie outside what the
+// row sees (a zero weight times such a value is a NaN in the product over a whole tile); slow and rare.  Lane l's
+// dimensions l * D / 32 .. in acc.
+template <int D, bool CAP>
+__device__ __forceinline__ void mod_row(const TcParams& p, const Job& jb, int64_t q_row, int32_t first, int32_t end,
+                                        int32_t pos, float slope, float (&acc)[D / 32]) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+  const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>(p.q + q_row * D);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 1
+  for (int32_t k0 = first; k0 < end; k0 += 32) {
+    const int32_t key = min(k0 + lane, end - 1);
+    int32_t slot = __ldg(p.table + static_cast<int64_t>(jb.table_row) * p.table_stride + key);
+    if (slot < 0 || slot >= p.num_slots) slot = 0;
+    const int64_t row = (static_cast<int64_t>(slot) * p.hkv + jb.kh) * D;
+    const __nv_bfloat162* k = reinterpret_cast<const __nv_bfloat162*>(p.k_pool + row);
+    float s = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D / 2; ++d) {
+      const float2 a = __bfloat1622float2(q[d]), b = __bfloat1622float2(k[d]);
+      s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
+    }
+    float x = CAP ? p.mod.cap_log2 * tanh_any(s * p.mod.cap_in) : s * p.scale_log2;
+    x = k0 + lane < end ? fmaf(-slope, fabsf(static_cast<float>(pos - key)), x) : -INFINITY;
+    float top = x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float m_new = fmaxf(m, top), m_sub = m_new == -INFINITY ? 0.f : m_new;
+    const float alpha = ex2(m - m_sub), w = ex2(x - m_sub);
+    m = m_new;
+    l = l * alpha + w;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= alpha;
+#pragma unroll 1
+    for (int i = 0; i < 32 && k0 + i < end; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const int64_t ri = __shfl_sync(0xffffffffu, row, i);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(wi, __bfloat162float(p.v_pool[ri + lane * V + v]), acc[v]);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] *= inv;
+}
+
 }  // namespace tc
 
 template <int D, int KS, int VS, int PASS>
@@ -270,6 +355,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   constexpr bool EXTEND = PASS != kPrefixPass;  // rows are tokens of one request, items come from a list
   constexpr bool DUAL = PASS == kTreeDualPass;
   constexpr bool TREE = PASS == kTreePass || DUAL;
+  constexpr bool CAP = PASS == kExtendCapPass;
+  constexpr bool MOD = PASS == kExtendModPass || CAP;
   constexpr int HALVES = D / 64;  // 128-byte (64-element) column blocks of a row
   // K/V stage release: one barrier per key tile t (ring of KVF), committed after the last MMA reading
   // K_t and V_t (PV of query tile 1).  KVF > max(KS, VS): a producer waiting for tile t's release
@@ -688,7 +775,21 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       const int tok = DUAL && jb.dual ? r / G : tile_tok;
       const bool row_valid = tok < jb.n_valid;
       int32_t lim;  // exclusive key limit of this row (tree: of the keys every row sees)
-      if constexpr (TREE) lim = jb.causal0;
+      int32_t first = 0, pos = 0;  // changed scores: the first key this row sees and its position
+      float slope = 0.f;           // and its head's bias per position, in log2 units
+      (void)first, (void)pos, (void)slope;
+      [[maybe_unused]] bool wide = false;  // scores beyond the polynomial's range were met
+      if constexpr (MOD) {
+        pos = jb.causal0 + tok;
+        lim = jb.kend;
+        first = jb.kbeg;
+        if (row_valid) {
+          lim = max(pos + 1, jb.mem0);
+          if (p.mod.window > 0) first = max(first, pos - p.mod.window + 1);
+          if (p.mod.first_key) first = max(first, __ldg(p.mod.first_key + jb.q_tok0 + tok));
+          if (p.mod.slopes) slope = __ldg(p.mod.slopes + jb.kh * G + r % G) * kLog2e;
+        }
+      } else if constexpr (TREE) lim = jb.causal0;
       else if constexpr (EXTEND) lim = row_valid ? jb.causal0 + tok + 1 : jb.kend;
       else lim = jb.kend;
       float m_used = -INFINITY, l = 0.f;
@@ -703,7 +804,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         }
         tc_fence_after();
         const int32_t key0 = jb.kbeg + tile_at(jb, j, ti) * kKeys;
-        const bool masked = key0 + kKeys > lim;
+        // (changed scores: also where a key lies behind the row's own position, for the bias by distance)
+        const bool masked = MOD ? key0 + kKeys > min(lim, pos + 1) || key0 < first : key0 + kKeys > lim;
         const bool warp_masked = __any_sync(0xffffffffu, masked);
         // tree: bit e of vis[c] = key key0 + 32 c + e is visible to this row
         uint32_t vis[4];
@@ -751,13 +853,29 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         float rowsum = 0.f, alpha = 1.f, m_ref = m_used;
         bool resc = false;
         bool exact = false;
+        const bool sees = !MOD || (first < key0 + kKeys && first < lim && key0 < lim);  // any key of this tile
+        if (MOD && !__any_sync(0xffffffffu, sees)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pk[0][e] = pk[1][e] = 0u;
+        } else
 #pragma unroll 1
-        for (int attempt = 0; attempt < 2; ++attempt) {
+        for (int attempt = 0; attempt < (MOD ? 3 : 2); ++attempt) {
           // row max of the raw scores (scale > 0 commutes with max), 8 independent chains
           float mx8[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+          // changed scores: any score in log2 units with its bias, -inf where it is hidden
+          [[maybe_unused]] auto score = [&](uint32_t sr, int32_t key) -> float {
+            const float s = __uint_as_float(sr);
+            const float x = CAP ? p.mod.cap_log2 * tanh_any(s * p.mod.cap_in) : s * p.scale_log2;
+            return key >= first && key < lim ? fmaf(-slope, fabsf(static_cast<float>(pos - key)), x) : -INFINITY;
+          };
           auto max_chunk = [&](const uint32_t (&sr)[32], int c) {
+            if constexpr (MOD) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], score(sr[e], key0 + c * 32 + e));
+              return;
+            }
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const bool hidden = TREE ? !(vis[c] >> e & 1u) : masked && key0 + c * 32 + e >= lim;
@@ -767,7 +885,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           };
           auto max_of = [&]() {
             return fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * p.scale_log2;
+                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * (MOD ? 1.f : p.scale_log2);
           };
           if (exact) {
             uint32_t ba[32], bb[32];
@@ -803,7 +921,58 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           uint64_t sum2[4] = {0, 0, 0, 0};  // 4 independent chains of (even, odd) partial sums
           // The causal / range mask is compiled only into the variant a warp takes when one of its rows
           // ends inside this tile: the other tiles issue no compare or select per score.
+          // changed scores: the largest |y| of the polynomial's arguments
+          [[maybe_unused]] float y_max = 0.f;
           auto exp_chunk = [&](const uint32_t (&sr)[32], int c, auto mask_tag) {
+            if constexpr (MOD) {
+              // 2: any score, one by one; 1: with hidden keys or keys behind the row's position; 0: neither.  The bias and
+              // the reference are one addend: linear in the key up to the row's position.
+              constexpr int kind = decltype(mask_tag)::value;
+              const float off = static_cast<float>(key0 + c * 32 - pos);
+              const uint64_t base2 = f2_pack(fmaf(slope, off, -m_sub), fmaf(slope, off, -m_sub));
+              const uint64_t slope2 = f2_pack(slope, slope);
+              const uint64_t in2 = f2_pack(p.mod.cap_in, p.mod.cap_in);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int32_t key = key0 + c * 32 + 2 * e;
+                float t0, t1;
+                if constexpr (kind == 2) {
+                  t0 = score(sr[2 * e], key) - m_sub;
+                  t1 = score(sr[2 * e + 1], key + 1) - m_sub;
+                } else {
+                  uint64_t add2;
+                  if constexpr (kind == 1)
+                    add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m_sub), fmaf(-slope, fabsf(off + (2 * e + 1)), -m_sub));
+                  else
+                    add2 = f2_fma(slope2, f2_pack(2 * e, 2 * e + 1), base2);
+                  const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+                  uint64_t t2;
+                  if constexpr (CAP) {
+                    const uint64_t y2 = f2_mul(s2, in2);
+                    const uint64_t z2 = f2_mul(y2, y2);
+                    float y0, y1;
+                    f2_unpack(y2, y0, y1);
+                    y_max = fmaxf(y_max, fmaxf(fabsf(y0), fabsf(y1)));
+                    auto coef = [&](int i) { return f2_pack(p.mod.cap_log2 * cap_coef(i), p.mod.cap_log2 * cap_coef(i)); };
+                    uint64_t h2 = coef(kCapTerms - 1);
+#pragma unroll
+                    for (int i = kCapTerms - 2; i >= 0; --i) h2 = f2_fma(h2, z2, coef(i));
+                    t2 = f2_fma(y2, h2, add2);
+                  } else {
+                    t2 = f2_fma(s2, scale2, add2);
+                  }
+                  f2_unpack(t2, t0, t1);
+                  if constexpr (kind == 1) {
+                    if (key < first || key >= lim) t0 = -INFINITY;
+                    if (key + 1 < first || key + 1 >= lim) t1 = -INFINITY;
+                  }
+                }
+                const float p0 = ex2(t0), p1 = ex2(t1);
+                sum2[e & 3] = f2_add(sum2[e & 3], f2_pack(p0, p1));
+                pk[c >> 1][(c & 1) * 16 + e] = pack_bf16x2(p0, p1);
+              }
+              return;
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float s0 = __uint_as_float(sr[2 * e]), s1 = __uint_as_float(sr[2 * e + 1]);
@@ -833,15 +1002,25 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             tc_wait_ld_regs(bb);
             exp_chunk(bb, 3, mask_tag);
           };
-          if (warp_masked) exp_tile(BoolTag<true>{});
-          else exp_tile(BoolTag<false>{});
+          if constexpr (MOD) {
+            if (exact || wide) exp_tile(KindTag<2>{});
+            else if (warp_masked) exp_tile(KindTag<1>{});
+            else exp_tile(KindTag<0>{});
+          } else {
+            if (warp_masked) exp_tile(BoolTag<true>{});
+            else exp_tile(BoolTag<false>{});
+          }
           float sum8[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sum8[2 * e], sum8[2 * e + 1]);
           rowsum = ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
           if (exact) break;
           // (a tree row may see no key of the first tile's chunk 0, or of any tile so far: no reference yet)
-          const bool stale = !(rowsum <= kFastSumLimit) || (TREE && m_ref == -INFINITY);
+          if (CAP && !wide && __any_sync(0xffffffffu, !(y_max <= kCapPolyMax))) {
+            wide = true;  // (for the rest of the item: tiles with such scores do not come alone)
+            continue;
+          }
+          const bool stale = !(rowsum <= kFastSumLimit) || ((TREE || MOD) && m_ref == -INFINITY && sees);
           if (!__any_sync(0xffffffffu, stale)) break;
           exact = true;
         }
@@ -900,7 +1079,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           l = l * own + b.y * other;
         }
       }
-      const float inv_l = TREE && l == 0.f ? 0.f : 1.f / l;  // a tree row that sees nothing gives 0
+      const float inv_l = (TREE || MOD) && l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing gives 0
       // O of this thread's row, all columns, as the epilogues write it (a dual item's two halves joined)
       auto load_o = [&](uint32_t (&oa)[D / 32][32]) {
 #pragma unroll
@@ -927,6 +1106,17 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         __nv_bfloat16* dst = p.o + ((jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G)) * static_cast<int64_t>(D);
         uint32_t oa[D / 32][32];
         load_o(oa);
+        [[maybe_unused]] bool redo = false;
+        if constexpr (MOD) {
+          // a result that is not finite may come from a value that this row does not see
+          float bad[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(oa[c][e]), 0.f, bad[e & 3]);
+          redo = row_valid && (first > jb.kbeg || lim < jb.kend) &&
+                 !((bad[0] + bad[1]) + (bad[2] + bad[3]) == 0.f);
+        }
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t (&ov)[32] = oa[c];
@@ -938,6 +1128,18 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
 #pragma unroll
             for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pko[4 * e], pko[4 * e + 1], pko[4 * e + 2], pko[4 * e + 3]);
+          }
+        }
+        if constexpr (MOD) {
+          for (uint32_t rows = __ballot_sync(0xffffffffu, redo); rows != 0; rows &= rows - 1) {
+            const int src = __ffs(rows) - 1;
+            const int64_t row = __shfl_sync(0xffffffffu, (jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G), src);
+            float y[D / 32];
+            mod_row<D, CAP>(p, jb, row, __shfl_sync(0xffffffffu, first, src), __shfl_sync(0xffffffffu, lim, src),
+                            __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, slope, src), y);
+            __syncwarp();  // (behind the row's own thread's stores)
+#pragma unroll
+            for (int v = 0; v < D / 32; ++v) p.o[row * D + lane * (D / 32) + v] = __float2bfloat16_rn(y[v]);
           }
         }
       } else {

@@ -10,6 +10,7 @@
 #include <cmath>
 
 #include "../../include/ra.h"
+#include "score_mod.cuh"
 
 namespace ra {
 
@@ -66,6 +67,7 @@ struct DecodeParams {
   const int32_t* st_loc;   // [batch] destination slots
   int32_t st_row_vecs;     // 16-byte vectors per slot row (hkv * D * 2 / 16)
   int64_t st_total;        // batch * st_row_vecs
+  ScoreMod mod;            // ra_decode_attention_mod
 };
 
 // The private keys of a decode call are cut into items on the device (decode_plan_kernel): at most
@@ -113,8 +115,17 @@ DecodeWorkspace layout_decode_workspace(int32_t batch, int32_t num_q_heads, int3
 
 // Point p's scratch members into a workspace of layout wl (p.batch set before).
 void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace);
+// Changed scores: the first key that request b of L tokens sees, in [0, L].
+__device__ __forceinline__ int32_t mod_start(const DecodeParams& p, int32_t b, int32_t L) {
+  int32_t first = p.mod.window > 0 ? L - p.mod.window : 0;
+  if (p.mod.first_key) first = max(first, __ldg(p.mod.first_key + b));
+  return min(max(first, 0), L);
+}
+
 // The call's plan kernel: CTA 0 plans, `store_ctas` more run the fused store.
 ra_status launch_decode_plan(const DecodeParams& p, int store_ctas, cudaStream_t stream);
+// The same for a call with changed scores (no groups, no store).
+ra_status launch_decode_plan_mod(const DecodeParams& p, cudaStream_t stream);
 
 // Tensor-core pass over each group's shared prefix: writes p.casc_o / p.casc_lse
 // for every member (defined with the tcgen05 attention kernel).

@@ -14,6 +14,7 @@ struct Item {
 // Claim `idx` = (position in the plan's longest-first order) * n_hgroups + hg.  The plan (written by
 // decode_plan_kernel) lists only non-empty items of valid requests.  Plan arrays are read with plain
 // loads: they are written on the device by the kernel before this one.
+template <bool MOD = false>
 __device__ __forceinline__ void decode_item(const DecodeParams& p, int32_t idx, Item& it) {
   it.hg = idx % p.n_hgroups;
   it.d = p.order[idx / p.n_hgroups];
@@ -23,8 +24,12 @@ __device__ __forceinline__ void decode_item(const DecodeParams& p, int32_t idx, 
   it.n_splits = p.req_item0[it.b + 1] - i0;
   it.row = __ldg(p.rpi + it.b);
   const int32_t L = min(__ldg(p.seq_lens + it.b), p.max_seq_len);
-  const int32_t start = p.key_start ? __ldg(p.key_start + it.b) : 0;
-  it.start = start < 0 ? 0 : (start > L ? L : start);
+  if constexpr (MOD) {
+    it.start = mod_start(p, it.b, L);
+  } else {
+    const int32_t start = p.key_start ? __ldg(p.key_start + it.b) : 0;
+    it.start = start < 0 ? 0 : (start > L ? L : start);
+  }
   const int32_t chunk = p.plan[1];
   it.k0 = it.start + it.split * chunk;
   it.k1 = min(L, it.k0 + chunk);

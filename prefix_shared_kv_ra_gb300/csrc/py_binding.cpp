@@ -32,6 +32,8 @@ decltype(&ra_step_slots) p_step_slots;
 decltype(&ra_tree_verify) p_tree_verify;
 decltype(&ra_tree_verify_greedy) p_tree_verify_greedy;
 decltype(&ra_tree_commit) p_tree_commit;
+decltype(&ra_extend_attention_mod) p_extend_mod;
+decltype(&ra_decode_attention_mod) p_decode_mod;
 
 PyObject* s_cuda_stream;
 
@@ -312,6 +314,65 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// extend: (k_pool, v_pool, q, o, table, rpi, prefix_lens, extend_lens, qo_indptr, max_extend_len, max_prefix_len, sm_scale,
+//  workspace, score_cap, window, slopes, first_key, full_lens, err, stream)
+// decode: (k_pool, v_pool, q, o, table, rpi, seq_lens, max_seq_len, sm_scale, workspace, score_cap, window, slopes,
+//  first_key, err, stream)
+PyObject* attention_mod(PyObject* const* a, Py_ssize_t n, bool extend) {
+  return method(extend ? "ra_extend_attention_mod" : "ra_decode_attention_mod", n, extend ? 20 : 16, [&] {
+    const at::Tensor &k = tensor(a[0], "k_pool", 3), &v = tensor(a[1], "v_pool", 3), &q = tensor(a[2], "q", 3),
+                     &o = tensor(a[3], "o", 3), &table = tensor(a[4], "req_to_token", 2),
+                     &rpi = tensor(a[5], "req_pool_indices", 1),
+                     &lens = tensor(a[6], extend ? "prefix_lens" : "seq_lens", 1);
+    const at::Device device = k.device();
+    const int32_t hkv = narrow(k.size(1), "Hkv"), d = narrow(k.size(2), "D"), hq = narrow(q.size(1), "Hq"),
+                  batch = narrow(rpi.size(0), "batch");
+    same_shape(v, k, "v_pool", "that of k_pool");
+    if (q.size(2) != d) wrong(PyExc_ValueError, "q: expected shape [%s, Hq, D]", extend ? "total_q" : "batch");
+    same_shape(o, q, "o", "that of q");
+    length(lens, batch, extend ? "prefix_lens" : "seq_lens", "[batch]");
+    if (!extend) length(q, batch, "q", "[batch, Hq, D]");
+    auto i32 = [&](const at::Tensor& t, const char* name) { return data<int32_t>(t, name, at::kInt, device); };
+    void *kp = data<void>(k, "k_pool", at::kBFloat16, device), *vp = data<void>(v, "v_pool", at::kBFloat16, device),
+         *qp = data<void>(q, "q", at::kBFloat16, device), *op = data<void>(o, "o", at::kBFloat16, device);
+    const int32_t *tp = i32(table, "req_to_token"), *rp = i32(rpi, "req_pool_indices"),
+                  *lp = i32(lens, extend ? "prefix_lens" : "seq_lens");
+    PyObject* const* b = a + (extend ? 9 : 7);  // max_extend_len, max_prefix_len or max_seq_len
+    PyObject* const* c = b + (extend ? 2 : 1);  // sm_scale, workspace, score_cap, window, slopes, first_key
+    const int32_t longest = int_of(b[0], extend ? "max_extend_len" : "max_seq_len"),
+                  prefix = extend ? int_of(b[1], "max_prefix_len") : 0;
+    const float scale = static_cast<float>(float_of(c[0])), cap = static_cast<float>(float_of(c[2]));
+    const Workspace ws = workspace_of(c[1], device);
+    const int32_t window = int_of(c[3], "window");
+    if (c[4] != Py_None) length(tensor(c[4], "slopes", 1), hq, "slopes", "[Hq]");
+    if (c[5] != Py_None)
+      length(tensor(c[5], "first_key", 1), q.size(0), "first_key", extend ? "[total_q]" : "[batch]");
+    const float* slopes = optional_data<float>(c[4], "slopes", at::kFloat, device);
+    const int32_t* first = optional_data<int32_t>(c[5], "first_key", at::kInt, device);
+    if (!extend) {
+      uint32_t* err = optional_data<uint32_t>(c[6], "device_error", at::kInt, device);
+      return launch(device, c[7], [&](ra_stream_t s) {
+        return p_decode_mod(kp, vp, k.size(0), hkv, d, qp, op, hq, scale, cap, window, slopes, first, tp, table.size(1),
+                            table.size(0), rp, lp, batch, longest, ws.at, ws.bytes, err, s);
+      });
+    }
+    const at::Tensor &news = tensor(a[7], "extend_lens", 1), &qo = tensor(a[8], "qo_indptr", 1);
+    length(news, batch, "extend_lens", "[batch]");
+    length(qo, static_cast<int64_t>(batch) + 1, "qo_indptr", "[batch + 1]");
+    if (c[6] != Py_None) length(tensor(c[6], "full_lens", 1), batch, "full_lens", "[batch]");
+    const int32_t *np = i32(news, "extend_lens"), *ip = i32(qo, "qo_indptr"),
+                  *full = optional_data<int32_t>(c[6], "full_lens", at::kInt, device);
+    uint32_t* err = optional_data<uint32_t>(c[7], "device_error", at::kInt, device);
+    return launch(device, c[8], [&](ra_stream_t s) {
+      return p_extend_mod(kp, vp, k.size(0), hkv, d, qp, op, hq, scale, cap, window, slopes, first, full, tp, table.size(1),
+                          table.size(0), rp, lp, np, ip, batch, q.size(0), longest, prefix, ws.at, ws.bytes, err, s);
+    });
+  });
+}
+
+PyObject* extend_mod(PyObject*, PyObject* const* a, Py_ssize_t n) { return attention_mod(a, n, true); }
+PyObject* decode_mod(PyObject*, PyObject* const* a, Py_ssize_t n) { return attention_mod(a, n, false); }
+
 // (table, rpi, seq_lens, new_lens, free_pages, free_count, out_cache_loc, positions, qo_indptr, seq_lens_out, page_size,
 //  free_count_out or None, err, stream)
 PyObject* step_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -453,8 +514,9 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // init(addresses of the entry points in the order of the declarations above)
 PyObject* init(PyObject*, PyObject* args) {
-  unsigned long long a[11];
-  if (!PyArg_ParseTuple(args, "KKKKKKKKKKK", a, a + 1, a + 2, a + 3, a + 4, a + 5, a + 6, a + 7, a + 8, a + 9, a + 10))
+  unsigned long long a[13];
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKKKKK", a, a + 1, a + 2, a + 3, a + 4, a + 5, a + 6, a + 7, a + 8, a + 9, a + 10,
+                        a + 11, a + 12))
     return nullptr;
   p_kv8_store = reinterpret_cast<decltype(p_kv8_store)>(a[0]);
   p_kv8_load = reinterpret_cast<decltype(p_kv8_load)>(a[1]);
@@ -467,6 +529,8 @@ PyObject* init(PyObject*, PyObject* args) {
   p_tree_verify = reinterpret_cast<decltype(p_tree_verify)>(a[8]);
   p_tree_verify_greedy = reinterpret_cast<decltype(p_tree_verify_greedy)>(a[9]);
   p_tree_commit = reinterpret_cast<decltype(p_tree_commit)>(a[10]);
+  p_extend_mod = reinterpret_cast<decltype(p_extend_mod)>(a[11]);
+  p_decode_mod = reinterpret_cast<decltype(p_decode_mod)>(a[12]);
   Py_RETURN_NONE;
 }
 
@@ -485,6 +549,8 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, "entry points of the libra
                          {"tree_verify", fast(tree_verify), METH_FASTCALL, nullptr},
                          {"tree_verify_greedy", fast(tree_verify_greedy), METH_FASTCALL, nullptr},
                          {"tree_commit", fast(tree_commit), METH_FASTCALL, nullptr},
+                         {"extend_mod", fast(extend_mod), METH_FASTCALL, nullptr},
+                         {"decode_mod", fast(decode_mod), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ra_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,57 @@
+// score_mod.cuh -- scores capped by a tanh and their masks, shared by the attention kernels with changed scores.
+//
+// A capped score is cap tanh(s / cap), wanted as t = cap log2(e) tanh(y) with y = s sm_scale / cap for the base-2
+// exponential.  The hardware's tanh is good to about 2^-11 only: at a score of 20 that is 1% of the weight, more than
+// the rounding of the weights to bf16.  For |y| <= 1.25 tanh(y) / y is taken as a polynomial of degree 6 in y^2 (a
+// minimax fit of the relative error, 7e-7 in fp32 arithmetic: at a score of 50, 4e-5 of the weight); it needs no special
+// function unit, which the exponential keeps busy.  Beyond, 1 - 2 / (e^2|y| + 1), whose cancellation is gone there.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ra_ptx.cuh"
+
+namespace ra {
+
+struct ScoreMod {
+  const float* slopes;       // [hq] bias per position of distance (subtracted), or nullptr
+  const int32_t* first_key;  // first position that a row sees ([total_q], decode: [batch]), or nullptr
+  const int32_t* full_lens;  // extend: [batch], positions below it are seen by every row; or nullptr
+  int32_t window;            // keys a row sees up to its own, 0: all
+  float cap_in;              // sm_scale / cap (0: no cap)
+  float cap_log2;            // cap log2(e)
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kCapPolyMax = 1.25f;
+constexpr int kCapTerms = 7;
+__device__ __forceinline__ constexpr float cap_coef(int i) {
+  constexpr float c[kCapTerms] = {0.9999994039535522f,    -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
+                                  0.018229123204946518f, -0.004626905079931021f, 0.0005844939732924104f};
+  return c[i];
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(y), |y| <= kCapPolyMax.
+__device__ __forceinline__ float tanh_small(float y) {
+  const float z = y * y;
+  float p = cap_coef(kCapTerms - 1);
+#pragma unroll
+  for (int i = kCapTerms - 2; i >= 0; --i) p = fmaf(p, z, cap_coef(i));
+  return y * p;
+}
+
+// tanh(y) of any y; NaN stays.
+__device__ __forceinline__ float tanh_any(float y) {
+  const float a = fabsf(y);
+  const float far = 1.f - 2.f * rcp_approx(ex2(a * (2.f * kLog2e)) + 1.f);
+  return a <= kCapPolyMax ? tanh_small(y) : copysignf(far, y);
+}
+
+}  // namespace ra

@@ -27,6 +27,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// Let the next kernel launch, every write of this CTA visible to it: the attention calls' planning kernels read lengths,
+// which these kernels write, before they wait for the kernel before them.
+__device__ __forceinline__ void launch_behind_writes() {
+  __threadfence();
+  __syncthreads();
+  griddep_launch();
+}
+
 // Inclusive sums of (a, b) over the CTA's threads; the totals in ta, tb.
 __device__ __forceinline__ void scan2(int64_t& a, int64_t& b, int64_t& ta, int64_t& tb) {
   __shared__ int64_t s_a[kThreads / 32], s_b[kThreads / 32];
@@ -79,7 +87,6 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
   __shared__ int32_t s_start[kThreads], s_cur[kThreads], s_row[kThreads], s_prev[kThreads], s_fresh[kThreads],
       s_base[kThreads];
   griddep_wait();  // the lengths and the free list may come from the kernels before
-  griddep_launch();
   const int t = threadIdx.x;
   const bool first_cta = cluster_rank() == 0;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kThreads + t, workers = static_cast<int64_t>(gridDim.x) * kThreads;
@@ -182,6 +189,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
       *p.free_count_out = static_cast<int32_t>(count - static_cast<int64_t>(s_used));
     }
   }
+  launch_behind_writes();
 }
 
 struct CommitParams {
@@ -207,7 +215,6 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
       s_first[kThreads];
   __shared__ int64_t s_free[kThreads];
   griddep_wait();
-  griddep_launch();
   const int t = threadIdx.x;
   const bool first_cta = cluster_rank() == 0;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kThreads + t, workers = static_cast<int64_t>(gridDim.x) * kThreads;
@@ -281,6 +288,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
     const int64_t now = count + freed;
     *p.free_count_out = static_cast<int32_t>(now < p.free_capacity ? now : p.free_capacity);
   }
+  launch_behind_writes();
 }
 
 // CTAs of the cluster: one while it gives a thread a few tokens (no barrier between SMs, and the whole call is the scan's

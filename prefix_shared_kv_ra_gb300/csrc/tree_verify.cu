@@ -41,6 +41,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Let the next kernel launch, every write of this CTA visible to it (the planning kernels of the attention calls read
+// lengths before they wait for the kernel before them).
+__device__ __forceinline__ void launch_behind_writes() {
+  __threadfence();
+  __syncthreads();
+  griddep_launch();
+}
 // Store 64 bits at this CTA's shared address `addr` of CTA `rank` of the cluster.
 __device__ __forceinline__ void st_cluster_b64(uint32_t addr, uint32_t rank, uint64_t v) {
   uint32_t remote;
@@ -134,7 +141,6 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
   __shared__ double s_t;
   __shared__ double s_total;
   griddep_wait();
-  griddep_launch();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int32_t b = blockIdx.x / ctas;
   const uint32_t rank = cluster_rank();
@@ -142,6 +148,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
   const int32_t T = request_rows(p.draft_lens, p.qo_indptr, b, p.max_draft, p.total_q, &first, p.err, rank == 0 && t == 0);
   if (T == 0) {  // (the whole cluster)
     if (rank == 0) nothing_verified(p.path, p.accept_lens, p.next_tokens, b, p.max_draft);
+    launch_behind_writes();
     return;
   }
   for (int32_t i = t; i < T; i += kThreads) {
@@ -379,6 +386,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
       for (int32_t i = t; i < p.max_draft; i += kThreads)
         p.path[static_cast<int64_t>(b) * p.max_draft + i] = i < s_node ? s_path[i] : -1;
     }
+    launch_behind_writes();
     return;
   }
 }
@@ -469,7 +477,6 @@ __global__ void __launch_bounds__(kThreads) tree_verify_greedy_kernel(const Gree
   __shared__ uint64_t s_rank[2][kMaxCluster];
   __shared__ int32_t s_next, s_token;
   griddep_wait();
-  griddep_launch();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int32_t b = blockIdx.x / ctas;
   const uint32_t rank = cluster_rank();
@@ -477,6 +484,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_greedy_kernel(const Gree
   const int32_t T = request_rows(p.draft_lens, p.qo_indptr, b, p.max_draft, p.total_q, &first, p.err, rank == 0 && t == 0);
   if (T == 0) {  // (the whole cluster)
     if (rank == 0) nothing_verified(p.path, p.accept_lens, p.next_tokens, b, p.max_draft);
+    launch_behind_writes();
     return;
   }
   for (int32_t i = t; i < T; i += kThreads) {
@@ -529,6 +537,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_greedy_kernel(const Gree
       p.next_tokens[b] = max(s_token, 0);
     }
   }
+  launch_behind_writes();
 }
 
 // CTAs per request: 8 (the most that any GPU of the architecture runs as one cluster) unless a slice would be less than a

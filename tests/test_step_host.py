@@ -150,3 +150,67 @@ def test_the_definition_keeps_the_targets_distribution():
                         r = np.maximum(r - r.sum() * q[0], 0)
                         out += weight * r / r.sum()
     assert np.abs(out - p[0]).max() < 1.5 / n, out
+
+
+def _extend_mod(lib, **over):
+    a = dict(k=FAKE, v=FAKE, S=1024, hkv=8, d=128, q=FAKE, o=FAKE, hq=32, scale=0.088, cap=30.0, window=100, slopes=FAKE,
+             first=FAKE, full=FAKE, table=FAKE, stride=4096, rows=64, rpi=FAKE, plen=FAKE, elen=FAKE, qo=FAKE, batch=4,
+             total=100, max_e=40, max_p=4000, ws=FAKE, wsb=1 << 30, err=None, stream=None)
+    a.update(over)
+    return lib.ra_extend_attention_mod(*a.values())
+
+
+def _decode_mod(lib, **over):
+    a = dict(k=FAKE, v=FAKE, S=1024, hkv=8, d=128, q=FAKE, o=FAKE, hq=32, scale=0.088, cap=30.0, window=100, slopes=FAKE,
+             first=FAKE, table=FAKE, stride=4096, rows=64, rpi=FAKE, lens=FAKE, batch=4, longest=4096, ws=FAKE, wsb=1 << 30,
+             err=None, stream=None)
+    a.update(over)
+    return lib.ra_decode_attention_mod(*a.values())
+
+
+def test_attention_mod_validation(lib):
+    nan, inf = float("nan"), float("inf")
+    for call in (_extend_mod, _decode_mod):
+        for wrong in (dict(cap=-1.0), dict(cap=nan), dict(cap=inf), dict(cap=1e-7), dict(cap=2e12), dict(window=-1),
+                      dict(scale=0.0), dict(scale=nan), dict(scale=3e38, cap=1e-3), dict(slopes=ODD), dict(first=ODD),
+                      dict(hq=30), dict(S=0), dict(batch=-1), dict(k=None), dict(q=ODD), dict(table=None), dict(rows=0),
+                      dict(stride=39), dict(ws=ctypes.c_void_p((1 << 20) + 8))):
+            assert call(lib, **wrong) == 1, (call, wrong)
+        assert call(lib, d=96) == 2
+        assert call(lib, wsb=15) == 3
+        assert call(lib, batch=0, k=None) == 0
+    assert _extend_mod(lib, hq=24) == 2                     # group 3 does not divide 128
+    assert _decode_mod(lib, hq=128) == 2                    # groups of up to 8
+    assert _extend_mod(lib, total=0, k=None) == 0
+    need = ra.ra_extend_mod_workspace_bytes(4, 100, 32, 8)
+    assert _extend_mod(lib, wsb=need - 1) == 3 and ra.ra_extend_mod_workspace_bytes(4, 100, 30, 8) == 0
+    assert ra.ra_extend_mod_workspace_bytes(4, 100, 24, 8) == 0
+
+
+def test_attention_mod_bindings_check_before_the_call():
+    bf = torch.bfloat16
+    i = lambda *s: torch.zeros(*s, dtype=I)
+    pool, q = torch.zeros(16, 2, 64, dtype=bf), torch.zeros(5, 8, 64, dtype=bf)
+    kw = dict(sm_scale=1.0, workspace=torch.zeros(64, dtype=torch.uint8))
+    ext = dict(kw, max_extend_len=3, max_prefix_len=4)
+    args = [pool, pool, q, q.clone(), i(2, 9), i(2), i(2), i(2), i(3)]
+    with pytest.raises(ValueError, match="CUDA"):
+        ra.ra_extend_attention_mod(*args, **ext)
+    for bad in (dict(slopes=torch.zeros(7)), dict(first_key=i(4)), dict(full_lens=i(3)), dict(window=1 << 40)):
+        with pytest.raises(ValueError):
+            ra.ra_extend_attention_mod(*args, **dict(ext, **bad))
+    for bad in (dict(slopes=torch.zeros(8, dtype=bf)), dict(first_key=torch.zeros(5)), dict(full_lens=i(2).long())):
+        with pytest.raises(TypeError):
+            ra.ra_extend_attention_mod(*args, **dict(ext, **bad))
+    for k, x in ((1, pool[:8]), (3, q[:4]), (6, i(3)), (7, i(1)), (8, i(2)), (4, i(9))):
+        with pytest.raises(ValueError):
+            ra.ra_extend_attention_mod(*[x if j == k else y for j, y in enumerate(args)], **ext)
+    dec = dict(kw, max_seq_len=9)
+    one = [pool, pool, q[:2], q[:2].clone(), i(2, 9), i(2), i(2)]
+    with pytest.raises(ValueError, match="CUDA"):
+        ra.ra_decode_attention_mod(*one, **dec)
+    for bad in (dict(slopes=torch.zeros(7)), dict(first_key=i(5))):
+        with pytest.raises(ValueError):
+            ra.ra_decode_attention_mod(*one, **dict(dec, **bad))
+    with pytest.raises(ValueError):
+        ra.ra_decode_attention_mod(pool, pool, q, q.clone(), i(2, 9), i(2), i(2), **dec)
