@@ -131,6 +131,10 @@ constexpr int kItemRing = 8;                // published items (the claimer runs
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// Changed scores: a row whose sum is outside these has its reference too far from its scores (weights that vanish or
+// overflow); capped ones: the bound up to which the reference is fixed, and the sum at which it is raised.
+constexpr float kSumFloor = 0x1p-90f, kSumCeiling = 0x1p110f;
+constexpr float kCapFixed = 80.f, kCapRaise = 0x1p60f;
 constexpr float kFastSumLimit = 32768.0f;  // single-pass acceptance: every p of the row <= 2^15
 // Register split: the softmax warpgroups (0, 1) hold a 128-key P row and two 32-column S chunks; the
 // gather and MMA warpgroups (2, 3) need few.  setmaxnreg moves registers between them within the
@@ -778,7 +782,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       int32_t first = 0, pos = 0;  // changed scores: the first key this row sees and its position
       float slope = 0.f;           // and its head's bias per position, in log2 units
       (void)first, (void)pos, (void)slope;
-      [[maybe_unused]] bool wide = false;  // scores beyond the polynomial's range were met
       if constexpr (MOD) {
         pos = jb.causal0 + tok;
         lim = jb.kend;
@@ -849,33 +852,256 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         // reference as stale: the warp then redoes the tile on the exact path -- row maximum first, lazy
         // reference update, then the exponentials.  P is held in registers until the pass is accepted,
         // since it overwrites S.
-        uint32_t pk[2][32];
+        [[maybe_unused]] uint32_t pk[2][32];
         float rowsum = 0.f, alpha = 1.f, m_ref = m_used;
         bool resc = false;
-        bool exact = false;
-        const bool sees = !MOD || (first < key0 + kKeys && first < lim && key0 < lim);  // any key of this tile
-        if (MOD && !__any_sync(0xffffffffu, sees)) {
+        if constexpr (CAP) {
+          // Capped scores are bounded, so nothing is redone for a stale reference: with a cap of up to kCapFixed log2 units
+          // the reference is 0 (weights of 2^-80 .. 2^80 are as exact as others in bf16 and fp32), beyond it an estimate
+          // from the row's first keys, raised between tiles when the sum has grown.  So a chunk's weights go to TMEM at
+          // once, over columns of S that are done with, and the tile is a short loop over 32-column chunks: holding the 64
+          // registers of P until the tile is settled, as below, left the polynomial too few, and unrolled code for the cases
+          // ran at the instruction cache's pace (1394 -> 612 us for 8 prompts of 700..1500 tokens, 64/8 heads).
+          //   t = cap log2(e) tanh(y) - slope |pos - key| - reference, y = s sm_scale / cap
+          // Up to the row's position the bias is linear in the key: it and the reference are one addend, stepped along the
+          // columns.  A chunk with a |y| beyond the polynomial's range is done again from S, 8 columns at a time.
+          const bool sees = first < key0 + kKeys && first < lim && key0 < lim;  // any key of this tile
+          if (!__any_sync(0xffffffffu, sees)) {
+            const uint32_t none[32] = {};
+            tmem_st32(tmem + lane_addr + col_s, none);
+            tmem_st32(tmem + lane_addr + col_s + 32, none);
+          } else {
+            const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
+            if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
+              float top = 0.f;
+              if (p.mod.cap_log2 > kCapFixed) {
+                uint32_t x[16];
+                tmem_ld16(tmem + lane_addr + col_s, x);
+                tc_wait_ld_regs16(x);
+                top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) pk[0][e] = pk[1][e] = 0u;
-        } else
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, e >= lo && e < hi ? __uint_as_float(x[e]) : -INFINITY);
+                top = top == -INFINITY ? 0.f : p.mod.cap_log2 * tanh_any(top * p.mod.cap_in);
+              }
+              // (with negative slopes the farthest key's bias is the largest)
+              if (m_used == -INFINITY && sees) m_ref = top + fmaxf(0.f, -slope * static_cast<float>(abs(pos - first)));
+            }
+            if (__any_sync(0xffffffffu, l > kCapRaise)) {
+              // (a power of two: the accumulators are only shifted)
+              const float up = l > kCapRaise ? static_cast<float>(static_cast<int32_t>(__float_as_uint(l) >> 23) - 127) : 0.f;
+              resc = up > 0.f;
+              m_ref += up;
+              alpha = ex2(-up);
+            }
+            const float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
+            uint64_t sum2[2] = {0, 0};
+            auto run = [&](auto edge_tag) {
+              constexpr bool edge = decltype(edge_tag)::value;  // hidden keys, or keys behind the row's position
+              const uint64_t in2 = f2_pack(p.mod.in2.x, p.mod.in2.y);
+              const uint64_t step2 = f2_pack(2.f * slope, 2.f * slope);
+              auto chunk = [&](const uint32_t (&sr)[32], int c) {
+                const float off = static_cast<float>(key0 + 32 * c - pos);  // minus the distance of the first column
+                const int32_t l0 = lo - 32 * c, h0 = hi - 32 * c;
+                uint64_t add2 = f2_pack(fmaf(slope, off, -m_sub), fmaf(slope, off + 1.f, -m_sub));
+                uint64_t part2[2] = {0, 0};
+                uint32_t pw[16];
+                float y_max = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+                  const uint64_t y2 = f2_mul(s2, in2);
+                  const uint64_t z2 = f2_mul(y2, y2);
+                  float y0, y1;
+                  f2_unpack(y2, y0, y1);
+                  y_max = fmaxf(y_max, fmaxf(fabsf(y0), fabsf(y1)));
+                  auto coef = [&](int i) { return f2_pack(p.mod.cap_poly[i].x, p.mod.cap_poly[i].y); };
+                  uint64_t h2 = coef(kCapTerms - 1);
+#pragma unroll
+                  for (int i = kCapTerms - 2; i >= 0; --i) h2 = f2_fma(h2, z2, coef(i));
+                  if (edge)
+                    add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m_sub), fmaf(-slope, fabsf(off + (2 * e + 1)), -m_sub));
+                  float t0, t1;
+                  f2_unpack(f2_fma(y2, h2, add2), t0, t1);
+                  if (!edge) add2 = f2_add(add2, step2);
+                  if (edge) {
+                    if (2 * e < l0 || 2 * e >= h0) t0 = -INFINITY;
+                    if (2 * e + 1 < l0 || 2 * e + 1 >= h0) t1 = -INFINITY;
+                  }
+                  const float p0 = ex2(t0), p1 = ex2(t1);
+                  part2[e & 1] = f2_add(part2[e & 1], f2_pack(p0, p1));
+                  pw[e] = pack_bf16x2(p0, p1);
+                }
+                if (__any_sync(0xffffffffu, !(y_max <= kCapPolyMax))) {
+                  part2[0] = part2[1] = 0;
 #pragma unroll 1
-        for (int attempt = 0; attempt < (MOD ? 3 : 2); ++attempt) {
+                  for (int q = 0; q < 4; ++q) {
+                    uint32_t x[8], w[4];
+                    tmem_ld8(tmem + lane_addr + col_s + 32 * c + 8 * q, x);
+                    tc_wait_ld_regs8(x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      float t[2];
+#pragma unroll
+                      for (int i = 0; i < 2; ++i) {
+                        const int32_t at = 8 * q + 2 * e + i;
+                        t[i] = p.mod.cap_log2 * tanh_any(__uint_as_float(x[2 * e + i]) * p.mod.cap_in);
+                        t[i] += fmaf(-slope, fabsf(off + static_cast<float>(at)), -m_sub);
+                        if (at < l0 || at >= h0) t[i] = -INFINITY;
+                        t[i] = ex2(t[i]);
+                      }
+                      part2[0] = f2_add(part2[0], f2_pack(t[0], t[1]));
+                      w[e] = pack_bf16x2(t[0], t[1]);
+                    }
+                    tmem_st4(tmem + lane_addr + col_s + 16 * c + 4 * q, w);
+                  }
+                } else {
+                  tmem_st16(tmem + lane_addr + col_s + 16 * c, pw);
+                }
+                sum2[0] = f2_add(sum2[0], part2[0]);
+                sum2[1] = f2_add(sum2[1], part2[1]);
+              };
+              uint32_t ba[32], bb[32];
+              tmem_ld32(tmem + lane_addr + col_s, ba);
+#pragma unroll 1
+              for (int c = 0; c < 4; c += 2) {
+                tc_wait_ld_regs(ba);
+                tmem_ld32(tmem + lane_addr + col_s + 32 * (c + 1), bb);
+                chunk(ba, c);
+                tc_wait_ld_regs(bb);
+                if (c == 0) tmem_ld32(tmem + lane_addr + col_s + 64, ba);
+                chunk(bb, c + 1);
+              }
+            };
+            if (warp_masked) run(BoolTag<true>{});
+            else run(BoolTag<false>{});
+            float a0, a1, a2, a3;
+            f2_unpack(sum2[0], a0, a1);
+            f2_unpack(sum2[1], a2, a3);
+            rowsum = (a0 + a1) + (a2 + a3);
+          }
+        } else if constexpr (MOD) {
+          // As below in 16-column steps, the bias and the reference one addend, stepped along the columns (up to the row's
+          // position the bias is linear in the key).  A tile that the single pass does not settle is rewritten in place as
+          // finished scores, -inf where hidden, with their maximum, and exponentiated from those; that pass is rare, so it
+          // is a loop.  A row's first reference is the largest of its first 16 scores with the
+          // largest bias that any of its keys has: taken with the bias of the first keys, far away, the reference would
+          // have to move in every tile.  It may lie far above the scores so far, which costs nothing while no weight
+          // leaves bf16's range; a row whose whole sum says that they might have is done again in the epilogue.
+          const bool sees = first < key0 + kKeys && first < lim && key0 < lim;  // any key of this tile
+          if (!__any_sync(0xffffffffu, sees)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pk[0][e] = pk[1][e] = 0u;
+          } else {
+            const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
+            auto visible = [&](int c) -> uint32_t {            // of columns 16 c .. 16 c + 15
+              const int32_t l = max(lo - 16 * c, 0), h = min(max(hi - 16 * c, 0), 16);
+              return l >= 16 ? 0u : ((1u << h) - 1u) & ~((1u << l) - 1u);
+            };
+            if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
+              uint32_t x[16];
+              tmem_ld16(tmem + lane_addr + col_s, x);
+              tc_wait_ld_regs16(x);
+              const uint32_t vis16 = visible(0);
+              float top = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, vis16 >> e & 1u ? __uint_as_float(x[e]) : -INFINITY);
+              top *= p.scale_log2;
+              // with the largest bias among the row's keys: 0 at its own position, or (negative slopes) the farthest key's
+              top += fmaxf(0.f, -slope * static_cast<float>(abs(pos - first)));
+              // (0 where the row's keys begin behind these columns)
+              if (m_used == -INFINITY) m_ref = !sees ? -INFINITY : vis16 ? top : 0.f;
+            }
+            uint64_t sum2[4];
+            float m_sub;
+            // kind 0: every key visible and none behind the row's position; 1: not so; 2: finished scores
+            auto exp_tile = [&](auto kind_tag) {
+              constexpr int kind = decltype(kind_tag)::value;
+              m_sub = m_ref == -INFINITY ? 0.f : m_ref;
+              sum2[0] = sum2[1] = sum2[2] = sum2[3] = 0;
+              const uint64_t step2 = f2_pack(2.f * slope, 2.f * slope);
+              const uint64_t in2 = f2_pack(p.mod.in2.x, p.mod.in2.y);
+              auto chunk = [&](const uint32_t (&sr)[16], int c) {
+                const float off = static_cast<float>(key0 + 16 * c - pos);  // minus the distance of the first column
+                uint64_t add2 = kind == 0 ? f2_pack(fmaf(slope, off, -m_sub), fmaf(slope, off + 1.f, -m_sub))
+                                          : f2_pack(-m_sub, -m_sub);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+                  uint64_t t2;
+                  if constexpr (kind == 2) {
+                    t2 = f2_add(s2, add2);
+                  } else {
+                    if (kind == 1)
+                      add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m_sub), fmaf(-slope, fabsf(off + (2 * e + 1)), -m_sub));
+                    t2 = f2_fma(s2, in2, add2);
+                    if (kind == 0) add2 = f2_add(add2, step2);
+                  }
+                  float t0, t1;
+                  f2_unpack(t2, t0, t1);
+                  if (kind == 1) {
+                    if (16 * c + 2 * e < lo || 16 * c + 2 * e >= hi) t0 = -INFINITY;
+                    if (16 * c + 2 * e + 1 < lo || 16 * c + 2 * e + 1 >= hi) t1 = -INFINITY;
+                  }
+                  const float p0 = ex2(t0), p1 = ex2(t1);
+                  sum2[e & 3] = f2_add(sum2[e & 3], f2_pack(p0, p1));
+                  pk[c >> 2][(c & 3) * 8 + e] = pack_bf16x2(p0, p1);
+                }
+              };
+              uint32_t ba[16], bb[16];
+              tmem_ld16(tmem + lane_addr + col_s, ba);
+#pragma unroll
+              for (int c = 0; c < 8; c += 2) {
+                tc_wait_ld_regs16(ba);
+                tmem_ld16(tmem + lane_addr + col_s + 16 * (c + 1), bb);
+                chunk(ba, c);
+                tc_wait_ld_regs16(bb);
+                if (c < 6) tmem_ld16(tmem + lane_addr + col_s + 16 * (c + 2), ba);
+                chunk(bb, c + 1);
+              }
+              float sum8[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sum8[2 * e], sum8[2 * e + 1]);
+              rowsum = ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
+            };
+            if (warp_masked) exp_tile(KindTag<1>{});
+            else exp_tile(KindTag<0>{});
+            const bool stale =
+                !(rowsum <= kFastSumLimit) || (m_used == -INFINITY && slope == 0.f && sees && !(rowsum >= kSumFloor));
+            if (__any_sync(0xffffffffu, stale)) {
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t x[16];
+                tmem_ld16(tmem + lane_addr + col_s + 16 * c, x);
+                tc_wait_ld_regs16(x);
+                const uint32_t vis16 = visible(c);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float s = __uint_as_float(x[e]);
+                  float t = fmaf(-slope, fabsf(static_cast<float>(pos - key0 - 16 * c - e)), s * p.scale_log2);
+                  t = vis16 >> e & 1u ? t : -INFINITY;
+                  top = fmaxf(top, t);
+                  x[e] = __float_as_uint(t);
+                }
+                tmem_st16(tmem + lane_addr + col_s + 16 * c, x);
+              }
+              tc_wait_st();
+              const float m_new = fmaxf(m_used, top);
+              resc = m_new > m_used + kRescaleThreshold;
+              m_ref = resc ? m_new : m_used;
+              exp_tile(KindTag<2>{});
+              alpha = resc ? ex2(m_used - m_sub) : 1.f;
+            }
+          }
+        } else {
+        bool exact = false;
+#pragma unroll 1
+        for (int attempt = 0; attempt < 2; ++attempt) {
           // row max of the raw scores (scale > 0 commutes with max), 8 independent chains
           float mx8[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
-          // changed scores: any score in log2 units with its bias, -inf where it is hidden
-          [[maybe_unused]] auto score = [&](uint32_t sr, int32_t key) -> float {
-            const float s = __uint_as_float(sr);
-            const float x = CAP ? p.mod.cap_log2 * tanh_any(s * p.mod.cap_in) : s * p.scale_log2;
-            return key >= first && key < lim ? fmaf(-slope, fabsf(static_cast<float>(pos - key)), x) : -INFINITY;
-          };
           auto max_chunk = [&](const uint32_t (&sr)[32], int c) {
-            if constexpr (MOD) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], score(sr[e], key0 + c * 32 + e));
-              return;
-            }
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const bool hidden = TREE ? !(vis[c] >> e & 1u) : masked && key0 + c * 32 + e >= lim;
@@ -885,7 +1111,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           };
           auto max_of = [&]() {
             return fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * (MOD ? 1.f : p.scale_log2);
+                         fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * p.scale_log2;
           };
           if (exact) {
             uint32_t ba[32], bb[32];
@@ -921,58 +1147,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           uint64_t sum2[4] = {0, 0, 0, 0};  // 4 independent chains of (even, odd) partial sums
           // The causal / range mask is compiled only into the variant a warp takes when one of its rows
           // ends inside this tile: the other tiles issue no compare or select per score.
-          // changed scores: the largest |y| of the polynomial's arguments
-          [[maybe_unused]] float y_max = 0.f;
           auto exp_chunk = [&](const uint32_t (&sr)[32], int c, auto mask_tag) {
-            if constexpr (MOD) {
-              // 2: any score, one by one; 1: with hidden keys or keys behind the row's position; 0: neither.  The bias and
-              // the reference are one addend: linear in the key up to the row's position.
-              constexpr int kind = decltype(mask_tag)::value;
-              const float off = static_cast<float>(key0 + c * 32 - pos);
-              const uint64_t base2 = f2_pack(fmaf(slope, off, -m_sub), fmaf(slope, off, -m_sub));
-              const uint64_t slope2 = f2_pack(slope, slope);
-              const uint64_t in2 = f2_pack(p.mod.cap_in, p.mod.cap_in);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int32_t key = key0 + c * 32 + 2 * e;
-                float t0, t1;
-                if constexpr (kind == 2) {
-                  t0 = score(sr[2 * e], key) - m_sub;
-                  t1 = score(sr[2 * e + 1], key + 1) - m_sub;
-                } else {
-                  uint64_t add2;
-                  if constexpr (kind == 1)
-                    add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m_sub), fmaf(-slope, fabsf(off + (2 * e + 1)), -m_sub));
-                  else
-                    add2 = f2_fma(slope2, f2_pack(2 * e, 2 * e + 1), base2);
-                  const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-                  uint64_t t2;
-                  if constexpr (CAP) {
-                    const uint64_t y2 = f2_mul(s2, in2);
-                    const uint64_t z2 = f2_mul(y2, y2);
-                    float y0, y1;
-                    f2_unpack(y2, y0, y1);
-                    y_max = fmaxf(y_max, fmaxf(fabsf(y0), fabsf(y1)));
-                    auto coef = [&](int i) { return f2_pack(p.mod.cap_log2 * cap_coef(i), p.mod.cap_log2 * cap_coef(i)); };
-                    uint64_t h2 = coef(kCapTerms - 1);
-#pragma unroll
-                    for (int i = kCapTerms - 2; i >= 0; --i) h2 = f2_fma(h2, z2, coef(i));
-                    t2 = f2_fma(y2, h2, add2);
-                  } else {
-                    t2 = f2_fma(s2, scale2, add2);
-                  }
-                  f2_unpack(t2, t0, t1);
-                  if constexpr (kind == 1) {
-                    if (key < first || key >= lim) t0 = -INFINITY;
-                    if (key + 1 < first || key + 1 >= lim) t1 = -INFINITY;
-                  }
-                }
-                const float p0 = ex2(t0), p1 = ex2(t1);
-                sum2[e & 3] = f2_add(sum2[e & 3], f2_pack(p0, p1));
-                pk[c >> 1][(c & 1) * 16 + e] = pack_bf16x2(p0, p1);
-              }
-              return;
-            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float s0 = __uint_as_float(sr[2 * e]), s1 = __uint_as_float(sr[2 * e + 1]);
@@ -1002,31 +1177,24 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             tc_wait_ld_regs(bb);
             exp_chunk(bb, 3, mask_tag);
           };
-          if constexpr (MOD) {
-            if (exact || wide) exp_tile(KindTag<2>{});
-            else if (warp_masked) exp_tile(KindTag<1>{});
-            else exp_tile(KindTag<0>{});
-          } else {
-            if (warp_masked) exp_tile(BoolTag<true>{});
-            else exp_tile(BoolTag<false>{});
-          }
+          if (warp_masked) exp_tile(BoolTag<true>{});
+          else exp_tile(BoolTag<false>{});
           float sum8[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sum8[2 * e], sum8[2 * e + 1]);
           rowsum = ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
           if (exact) break;
           // (a tree row may see no key of the first tile's chunk 0, or of any tile so far: no reference yet)
-          if (CAP && !wide && __any_sync(0xffffffffu, !(y_max <= kCapPolyMax))) {
-            wide = true;  // (for the rest of the item: tiles with such scores do not come alone)
-            continue;
-          }
-          const bool stale = !(rowsum <= kFastSumLimit) || ((TREE || MOD) && m_ref == -INFINITY && sees);
+          const bool stale = !(rowsum <= kFastSumLimit) || (TREE && m_ref == -INFINITY);
           if (!__any_sync(0xffffffffu, stale)) break;
           exact = true;
         }
+        }
         // P (bf16 pairs) over the first 64 columns of S, read by the PV MMA
-        tmem_st32(tmem + lane_addr + col_s, pk[0]);
-        tmem_st32(tmem + lane_addr + col_s + 32, pk[1]);
+        if constexpr (!CAP) {
+          tmem_st32(tmem + lane_addr + col_s, pk[0]);
+          tmem_st32(tmem + lane_addr + col_s + 32, pk[1]);
+        }
         l = l * alpha + rowsum;
         if (j > 0 && __any_sync(0xffffffffu, resc)) {
           // O_i holds PV_i(j-1): the commit that signalled S_i(j) covers every earlier MMA
@@ -1108,14 +1276,14 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         load_o(oa);
         [[maybe_unused]] bool redo = false;
         if constexpr (MOD) {
-          // a result that is not finite may come from a value that this row does not see
+          // a result that is not finite may come from a value that this row does not see, or from the reference
           float bad[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(oa[c][e]), 0.f, bad[e & 3]);
-          redo = row_valid && (first > jb.kbeg || lim < jb.kend) &&
-                 !((bad[0] + bad[1]) + (bad[2] + bad[3]) == 0.f);
+          redo = row_valid && first < lim &&
+                 (!((bad[0] + bad[1]) + (bad[2] + bad[3]) == 0.f) || !(l >= kSumFloor && l <= kSumCeiling));
         }
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {

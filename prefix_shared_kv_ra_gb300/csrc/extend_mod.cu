@@ -4,9 +4,9 @@
 //
 // The masks are ranges of keys per row, so they act twice: in the work list, where an item (a query tile of a request) gets
 // only the keys that one of its rows sees -- a window of 1024 over a context of 3300 reads a third -- and in the kernel,
-// where tiles that lie inside every row's range are exponentiated without looking at it.  The softmax warps, not the
-// tensor cores, bound this kernel: the cap costs them nine packed instructions per pair of scores beside the
-// exponentials (score_mod.cuh).
+// where tiles that lie inside every row's range are exponentiated without looking at it.  The cap itself is nine packed
+// instructions per pair of scores (score_mod.cuh) where the softmax warps wait on latencies most of the time: 612 us with
+// it, 603 without, 558 for the plain call (8 prompts of 700..1500 tokens over 0..2000 cached, 64/8 heads).
 #include <algorithm>
 
 #include "api_common.h"

@@ -14,6 +14,15 @@
 
 namespace ra {
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kCapPolyMax = 1.25f;
+constexpr int kCapTerms = 7;
+__host__ __device__ __forceinline__ constexpr float cap_coef(int i) {
+  constexpr float c[kCapTerms] = {0.9999994039535522f,    -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
+                                  0.018229123204946518f, -0.004626905079931021f, 0.0005844939732924104f};
+  return c[i];
+}
+
 struct ScoreMod {
   const float* slopes;       // [hq] bias per position of distance (subtracted), or nullptr
   const int32_t* first_key;  // first position that a row sees ([total_q], decode: [batch]), or nullptr
@@ -21,16 +30,9 @@ struct ScoreMod {
   int32_t window;            // keys a row sees up to its own, 0: all
   float cap_in;              // sm_scale / cap (0: no cap)
   float cap_log2;            // cap log2(e)
+  float2 in2;                  // pairs of equal values: cap_in, or sm_scale log2(e) without a cap;
+  float2 cap_poly[kCapTerms];  // cap log2(e) times the coefficients
 };
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kCapPolyMax = 1.25f;
-constexpr int kCapTerms = 7;
-__device__ __forceinline__ constexpr float cap_coef(int i) {
-  constexpr float c[kCapTerms] = {0.9999994039535522f,    -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
-                                  0.018229123204946518f, -0.004626905079931021f, 0.0005844939732924104f};
-  return c[i];
-}
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;

@@ -19,12 +19,15 @@ inline ra_status score_mod(ScoreMod* mod, float sm_scale, float score_cap, int32
   mod->first_key = first_key;
   mod->full_lens = full_lens;
   mod->window = window;
+  mod->in2 = make_float2(sm_scale * kLog2e, sm_scale * kLog2e);
   if (score_cap > 0.f) {
     // beyond these the cap's products leave fp32 (and no score of one is anything but 0 or uncapped)
     RA_REQUIRE(score_cap >= 1e-6f && score_cap <= 1e12f, "score_cap must be in [1e-6, 1e12]");
     mod->cap_in = sm_scale / score_cap;
     RA_REQUIRE(std::isfinite(mod->cap_in) && mod->cap_in > 1e-30f, "sm_scale / score_cap out of range");
+    mod->in2 = make_float2(mod->cap_in, mod->cap_in);
     mod->cap_log2 = score_cap * kLog2e;
+    for (int i = 0; i < kCapTerms; ++i) mod->cap_poly[i] = make_float2(mod->cap_log2 * cap_coef(i), mod->cap_log2 * cap_coef(i));
   }
   return RA_OK;
 }
