@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 512;  // also the requests of one round of the scan
 constexpr int kMaxCluster = 8;
+constexpr int kRun = 4;        // consecutive tokens of a thread
 
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -77,17 +78,25 @@ struct StepParams {
   const int32_t* free_count;
   int32_t* free_count_out;
   int32_t page;
+  uint32_t page_mul;   // n / page = n * page_mul >> page_shift for 0 <= n < 2^31
+  int32_t page_shift;
+  int32_t last_page;   // the last whose slots fit 32 bits
   int32_t *loc, *positions;
+  bool vectors;        // both are 16-byte aligned
   int64_t num_tokens;
   int32_t *qo_indptr, *seq_out;
   uint32_t* err;
+  __device__ __forceinline__ int32_t page_div(int32_t n) const {
+    return static_cast<int32_t>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * page_mul >> page_shift);
+  }
 };
 
 __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p) {
   __shared__ int32_t s_start[kThreads], s_cur[kThreads], s_row[kThreads], s_prev[kThreads], s_fresh[kThreads],
       s_base[kThreads];
+  __shared__ int64_t s_used[kThreads / 32];
   griddep_wait();  // the lengths and the free list may come from the kernels before
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const bool first_cta = cluster_rank() == 0;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kThreads + t, workers = static_cast<int64_t>(gridDim.x) * kThreads;
   int64_t count = __ldg(p.free_count);
@@ -96,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
     count = count < 0 ? 0 : p.free_capacity;
   }
   int64_t tokens = 0, pages = 0;   // of the requests before this round's
-  int64_t used = 0;                // pages that this thread's requests end at
+  int64_t taken = 0;               // pages taken so far
   for (int32_t r0 = 0; r0 < p.batch; r0 += kThreads) {
     const int32_t b = r0 + t;
     const int n = min(kThreads, p.batch - r0);
@@ -114,9 +123,9 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
       }
       if (static_cast<int64_t>(cur) + len > p.table_stride) bad = RA_DEVERR_LENGTH;
       if (row < 0 || row >= p.table_rows) bad |= RA_DEVERR_TABLE;
-      have = static_cast<int32_t>((static_cast<int64_t>(cur) + p.page - 1) / p.page);
+      have = cur > 0 ? p.page_div(cur - 1) + 1 : 0;
       add = len;
-      if (!bad) need = (static_cast<int64_t>(cur) + len + p.page - 1) / p.page - have;
+      if (!bad && len > 0) need = p.page_div(cur + len - 1) + 1 - have;  // (cur + len is within the table)
     }
     int64_t end = add, page_end = need, all_tokens, all_pages;
     scan2(end, page_end, all_tokens, all_pages);
@@ -125,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
     // a request that the arrays or the free list do not hold takes no pages; nor does any after it that needs some
     if (!bad && need > 0 && page_end > count) bad = RA_DEVERR_FULL;
     if (end > p.num_tokens) bad |= RA_DEVERR_LENGTH;
-    if (!bad && need > 0 && page_end > used) used = page_end;
+    const int64_t used = !bad && need > 0 ? page_end : 0;
     const bool ok = b < p.batch && bad == 0;
     if (b < p.batch) {
       s_start[t] = static_cast<int32_t>(end - add < p.num_tokens ? end - add : p.num_tokens);
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
       s_base[t] = static_cast<int32_t>(page_end - need);
       // tokens that fall into the request's last page follow its last slot
       int32_t prev = 0;
-      if (ok && len > 0 && cur % p.page != 0) {
+      if (ok && len > 0 && have * static_cast<int64_t>(p.page) != cur) {
         prev = p.table[static_cast<int64_t>(row) * p.table_stride + cur - 1];
         if (prev < 0 || prev > INT32_MAX - p.page) {
           prev = INT32_MIN;
@@ -145,29 +154,86 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
       s_prev[t] = prev;
       if (bad && first_cta) flag_error(p.err, bad);
     }
+    // the largest end of a request that took pages (they take them in order)
+    const uint32_t takers = __ballot_sync(0xffffffffu, used > 0);
+    if (takers && lane == 31 - __clz(takers)) s_used[warp] = used;
+    if (!takers && lane == 0) s_used[warp] = 0;
     cluster_sync_all();  // every CTA has read this round's lengths and last slots (and wrote its shared arrays)
+    for (int w = 0; w < kThreads / 32; ++w) taken = s_used[w] > taken ? s_used[w] : taken;
     if (first_cta && b < p.batch) {
       p.qo_indptr[b + 1] = static_cast<int32_t>(end < p.num_tokens ? end : p.num_tokens);
       p.seq_out[b] = ok ? cur + len : cur;
     }
     const int64_t stop = tokens + all_tokens < p.num_tokens ? tokens + all_tokens : p.num_tokens;
-    for (int64_t i = tokens + worker; i < stop; i += workers) {
-      const int r = request_of(s_start, n, static_cast<int32_t>(i));
-      const int32_t pos = s_cur[r] + static_cast<int32_t>(i - s_start[r]);
-      int32_t slot = 0;
-      if (s_row[r] >= 0) {
-        const int32_t pg = pos / p.page - s_fresh[r];  // >= 0: in a page taken by this call
-        if (pg >= 0) {
-          const int32_t id = __ldg(p.free_pages + (count - 1 - s_base[r] - pg));
-          if (id >= 0 && id <= (INT32_MAX - p.page) / p.page) slot = id * p.page + pos % p.page;
-          else flag_error(p.err, RA_DEVERR_SLOT);
-        } else if (s_prev[r] >= 0) {
-          slot = s_prev[r] + 1 + (pos - s_cur[r]);
+    // Runs of kRun tokens per thread: one search and one division each where the run lies in one request, its page ids
+    // on the way at once.  (Token by token, with two runtime divisions, the 65,000 tokens of a prefill took 10 us of a
+    // cluster's issue slots.)
+    for (int64_t i0 = tokens + worker * kRun; i0 < stop; i0 += workers * kRun) {
+      int r = request_of(s_start, n, static_cast<int32_t>(i0));
+      int32_t pos[kRun], slot[kRun], id[kRun], in_page[kRun];
+      int32_t* row[kRun];
+      int32_t next = r + 1 < n ? s_start[r + 1] : INT32_MAX;
+      bool fresh = true;  // look the request up
+      int32_t pg = 0, off = 0, p0 = 0;
+      const int32_t* ids = nullptr;
+      int32_t* out = nullptr;
+      int32_t prev = 0;
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        const int32_t i = static_cast<int32_t>(i0) + k;
+        slot[k] = 0;
+        id[k] = INT32_MIN;
+        row[k] = nullptr;
+        if (i >= stop) continue;
+        while (i >= next) {  // (over requests without new tokens)
+          ++r;
+          next = r + 1 < n ? s_start[r + 1] : INT32_MAX;
+          fresh = true;
         }
-        p.table[static_cast<int64_t>(s_row[r]) * p.table_stride + pos] = slot;
+        if (fresh) {
+          fresh = false;
+          const int32_t cur = s_cur[r];
+          p0 = cur + (i - s_start[r]) - i;  // position of token i: p0 + i
+          pg = p.page_div(p0 + i);
+          off = p0 + i - pg * p.page;
+          pg -= s_fresh[r];
+          ids = p.free_pages + (count - 1 - s_base[r]);
+          out = s_row[r] >= 0 ? p.table + static_cast<int64_t>(s_row[r]) * p.table_stride : nullptr;
+          prev = s_prev[r] >= 0 ? s_prev[r] + 1 - cur : INT32_MIN;
+        }
+        pos[k] = p0 + i;
+        in_page[k] = off;
+        if (out) {
+          row[k] = out + pos[k];
+          if (pg >= 0) {  // in a page taken by this call
+            id[k] = __ldg(ids - pg);
+            slot[k] = -1;
+          } else if (prev != INT32_MIN) {
+            slot[k] = prev + pos[k];
+          }
+        }
+        if (++off == p.page) off = 0, ++pg;
       }
-      p.loc[i] = slot;
-      p.positions[i] = pos;
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        if (slot[k] < 0) {
+          slot[k] = 0;
+          if (id[k] >= 0 && id[k] <= p.last_page) slot[k] = id[k] * p.page + in_page[k];
+          else flag_error(p.err, RA_DEVERR_SLOT);
+        }
+        if (row[k]) *row[k] = slot[k];
+      }
+      if (p.vectors && i0 % kRun == 0 && i0 + kRun <= stop) {
+        *reinterpret_cast<int4*>(p.loc + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        *reinterpret_cast<int4*>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+          if (i0 + k >= stop) break;
+          p.loc[i0 + k] = slot[k];
+          p.positions[i0 + k] = pos[k];
+        }
+      }
     }
     tokens += all_tokens;
     pages += all_pages;
@@ -178,16 +244,9 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
     p.loc[i] = 0;
     p.positions[i] = 0;
   }
-  if (first_cta) {
-    __shared__ unsigned long long s_used;
-    if (t == 0) s_used = 0;
-    __syncthreads();
-    if (used > 0) atomicMax(&s_used, static_cast<unsigned long long>(used));
-    __syncthreads();
-    if (t == 0) {
-      p.qo_indptr[0] = 0;
-      *p.free_count_out = static_cast<int32_t>(count - static_cast<int64_t>(s_used));
-    }
+  if (first_cta && t == 0) {
+    p.qo_indptr[0] = 0;
+    *p.free_count_out = static_cast<int32_t>(count - taken);
   }
   launch_behind_writes();
 }
@@ -343,9 +402,34 @@ extern "C" ra_status ra_step_slots(int32_t* req_to_token, int64_t table_stride, 
                  aligned4(free_pages) && aligned4(free_count) && aligned4(free_count_out) && aligned4(out_cache_loc) &&
                  aligned4(positions) && aligned4(qo_indptr) && aligned4(seq_lens_out),
              "index arrays must be 4-byte aligned");
-  const StepParams p{req_to_token, table_stride,  table_rows,     req_pool_indices, seq_lens,      new_lens,
-                     batch,        free_pages,    free_capacity,  free_count,       free_count_out, page_size,
-                     out_cache_loc, positions,    num_tokens,     qo_indptr,        seq_lens_out,  device_error};
+  // n / d for n < 2^31 by a product: with l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1 fits 32 bits and exceeds
+  // 2^(31 + l) / d by at most 1, so that n m / 2^(31 + l) is less than 1 / d above n / d
+  int32_t shift = 31;
+  while ((int64_t(1) << (shift - 31)) < page_size) ++shift;
+  const uint32_t mul = static_cast<uint32_t>((int64_t(1) << shift) / page_size + 1);
+  StepParams p{};
+  p.table = req_to_token;
+  p.table_stride = table_stride;
+  p.table_rows = table_rows;
+  p.rpi = req_pool_indices;
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.batch = batch;
+  p.free_pages = free_pages;
+  p.free_capacity = free_capacity;
+  p.free_count = free_count;
+  p.free_count_out = free_count_out;
+  p.page = page_size;
+  p.page_mul = mul;
+  p.page_shift = shift;
+  p.last_page = (INT32_MAX - page_size) / page_size;
+  p.loc = out_cache_loc;
+  p.positions = positions;
+  p.vectors = aligned16(out_cache_loc) && aligned16(positions);
+  p.num_tokens = num_tokens;
+  p.qo_indptr = qo_indptr;
+  p.seq_out = seq_lens_out;
+  p.err = device_error;
   return launch_cluster("step_slots_kernel", step_slots_kernel, batch == 0 ? 1 : cluster_ctas(num_tokens),
                         reinterpret_cast<cudaStream_t>(stream), p);
 }

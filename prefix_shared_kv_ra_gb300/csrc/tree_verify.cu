@@ -80,6 +80,31 @@ __device__ __forceinline__ Pair residual(float p, float q, float th, float tl) {
   return __fadd_rn(d, lo) > 0.f ? Pair{d, lo} : Pair{0.f, 0.f};  // (also 0 for a NaN)
 }
 
+__device__ __forceinline__ void pair_reduce(Pair& acc) {  // over the warp; lane 0's result counts
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float hi = __shfl_xor_sync(0xffffffffu, acc.hi, off), lo = __shfl_xor_sync(0xffffffffu, acc.lo, off);
+    pair_add(acc, hi, lo);
+  }
+}
+
+// The first lane whose prefix sum exceeds the goal (`base`, then the lanes' values in turn), and the sum before it; where
+// there is none, the last lane with any weight.  Warp-collective.
+__device__ __forceinline__ int place(double mine, double base, double goal, double* before) {
+  const int lane = threadIdx.x & 31;
+  double incl = mine;
+#pragma unroll
+  for (int off = 1; off < kWarps; off <<= 1) {  // (at most kWarps lanes hold values)
+    const double y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  const uint32_t over = __ballot_sync(0xffffffffu, base + incl > goal && mine > 0.0);
+  const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
+  const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
+  *before = base + __shfl_sync(0xffffffffu, incl - mine, at);
+  return at;
+}
+
 struct VerifyParams {
   const float* target;  // [total_q, vocab] rows at target_stride
   int64_t target_stride;
@@ -131,15 +156,15 @@ __device__ __forceinline__ void nothing_verified(int32_t* path, int32_t* accept_
 enum Command { kSum = 0, kDraw = 1 };
 
 template <bool DRAWN>
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParams p, int32_t ctas) {
+__global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyParams p, int32_t ctas) {
   __shared__ Tree s_tree;
   __shared__ float s_p[kMaxTree], s_q[kMaxTree], s_u[kMaxTree];
   __shared__ int32_t s_path[kMaxTree];
   __shared__ double s_warp[kWarps];                  // this CTA's slices' sums
   __shared__ double s_rank[2][kMaxCluster];          // every CTA's sum, by the pass's parity
-  __shared__ int32_t s_command, s_node, s_more;
-  __shared__ double s_t;
-  __shared__ double s_total;
+  __shared__ int32_t s_command, s_node, s_more, s_owner, s_who;
+  __shared__ double s_part[kWarps];
+  __shared__ double s_t, s_total, s_before, s_goal;
   griddep_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int32_t b = blockIdx.x / ctas;
@@ -226,14 +251,16 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
         if (s_tree.parent[i] == at && s_tree.token[i] == v) return true;
       return false;
     };
-    bool holes = false;  // refused tokens lie in this warp's slice
-    if (!DRAWN) {
+    auto refused_between = [&](int32_t from, int32_t to) -> bool {  // any of them in [from, to) (warp-collective)
+      bool any = false;
       for (int32_t i = at + 1; i < T; i += 32) {
-        const bool mine = i + lane < T && s_tree.parent[i + lane] == at && s_tree.token[i + lane] >= v0 &&
-                          s_tree.token[i + lane] < v1;
-        holes = holes || __any_sync(0xffffffffu, mine);
+        const bool mine = i + lane < T && s_tree.parent[i + lane] == at && s_tree.token[i + lane] >= from &&
+                          s_tree.token[i + lane] < to;
+        any = any || __any_sync(0xffffffffu, mine);
       }
-    }
+      return any;
+    };
+    bool holes = DRAWN || plain ? false : refused_between(v0, v1);  // refused tokens lie in this warp's slice
     auto weight = [&](int32_t v) -> Pair {
       const float x = __ldg(prow + v);
       if (DRAWN && !plain) return residual(x, __ldg(qrow + v), th, tl);
@@ -264,18 +291,13 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
         const Pair w = weight(v);
         pair_add(acc, w.hi, w.lo);
       }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        const float hi = __shfl_xor_sync(0xffffffffu, acc.hi, off), lo = __shfl_xor_sync(0xffffffffu, acc.lo, off);
-        pair_add(acc, hi, lo);
-      }
-      // (xor order: the lanes' sums differ in their last bits; lane 0's counts)
+      pair_reduce(acc);
       if (lane == 0) s_warp[warp] = pair_value(acc);
       __syncthreads();
       if (warp == 0) {
         double s = lane < kWarps ? s_warp[lane] : 0.0;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        for (int off = kWarps / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         s = __shfl_sync(0xffffffffu, s, 0);
         if (lane < ctas)
           st_cluster_b64(smem_u32(&s_rank[parity][rank]), lane, static_cast<uint64_t>(__double_as_longlong(s)));
@@ -304,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
     if (!(sum > 0.0) && (DRAWN ? tt > 0.0 : true)) {
       // nothing left of the residual (rounding, or refused tokens that held all of p): p itself
       __syncthreads();
-      plain = true;
+      plain = true;  // (given drafts: without the refused tokens' holes)
       th = tl = 0.f;
       holes = false;
       sum = row_sum(parity ^= 1);
@@ -314,71 +336,59 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
         if (t == 0) flag_error(p.err, RA_DEVERR_VALUE), p.next_tokens[b] = 0;
       }
     } else {
-      // the CTA, the warp and the place in its slice where the prefix sums first exceed u S; where rounding leaves none,
-      // the last with any weight
-      const double goal = static_cast<double>(__ldg(p.u_final + b)) * sum;
-      double before = 0.0;
-      int32_t owner = -1, last = 0;
-      double at_owner = 0.0, at_last = 0.0;
-      for (int r = 0; r < ctas; ++r) {
-        const double s = s_rank[parity][r];
-        if (s > 0.0) last = r, at_last = before;
-        if (owner < 0 && before + s > goal) owner = r, at_owner = before;
-        before += s;
-      }
-      const bool end = owner < 0;
-      if (end) owner = last, at_owner = at_last;
-      if (static_cast<int32_t>(rank) == owner) {
-        int32_t who = -1, tail = 0;
-        double base = 0.0, tail_base = 0.0, run = at_owner;
-        for (int w = 0; w < kWarps; ++w) {
-          const double s = s_warp[w];
-          if (s > 0.0) tail = w, tail_base = run;
-          if (who < 0 && !end && run + s > goal) who = w, base = run;
-          run += s;
+      // The CTA, then the warp's slice where the prefix sums first exceed u S, by warp 0 of every CTA; then the owner's
+      // whole CTA over that slice.  Where rounding leaves no place, the last with any weight.
+      if (warp == 0) {
+        const double goal = static_cast<double>(__ldg(p.u_final + b)) * sum;
+        double before;
+        const int owner = place(lane < ctas ? s_rank[parity][lane] : 0.0, 0.0, goal, &before);
+        if (lane == 0) s_owner = owner;
+        if (owner == static_cast<int>(rank)) {
+          const int who = place(lane < kWarps ? s_warp[lane] : 0.0, before, goal, &before);
+          if (lane == 0) s_who = who, s_before = before, s_goal = goal;
         }
-        if (who < 0) who = tail, base = tail_base;
-        if (warp == who) {
-          // lane l sums the l-th part of the slice; then a lane per token of the part that holds the goal
-          const int32_t part = (v1 - v0 + 31) / 32;
-          const int32_t a0 = min(v0 + lane * part, v1), a1 = min(a0 + part, v1);
-          Pair acc{0.f, 0.f};
-          for (int32_t v = a0; v < a1; ++v) {
-            const Pair w = weight(v);
-            pair_add(acc, w.hi, w.lo);
-          }
-          const double mine = pair_value(acc);
-          double incl = mine;
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-          }
-          const uint32_t above = __ballot_sync(0xffffffffu, !end && base + incl > goal && mine > 0.0);
-          const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
-          const int from = above ? __ffs(above) - 1 : 31 - __clz(some);
-          const int32_t c0 = __shfl_sync(0xffffffffu, a0, from), c1 = __shfl_sync(0xffffffffu, a1, from);
-          double run2 = base + __shfl_sync(0xffffffffu, incl - mine, from);
-          int32_t found = -1, tail_v = c0;
+      }
+      __syncthreads();
+      if (s_owner == static_cast<int>(rank)) {
+        const int64_t slice0 = static_cast<int64_t>(slice) * (rank * kWarps + s_who);
+        const int32_t e0 = static_cast<int32_t>(slice0 < p.vocab ? slice0 : p.vocab);
+        const int32_t e1 = static_cast<int32_t>(slice0 + slice < p.vocab ? slice0 + slice : p.vocab);
+        const int32_t part = (e1 - e0 + kWarps - 1) / kWarps;
+        const int32_t c0 = min(e0 + warp * part, e1), c1 = min(c0 + part, e1);
+        if (!DRAWN) holes = !plain && refused_between(c0, c1);
+        const double goal = s_goal;
+        Pair acc{0.f, 0.f};
+        for (int32_t v = c0 + lane; v < c1; v += 32) {
+          const Pair w = weight(v);
+          pair_add(acc, w.hi, w.lo);
+        }
+        pair_reduce(acc);
+        if (lane == 0) s_part[warp] = pair_value(acc);
+        __syncthreads();
+        double before = s_before;
+        const int who = place(lane < kWarps ? s_part[lane] : 0.0, before, goal, &before);
+        if (who == warp) {
+          // the groups of 32 tokens in turn
+          int32_t found = -1, tail = c0;
           for (int32_t v = c0; v < c1 && found < 0; v += 32) {
-            double w = 0.0;
-            if (v + lane < c1) w = pair_value(weight(v + lane));
-            double in = w;
+            const double w = v + lane < c1 ? pair_value(weight(v + lane)) : 0.0;
+            double incl = w;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-              const double y = __shfl_up_sync(0xffffffffu, in, off);
-              if (lane >= off) in += y;
+              const double y = __shfl_up_sync(0xffffffffu, incl, off);
+              if (lane >= off) incl += y;
             }
-            const uint32_t over = __ballot_sync(0xffffffffu, above && run2 + in > goal && w > 0.0);
+            const uint32_t over = __ballot_sync(0xffffffffu, before + incl > goal && w > 0.0);
             const uint32_t any = __ballot_sync(0xffffffffu, w > 0.0);
             if (over) found = v + __ffs(over) - 1;
-            if (any) tail_v = v + 31 - __clz(any);
-            run2 += __shfl_sync(0xffffffffu, in, 31);
+            if (any) tail = v + 31 - __clz(any);
+            before += __shfl_sync(0xffffffffu, incl, 31);
           }
-          if (lane == 0) p.next_tokens[b] = found >= 0 ? found : tail_v;
+          if (lane == 0) p.next_tokens[b] = found >= 0 ? found : tail;
         }
       }
     }
+    __syncthreads();
     if (rank == 0) {
       // (warp 0's count, through the path's end)
       if (t == 0) p.accept_lens[b] = count, s_node = count;
@@ -470,7 +480,7 @@ __device__ __forceinline__ uint64_t row_largest(const E* row, int32_t vocab, int
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) tree_verify_greedy_kernel(const GreedyParams p, int32_t ctas) {
+__global__ void __launch_bounds__(kThreads, 2) tree_verify_greedy_kernel(const GreedyParams p, int32_t ctas) {
   __shared__ Tree s_tree;
   __shared__ int32_t s_path[kMaxTree];
   __shared__ uint64_t s_warp[kWarps];
@@ -541,10 +551,11 @@ __global__ void __launch_bounds__(kThreads) tree_verify_greedy_kernel(const Gree
 }
 
 // CTAs per request: 8 (the most that any GPU of the architecture runs as one cluster) unless a slice would be less than a
-// few loads per thread.
-int cluster_ctas(int32_t vocab) {
+// load or two per thread, or the requests then no longer run all at once, two CTAs an SM.
+int cluster_ctas(int32_t vocab, int32_t batch, int sms) {
   int c = kMaxCluster;
   while (c > 1 && static_cast<int64_t>(vocab) < static_cast<int64_t>(c) * kThreads) c /= 2;
+  while (c > 1 && static_cast<int64_t>(batch) * c > 2 * sms) c /= 2;
   return c;
 }
 
@@ -602,8 +613,11 @@ extern "C" ra_status ra_tree_verify(const float* target_probs, int64_t target_st
                        parents,      draft_lens,    qo_indptr,   accept_uniforms, final_uniforms, total_q,
                        max_draft_len, path,         accept_lens, next_tokens,  device_error};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return draft_probs ? launch_requests("tree_verify_kernel", tree_verify_kernel<true>, batch, cluster_ctas(vocab), s, p)
-                     : launch_requests("tree_verify_kernel", tree_verify_kernel<false>, batch, cluster_ctas(vocab), s, p);
+  DeviceInfo dev;
+  if (ra_status st = current_device(&dev)) return st;
+  const int ctas = cluster_ctas(vocab, batch, dev.num_sms);
+  return draft_probs ? launch_requests("tree_verify_kernel", tree_verify_kernel<true>, batch, ctas, s, p)
+                     : launch_requests("tree_verify_kernel", tree_verify_kernel<false>, batch, ctas, s, p);
 }
 
 extern "C" ra_status ra_tree_verify_greedy(const void* target_logits, int32_t logits_fp32, int64_t logits_stride,
@@ -626,7 +640,9 @@ extern "C" ra_status ra_tree_verify_greedy(const void* target_logits, int32_t lo
   const GreedyParams p{target_logits, logits_stride, vocab,         draft_tokens, parents,     draft_lens,  qo_indptr,
                        total_q,       max_draft_len, path,          accept_lens,  next_tokens, device_error};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int ctas = cluster_ctas(vocab);
+  DeviceInfo dev;
+  if (ra_status st = current_device(&dev)) return st;
+  const int ctas = cluster_ctas(vocab, batch, dev.num_sms);
   return logits_fp32
              ? launch_requests("tree_verify_greedy_kernel", tree_verify_greedy_kernel<float>, batch, ctas, s, p)
              : launch_requests("tree_verify_greedy_kernel", tree_verify_greedy_kernel<__nv_bfloat16>, batch, ctas, s, p);
