@@ -13,9 +13,9 @@
 // slice, then the slice that holds u S, then its place there.
 //
 // Precision: the drawn token is a whole number that depends on where u S falls between neighbouring prefix sums, as little
-// as 1e-9 apart at a vocabulary of 100,000; fp32 sums would move one draw in hundreds.  p - t q and its sums are held in
-// pairs of floats (an unevaluated sum, about 2^-45 relative) in the fp32 pipe: this GPU's 64-bit rate (2 a clock and SM)
-// would cost 15 us for the 8M values of 64 rows.  Products of a few values and the last sums are in 64 bits.
+// as 1e-9 apart at a vocabulary of 100,000; fp32 sums would move one draw in hundreds.  p - t q, the sums and what they are
+// compared with are held as pairs of floats (unevaluated sums, about 2^-45 relative) in the fp32 pipe: this GPU's 64-bit
+// rate is two values a clock and SM, and even the few scans and comparisons of a draw took 5 us of a call in it.
 //
 // Bound: the rows read, once each (a pass over 64 pairs of rows of 128,000 is 66 MB, 10 us of HBM), and for few requests
 // the chain of gather, pass and search, about 1.5 us each.
@@ -55,7 +55,8 @@ __device__ __forceinline__ void st_cluster_b64(uint32_t addr, uint32_t rank, uin
   asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
 }
 
-// ---- unevaluated sums of two floats (error-free transformations of a sum: Knuth; of a product: one fma)
+// ---- unevaluated sums of two floats, |lo| at most half a last place of hi where they are results (error-free
+// transformations: of a sum, Knuth; of a product, one fma)
 struct Pair {
   float hi, lo;
 };
@@ -64,44 +65,60 @@ __device__ __forceinline__ float sum_error(float a, float b, float s) {
   const float bb = __fsub_rn(s, a);
   return __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
 }
-__device__ __forceinline__ void pair_add(Pair& acc, float hi, float lo) {
-  const float s = __fadd_rn(acc.hi, hi);
-  acc.lo = __fadd_rn(acc.lo, __fadd_rn(sum_error(acc.hi, hi, s), lo));
+__device__ __forceinline__ Pair pair_of(float hi, float lo) {  // |lo| well below |hi|
+  const float s = __fadd_rn(hi, lo);
+  return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const float s = __fadd_rn(a.hi, b.hi);
+  return pair_of(s, __fadd_rn(sum_error(a.hi, b.hi, s), __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) { return a + Pair{-b.hi, -b.lo}; }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  const float m = __fmul_rn(a.hi, b.hi);
+  return pair_of(m, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -m))));
+}
+__device__ __forceinline__ bool operator<(Pair a, Pair b) { return (a - b).hi < 0.f; }
+// Running sums: two floats' worth without the normalisation of every step.
+__device__ __forceinline__ void pair_add(Pair& acc, float x) {
+  const float s = __fadd_rn(acc.hi, x);
+  acc.lo = __fadd_rn(acc.lo, sum_error(acc.hi, x, s));
   acc.hi = s;
 }
-__device__ __forceinline__ double pair_value(const Pair& a) { return static_cast<double>(a.hi) + static_cast<double>(a.lo); }
-
-// max(p - t q, 0) as a pair; t = th + tl.
-__device__ __forceinline__ Pair residual(float p, float q, float th, float tl) {
-  const float m = __fmul_rn(th, q);
-  const float me = __fmaf_rn(th, q, -m);
-  const float d = __fsub_rn(p, m);
-  const float lo = __fmaf_rn(-tl, q, __fsub_rn(sum_error(p, -m, d), me));
-  return __fadd_rn(d, lo) > 0.f ? Pair{d, lo} : Pair{0.f, 0.f};  // (also 0 for a NaN)
+__device__ __forceinline__ Pair pair_shfl(Pair a, int lane) {
+  return {__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+__device__ __forceinline__ Pair pair_reduce(Pair a) {  // over the warp; lane 0's result counts
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    a = a + Pair{__shfl_xor_sync(0xffffffffu, a.hi, off), __shfl_xor_sync(0xffffffffu, a.lo, off)};
+  return a;
+}
+__device__ __forceinline__ Pair pair_scan(Pair a) {  // inclusive, over the warp
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const Pair b{__shfl_up_sync(0xffffffffu, a.hi, off), __shfl_up_sync(0xffffffffu, a.lo, off)};
+    if (lane >= off) a = a + b;
+  }
+  return a;
 }
 
-__device__ __forceinline__ void pair_reduce(Pair& acc) {  // over the warp; lane 0's result counts
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float hi = __shfl_xor_sync(0xffffffffu, acc.hi, off), lo = __shfl_xor_sync(0xffffffffu, acc.lo, off);
-    pair_add(acc, hi, lo);
-  }
+// max(p - t q, 0); 0 also for a NaN.
+__device__ __forceinline__ Pair residual(float p, float q, Pair t) {
+  const float m = __fmul_rn(t.hi, q), d = __fsub_rn(p, m);
+  const Pair r = pair_of(d, __fmaf_rn(-t.lo, q, __fsub_rn(sum_error(p, -m, d), __fmaf_rn(t.hi, q, -m))));
+  return r.hi > 0.f ? r : Pair{0.f, 0.f};
 }
 
 // The first lane whose prefix sum exceeds the goal (`base`, then the lanes' values in turn), and the sum before it; where
 // there is none, the last lane with any weight.  Warp-collective.
-__device__ __forceinline__ int place(double mine, double base, double goal, double* before) {
-  const int lane = threadIdx.x & 31;
-  double incl = mine;
-#pragma unroll
-  for (int off = 1; off < kWarps; off <<= 1) {  // (at most kWarps lanes hold values)
-    const double y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
-  }
-  const uint32_t over = __ballot_sync(0xffffffffu, base + incl > goal && mine > 0.0);
-  const uint32_t some = __ballot_sync(0xffffffffu, mine > 0.0);
+__device__ __forceinline__ int place(Pair mine, Pair base, Pair goal, Pair* before) {
+  const Pair incl = base + pair_scan(mine);
+  const uint32_t over = __ballot_sync(0xffffffffu, goal < incl && mine.hi > 0.f);
+  const uint32_t some = __ballot_sync(0xffffffffu, mine.hi > 0.f);
   const int at = over ? __ffs(over) - 1 : some ? 31 - __clz(some) : 0;
-  *before = base + __shfl_sync(0xffffffffu, incl - mine, at);
+  *before = at > 0 ? pair_shfl(incl, (at + 31) & 31) : base;
   return at;
 }
 
@@ -146,6 +163,16 @@ __device__ __forceinline__ int32_t next_child(const Tree& tree, int32_t node, in
   return T;
 }
 
+// Whether a child of `node` before `child` has its token (warp-collective).
+__device__ __forceinline__ bool refused_before(const Tree& tree, int32_t node, int32_t child) {
+  const int lane = threadIdx.x & 31;
+  for (int32_t i = node + 1; i < child; i += 32) {
+    const bool same = i + lane < child && tree.parent[i + lane] == node && tree.token[i + lane] == tree.token[child];
+    if (__any_sync(0xffffffffu, same)) return true;
+  }
+  return false;
+}
+
 // A request of a padded batch, or one whose lengths are wrong.
 __device__ __forceinline__ void nothing_verified(int32_t* path, int32_t* accept_lens, int32_t* next_tokens, int32_t b,
                                                  int32_t max_draft) {
@@ -160,11 +187,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
   __shared__ Tree s_tree;
   __shared__ float s_p[kMaxTree], s_q[kMaxTree], s_u[kMaxTree];
   __shared__ int32_t s_path[kMaxTree];
-  __shared__ double s_warp[kWarps];                  // this CTA's slices' sums
-  __shared__ double s_rank[2][kMaxCluster];          // every CTA's sum, by the pass's parity
+  __shared__ Pair s_warp[kWarps];                      // this CTA's slices' sums
+  __shared__ __align__(8) Pair s_rank[2][kMaxCluster];  // every CTA's sum, by the pass's parity
   __shared__ int32_t s_command, s_node, s_more, s_owner, s_who;
-  __shared__ double s_part[kWarps];
-  __shared__ double s_t, s_total, s_before, s_goal;
+  __shared__ Pair s_part[kWarps];
+  __shared__ Pair s_t, s_total, s_before, s_goal;
   griddep_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int32_t b = blockIdx.x / ctas;
@@ -183,10 +210,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
     s_tree.parent[i] = child ? parent : -1;
     if (child && !known && rank == 0) flag_error(p.err, RA_DEVERR_VALUE);
     const int64_t row = first + parent;
-    s_p[i] = child && known ? __ldg(p.target + row * p.target_stride + x) : 0.f;
-    if (DRAWN) s_q[i] = child && known ? __ldg(p.draft + row * p.draft_stride + x) : 0.f;
+    s_p[i] = child && known ? fmaxf(__ldg(p.target + row * p.target_stride + x), 0.f) : 0.f;
+    if (DRAWN) s_q[i] = child && known ? fmaxf(__ldg(p.draft + row * p.draft_stride + x), 0.f) : 0.f;
     s_u[i] = __ldg(p.u_accept + first + i);
   }
+  const float u_final = __ldg(p.u_final + b);
   // this warp's slice of a row
   const int32_t slice = (p.vocab + ctas * kWarps - 1) / (ctas * kWarps);
   const int64_t begin = static_cast<int64_t>(slice) * (rank * kWarps + warp);
@@ -194,9 +222,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
   const int32_t v1 = static_cast<int32_t>(begin + slice < p.vocab ? begin + slice : p.vocab);
   __syncthreads();
 
+  const Pair kNone{0.f, 0.f}, kOne{1.f, 0.f};
   // The walk's state, in every lane of warp 0.
   int32_t node = 0, child = 0, count = 1;
-  double tq = 0.0, total = 1.0;
+  Pair tq = kNone, total = kOne;
   if (t == 0) s_path[0] = 0;
   for (int32_t pass = 0;; ++pass) {
     if (warp == 0) {
@@ -205,32 +234,28 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
       for (;;) {
         child = next_child(s_tree, node, child, T);
         if (child == T) break;
-        const double u = s_u[child], px = s_p[child], qx = DRAWN ? s_q[child] : 1.0;
-        double r = px;
+        const Pair u{s_u[child], 0.f};
+        const float px = s_p[child], qx = DRAWN ? s_q[child] : 1.f;
+        Pair r{px, 0.f};
         if (DRAWN) {
-          r = fmax(px - tq * qx, 0.0);
-        } else {
-          // a token refused at this node already has no weight left
-          for (int32_t i = node + 1; i < child; i += 32) {
-            const bool same = i + lane < child && s_tree.parent[i + lane] == node &&
-                              s_tree.token[i + lane] == s_tree.token[child];
-            if (__any_sync(0xffffffffu, same)) r = 0.0;
-          }
+          r = residual(px, qx, tq);
+        } else if (refused_before(s_tree, node, child)) {
+          r = kNone;  // a token refused at this node already has no weight left
         }
-        if (u * qx * total < r) {
+        if (u * Pair{qx, 0.f} * total < r) {
           if (lane == 0) s_path[count] = child;
           ++count;
           node = child;  // (its children are behind it)
-          tq = 0.0;
-          total = 1.0;
+          tq = kNone;
+          total = kOne;
           continue;
         }
         if (DRAWN) {
-          tq += total;
+          tq = tq + total;
           command = kSum;
           break;
         }
-        total -= r;
+        total = total - r;
       }
       if (lane == 0) {
         s_command = command;
@@ -241,77 +266,86 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
     __syncthreads();
     const bool draw = s_command == kDraw;
     const int32_t at = s_node;
-    const double tt = s_t;
-    float th = static_cast<float>(tt), tl = static_cast<float>(tt - static_cast<double>(th));
+    Pair tt = s_t;
     const float* prow = p.target + (first + at) * p.target_stride;
     const float* qrow = DRAWN ? p.draft + (first + at) * p.draft_stride : nullptr;
-    bool plain = DRAWN && tt == 0.0;  // the residual is p itself
-    auto refused = [&](int32_t v) -> bool {  // given drafts: v is a child's token (all were refused)
-      for (int32_t i = at + 1; i < T; ++i)
-        if (s_tree.parent[i] == at && s_tree.token[i] == v) return true;
-      return false;
+    bool plain = DRAWN && tt.hi == 0.f;  // the residual is p itself
+    // given drafts: the children of the node (all were refused) with tokens in [from, to), each distinct token once
+    // (warp-collective): f(child)
+    auto for_refused = [&](int32_t from, int32_t to, auto f) {
+      for (int32_t i = at; (i = next_child(s_tree, at, i, T)) < T;)
+        if (s_tree.token[i] >= from && s_tree.token[i] < to && !refused_before(s_tree, at, i)) f(i);
     };
-    auto refused_between = [&](int32_t from, int32_t to) -> bool {  // any of them in [from, to) (warp-collective)
-      bool any = false;
-      for (int32_t i = at + 1; i < T; i += 32) {
-        const bool mine = i + lane < T && s_tree.parent[i + lane] == at && s_tree.token[i + lane] >= from &&
-                          s_tree.token[i + lane] < to;
-        any = any || __any_sync(0xffffffffu, mine);
-      }
-      return any;
-    };
-    bool holes = DRAWN || plain ? false : refused_between(v0, v1);  // refused tokens lie in this warp's slice
+    bool holes = false;  // the tokens looked at include refused ones
     auto weight = [&](int32_t v) -> Pair {
-      const float x = __ldg(prow + v);
-      if (DRAWN && !plain) return residual(x, __ldg(qrow + v), th, tl);
-      if (!DRAWN && holes && refused(v)) return Pair{0.f, 0.f};
-      return Pair{fmaxf(x, 0.f), 0.f};
+      const float x = fmaxf(__ldg(prow + v), 0.f);
+      if (DRAWN && !plain) return residual(x, fmaxf(__ldg(qrow + v), 0.f), tt);
+      if (!DRAWN && holes) {
+        for (int32_t i = at + 1; i < T; ++i)
+          if (s_tree.parent[i] == at && s_tree.token[i] == v) return kNone;
+      }
+      return {x, 0.f};
     };
     // the sum of the residual over the row: each warp its slice, then the CTA, then the cluster
-    auto row_sum = [&](int parity) -> double {
-      Pair acc{0.f, 0.f};
+    auto row_sum = [&](int parity) -> Pair {
+      // sum max(p - t q, 0) = (sum of p - t sum of q) over the tokens with p > t q: the sums of p and q of those are held as
+      // pairs, a third fewer instructions than a pair per residual, and as good while the sum is not far below 1
+      Pair acc = kNone, qacc = kNone;
+      const bool both = DRAWN && !plain;
       int32_t v = v0 + lane;
-      if (!holes) {
+      if (both) {
         constexpr int kU = 8;  // loads in flight per lane and row
-        for (; v + 32 * (kU - 1) < v1; v += 32 * kU) {
+        for (; v < v1; v += 32 * kU) {
           float x[kU], y[kU];
 #pragma unroll
           for (int k = 0; k < kU; ++k) {
-            x[k] = __ldg(prow + v + 32 * k);
-            y[k] = DRAWN && !plain ? __ldg(qrow + v + 32 * k) : 0.f;
+            const bool in = v + 32 * k < v1;
+            x[k] = in ? __ldg(prow + v + 32 * k) : 0.f;
+            y[k] = in ? __ldg(qrow + v + 32 * k) : 0.f;
           }
 #pragma unroll
           for (int k = 0; k < kU; ++k) {
-            const Pair w = DRAWN ? residual(x[k], y[k], th, tl) : Pair{fmaxf(x[k], 0.f), 0.f};
-            pair_add(acc, w.hi, w.lo);
+            y[k] = fmaxf(y[k], 0.f);
+            // (the first fma has the sign of the exact difference)
+            const bool keep = __fmaf_rn(-tt.lo, y[k], __fmaf_rn(-tt.hi, y[k], x[k])) > 0.f;
+            pair_add(acc, keep ? x[k] : 0.f);
+            pair_add(qacc, keep ? y[k] : 0.f);
           }
         }
+      } else {
+        constexpr int kU = 16;
+        for (; v < v1; v += 32 * kU) {
+          float x[kU];
+#pragma unroll
+          for (int k = 0; k < kU; ++k) x[k] = v + 32 * k < v1 ? __ldg(prow + v + 32 * k) : 0.f;
+#pragma unroll
+          for (int k = 0; k < kU; ++k) pair_add(acc, fmaxf(x[k], 0.f));
+        }
       }
-      for (; v < v1; v += 32) {
-        const Pair w = weight(v);
-        pair_add(acc, w.hi, w.lo);
+      acc = pair_reduce(pair_of(acc.hi, acc.lo));
+      if (both) {
+        acc = acc - tt * pair_reduce(pair_of(qacc.hi, qacc.lo));
+      } else if (!DRAWN && !plain) {
+        for_refused(v0, v1, [&](int32_t i) { acc = acc - Pair{s_p[i], 0.f}; });
       }
-      pair_reduce(acc);
-      if (lane == 0) s_warp[warp] = pair_value(acc);
+      if (!(acc.hi > 0.f) && acc.hi == acc.hi) acc = kNone;  // (rounding; a NaN stays)
+      if (lane == 0) s_warp[warp] = acc;
       __syncthreads();
       if (warp == 0) {
-        double s = lane < kWarps ? s_warp[lane] : 0.0;
-#pragma unroll
-        for (int off = kWarps / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s = __shfl_sync(0xffffffffu, s, 0);
-        if (lane < ctas)
-          st_cluster_b64(smem_u32(&s_rank[parity][rank]), lane, static_cast<uint64_t>(__double_as_longlong(s)));
+        const Pair sum = pair_reduce(lane < kWarps ? s_warp[lane] : kNone);
+        const uint64_t bits = static_cast<uint64_t>(__float_as_uint(sum.lo)) << 32 | __float_as_uint(sum.hi);
+        const uint64_t first_bits = __shfl_sync(0xffffffffu, bits, 0);
+        if (lane < ctas) st_cluster_b64(smem_u32(&s_rank[parity][rank]), lane, first_bits);
       }
       cluster_sync_all();
-      if (t == 0) {
-        double s = 0.0;
-        for (int r = 0; r < ctas; ++r) s += s_rank[parity][r];
-        s_total = s;
+      if (warp == 0) {
+        const Pair sum = pair_reduce(lane < ctas ? s_rank[parity][lane] : kNone);
+        if (lane == 0) s_total = sum;
       }
       __syncthreads();
       return s_total;
     };
-    double sum = row_sum(pass & 1);
+    Pair sum = row_sum(pass & 1);
     if (!draw) {
       total = sum;
       // the last refused child may have been the node's last: then this sum is the draw's
@@ -323,15 +357,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
       if (s_more) continue;
     }
     int parity = pass & 1;
-    if (!(sum > 0.0) && (DRAWN ? tt > 0.0 : true)) {
+    if (!(sum.hi > 0.f) && !plain) {
       // nothing left of the residual (rounding, or refused tokens that held all of p): p itself
       __syncthreads();
-      plain = true;  // (given drafts: without the refused tokens' holes)
-      th = tl = 0.f;
-      holes = false;
+      plain = true;
       sum = row_sum(parity ^= 1);
     }
-    if (!(sum > 0.0)) {  // (also where a weight is infinite: its pair's low part is a NaN)
+    if (!(sum.hi > 0.f && sum.hi < INFINITY)) {  // (also a NaN)
       if (rank == 0) {
         if (t == 0) flag_error(p.err, RA_DEVERR_VALUE), p.next_tokens[b] = 0;
       }
@@ -339,12 +371,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
       // The CTA, then the warp's slice where the prefix sums first exceed u S, by warp 0 of every CTA; then the owner's
       // whole CTA over that slice.  Where rounding leaves no place, the last with any weight.
       if (warp == 0) {
-        const double goal = static_cast<double>(__ldg(p.u_final + b)) * sum;
-        double before;
-        const int owner = place(lane < ctas ? s_rank[parity][lane] : 0.0, 0.0, goal, &before);
+        const Pair goal = Pair{u_final, 0.f} * sum;
+        Pair before;
+        const int owner = place(lane < ctas ? s_rank[parity][lane] : kNone, kNone, goal, &before);
         if (lane == 0) s_owner = owner;
         if (owner == static_cast<int>(rank)) {
-          const int who = place(lane < kWarps ? s_warp[lane] : 0.0, before, goal, &before);
+          const int who = place(lane < kWarps ? s_warp[lane] : kNone, before, goal, &before);
           if (lane == 0) s_who = who, s_before = before, s_goal = goal;
         }
       }
@@ -355,34 +387,25 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
         const int32_t e1 = static_cast<int32_t>(slice0 + slice < p.vocab ? slice0 + slice : p.vocab);
         const int32_t part = (e1 - e0 + kWarps - 1) / kWarps;
         const int32_t c0 = min(e0 + warp * part, e1), c1 = min(c0 + part, e1);
-        if (!DRAWN) holes = !plain && refused_between(c0, c1);
-        const double goal = s_goal;
-        Pair acc{0.f, 0.f};
-        for (int32_t v = c0 + lane; v < c1; v += 32) {
-          const Pair w = weight(v);
-          pair_add(acc, w.hi, w.lo);
-        }
-        pair_reduce(acc);
-        if (lane == 0) s_part[warp] = pair_value(acc);
+        if (!DRAWN && !plain) for_refused(c0, c1, [&](int32_t) { holes = true; });
+        const Pair goal = s_goal;
+        Pair before = s_before, acc = kNone;
+        for (int32_t v = c0 + lane; v < c1; v += 32) acc = acc + weight(v);
+        acc = pair_reduce(acc);
+        if (lane == 0) s_part[warp] = acc;
         __syncthreads();
-        double before = s_before;
-        const int who = place(lane < kWarps ? s_part[lane] : 0.0, before, goal, &before);
+        const int who = place(lane < kWarps ? s_part[lane] : kNone, before, goal, &before);
         if (who == warp) {
           // the groups of 32 tokens in turn
           int32_t found = -1, tail = c0;
           for (int32_t v = c0; v < c1 && found < 0; v += 32) {
-            const double w = v + lane < c1 ? pair_value(weight(v + lane)) : 0.0;
-            double incl = w;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-              const double y = __shfl_up_sync(0xffffffffu, incl, off);
-              if (lane >= off) incl += y;
-            }
-            const uint32_t over = __ballot_sync(0xffffffffu, before + incl > goal && w > 0.0);
-            const uint32_t any = __ballot_sync(0xffffffffu, w > 0.0);
+            const Pair w = v + lane < c1 ? weight(v + lane) : kNone;
+            const Pair incl = before + pair_scan(w);
+            const uint32_t over = __ballot_sync(0xffffffffu, goal < incl && w.hi > 0.f);
+            const uint32_t any = __ballot_sync(0xffffffffu, w.hi > 0.f);
             if (over) found = v + __ffs(over) - 1;
             if (any) tail = v + 31 - __clz(any);
-            before += __shfl_sync(0xffffffffu, incl, 31);
+            before = pair_shfl(incl, 31);
           }
           if (lane == 0) p.next_tokens[b] = found >= 0 ? found : tail;
         }
@@ -421,6 +444,12 @@ __device__ __forceinline__ uint64_t key_of(float x, int32_t v) {
   return static_cast<uint64_t>(ordered) << 32 | (0xffffffffu - static_cast<uint32_t>(v));
 }
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+// The warp's largest, in two 32-bit reductions (five shuffle steps of 64 bits took longer than the row's loads).
+__device__ __forceinline__ uint64_t warp_max64(uint64_t x) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(x >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(x >> 32) == hi ? static_cast<uint32_t>(x) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
 
 template <typename E>
 __device__ __forceinline__ float value_of(E x);
@@ -510,20 +539,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_greedy_kernel(const G
     ++count;
     uint64_t best = row_largest(static_cast<const E*>(p.logits) + (first + node) * p.stride, p.vocab,
                                 static_cast<int64_t>(rank) * kThreads + t, static_cast<int64_t>(ctas) * kThreads);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) best = max64(best, __shfl_xor_sync(0xffffffffu, best, off));
+    best = warp_max64(best);
     if (lane == 0) s_warp[warp] = best;
     __syncthreads();
     if (warp == 0) {
-      best = lane < kWarps ? s_warp[lane] : 0;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) best = max64(best, __shfl_xor_sync(0xffffffffu, best, off));
+      best = warp_max64(lane < kWarps ? s_warp[lane] : 0);
       if (lane < ctas) st_cluster_b64(smem_u32(&s_rank[pass & 1][rank]), lane, best);
     }
     cluster_sync_all();
     if (warp == 0) {
-      best = 0;
-      for (int r = 0; r < ctas; ++r) best = max64(best, s_rank[pass & 1][r]);
+      best = warp_max64(lane < ctas ? s_rank[pass & 1][lane] : 0);
       // (0: a row of NaN; no child's token then)
       const int32_t token = best ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
       int32_t next = -1;
@@ -551,7 +576,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_greedy_kernel(const G
 }
 
 // CTAs per request: 8 (the most that any GPU of the architecture runs as one cluster) unless a slice would be less than a
-// load or two per thread, or the requests then no longer run all at once, two CTAs an SM.
+// load or two per thread, or the requests then no longer run all at once, two CTAs an SM (64 trees of 16 drafts, drawn /
+// given / greedy, over 32,000 tokens: 12.5 / 9.9 / 17.7 us with 4 CTAs, 18.5 / 16.0 / 24.4 with 8 in two waves; over
+// 128,000: 34.2 / 14.1 / 25.4 and 31.7 / 19.5 / 25.9).
 int cluster_ctas(int32_t vocab, int32_t batch, int sms) {
   int c = kMaxCluster;
   while (c > 1 && static_cast<int64_t>(vocab) < static_cast<int64_t>(c) * kThreads) c /= 2;
