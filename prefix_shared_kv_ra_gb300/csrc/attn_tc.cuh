@@ -107,7 +107,8 @@ struct TcParams {
   float* part_o;              // [slots, hkv, part_rows, D]
   float* part_lse;            // [slots, hkv, part_rows]
   // extend with changed scores (the extend arrays; work_items are [4 * entries]: request, query tile, first key of the
-  // tile's rows, end of their keys)
+  // tile's rows, end of their keys; part_* as for the tree, for the pieces of split key ranges)
+  const int32_t* work_slots;  // [entries]: partial slot, or -1
   ScoreMod mod;
 };
 
@@ -132,9 +133,11 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Changed scores: a row whose sum is outside these has its reference too far from its scores (weights that vanish or
-// overflow); capped ones: the bound up to which the reference is fixed, and the sum at which it is raised.
+// overflow); the sum at which a row's reference is raised, and by how much a score has to exceed it then; the cap (in
+// log2 units) up to which the reference is fixed.
 constexpr float kSumFloor = 0x1p-90f, kSumCeiling = 0x1p110f;
-constexpr float kCapFixed = 80.f, kCapRaise = 0x1p60f;
+constexpr float kRaiseSum = 0x1p60f, kRaiseStep = 8.f;
+constexpr float kCapFixed = 95.f;
 constexpr float kFastSumLimit = 32768.0f;  // single-pass acceptance: every p of the row <= 2^15
 // Register split: the softmax warpgroups (0, 1) hold a 128-key P row and two 32-column S chunks; the
 // gather and MMA warpgroups (2, 3) need few.  setmaxnreg moves registers between them within the
@@ -159,10 +162,6 @@ __device__ __forceinline__ bool aborted(volatile int* flag) { return *flag != 0;
 template <bool B>
 struct BoolTag {
   static constexpr bool value = B;
-};
-template <int K>
-struct KindTag {
-  static constexpr int value = K;
 };
 
 // One work item: key range, table row and query rows.
@@ -231,6 +230,7 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
     j.causal0 = P + e.y * kTiles * T;
     j.kbeg = e.z;
     j.kend = e.w;
+    j.slot = __ldg(p.work_slots + rest);
     j.mem0 = p.mod.full_lens ? min(__ldg(p.mod.full_lens + e.x), P + E) : 0;
     j.q_tok0 = q_first + e.y * kTiles * T;
   } else if constexpr (PASS == kExtendPass) {
@@ -296,13 +296,20 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
   return j.nt > 0;
 }
 
+// The largest bias of the keys [first, end) for a row at `pos`: the nearest one's, or (negative slopes) the farthest's.
+__device__ __forceinline__ float bias_bound(int32_t first, int32_t end, int32_t pos, float slope) {
+  const int32_t near = pos < first ? first - pos : pos >= end ? pos - end + 1 : 0;
+  const int32_t far = max(abs(pos - first), abs(pos - end + 1));
+  return -slope * static_cast<float>(slope >= 0.f ? near : far);
+}
+
 // Attention of one row with changed scores, by a warp: a key per lane for the scores, D / 32 dimensions per lane for the
-// values.  For rows whose tensor-core result is not finite although values that are not finite may lie outside what the
+// values; its log2-sum-exp in lse.  For rows whose tensor-core result is not finite although values that are not finite may lie outside what the
 // row sees (a zero weight times such a value is a NaN in the product over a whole tile); slow and rare.  Lane l's
 // dimensions l * D / 32 .. in acc.
 template <int D, bool CAP>
 __device__ __forceinline__ void mod_row(const TcParams& p, const Job& jb, int64_t q_row, int32_t first, int32_t end,
-                                        int32_t pos, float slope, float (&acc)[D / 32]) {
+                                        int32_t pos, float slope, float (&acc)[D / 32], float& lse) {
   constexpr int V = D / 32;
   const int lane = threadIdx.x & 31;
   const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>(p.q + q_row * D);
@@ -346,6 +353,7 @@ __device__ __forceinline__ void mod_row(const TcParams& p, const Job& jb, int64_
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] *= inv;
+  lse = l == 0.f ? -INFINITY : m + __log2f(l);
 }
 
 }  // namespace tc
@@ -787,7 +795,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         lim = jb.kend;
         first = jb.kbeg;
         if (row_valid) {
-          lim = max(pos + 1, jb.mem0);
+          lim = min(max(pos + 1, jb.mem0), jb.kend);
           if (p.mod.window > 0) first = max(first, pos - p.mod.window + 1);
           if (p.mod.first_key) first = max(first, __ldg(p.mod.first_key + jb.q_tok0 + tok));
           if (p.mod.slopes) slope = __ldg(p.mod.slopes + jb.kh * G + r % G) * kLog2e;
@@ -855,16 +863,20 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         [[maybe_unused]] uint32_t pk[2][32];
         float rowsum = 0.f, alpha = 1.f, m_ref = m_used;
         bool resc = false;
-        if constexpr (CAP) {
-          // Capped scores are bounded, so nothing is redone for a stale reference: with a cap of up to kCapFixed log2 units
-          // the reference is 0 (weights of 2^-80 .. 2^80 are as exact as others in bf16 and fp32), beyond it an estimate
-          // from the row's first keys, raised between tiles when the sum has grown.  So a chunk's weights go to TMEM at
-          // once, over columns of S that are done with, and the tile is a short loop over 32-column chunks: holding the 64
-          // registers of P until the tile is settled, as below, left the polynomial too few, and unrolled code for the cases
-          // ran at the instruction cache's pace (1394 -> 612 us for 8 prompts of 700..1500 tokens, 64/8 heads).
-          //   t = cap log2(e) tanh(y) - slope |pos - key| - reference, y = s sm_scale / cap
+        if constexpr (MOD) {
+          // The same with the scores' changes, a chunk's weights going to TMEM at once, over columns of S that are done with,
+          // and the tile a short loop over 32-column chunks: holding the 64 registers of P until a tile is settled, as below,
+          // left the cap's polynomial too few, and unrolled code for all cases ran at the instruction cache's pace (1394 ->
+          // 612 us for 8 prompts of 700..1500 tokens, 64/8 heads, capped).
+          //   t = cap log2(e) tanh(y) - slope |pos - key| - reference, y = s sm_scale / cap; or s sm_scale log2(e) - ...
           // Up to the row's position the bias is linear in the key: it and the reference are one addend, stepped along the
-          // columns.  A chunk with a |y| beyond the polynomial's range is done again from S, 8 columns at a time.
+          // columns.  The reference only has to keep weights and sums in range (2^60 weighs as exactly as 1 in bf16 and
+          // fp32): with a cap of up to kCapFixed log2 units it is 0 (no chunk's sum can leave fp32 then), else the largest of the row's first 16 scores with the
+          // largest bias that any of its keys has (with the first keys' bias, far away, it would have to move in every
+          // tile).  It is raised by whole powers of two: between tiles when the sum has grown, and within one when a
+          // chunk's sum leaves the range, which scales what the tile has stored so far.  That and scores beyond the
+          // polynomial's range take a chunk through a loop of its own, from S, 8 columns at a time.  A row whose whole sum
+          // is too small for its reference is done again in the epilogue.
           const bool sees = first < key0 + kKeys && first < lim && key0 < lim;  // any key of this tile
           if (!__any_sync(0xffffffffu, sees)) {
             const uint32_t none[32] = {};
@@ -874,26 +886,26 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
             if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
               float top = 0.f;
-              if (p.mod.cap_log2 > kCapFixed) {
+              if (!CAP || p.mod.cap_log2 > kCapFixed) {
                 uint32_t x[16];
                 tmem_ld16(tmem + lane_addr + col_s, x);
                 tc_wait_ld_regs16(x);
                 top = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, e >= lo && e < hi ? __uint_as_float(x[e]) : -INFINITY);
-                top = top == -INFINITY ? 0.f : p.mod.cap_log2 * tanh_any(top * p.mod.cap_in);
+                if (top == -INFINITY) top = 0.f;  // (the row's keys begin behind these columns)
+                else top = CAP ? p.mod.cap_log2 * tanh_any(top * p.mod.cap_in) : top * p.scale_log2;
               }
-              // (with negative slopes the farthest key's bias is the largest)
-              if (m_used == -INFINITY && sees) m_ref = top + fmaxf(0.f, -slope * static_cast<float>(abs(pos - first)));
+              if (m_used == -INFINITY && sees) m_ref = top + bias_bound(first, lim, pos, slope);
             }
-            if (__any_sync(0xffffffffu, l > kCapRaise)) {
-              // (a power of two: the accumulators are only shifted)
-              const float up = l > kCapRaise ? static_cast<float>(static_cast<int32_t>(__float_as_uint(l) >> 23) - 127) : 0.f;
+            if (__any_sync(0xffffffffu, l > kRaiseSum)) {
+              const float up = l > kRaiseSum ? static_cast<float>(static_cast<int32_t>(__float_as_uint(l) >> 23) - 127) : 0.f;
               resc = up > 0.f;
               m_ref += up;
               alpha = ex2(-up);
             }
-            const float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
+            const bool fixed_ref = CAP && p.mod.cap_log2 <= kCapFixed;
+            float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
             uint64_t sum2[2] = {0, 0};
             auto run = [&](auto edge_tag) {
               constexpr bool edge = decltype(edge_tag)::value;  // hidden keys, or keys behind the row's position
@@ -909,19 +921,23 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-                  const uint64_t y2 = f2_mul(s2, in2);
-                  const uint64_t z2 = f2_mul(y2, y2);
-                  float y0, y1;
-                  f2_unpack(y2, y0, y1);
-                  y_max = fmaxf(y_max, fmaxf(fabsf(y0), fabsf(y1)));
-                  auto coef = [&](int i) { return f2_pack(p.mod.cap_poly[i].x, p.mod.cap_poly[i].y); };
-                  uint64_t h2 = coef(kCapTerms - 1);
-#pragma unroll
-                  for (int i = kCapTerms - 2; i >= 0; --i) h2 = f2_fma(h2, z2, coef(i));
                   if (edge)
                     add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m_sub), fmaf(-slope, fabsf(off + (2 * e + 1)), -m_sub));
                   float t0, t1;
-                  f2_unpack(f2_fma(y2, h2, add2), t0, t1);
+                  if constexpr (CAP) {
+                    const uint64_t y2 = f2_mul(s2, in2);
+                    const uint64_t z2 = f2_mul(y2, y2);
+                    float y0, y1;
+                    f2_unpack(y2, y0, y1);
+                    y_max = fmaxf(y_max, fmaxf(fabsf(y0), fabsf(y1)));
+                    auto coef = [&](int i) { return f2_pack(p.mod.cap_poly[i].x, p.mod.cap_poly[i].y); };
+                    uint64_t h2 = coef(kCapTerms - 1);
+#pragma unroll
+                    for (int i = kCapTerms - 2; i >= 0; --i) h2 = f2_fma(h2, z2, coef(i));
+                    f2_unpack(f2_fma(y2, h2, add2), t0, t1);
+                  } else {
+                    f2_unpack(f2_fma(s2, in2, add2), t0, t1);
+                  }
                   if (!edge) add2 = f2_add(add2, step2);
                   if (edge) {
                     if (2 * e < l0 || 2 * e >= h0) t0 = -INFINITY;
@@ -931,26 +947,68 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                   part2[e & 1] = f2_add(part2[e & 1], f2_pack(p0, p1));
                   pw[e] = pack_bf16x2(p0, p1);
                 }
-                if (__any_sync(0xffffffffu, !(y_max <= kCapPolyMax))) {
-                  part2[0] = part2[1] = 0;
-#pragma unroll 1
-                  for (int q = 0; q < 4; ++q) {
-                    uint32_t x[8], w[4];
+                bool out = CAP && !(y_max <= kCapPolyMax);
+                if (!fixed_ref) {
+                  float q0, q1, q2, q3;
+                  f2_unpack(part2[0], q0, q1);
+                  f2_unpack(part2[1], q2, q3);
+                  out = out || !((q0 + q1) + (q2 + q3) <= kRaiseSum);
+                }
+                if (__any_sync(0xffffffffu, out)) {
+                  // any score of 8 columns, finished but for the reference
+                  auto finish = [&](int q, float (&t)[8]) {
+                    uint32_t x[8];
                     tmem_ld8(tmem + lane_addr + col_s + 32 * c + 8 * q, x);
                     tc_wait_ld_regs8(x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      float t[2];
+                    for (int e = 0; e < 8; ++e) {
+                      const float s1 = __uint_as_float(x[e]);
+                      t[e] = CAP ? p.mod.cap_log2 * tanh_any(s1 * p.mod.cap_in) : s1 * p.scale_log2;
+                      t[e] = fmaf(-slope, fabsf(off + static_cast<float>(8 * q + e)), t[e]);
+                      if (8 * q + e < l0 || 8 * q + e >= h0) t[e] = -INFINITY;
+                    }
+                  };
+                  float top = -INFINITY;
+#pragma unroll 1
+                  for (int q = 0; q < 4; ++q) {
+                    float t[8];
+                    finish(q, t);
 #pragma unroll
-                      for (int i = 0; i < 2; ++i) {
-                        const int32_t at = 8 * q + 2 * e + i;
-                        t[i] = p.mod.cap_log2 * tanh_any(__uint_as_float(x[2 * e + i]) * p.mod.cap_in);
-                        t[i] += fmaf(-slope, fabsf(off + static_cast<float>(at)), -m_sub);
-                        if (at < l0 || at >= h0) t[i] = -INFINITY;
-                        t[i] = ex2(t[i]);
-                      }
-                      part2[0] = f2_add(part2[0], f2_pack(t[0], t[1]));
-                      w[e] = pack_bf16x2(t[0], t[1]);
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, t[e]);
+                  }
+                  // (whole powers of two: what is stored is scaled without rounding)
+                  const float up = top > m_sub + kRaiseStep ? ceilf(top - m_sub) : 0.f, down = ex2(-up);
+                  if (__any_sync(0xffffffffu, up > 0.f)) {
+                    m_sub += up;
+                    if (up > 0.f) m_ref = m_sub;
+                    alpha *= down;
+                    resc = resc || up > 0.f;
+                    const uint64_t down2 = f2_pack(down, down);
+                    sum2[0] = f2_mul(sum2[0], down2);
+                    sum2[1] = f2_mul(sum2[1], down2);
+#pragma unroll 1
+                    for (int q = 0; q < 2 * c; ++q) {
+                      uint32_t w[8];
+                      tmem_ld8(tmem + lane_addr + col_s + 8 * q, w);
+                      tc_wait_ld_regs8(w);
+#pragma unroll
+                      for (int e = 0; e < 8; ++e)
+                        w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down);
+                      tmem_st8(tmem + lane_addr + col_s + 8 * q, w);
+                    }
+                  }
+                  part2[0] = part2[1] = 0;
+#pragma unroll 1
+                  for (int q = 0; q < 4; ++q) {
+                    float t[8];
+                    uint32_t w[4];
+                    finish(q, t);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[e] = ex2(t[e] - m_sub);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      part2[0] = f2_add(part2[0], f2_pack(t[2 * e], t[2 * e + 1]));
+                      w[e] = pack_bf16x2(t[2 * e], t[2 * e + 1]);
                     }
                     tmem_st4(tmem + lane_addr + col_s + 16 * c + 4 * q, w);
                   }
@@ -978,120 +1036,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             f2_unpack(sum2[0], a0, a1);
             f2_unpack(sum2[1], a2, a3);
             rowsum = (a0 + a1) + (a2 + a3);
-          }
-        } else if constexpr (MOD) {
-          // As below in 16-column steps, the bias and the reference one addend, stepped along the columns (up to the row's
-          // position the bias is linear in the key).  A tile that the single pass does not settle is rewritten in place as
-          // finished scores, -inf where hidden, with their maximum, and exponentiated from those; that pass is rare, so it
-          // is a loop.  A row's first reference is the largest of its first 16 scores with the
-          // largest bias that any of its keys has: taken with the bias of the first keys, far away, the reference would
-          // have to move in every tile.  It may lie far above the scores so far, which costs nothing while no weight
-          // leaves bf16's range; a row whose whole sum says that they might have is done again in the epilogue.
-          const bool sees = first < key0 + kKeys && first < lim && key0 < lim;  // any key of this tile
-          if (!__any_sync(0xffffffffu, sees)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) pk[0][e] = pk[1][e] = 0u;
-          } else {
-            const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
-            auto visible = [&](int c) -> uint32_t {            // of columns 16 c .. 16 c + 15
-              const int32_t l = max(lo - 16 * c, 0), h = min(max(hi - 16 * c, 0), 16);
-              return l >= 16 ? 0u : ((1u << h) - 1u) & ~((1u << l) - 1u);
-            };
-            if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-              uint32_t x[16];
-              tmem_ld16(tmem + lane_addr + col_s, x);
-              tc_wait_ld_regs16(x);
-              const uint32_t vis16 = visible(0);
-              float top = -INFINITY;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) top = fmaxf(top, vis16 >> e & 1u ? __uint_as_float(x[e]) : -INFINITY);
-              top *= p.scale_log2;
-              // with the largest bias among the row's keys: 0 at its own position, or (negative slopes) the farthest key's
-              top += fmaxf(0.f, -slope * static_cast<float>(abs(pos - first)));
-              // (0 where the row's keys begin behind these columns)
-              if (m_used == -INFINITY) m_ref = !sees ? -INFINITY : vis16 ? top : 0.f;
-            }
-            uint64_t sum2[4];
-            float m_sub;
-            // kind 0: every key visible and none behind the row's position; 1: not so; 2: finished scores
-            auto exp_tile = [&](auto kind_tag) {
-              constexpr int kind = decltype(kind_tag)::value;
-              m_sub = m_ref == -INFINITY ? 0.f : m_ref;
-              sum2[0] = sum2[1] = sum2[2] = sum2[3] = 0;
-              const uint64_t step2 = f2_pack(2.f * slope, 2.f * slope);
-              const uint64_t in2 = f2_pack(p.mod.in2.x, p.mod.in2.y);
-              auto chunk = [&](const uint32_t (&sr)[16], int c) {
-                const float off = static_cast<float>(key0 + 16 * c - pos);  // minus the distance of the first column
-                uint64_t add2 = kind == 0 ? f2_pack(fmaf(slope, off, -m_sub), fmaf(slope, off + 1.f, -m_sub))
-                                          : f2_pack(-m_sub, -m_sub);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-                  uint64_t t2;
-                  if constexpr (kind == 2) {
-                    t2 = f2_add(s2, add2);
-                  } else {
-                    if (kind == 1)
-                      add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m_sub), fmaf(-slope, fabsf(off + (2 * e + 1)), -m_sub));
-                    t2 = f2_fma(s2, in2, add2);
-                    if (kind == 0) add2 = f2_add(add2, step2);
-                  }
-                  float t0, t1;
-                  f2_unpack(t2, t0, t1);
-                  if (kind == 1) {
-                    if (16 * c + 2 * e < lo || 16 * c + 2 * e >= hi) t0 = -INFINITY;
-                    if (16 * c + 2 * e + 1 < lo || 16 * c + 2 * e + 1 >= hi) t1 = -INFINITY;
-                  }
-                  const float p0 = ex2(t0), p1 = ex2(t1);
-                  sum2[e & 3] = f2_add(sum2[e & 3], f2_pack(p0, p1));
-                  pk[c >> 2][(c & 3) * 8 + e] = pack_bf16x2(p0, p1);
-                }
-              };
-              uint32_t ba[16], bb[16];
-              tmem_ld16(tmem + lane_addr + col_s, ba);
-#pragma unroll
-              for (int c = 0; c < 8; c += 2) {
-                tc_wait_ld_regs16(ba);
-                tmem_ld16(tmem + lane_addr + col_s + 16 * (c + 1), bb);
-                chunk(ba, c);
-                tc_wait_ld_regs16(bb);
-                if (c < 6) tmem_ld16(tmem + lane_addr + col_s + 16 * (c + 2), ba);
-                chunk(bb, c + 1);
-              }
-              float sum8[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) f2_unpack(sum2[e], sum8[2 * e], sum8[2 * e + 1]);
-              rowsum = ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) + ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
-            };
-            if (warp_masked) exp_tile(KindTag<1>{});
-            else exp_tile(KindTag<0>{});
-            const bool stale =
-                !(rowsum <= kFastSumLimit) || (m_used == -INFINITY && slope == 0.f && sees && !(rowsum >= kSumFloor));
-            if (__any_sync(0xffffffffu, stale)) {
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t x[16];
-                tmem_ld16(tmem + lane_addr + col_s + 16 * c, x);
-                tc_wait_ld_regs16(x);
-                const uint32_t vis16 = visible(c);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float s = __uint_as_float(x[e]);
-                  float t = fmaf(-slope, fabsf(static_cast<float>(pos - key0 - 16 * c - e)), s * p.scale_log2);
-                  t = vis16 >> e & 1u ? t : -INFINITY;
-                  top = fmaxf(top, t);
-                  x[e] = __float_as_uint(t);
-                }
-                tmem_st16(tmem + lane_addr + col_s + 16 * c, x);
-              }
-              tc_wait_st();
-              const float m_new = fmaxf(m_used, top);
-              resc = m_new > m_used + kRescaleThreshold;
-              m_ref = resc ? m_new : m_used;
-              exp_tile(KindTag<2>{});
-              alpha = resc ? ex2(m_used - m_sub) : 1.f;
-            }
           }
         } else {
         bool exact = false;
@@ -1191,7 +1135,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         }
         }
         // P (bf16 pairs) over the first 64 columns of S, read by the PV MMA
-        if constexpr (!CAP) {
+        if constexpr (!MOD) {
           tmem_st32(tmem + lane_addr + col_s, pk[0]);
           tmem_st32(tmem + lane_addr + col_s + 32, pk[1]);
         }
@@ -1270,21 +1214,23 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           }
         }
       };
-      if (EXTEND && (!TREE || jb.slot < 0)) {
+      // changed scores: a result that is not finite may come from a value that this row does not see, or from the reference
+      [[maybe_unused]] auto redo_row = [&](const uint32_t (&oa)[D / 32][32]) -> bool {
+        float bad[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(oa[c][e]), 0.f, bad[e & 3]);
+        return row_valid && (!((bad[0] + bad[1]) + (bad[2] + bad[3]) == 0.f) ||
+                             (first < lim && !(l >= kSumFloor && l <= kSumCeiling)));
+      };
+      [[maybe_unused]] bool redo = false;
+      [[maybe_unused]] int64_t part_row = 0;
+      if (EXTEND && (!(TREE || MOD) || jb.slot < 0)) {
         __nv_bfloat16* dst = p.o + ((jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G)) * static_cast<int64_t>(D);
         uint32_t oa[D / 32][32];
         load_o(oa);
-        [[maybe_unused]] bool redo = false;
-        if constexpr (MOD) {
-          // a result that is not finite may come from a value that this row does not see, or from the reference
-          float bad[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(oa[c][e]), 0.f, bad[e & 3]);
-          redo = row_valid && first < lim &&
-                 (!((bad[0] + bad[1]) + (bad[2] + bad[3]) == 0.f) || !(l >= kSumFloor && l <= kSumCeiling));
-        }
+        if constexpr (MOD) redo = redo_row(oa);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t (&ov)[32] = oa[c];
@@ -1298,34 +1244,23 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pko[4 * e], pko[4 * e + 1], pko[4 * e + 2], pko[4 * e + 3]);
           }
         }
-        if constexpr (MOD) {
-          for (uint32_t rows = __ballot_sync(0xffffffffu, redo); rows != 0; rows &= rows - 1) {
-            const int src = __ffs(rows) - 1;
-            const int64_t row = __shfl_sync(0xffffffffu, (jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G), src);
-            float y[D / 32];
-            mod_row<D, CAP>(p, jb, row, __shfl_sync(0xffffffffu, first, src), __shfl_sync(0xffffffffu, lim, src),
-                            __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, slope, src), y);
-            __syncwarp();  // (behind the row's own thread's stores)
-#pragma unroll
-            for (int v = 0; v < D / 32; ++v) p.o[row * D + lane * (D / 32) + v] = __float2bfloat16_rn(y[v]);
-          }
-        }
       } else {
         // fp32 partial rows, one per thread, at [slot][member][q head] (the G heads of a member contiguous),
         // written in whole 32-byte sectors
-        // (tree: at [slot][kv head][row of the item])
+        // (tree, changed scores: at [slot][kv head][row of the item])
         bool write = row_valid;
         int64_t ps;
-        if constexpr (TREE) {
+        if constexpr (TREE || MOD) {
           ps = (static_cast<int64_t>(jb.slot) * p.hkv + jb.kh) * p.part_rows + (row_valid ? ti * kRows + r : 0);
         } else {
           const int32_t member = __ldg(p.group_reqs + jb.mem0 + (row_valid ? tok : 0));
           write = row_valid && member >= 0 && member < p.batch;
           ps = (static_cast<int64_t>(jb.slot) * p.batch + (write ? member : 0)) * p.hq + jb.kh * G + (r % G);
         }
-        float* dst = (TREE ? p.part_o : p.casc_o) + ps * D;
+        float* dst = (TREE || MOD ? p.part_o : p.casc_o) + ps * D;
         uint32_t oa[D / 32][32];
         load_o(oa);
+        if constexpr (MOD) redo = redo_row(oa), part_row = ps;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t (&ov)[32] = oa[c];
@@ -1339,7 +1274,25 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                            __uint_as_float(ov[8 * e + 7]) * inv_l);
           }
         }
-        if (write) (TREE ? p.part_lse : p.casc_lse)[ps] = m_used + __log2f(l);
+        if (write) (TREE || MOD ? p.part_lse : p.casc_lse)[ps] = m_used + __log2f(l);
+      }
+      if constexpr (MOD) {
+        // such rows of the warp one by one, behind their own threads' stores
+        for (uint32_t rows = __ballot_sync(0xffffffffu, redo); rows != 0; rows &= rows - 1) {
+          const int src = __ffs(rows) - 1;
+          const int64_t row = __shfl_sync(0xffffffffu, (jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G), src);
+          float y[D / 32], lse;
+          mod_row<D, CAP>(p, jb, row, __shfl_sync(0xffffffffu, first, src), __shfl_sync(0xffffffffu, lim, src),
+                          __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, slope, src), y, lse);
+          __syncwarp();
+          const int64_t at = __shfl_sync(0xffffffffu, part_row, src);
+#pragma unroll
+          for (int v = 0; v < D / 32; ++v) {
+            if (jb.slot < 0) p.o[row * D + lane * (D / 32) + v] = __float2bfloat16_rn(y[v]);
+            else p.part_o[at * D + lane * (D / 32) + v] = y[v];
+          }
+          if (jb.slot >= 0 && lane == 0) p.part_lse[at] = lse;
+        }
       }
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_ofree[ti]));

@@ -13,31 +13,57 @@
 #include "attn_tc.cuh"
 #include "attn_tc_host.h"
 #include "score_mod_host.h"
+#include "slab_ring.cuh"
 
 namespace ra {
 
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBins = 4096;  // key-tile counts above kPlanBins - 1 share the first bin
+constexpr int kModSms = 152;     // GB300; a constant, so that the workspace does not depend on the device
+constexpr int kSplitItems = 2 * kModSms;  // calls of fewer items (query tiles x kv heads) may split their key ranges, into
+                                          // at most so many
+constexpr int kMergeThreads = 256;
 
 struct ModWorkspace {
-  int32_t* count;
-  int32_t* counter;
-  int32_t* items;  // [4 * cap]
-  int64_t cap;
+  int32_t* header;  // [8]: items listed, claim counter, query tiles split
+  int32_t* items;   // [4 * cap]: request, query tile, first key, end of keys
+  int32_t* slots;   // [cap]: partial slot, or -1
+  int32_t* merges;  // [4 * cap_parts]: request, query tile, first partial slot, pieces
+  float* part_lse;  // [cap_parts, hkv, part_rows]
+  float* part_o;    // [cap_parts, hkv, part_rows, D]
+  int64_t cap, cap_parts;
+  int32_t part_rows;
   size_t total;
 };
 
-// Entries are at most sum_b ceil(E_b / tokens_per_cta) <= total_q / tokens_per_cta + batch.
-ModWorkspace layout_mod_workspace(int32_t batch, int64_t total_q, int32_t tokens_per_cta, void* base) {
+// Entries are at most sum_b ceil(E_b / tokens_per_cta) <= total_q / tokens_per_cta + batch; at least total_q /
+// tokens_per_cta of them (in a call that fills its rows), so that calls of many tokens need no partials.
+ModWorkspace layout_mod_workspace(int32_t batch, int64_t total_q, int32_t tokens_per_cta, int32_t group, int32_t hkv,
+                                  void* base) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   ModWorkspace w{};
-  w.cap = (total_q + tokens_per_cta - 1) / tokens_per_cta + batch;
-  w.total = 16 + static_cast<size_t>(w.cap) * 16;
-  uint8_t* b = static_cast<uint8_t*>(base);
-  w.count = reinterpret_cast<int32_t*>(b);
-  w.counter = reinterpret_cast<int32_t*>(b ? b + 4 : nullptr);
-  w.items = reinterpret_cast<int32_t*>(b ? b + 16 : nullptr);
+  const int64_t least = total_q / tokens_per_cta;
+  w.cap_parts = least * hkv < kSplitItems ? kSplitItems / hkv : 0;
+  w.cap = (total_q + tokens_per_cta - 1) / tokens_per_cta + batch + w.cap_parts;
+  w.part_rows = static_cast<int32_t>((total_q < tokens_per_cta ? total_q : tokens_per_cta) * group);
+  uint8_t* b = workspace_base(base);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* at = b ? b + off : nullptr;
+    off += up(bytes);
+    return at;
+  };
+  w.header = reinterpret_cast<int32_t*>(take(32));
+  w.items = reinterpret_cast<int32_t*>(take(static_cast<size_t>(w.cap) * 16));
+  w.slots = reinterpret_cast<int32_t*>(take(static_cast<size_t>(w.cap) * 4));
+  w.merges = reinterpret_cast<int32_t*>(take(static_cast<size_t>(w.cap_parts) * 16));
+  const size_t rows = static_cast<size_t>(w.cap_parts) * hkv * w.part_rows;
+  w.part_lse = reinterpret_cast<float*>(take(rows * 4));
+  w.part_o = reinterpret_cast<float*>(take(rows * 128 * 4));
+  w.total = off + kWorkspaceSlack;
   return w;
 }
 
@@ -48,8 +74,8 @@ struct PlanArgs {
   int32_t tokens_per_cta;
   const int32_t *first_key, *full_lens;
   int32_t window;
-  int32_t *count, *counter, *items;
-  int64_t cap;
+  int32_t hkv;
+  ModWorkspace ws;
   uint32_t* err;
 };
 
@@ -57,15 +83,17 @@ struct PlanArgs {
 // request: without first_key a lane per query tile, with it the lanes share a tile's tokens.
 __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const PlanArgs a) {
   __shared__ int32_t s_bin[kPlanBins];
-  __shared__ int32_t s_warp[kPlanThreads / 32];
+  __shared__ int32_t s_warp[kPlanWarps], s_cost[kPlanWarps], s_chunk[kPlanWarps], s_nt[kSplitItems];
+  __shared__ int32_t s_entries, s_longest, s_parts, s_merges;
   griddep_launch();  // the attention kernel may start its launch; it waits for this grid before reading the list
   // (this grid waits for the previous one before its first write, so its completion implies that one's)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) s_bin[i] = 0;
+  if (threadIdx.x == 0) s_entries = s_longest = s_parts = s_merges = 0;
   __syncthreads();
   // f(b, tile, first key, end of keys) for every query tile of this warp's requests, called by one lane
   auto for_tiles = [&](bool report, auto f) {
-    for (int b = warp; b < a.batch; b += kPlanThreads / 32) {
+    for (int b = warp; b < a.batch; b += kPlanWarps) {
       int32_t E = __ldg(a.extend_lens + b);
       const int32_t P = __ldg(a.prefix_lens + b);
       if (E < 0 || E > a.max_extend_len || P < 0 || P > a.max_prefix_len) {
@@ -102,11 +130,46 @@ __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const Pla
       }
     }
   };
-  auto bin_of = [](int32_t first, int32_t end) {
-    return kPlanBins - 1 - min((end - first + tc::kKeys - 1) / tc::kKeys, kPlanBins - 1);  // bin 0 = longest
-  };
-  for_tiles(true, [&](int32_t, int32_t, int32_t first, int32_t end) { atomicAdd(&s_bin[bin_of(first, end)], 1); });
+  auto tiles_of = [](int32_t first, int32_t end) { return (end - first + tc::kKeys - 1) / tc::kKeys; };
+  auto bin_of = [](int32_t tiles) { return kPlanBins - 1 - min(tiles, kPlanBins - 1); };  // bin 0 = longest
+  for_tiles(true, [&](int32_t, int32_t, int32_t first, int32_t end) {
+    const int32_t nt = tiles_of(first, end), at = atomicAdd(&s_entries, 1);
+    if (at < kSplitItems) s_nt[at] = nt;
+    atomicMax(&s_longest, nt);
+    atomicAdd(&s_bin[bin_of(nt)], 1);
+  });
   __syncthreads();
+  // Few items leave SMs idle (an item's tiles are one chain of products and softmax, 3 us each, and no second item hides
+  // it): their key ranges are cut into pieces of `chunk` tiles, the partial results joined by a kernel of their own.  Each
+  // warp weighs one number of pieces of the longest range: rounds of pieces over the SMs, a piece costing its tiles and
+  // about 3 more, and the join.
+  const int32_t entries = s_entries, longest = s_longest;
+  int32_t chunk = longest;
+  if (a.ws.cap_parts > 0 && static_cast<int64_t>(entries) * a.hkv < kSplitItems) {
+    const int32_t c = max(1, (longest + warp) / (warp + 1));
+    int32_t pieces = 0;
+    for (int32_t i = lane; i < entries; i += 32) pieces += (s_nt[i] + c - 1) / c;
+    pieces = __reduce_add_sync(0xffffffffu, pieces);
+    const int32_t rounds = (pieces * a.hkv + kModSms - 1) / kModSms;
+    if (lane == 0) {
+      s_cost[warp] = c >= longest ? rounds * (longest + 3) : pieces > a.ws.cap_parts ? INT32_MAX : rounds * (c + 3) + 3;
+      s_chunk[warp] = c;
+    }
+    __syncthreads();
+    int32_t best = INT32_MAX;
+    for (int w = 0; w < kPlanWarps; ++w)
+      if (s_cost[w] < best) best = s_cost[w], chunk = s_chunk[w];  // (on a tie the longer piece)
+    if (chunk < longest) {  // the pieces' bins (few entries: all in s_nt)
+      for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) s_bin[i] = 0;
+      __syncthreads();
+      for (int32_t i = threadIdx.x; i < entries; i += kPlanThreads) {
+        const int32_t full = s_nt[i] / chunk, rest = s_nt[i] - full * chunk;
+        if (full > 0) atomicAdd(&s_bin[bin_of(chunk)], full);
+        if (rest > 0) atomicAdd(&s_bin[bin_of(rest)], 1);
+      }
+      __syncthreads();
+    }
+  }
   // exclusive scan of the bins: thread i owns bins [4i, 4i + 4)
   constexpr int kPer = kPlanBins / kPlanThreads;
   int32_t v[kPer], run = 0;
@@ -134,24 +197,74 @@ __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const Pla
   }
   __syncthreads();
   const int32_t base = (warp > 0 ? s_warp[warp - 1] : 0) + incl - run;
-  const int32_t total = s_warp[kPlanThreads / 32 - 1];
+  const int32_t total = s_warp[kPlanWarps - 1];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) s_bin[threadIdx.x * kPer + e] = base + v[e];
   __syncthreads();
   griddep_wait();  // the previous kernel may be the previous call's, still claiming from this list and counter
   for_tiles(false, [&](int32_t b, int32_t t, int32_t first, int32_t end) {
-    const int32_t pos = atomicAdd(&s_bin[bin_of(first, end)], 1);
-    if (pos < a.cap) reinterpret_cast<int4*>(a.items)[pos] = make_int4(b, t, first, end);
-    else flag_error(a.err, RA_DEVERR_LENGTH);  // extend_lens sum above total_q
+    const int32_t nt = tiles_of(first, end), pieces = (nt + chunk - 1) / chunk;
+    int32_t slot = -1;
+    if (pieces > 1) {
+      slot = atomicAdd(&s_parts, pieces);
+      reinterpret_cast<int4*>(a.ws.merges)[atomicAdd(&s_merges, 1)] = make_int4(b, t, slot, pieces);
+    }
+    for (int32_t s = 0; s < pieces; ++s) {
+      const int32_t n = min(chunk, nt - s * chunk), pos = atomicAdd(&s_bin[bin_of(n)], 1);
+      if (pos < a.ws.cap) {
+        const int32_t k0 = first + s * chunk * tc::kKeys;
+        reinterpret_cast<int4*>(a.ws.items)[pos] = make_int4(b, t, k0, s + 1 < pieces ? k0 + chunk * tc::kKeys : end);
+        a.ws.slots[pos] = slot < 0 ? -1 : slot + s;
+      } else {
+        flag_error(a.err, RA_DEVERR_LENGTH);  // extend_lens sum above total_q
+      }
+    }
   });
+  __syncthreads();
   if (threadIdx.x == 0) {
-    *a.count = static_cast<int32_t>(static_cast<int64_t>(total) < a.cap ? total : a.cap);
-    *a.counter = 0;
+    a.ws.header[0] = static_cast<int32_t>(static_cast<int64_t>(total) < a.ws.cap ? total : a.ws.cap);
+    a.ws.header[1] = 0;
+    a.ws.header[2] = s_merges;
+  }
+}
+
+// Join the pieces of split query tiles: o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M), 8 lanes per row.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) extend_mod_merge_kernel(const __grid_constant__ TcParams p,
+                                                                         const ModWorkspace ws) {
+  constexpr int LPR = 8, V = D / LPR;
+  griddep_launch();
+  // (the list was complete before the attention kernel let this one launch; the partials are once that is)
+  const int sub = threadIdx.x % LPR, T = 2 * (tc::kRows / p.group);
+  const int32_t tile_rows = p.hkv * ws.part_rows, per_cta = kMergeThreads / LPR;
+  const int32_t chunks = (tile_rows + per_cta - 1) / per_cta;
+  const int64_t units = static_cast<int64_t>(__ldcg(ws.header + 2)) * chunks;
+  griddep_wait();
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(ws.merges) + u / chunks);
+    const int32_t flat = static_cast<int32_t>(u % chunks) * per_cta + static_cast<int32_t>(threadIdx.x) / LPR;
+    const int32_t kh = flat / ws.part_rows, r = flat - kh * ws.part_rows;
+    const int32_t tok = e.y * T + r / p.group;
+    const int32_t E = min(max(__ldg(p.extend_lens + e.x), 0), p.max_extend_len);
+    const int64_t first = __ldg(p.qo_indptr + e.x);
+    const int32_t table_row = __ldg(p.rpi + e.x);
+    // (a request whose rows or table row are out of range wrote no partials)
+    const bool live = flat < tile_rows && tok < E && first >= 0 && first + E <= p.total_q && table_row >= 0 &&
+                      table_row < p.table_rows;
+    const int64_t step = static_cast<int64_t>(p.hkv) * ws.part_rows;  // rows between slots
+    const int64_t row0 = (static_cast<int64_t>(e.z) * p.hkv + kh) * ws.part_rows + r;
+    float acc[V], sum;
+    merge_rows<LPR, V, 256 / D>(
+        live ? e.w : 0, [&](int s) { return __ldcg(ws.part_lse + row0 + s * step); },
+        [&](int s, float(&x)[V]) { load_row_part<LPR, V>(ws.part_o + (row0 + s * step) * D, sub, x); }, acc, sum);
+    if (live)
+      store_row_part<LPR, V>(p.o + ((first + tok) * p.hq + kh * p.group + r % p.group) * D, sub, acc,
+                             sum == 0.f ? 0.f : 1.f / sum);
   }
 }
 
 template <int D, int PASS>
-ra_status launch_mod(const TcParams& p, const CUtensorMap& qmap, int64_t entries, cudaStream_t s) {
+ra_status launch_mod(const TcParams& p, const ModWorkspace& ws, const CUtensorMap& qmap, int64_t entries, cudaStream_t s) {
   CUtensorMap kmap, vmap;
   if (ra_status st = row_gather_map(&kmap, p.k_pool, p.num_slots * p.hkv, D)) return st;
   if (ra_status st = row_gather_map(&vmap, p.v_pool, p.num_slots * p.hkv, D)) return st;
@@ -163,10 +276,17 @@ ra_status launch_mod(const TcParams& p, const CUtensorMap& qmap, int64_t entries
   if (L::kDynSmem > dev.max_smem_optin)
     return fail(RA_ERR_UNSUPPORTED, "extend kernel needs %d bytes of shared memory", L::kDynSmem);
   if (ra_status st = set_smem(kern, L::kDynSmem, configured, dev.device)) return st;
-  const int64_t items = entries * p.hkv;
+  const int64_t items = (entries + ws.cap_parts) * p.hkv;
   dim3 grid(static_cast<unsigned>(items < dev.num_sms ? items : dev.num_sms));
-  return launch_pdl("attn_tc_kernel<extend, changed scores>", kern, grid, dim3(tc::kThreads), L::kDynSmem, s, p, qmap,
-                    kmap, vmap);
+  if (ra_status st = launch_pdl("attn_tc_kernel<extend, changed scores>", kern, grid, dim3(tc::kThreads), L::kDynSmem, s,
+                                p, qmap, kmap, vmap))
+    return st;
+  if (ws.cap_parts == 0) return RA_OK;
+  // (at most cap_parts / 2 query tiles are split, each into two pieces or more)
+  const int64_t rows = std::max<int64_t>(1, std::min(entries, ws.cap_parts / 2)) * p.hkv * ws.part_rows;
+  const int64_t want = (rows + kMergeThreads / 8 - 1) / (kMergeThreads / 8), most = static_cast<int64_t>(dev.num_sms) * 8;
+  return launch_pdl("extend_mod_merge_kernel", extend_mod_merge_kernel<D>,
+                    dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kMergeThreads), 0, s, p, ws);
 }
 
 }  // namespace
@@ -205,7 +325,7 @@ extern "C" ra_status ra_extend_attention_mod(
                  aligned4(qo_indptr),
              "index arrays must be 4-byte aligned");
   const int tokens_per_cta = tc::kTiles * (128 / group);
-  const ModWorkspace ws = layout_mod_workspace(batch, total_q, tokens_per_cta, workspace);
+  const ModWorkspace ws = layout_mod_workspace(batch, total_q, tokens_per_cta, group, num_kv_heads, workspace);
   if (!workspace || workspace_bytes < ws.total)
     return fail(RA_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace ? workspace_bytes : 0, ws.total);
   RA_REQUIRE(aligned16(workspace), "workspace must be 16-byte aligned");
@@ -235,24 +355,27 @@ extern "C" ra_status ra_extend_attention_mod(
   p.max_prefix_len = max_prefix_len;
   p.total_q = total_q;
   p.o = static_cast<__nv_bfloat16*>(o);
-  p.work_count = ws.count;
-  p.work_counter = ws.counter;
+  p.work_count = ws.header;
+  p.work_counter = ws.header + 1;
   p.work_items = ws.items;
+  p.work_slots = ws.slots;
+  p.part_rows = ws.part_rows;
+  p.part_o = ws.part_o;
+  p.part_lse = ws.part_lse;
   p.mod = mod;
   const PlanArgs a{extend_lens, prefix_lens, qo_indptr, batch,  max_extend_len, max_prefix_len, table_stride, total_q,
-                   tokens_per_cta, first_key, full_lens, window, ws.count,       ws.counter,     ws.items,     ws.cap,
-                   device_error};
+                   tokens_per_cta, first_key, full_lens, window, num_kv_heads,   ws,             device_error};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (ra_status st = launch_pdl("extend_mod_plan_kernel", extend_mod_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a))
     return st;
   // at most sum_b ceil(E_b / tokens_per_cta) entries; CTAs past the listed count return at once
   const int64_t entries = std::min<int64_t>(
-      ws.cap, static_cast<int64_t>(batch) * ((max_extend_len + tokens_per_cta - 1) / tokens_per_cta));
+      ws.cap - ws.cap_parts, static_cast<int64_t>(batch) * ((max_extend_len + tokens_per_cta - 1) / tokens_per_cta));
   if (mod.cap_in > 0.f)
-    return head_dim == 128 ? launch_mod<128, kExtendCapPass>(p, qmap, entries, s)
-                           : launch_mod<64, kExtendCapPass>(p, qmap, entries, s);
-  return head_dim == 128 ? launch_mod<128, kExtendModPass>(p, qmap, entries, s)
-                         : launch_mod<64, kExtendModPass>(p, qmap, entries, s);
+    return head_dim == 128 ? launch_mod<128, kExtendCapPass>(p, ws, qmap, entries, s)
+                           : launch_mod<64, kExtendCapPass>(p, ws, qmap, entries, s);
+  return head_dim == 128 ? launch_mod<128, kExtendModPass>(p, ws, qmap, entries, s)
+                         : launch_mod<64, kExtendModPass>(p, ws, qmap, entries, s);
 }
 
 extern "C" size_t ra_extend_mod_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_heads,
@@ -260,5 +383,5 @@ extern "C" size_t ra_extend_mod_workspace_bytes(int32_t batch, int64_t total_q, 
   if (batch < 0 || total_q < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
   const int32_t group = num_q_heads / num_kv_heads;
   if (128 % group != 0) return 0;
-  return ra::layout_mod_workspace(batch, total_q, ra::tc::kTiles * (128 / group), nullptr).total;
+  return ra::layout_mod_workspace(batch, total_q, ra::tc::kTiles * (128 / group), group, num_kv_heads, nullptr).total;
 }
