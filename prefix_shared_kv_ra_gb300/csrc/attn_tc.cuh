@@ -907,11 +907,12 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             const bool fixed_ref = CAP && p.mod.cap_log2 <= kCapFixed;
             float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
             uint64_t sum2[2] = {0, 0};
-            auto run = [&](auto edge_tag) {
+            // the chunks taken: 4, or the index of the first one that needs more
+            auto run = [&](auto edge_tag) -> int {
               constexpr bool edge = decltype(edge_tag)::value;  // hidden keys, or keys behind the row's position
               const uint64_t in2 = f2_pack(p.mod.in2.x, p.mod.in2.y);
               const uint64_t step2 = f2_pack(2.f * slope, 2.f * slope);
-              auto chunk = [&](const uint32_t (&sr)[32], int c) {
+              auto chunk = [&](const uint32_t (&sr)[32], int c) -> bool {
                 const float off = static_cast<float>(key0 + 32 * c - pos);  // minus the distance of the first column
                 const int32_t l0 = lo - 32 * c, h0 = hi - 32 * c;
                 uint64_t add2 = f2_pack(fmaf(slope, off, -m_sub), fmaf(slope, off + 1.f, -m_sub));
@@ -947,6 +948,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                   part2[e & 1] = f2_add(part2[e & 1], f2_pack(p0, p1));
                   pw[e] = pack_bf16x2(p0, p1);
                 }
+                // a score beyond the polynomial, or a sum out of range
                 bool out = CAP && !(y_max <= kCapPolyMax);
                 if (!fixed_ref) {
                   float q0, q1, q2, q3;
@@ -954,69 +956,11 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                   f2_unpack(part2[1], q2, q3);
                   out = out || !((q0 + q1) + (q2 + q3) <= kRaiseSum);
                 }
-                if (__any_sync(0xffffffffu, out)) {
-                  // any score of 8 columns, finished but for the reference
-                  auto finish = [&](int q, float (&t)[8]) {
-                    uint32_t x[8];
-                    tmem_ld8(tmem + lane_addr + col_s + 32 * c + 8 * q, x);
-                    tc_wait_ld_regs8(x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                      const float s1 = __uint_as_float(x[e]);
-                      t[e] = CAP ? p.mod.cap_log2 * tanh_any(s1 * p.mod.cap_in) : s1 * p.scale_log2;
-                      t[e] = fmaf(-slope, fabsf(off + static_cast<float>(8 * q + e)), t[e]);
-                      if (8 * q + e < l0 || 8 * q + e >= h0) t[e] = -INFINITY;
-                    }
-                  };
-                  float top = -INFINITY;
-#pragma unroll 1
-                  for (int q = 0; q < 4; ++q) {
-                    float t[8];
-                    finish(q, t);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, t[e]);
-                  }
-                  // (whole powers of two: what is stored is scaled without rounding)
-                  const float up = top > m_sub + kRaiseStep ? ceilf(top - m_sub) : 0.f, down = ex2(-up);
-                  if (__any_sync(0xffffffffu, up > 0.f)) {
-                    m_sub += up;
-                    if (up > 0.f) m_ref = m_sub;
-                    alpha *= down;
-                    resc = resc || up > 0.f;
-                    const uint64_t down2 = f2_pack(down, down);
-                    sum2[0] = f2_mul(sum2[0], down2);
-                    sum2[1] = f2_mul(sum2[1], down2);
-#pragma unroll 1
-                    for (int q = 0; q < 2 * c; ++q) {
-                      uint32_t w[8];
-                      tmem_ld8(tmem + lane_addr + col_s + 8 * q, w);
-                      tc_wait_ld_regs8(w);
-#pragma unroll
-                      for (int e = 0; e < 8; ++e)
-                        w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down);
-                      tmem_st8(tmem + lane_addr + col_s + 8 * q, w);
-                    }
-                  }
-                  part2[0] = part2[1] = 0;
-#pragma unroll 1
-                  for (int q = 0; q < 4; ++q) {
-                    float t[8];
-                    uint32_t w[4];
-                    finish(q, t);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) t[e] = ex2(t[e] - m_sub);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      part2[0] = f2_add(part2[0], f2_pack(t[2 * e], t[2 * e + 1]));
-                      w[e] = pack_bf16x2(t[2 * e], t[2 * e + 1]);
-                    }
-                    tmem_st4(tmem + lane_addr + col_s + 16 * c + 4 * q, w);
-                  }
-                } else {
-                  tmem_st16(tmem + lane_addr + col_s + 16 * c, pw);
-                }
+                if (__any_sync(0xffffffffu, out)) return false;
+                tmem_st16(tmem + lane_addr + col_s + 16 * c, pw);
                 sum2[0] = f2_add(sum2[0], part2[0]);
                 sum2[1] = f2_add(sum2[1], part2[1]);
+                return true;
               };
               uint32_t ba[32], bb[32];
               tmem_ld32(tmem + lane_addr + col_s, ba);
@@ -1024,14 +968,72 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
               for (int c = 0; c < 4; c += 2) {
                 tc_wait_ld_regs(ba);
                 tmem_ld32(tmem + lane_addr + col_s + 32 * (c + 1), bb);
-                chunk(ba, c);
+                const bool first_done = chunk(ba, c);
                 tc_wait_ld_regs(bb);
+                if (!first_done) return c;
                 if (c == 0) tmem_ld32(tmem + lane_addr + col_s + 64, ba);
-                chunk(bb, c + 1);
+                if (!chunk(bb, c + 1)) {
+                  if (c == 0) tc_wait_ld_regs(ba);  // (no load in flight when its registers are given up)
+                  return c + 1;
+                }
               }
+              return 4;
             };
-            if (warp_masked) run(BoolTag<true>{});
-            else run(BoolTag<false>{});
+            const int done = warp_masked ? run(BoolTag<true>{}) : run(BoolTag<false>{});
+            // the chunks from one that was refused on: any scores, from S, 8 columns at a time
+#pragma unroll 1
+            for (int c = done; c < 4; ++c) {
+              float top = -INFINITY, down = 1.f;
+#pragma unroll 1
+              for (int q = 0; q < 8; ++q) {  // the largest score (q < 4), then the weights
+                uint32_t x[8], w[4];
+                tmem_ld8(tmem + lane_addr + col_s + 32 * c + 8 * (q & 3), x);
+                tc_wait_ld_regs8(x);
+                const int32_t at = 32 * c + 8 * (q & 3);
+                float t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float s1 = __uint_as_float(x[e]);
+                  t[e] = CAP ? p.mod.cap_log2 * tanh_any(s1 * p.mod.cap_in) : s1 * p.scale_log2;
+                  t[e] = fmaf(-slope, fabsf(static_cast<float>(key0 + at + e - pos)), t[e]);
+                  if (at + e < lo || at + e >= hi) t[e] = -INFINITY;
+                }
+                if (q < 4) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) top = fmaxf(top, t[e]);
+                  continue;
+                }
+                if (q == 4) {
+                  // (whole powers of two: what is stored is scaled without rounding)
+                  const float up = top > m_sub + kRaiseStep ? ceilf(top - m_sub) : 0.f;
+                  if (__any_sync(0xffffffffu, up > 0.f)) {
+                    down = ex2(-up);
+                    m_sub += up;
+                    if (up > 0.f) m_ref = m_sub, resc = true;
+                    alpha *= down;
+                    sum2[0] = f2_mul(sum2[0], f2_pack(down, down));
+                    sum2[1] = f2_mul(sum2[1], f2_pack(down, down));
+#pragma unroll 1
+                    for (int k = 0; k < 2 * c; ++k) {
+                      uint32_t y[8];
+                      tmem_ld8(tmem + lane_addr + col_s + 8 * k, y);
+                      tc_wait_ld_regs8(y);
+#pragma unroll
+                      for (int e = 0; e < 8; ++e)
+                        y[e] = pack_bf16x2(__uint_as_float(y[e] << 16) * down, __uint_as_float(y[e] & 0xffff0000u) * down);
+                      tmem_st8(tmem + lane_addr + col_s + 8 * k, y);
+                    }
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float p0 = ex2(t[2 * e] - m_sub), p1 = ex2(t[2 * e + 1] - m_sub);
+                  sum2[0] = f2_add(sum2[0], f2_pack(p0, p1));
+                  w[e] = pack_bf16x2(p0, p1);
+                }
+                tmem_st4(tmem + lane_addr + col_s + 16 * c + 4 * (q & 3), w);
+              }
+            }
             float a0, a1, a2, a3;
             f2_unpack(sum2[0], a0, a1);
             f2_unpack(sum2[1], a2, a3);
