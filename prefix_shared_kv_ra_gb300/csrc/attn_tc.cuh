@@ -113,8 +113,17 @@ struct TcParams {
 };
 
 // kTreeDualPass: the tree pass for calls whose items all have one live query tile.
-// kExtendModPass, kExtendCapPass: extend with changed scores, without and with a cap.
-enum TcPass { kPrefixPass = 0, kExtendPass = 1, kTreePass = 2, kTreeDualPass = 3, kExtendModPass = 4, kExtendCapPass = 5 };
+// kExtendModPass, kExtendCapPass: extend with changed scores, without and with a cap; kExtendFixedPass: with a cap of at
+// most kCapFixed log2 units, under which no reference is needed.
+enum TcPass {
+  kPrefixPass = 0,
+  kExtendPass = 1,
+  kTreePass = 2,
+  kTreeDualPass = 3,
+  kExtendModPass = 4,
+  kExtendCapPass = 5,
+  kExtendFixedPass = 6
+};
 
 namespace tc {
 
@@ -123,10 +132,6 @@ constexpr int kTiles = 2;      // query tiles per item
 constexpr int kKeys = 128;     // keys per tile (MMA N of S, K of PV)
 constexpr int kKWarps = 4;                 // TMA gather throughput grows with the number of issuing warps;
 constexpr int kVWarps = 3;                 // the tensor core waits on K first, so K gets one warp more
-constexpr int kKWarp0 = 8;                 // K gather warps 8..11
-constexpr int kVWarp0 = kKWarp0 + kKWarps;  // V gather warps 12..14
-constexpr int kMmaWarp = kVWarp0 + kVWarps;  // warp 15
-constexpr int kThreads = 32 * (kMmaWarp + 1);  // 512
 constexpr int kGroups = kKeys / 4;          // 4-key gather groups per tile
 constexpr int kItemRing = 8;                // published items (the claimer runs <= KS + 2 items ahead)
 constexpr uint32_t kTmemCols = 512;
@@ -134,18 +139,30 @@ constexpr uint32_t kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Changed scores: a row whose sum is outside these has its reference too far from its scores (weights that vanish or
 // overflow); the sum at which a row's reference is raised, and by how much a score has to exceed it then; the cap (in
-// log2 units) up to which the reference is fixed.
+// log2 units) up to which none is needed: weights of 2^-80 .. 2^80 are as exact as others in bf16 and fp32, and the sum
+// of 2^24 of them stays below 2^104.
 constexpr float kSumFloor = 0x1p-90f, kSumCeiling = 0x1p110f;
 constexpr float kRaiseSum = 0x1p60f, kRaiseStep = 8.f;
-constexpr float kCapFixed = 95.f;
 constexpr float kFastSumLimit = 32768.0f;  // single-pass acceptance: every p of the row <= 2^15
-// Register split: the softmax warpgroups (0, 1) hold a 128-key P row and two 32-column S chunks; the
-// gather and MMA warpgroups (2, 3) need few.  setmaxnreg moves registers between them within the
-// block's launch allocation (kThreads x kLaunchRegs), which the split must add up to exactly.
-constexpr int kLaunchRegs = 65536 / kThreads;  // what __launch_bounds__(kThreads, 1) compiles to
-constexpr int kSoftmaxRegs = 184;
-constexpr int kOtherRegs = 72;
-static_assert(2 * 128 * kSoftmaxRegs + 2 * 128 * kOtherRegs == kThreads * kLaunchRegs, "register split");
+// Warps of a pass, and the register split: the softmax warpgroups hold a 128-key P row and two 32-column S chunks; the gather
+// and MMA warpgroups (the last two) need few.  setmaxnreg moves registers between them within the block's launch allocation
+// (kThreads x kLaunchRegs), which the split must add up to exactly.  Four softmax warpgroups where the two halves of a
+// row need not agree on anything until its end: two per query tile leave a scheduler two warps to hide each other's
+// latencies, four fill it better.
+template <int PASS>
+struct Roles {
+  static constexpr bool kWide = PASS == kExtendFixedPass;
+  static constexpr int kSoftWarps = kWide ? 16 : 8;
+  static constexpr int kTileThreads = 32 * kSoftWarps / kTiles;  // softmax threads of a query tile
+  static constexpr int kKWarp0 = kSoftWarps;                 // K gather warps 8..11
+  static constexpr int kVWarp0 = kKWarp0 + kKWarps;          // V gather warps 12..14
+  static constexpr int kMmaWarp = kVWarp0 + kVWarps;         // warp 15
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);       // 512
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;  // what __launch_bounds__(kThreads, 1) compiles to
+  static constexpr int kSoftmaxRegs = kWide ? 96 : 184;
+  static constexpr int kOtherRegs = kWide ? 48 : 72;
+  static_assert(32 * kSoftWarps * kSoftmaxRegs + 256 * kOtherRegs == kThreads * kLaunchRegs, "register split");
+};
 
 template <int D, int KS, int VS>
 struct Layout {
@@ -211,7 +228,7 @@ __device__ __forceinline__ bool tc_job(const TcParams& p, int32_t item, Job& j, 
     j.q_tok0 = f.w + e.y * kTiles * T;
     j.slot = e.w;
     j.odd = __ldg(p.tree_odd + static_cast<int64_t>(e.x) * p.hkv + j.kh);
-  } else if constexpr (PASS == kExtendModPass || PASS == kExtendCapPass) {
+  } else if constexpr (PASS == kExtendModPass || PASS == kExtendCapPass || PASS == kExtendFixedPass) {
     // (as below; the list's builder found the tile's key range)
     const int4 e = __ldg(reinterpret_cast<const int4*>(p.work_items) + rest);
     const int32_t E = min(max(__ldg(p.extend_lens + e.x), 0), p.max_extend_len);
@@ -359,14 +376,18 @@ __device__ __forceinline__ void mod_row(const TcParams& p, const Job& jb, int64_
 }  // namespace tc
 
 template <int D, int KS, int VS, int PASS>
-__global__ void __launch_bounds__(tc::kThreads, 1)
+__global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using namespace tc;
   using L = Layout<D, KS, VS>;
+  using R = Roles<PASS>;
+  constexpr int kKWarp0 = R::kKWarp0, kVWarp0 = R::kVWarp0, kMmaWarp = R::kMmaWarp;
+  constexpr int kSoftmaxRegs = R::kSoftmaxRegs, kOtherRegs = R::kOtherRegs;
   constexpr bool EXTEND = PASS != kPrefixPass;  // rows are tokens of one request, items come from a list
   constexpr bool DUAL = PASS == kTreeDualPass;
   constexpr bool TREE = PASS == kTreePass || DUAL;
+  constexpr bool FIXED = PASS == kExtendFixedPass;  // the softmax below FIXED's is not this pass's
   constexpr bool CAP = PASS == kExtendCapPass;
   constexpr bool MOD = PASS == kExtendModPass || CAP;
   constexpr int HALVES = D / 64;  // 128-byte (64-element) column blocks of a row
@@ -382,6 +403,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t bar_join[2];  // tree, dual items: tile 1's sums are in s_join; its O has been read
+                                                 // (fixed reference: the sums of tile i's rows are in TMEM)
   __shared__ float2 s_join[DUAL ? kRows : 1];    // (reference, sum) of tile 1's rows
 
   const int warp = threadIdx.x >> 5;
@@ -403,14 +425,14 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(smem_u32(&bar_q[i]), EXTEND ? 1 : kKWarps / kTiles);
       mbar_init(smem_u32(&bar_s[i]), 1);
-      mbar_init(smem_u32(&bar_p[i]), 128);
+      mbar_init(smem_u32(&bar_p[i]), R::kTileThreads);
       mbar_init(smem_u32(&bar_o[i]), 1);
-      mbar_init(smem_u32(&bar_ofree[i]), 128);
+      mbar_init(smem_u32(&bar_ofree[i]), R::kTileThreads);
     }
     for (int s = 0; s < kItemRing; ++s) mbar_init(smem_u32(&bar_item[s]), 1);
     mbar_init(smem_u32(&bar_done), 1);
-    mbar_init(smem_u32(&bar_join[0]), 128);
-    mbar_init(smem_u32(&bar_join[1]), 128);
+    mbar_init(smem_u32(&bar_join[0]), R::kTileThreads);
+    mbar_init(smem_u32(&bar_join[1]), R::kTileThreads);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -698,7 +720,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         const uint64_t vd = desc_v0 + st * kTile16;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16 && live; ++kk) {
-          tc_mma_ts(tmem + kColO + i * 128, tmem + i * kKeys + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
+          // (fixed reference: each half's P is over its own half of S)
+          tc_mma_ts(tmem + kColO + i * 128, tmem + i * kKeys + (FIXED ? (kk >> 2) * 64 + (kk & 3) * 8 : kk * 8), vd + kk * (2048 >> 4), idesc_pv,
                     (j > 0 || kk > 0) ? 1u : 0u);
         }
         // Each commit stalls the tensor pipe briefly, so there are three per key tile: S_0, S_1 and the
@@ -767,6 +790,220 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     if (lane == 0) tc_commit(smem_u32(&bar_done));  // all MMAs of this CTA retired before TMEM is freed
     __syncwarp();
     mbar_wait(smem_u32(&bar_done), 0);
+  } else if constexpr (FIXED) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ================================================================ softmax under a fixed reference (warps 0-15)
+    // Capped scores are bounded, and so are their weights: t = cap log2(e) tanh(y) - slope |pos - key| - reference, where
+    // the reference is only the largest bias of the row's keys.  Nothing is looked up, moved or rescaled, so each half of a
+    // row's keys has a thread of its own (warpgroups 2 i and 2 i + 1 of query tile i); they add up their sums at the end.
+    // P goes over the first half of the S columns it came from, 32 keys at a time; a chunk with a |y| beyond the
+    // polynomial's range is done by a loop of its own, 8 columns at a time.
+    const int ti = warp >> 3, half = (warp >> 2) & 1;
+    const int r = threadIdx.x & 127;  // row of the tile = TMEM lane
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t col = tmem + lane_addr + ti * kKeys + half * 64;
+    const uint32_t col_o = tmem + lane_addr + kColO + ti * 128 + half * (D / 2);
+    const int tok = ti * T + r / G;
+    bool ok = true;
+    int32_t g = 0;
+    for (int32_t n = 0;; ++n) {
+      Job jb;
+      const int ri = wait_item(n, jb);
+      if (__any_sync(0xffffffffu, ri < 0)) { ok = false; break; }
+      if (ri == 0) break;
+      const bool row_valid = tok < jb.n_valid;
+      const int32_t pos = jb.causal0 + tok;
+      int32_t lim = jb.kend, first = jb.kbeg;  // the keys this row sees: [first, lim)
+      float slope = 0.f;
+      if (row_valid) {
+        lim = min(max(pos + 1, jb.mem0), jb.kend);
+        if (p.mod.window > 0) first = max(first, pos - p.mod.window + 1);
+        if (p.mod.first_key) first = max(first, __ldg(p.mod.first_key + jb.q_tok0 + tok));
+        if (p.mod.slopes) slope = __ldg(p.mod.slopes + jb.kh * G + r % G) * kLog2e;
+      }
+      const float m = first < lim ? bias_bound(first, lim, pos, slope) : 0.f;
+      float l = 0.f;
+      for (int j = 0; j < jb.nt; ++j) {
+        const bool fail_here = !mbar_wait(smem_u32(&bar_s[ti]), (g + j) & 1);
+        if (__any_sync(0xffffffffu, fail_here)) { ok = false; break; }
+        if (ti >= jb.tiles) {  // an empty query tile: no S was computed; keep bar_p's phase
+          mbar_arrive(smem_u32(&bar_p[ti]));
+          continue;
+        }
+        tc_fence_after();
+        const int32_t key0 = jb.kbeg + j * kKeys + half * 64;
+        const bool edge_here = key0 + 64 > min(lim, pos + 1) || key0 < first;  // hidden keys, or keys behind the row's own
+        const bool sees = first < key0 + 64 && first < lim && key0 < lim;
+        if (!__any_sync(0xffffffffu, sees)) {
+          const uint32_t none[32] = {};
+          tmem_st32(col, none);
+        } else {
+          const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
+          uint64_t sum2[2] = {0, 0};
+          // the 32-column chunks taken: 2, or the index of the first one beyond the polynomial
+          auto run = [&](auto edge_tag) -> int {
+            constexpr bool edge = decltype(edge_tag)::value;
+            const uint64_t in2 = f2_pack(p.mod.in2.x, p.mod.in2.y);
+            const uint64_t step2 = f2_pack(2.f * slope, 2.f * slope);
+            uint32_t ba[16], bb[16], pw[16];
+            float y_max = 0.f;
+            uint64_t part2[2];
+            auto part = [&](const uint32_t (&sr)[16], int c, int at) {  // columns c .. c + 15, weights to pw[at ..]
+              const float off = static_cast<float>(key0 + c - pos);  // minus the distance of the first column
+              const int32_t l0 = lo - c, h0 = hi - c;
+              uint64_t add2 = f2_pack(fmaf(slope, off, -m), fmaf(slope, off + 1.f, -m));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint64_t y2 = f2_mul(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), in2);
+                const uint64_t z2 = f2_mul(y2, y2);
+                float y0, y1;
+                f2_unpack(y2, y0, y1);
+                y_max = fmaxf(y_max, fmaxf(fabsf(y0), fabsf(y1)));
+                auto coef = [&](int i) { return f2_pack(p.mod.cap_poly[i].x, p.mod.cap_poly[i].y); };
+                uint64_t h2 = coef(kCapTerms - 1);
+#pragma unroll
+                for (int i = kCapTerms - 2; i >= 0; --i) h2 = f2_fma(h2, z2, coef(i));
+                if (edge) add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m), fmaf(-slope, fabsf(off + (2 * e + 1)), -m));
+                float t0, t1;
+                f2_unpack(f2_fma(y2, h2, add2), t0, t1);
+                if (!edge) add2 = f2_add(add2, step2);
+                if (edge) {
+                  if (2 * e < l0 || 2 * e >= h0) t0 = -INFINITY;
+                  if (2 * e + 1 < l0 || 2 * e + 1 >= h0) t1 = -INFINITY;
+                }
+                const float p0 = ex2(t0), p1 = ex2(t1);
+                part2[e & 1] = f2_add(part2[e & 1], f2_pack(p0, p1));
+                pw[at + e] = pack_bf16x2(p0, p1);
+              }
+            };
+            tmem_ld16(col, ba);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              part2[0] = part2[1] = 0;
+              tc_wait_ld_regs16(ba);
+              tmem_ld16(col + 32 * c + 16, bb);
+              part(ba, 32 * c, 0);
+              tc_wait_ld_regs16(bb);
+              if (c == 0) tmem_ld16(col + 32, ba);
+              part(bb, 32 * c + 16, 8);
+              if (__any_sync(0xffffffffu, !(y_max <= kCapPolyMax))) {
+                if (c == 0) tc_wait_ld_regs16(ba);  // (no load in flight when its registers are given up)
+                return c;
+              }
+              tmem_st16(col + 16 * c, pw);
+              sum2[0] = f2_add(sum2[0], part2[0]);
+              sum2[1] = f2_add(sum2[1], part2[1]);
+            }
+            return 2;
+          };
+          const int done = __any_sync(0xffffffffu, edge_here) ? run(BoolTag<true>{}) : run(BoolTag<false>{});
+#pragma unroll 1
+          for (int q = 4 * done; q < 8; ++q) {
+            uint32_t x[8], w[4];
+            tmem_ld8(col + 8 * q, x);
+            tc_wait_ld_regs8(x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float t[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int32_t at = 8 * q + 2 * e + i;
+                t[i] = p.mod.cap_log2 * tanh_any(__uint_as_float(x[2 * e + i]) * p.mod.cap_in);
+                t[i] += fmaf(-slope, fabsf(static_cast<float>(key0 + at - pos)), -m);
+                if (at < lo || at >= hi) t[i] = -INFINITY;
+                t[i] = ex2(t[i]);
+              }
+              sum2[0] = f2_add(sum2[0], f2_pack(t[0], t[1]));
+              w[e] = pack_bf16x2(t[0], t[1]);
+            }
+            tmem_st4(col + 4 * q, w);
+          }
+          float a0, a1, a2, a3;
+          f2_unpack(sum2[0], a0, a1);
+          f2_unpack(sum2[1], a2, a3);
+          l += (a0 + a1) + (a2 + a3);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&bar_p[ti]));
+      }
+      if (!ok) break;
+      g += jb.nt;
+      // ---- epilogue: O / l, this thread's half of the columns.  A row's halves hand each other their sums in the first of
+      // the columns that they have read (shared memory is full); then O_i is released to the next item's first PV.
+      const bool late = !mbar_wait(smem_u32(&bar_o[ti]), n & 1);
+      if (__any_sync(0xffffffffu, late)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t oa[D / 64][32];
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) tmem_ld32(col_o + c * 32, oa[c]);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) tc_wait_ld_regs(oa[c]);
+      // a result that is not finite may come from a value that this row does not see: it is handed on as a sum out of range
+      float bad[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(oa[c][e]), 0.f, bad[e & 3]);
+      l += (bad[0] + bad[1]) + (bad[2] + bad[3]);
+      tmem_st1(col_o, __float_as_uint(l));
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&bar_join[ti]));
+      const bool stuck = !mbar_wait(smem_u32(&bar_join[ti]), n & 1);
+      if (__any_sync(0xffffffffu, stuck)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t other;
+      tmem_ld1(half == 0 ? col_o + D / 2 : col_o - D / 2, other);
+      l += __uint_as_float(other);
+      tc_fence_before();
+      mbar_arrive(smem_u32(&bar_ofree[ti]));
+      const bool redo = row_valid && !(l >= kSumFloor && l <= kSumCeiling) && !(first >= lim && l == 0.f);
+      const float inv_l = l == 0.f ? 0.f : 1.f / l;
+      const int64_t row = (jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G);
+      const int64_t part_row = (static_cast<int64_t>(jb.slot) * p.hkv + jb.kh) * p.part_rows + ti * kRows + r;
+      if (row_valid && !redo) {
+        if (jb.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + half * (D / 2));
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_bf16x2(__uint_as_float(oa[c][8 * e + 2 * k]) * inv_l, __uint_as_float(oa[c][8 * e + 2 * k + 1]) * inv_l);
+              dst[4 * c + e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+          float* dst = p.part_o + part_row * D + half * (D / 2);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(oa[c][8 * e + k]) * inv_l;
+              st_global_v8(dst + 32 * c + 8 * e, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+            }
+          if (half == 0) p.part_lse[part_row] = m + __log2f(l);
+        }
+      }
+      for (uint32_t rows = half == 0 ? __ballot_sync(0xffffffffu, redo) : 0u; rows != 0; rows &= rows - 1) {
+        const int src = __ffs(rows) - 1;
+        const int64_t row1 = __shfl_sync(0xffffffffu, row, src), at = __shfl_sync(0xffffffffu, part_row, src);
+        float y[D / 32], lse;
+        mod_row<D, true>(p, jb, row1, __shfl_sync(0xffffffffu, first, src), __shfl_sync(0xffffffffu, lim, src),
+                         __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, slope, src), y, lse);
+#pragma unroll
+        for (int v = 0; v < D / 32; ++v) {
+          if (jb.slot < 0) p.o[row1 * D + lane * (D / 32) + v] = __float2bfloat16_rn(y[v]);
+          else p.part_o[at * D + lane * (D / 32) + v] = y[v];
+        }
+        if (jb.slot >= 0 && lane == 0) p.part_lse[at] = lse;
+      }
+    }
+    if (!ok) give_up();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ================================================================ softmax (warps 0-7)
@@ -866,17 +1103,16 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         if constexpr (MOD) {
           // The same with the scores' changes, a chunk's weights going to TMEM at once, over columns of S that are done with,
           // and the tile a short loop over 32-column chunks: holding the 64 registers of P until a tile is settled, as below,
-          // left the cap's polynomial too few, and unrolled code for all cases ran at the instruction cache's pace (1394 ->
-          // 612 us for 8 prompts of 700..1500 tokens, 64/8 heads, capped).
+          // left too few for the rest, and unrolled code for all cases ran at the instruction cache's pace (603 -> 435 us for
+          // 8 prompts of 700..1500 tokens, 64/8 heads, uncapped).
           //   t = cap log2(e) tanh(y) - slope |pos - key| - reference, y = s sm_scale / cap; or s sm_scale log2(e) - ...
           // Up to the row's position the bias is linear in the key: it and the reference are one addend, stepped along the
           // columns.  The reference only has to keep weights and sums in range (2^60 weighs as exactly as 1 in bf16 and
-          // fp32): with a cap of up to kCapFixed log2 units it is 0 (no chunk's sum can leave fp32 then), else the largest of the row's first 16 scores with the
-          // largest bias that any of its keys has (with the first keys' bias, far away, it would have to move in every
-          // tile).  It is raised by whole powers of two: between tiles when the sum has grown, and within one when a
-          // chunk's sum leaves the range, which scales what the tile has stored so far.  That and scores beyond the
-          // polynomial's range take a chunk through a loop of its own, from S, 8 columns at a time.  A row whose whole sum
-          // is too small for its reference is done again in the epilogue.
+          // fp32): it is the largest of the row's first 16 scores with the largest bias that any of its keys has (with the
+          // first keys' bias, far away, it would have to move in every tile).  It is raised by whole powers of two: between
+          // tiles when the sum has grown, and within one when a chunk's sum leaves the range, which scales what the tile has
+          // stored so far.  That and scores beyond the polynomial's range take a chunk through a loop of its own, from S, 8
+          // columns at a time.  A row whose whole sum is too small for its reference is done again in the epilogue.
           const bool sees = first < key0 + kKeys && first < lim && key0 < lim;  // any key of this tile
           if (!__any_sync(0xffffffffu, sees)) {
             const uint32_t none[32] = {};
@@ -885,17 +1121,14 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           } else {
             const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
             if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-              float top = 0.f;
-              if (!CAP || p.mod.cap_log2 > kCapFixed) {
-                uint32_t x[16];
-                tmem_ld16(tmem + lane_addr + col_s, x);
-                tc_wait_ld_regs16(x);
-                top = -INFINITY;
+              uint32_t x[16];
+              tmem_ld16(tmem + lane_addr + col_s, x);
+              tc_wait_ld_regs16(x);
+              float top = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, e >= lo && e < hi ? __uint_as_float(x[e]) : -INFINITY);
-                if (top == -INFINITY) top = 0.f;  // (the row's keys begin behind these columns)
-                else top = CAP ? p.mod.cap_log2 * tanh_any(top * p.mod.cap_in) : top * p.scale_log2;
-              }
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, e >= lo && e < hi ? __uint_as_float(x[e]) : -INFINITY);
+              if (top == -INFINITY) top = 0.f;  // (the row's keys begin behind these columns)
+              else top = CAP ? p.mod.cap_log2 * tanh_any(top * p.mod.cap_in) : top * p.scale_log2;
               if (m_used == -INFINITY && sees) m_ref = top + bias_bound(first, lim, pos, slope);
             }
             if (__any_sync(0xffffffffu, l > kRaiseSum)) {
@@ -904,7 +1137,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
               m_ref += up;
               alpha = ex2(-up);
             }
-            const bool fixed_ref = CAP && p.mod.cap_log2 <= kCapFixed;
             float m_sub = m_ref == -INFINITY ? 0.f : m_ref;
             uint64_t sum2[2] = {0, 0};
             // the chunks taken: 4, or the index of the first one that needs more
@@ -949,13 +1181,10 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                   pw[e] = pack_bf16x2(p0, p1);
                 }
                 // a score beyond the polynomial, or a sum out of range
-                bool out = CAP && !(y_max <= kCapPolyMax);
-                if (!fixed_ref) {
-                  float q0, q1, q2, q3;
-                  f2_unpack(part2[0], q0, q1);
-                  f2_unpack(part2[1], q2, q3);
-                  out = out || !((q0 + q1) + (q2 + q3) <= kRaiseSum);
-                }
+                float q0, q1, q2, q3;
+                f2_unpack(part2[0], q0, q1);
+                f2_unpack(part2[1], q2, q3);
+                const bool out = !((q0 + q1) + (q2 + q3) <= kRaiseSum) || (CAP && !(y_max <= kCapPolyMax));
                 if (__any_sync(0xffffffffu, out)) return false;
                 tmem_st16(tmem + lane_addr + col_s + 16 * c, pw);
                 sum2[0] = f2_add(sum2[0], part2[0]);

@@ -155,11 +155,11 @@ ra_status launch_extend(const TcParams& p, const CUtensorMap& qmap, int64_t entr
   if (ra_status st = current_device(&dev)) return st;
   if (L::kDynSmem > dev.max_smem_optin)
     return fail(RA_ERR_UNSUPPORTED, "extend kernel needs %d bytes of shared memory", L::kDynSmem);
-  if (ra_status st = set_smem(kern, L::kDynSmem, configured, dev.device)) return st;
+  if (ra_status st = set_smem<kExtendPass>(kern, L::kDynSmem, configured, dev.device)) return st;
   // persistent: one CTA per SM (at most one per item)
   const int64_t items = entries * p.hkv;
   dim3 grid(static_cast<unsigned>(items < dev.num_sms ? items : dev.num_sms));
-  return launch_pdl("attn_tc_kernel<extend>", kern, grid, dim3(tc::kThreads), L::kDynSmem, s, p, qmap, kmap, vmap);
+  return launch_pdl("attn_tc_kernel<extend>", kern, grid, dim3(tc::Roles<kExtendPass>::kThreads), L::kDynSmem, s, p, qmap, kmap, vmap);
 }
 
 template <int D>
@@ -171,7 +171,7 @@ ra_status launch_prefix(const TcParams& p, int grid_x, int num_groups, int32_t w
   if (ra_status st = current_device(&dev)) return st;
   if (L::kDynSmem > dev.max_smem_optin)
     return fail(RA_ERR_UNSUPPORTED, "prefix kernel needs %d bytes of shared memory", L::kDynSmem);
-  if (ra_status st = set_smem(kern, L::kDynSmem, configured, dev.device)) return st;
+  if (ra_status st = set_smem<kPrefixPass>(kern, L::kDynSmem, configured, dev.device)) return st;
   CUtensorMap qmap, kmap, vmap;
   if (ra_status st = row_gather_map(&qmap, p.q, static_cast<int64_t>(p.batch) * p.hq, D)) return st;
   if (ra_status st = row_gather_map(&kmap, p.k_pool, p.num_slots * p.hkv, D)) return st;
@@ -184,7 +184,7 @@ ra_status launch_prefix(const TcParams& p, int grid_x, int num_groups, int32_t w
   if (wave > 0 && wave < cap) cap = wave;
   dim3 grid(static_cast<unsigned>(items < cap ? items : cap));
   *ctas = static_cast<int32_t>(grid.x);
-  return launch_pdl("attn_tc_kernel<cascade prefix>", kern, grid, dim3(tc::kThreads), L::kDynSmem, s, p, qmap, kmap,
+  return launch_pdl("attn_tc_kernel<cascade prefix>", kern, grid, dim3(tc::Roles<kPrefixPass>::kThreads), L::kDynSmem, s, p, qmap, kmap,
                     vmap);
 }
 

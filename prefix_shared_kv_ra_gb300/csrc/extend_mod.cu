@@ -275,10 +275,10 @@ ra_status launch_mod(const TcParams& p, const ModWorkspace& ws, const CUtensorMa
   if (ra_status st = current_device(&dev)) return st;
   if (L::kDynSmem > dev.max_smem_optin)
     return fail(RA_ERR_UNSUPPORTED, "extend kernel needs %d bytes of shared memory", L::kDynSmem);
-  if (ra_status st = set_smem(kern, L::kDynSmem, configured, dev.device)) return st;
+  if (ra_status st = set_smem<PASS>(kern, L::kDynSmem, configured, dev.device)) return st;
   const int64_t items = (entries + ws.cap_parts) * p.hkv;
   dim3 grid(static_cast<unsigned>(items < dev.num_sms ? items : dev.num_sms));
-  if (ra_status st = launch_pdl("attn_tc_kernel<extend, changed scores>", kern, grid, dim3(tc::kThreads), L::kDynSmem, s,
+  if (ra_status st = launch_pdl("attn_tc_kernel<extend, changed scores>", kern, grid, dim3(tc::Roles<PASS>::kThreads), L::kDynSmem, s,
                                 p, qmap, kmap, vmap))
     return st;
   if (ws.cap_parts == 0) return RA_OK;
@@ -371,6 +371,9 @@ extern "C" ra_status ra_extend_attention_mod(
   // at most sum_b ceil(E_b / tokens_per_cta) entries; CTAs past the listed count return at once
   const int64_t entries = std::min<int64_t>(
       ws.cap - ws.cap_parts, static_cast<int64_t>(batch) * ((max_extend_len + tokens_per_cta - 1) / tokens_per_cta));
+  if (mod.cap_in > 0.f && mod.cap_log2 <= kCapFixed)
+    return head_dim == 128 ? launch_mod<128, kExtendFixedPass>(p, ws, qmap, entries, s)
+                           : launch_mod<64, kExtendFixedPass>(p, ws, qmap, entries, s);
   if (mod.cap_in > 0.f)
     return head_dim == 128 ? launch_mod<128, kExtendCapPass>(p, ws, qmap, entries, s)
                            : launch_mod<64, kExtendCapPass>(p, ws, qmap, entries, s);

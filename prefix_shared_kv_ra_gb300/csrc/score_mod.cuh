@@ -17,6 +17,7 @@ namespace ra {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kCapPolyMax = 1.25f;
 constexpr int kCapTerms = 7;
+constexpr float kCapFixed = 80.f;
 __host__ __device__ __forceinline__ constexpr float cap_coef(int i) {
   constexpr float c[kCapTerms] = {0.9999994039535522f,    -0.3332934081554413f, 0.1329064816236496f, -0.052205443382263184f,
                                   0.018229123204946518f, -0.004626905079931021f, 0.0005844939732924104f};

@@ -490,7 +490,7 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
   static bool configured[64] = {};
   if (L::kDynSmem > dev.max_smem_optin)
     return fail(RA_ERR_UNSUPPORTED, "tree kernel needs %d bytes of shared memory", L::kDynSmem);
-  if (ra_status st = set_smem(kern, L::kDynSmem, configured, dev.device)) return st;
+  if (ra_status st = set_smem<PASS>(kern, L::kDynSmem, configured, dev.device)) return st;
   TcParams tp{};
   tp.k_pool = p.k_pool;
   tp.v_pool = p.v_pool;
@@ -518,7 +518,7 @@ ra_status launch_wide(const TreeParams& p, cudaStream_t s, const DeviceInfo& dev
   tp.part_lse = p.ws.part_lse;
   const int64_t items = p.ws.cap * p.hkv;
   const int grid = static_cast<int>(items < dev.num_sms ? items : dev.num_sms);
-  return launch_pdl("attn_tc_kernel<tree>", kern, dim3(grid), dim3(tc::kThreads), L::kDynSmem, s, tp, qmap, kmap, vmap);
+  return launch_pdl("attn_tc_kernel<tree>", kern, dim3(grid), dim3(tc::Roles<PASS>::kThreads), L::kDynSmem, s, tp, qmap, kmap, vmap);
 }
 
 // 0: the plan kernel's list; 1 or 2: a small call, of so many query tiles per lane.  (Requests in several narrow
