@@ -796,8 +796,10 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
     // Capped scores are bounded, and so are their weights: t = cap log2(e) tanh(y) - slope |pos - key| - reference, where
     // the reference is only the largest bias of the row's keys.  Nothing is looked up, moved or rescaled, so each half of a
     // row's keys has a thread of its own (warpgroups 2 i and 2 i + 1 of query tile i); they add up their sums at the end.
-    // P goes over the first half of the S columns it came from, 32 keys at a time; a chunk with a |y| beyond the
-    // polynomial's range is done by a loop of its own, 8 columns at a time.
+    // P goes over the first half of the S columns it came from, 32 keys at a time.  Here tanh(y) is 1 - 2 / (e^2y + 1) for
+    // every y: where y is small it is off by 2^-22, which a cap this small makes 2e-5 of a weight, and the special function
+    // units have time for the two more calls that the fp32 pipe has not for the polynomial (642 -> 602 us for 8 prompts of
+    // 700..1500 tokens, 64/8 heads).
     const int ti = warp >> 3, half = (warp >> 2) & 1;
     const int r = threadIdx.x & 127;  // row of the tile = TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -840,84 +842,48 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
         } else {
           const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
           uint64_t sum2[2] = {0, 0};
-          // the 32-column chunks taken: 2, or the index of the first one beyond the polynomial
-          auto run = [&](auto edge_tag) -> int {
+          auto run = [&](auto edge_tag) {
             constexpr bool edge = decltype(edge_tag)::value;
-            const uint64_t in2 = f2_pack(p.mod.in2.x, p.mod.in2.y);
+            const uint64_t in2 = f2_pack(p.mod.exp2y.x, p.mod.exp2y.y), one2 = f2_pack(1.f, 1.f);
+            const uint64_t cap2 = f2_pack(-2.f * p.mod.cap_log2, -2.f * p.mod.cap_log2);
             const uint64_t step2 = f2_pack(2.f * slope, 2.f * slope);
+            const float top = p.mod.cap_log2 - m;
             uint32_t ba[16], bb[16], pw[16];
-            float y_max = 0.f;
-            uint64_t part2[2];
             auto part = [&](const uint32_t (&sr)[16], int c, int at) {  // columns c .. c + 15, weights to pw[at ..]
               const float off = static_cast<float>(key0 + c - pos);  // minus the distance of the first column
               const int32_t l0 = lo - c, h0 = hi - c;
-              uint64_t add2 = f2_pack(fmaf(slope, off, -m), fmaf(slope, off + 1.f, -m));
+              uint64_t add2 = f2_pack(fmaf(slope, off, top), fmaf(slope, off + 1.f, top));
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const uint64_t y2 = f2_mul(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), in2);
-                const uint64_t z2 = f2_mul(y2, y2);
-                float y0, y1;
-                f2_unpack(y2, y0, y1);
-                y_max = fmaxf(y_max, fmaxf(fabsf(y0), fabsf(y1)));
-                auto coef = [&](int i) { return f2_pack(p.mod.cap_poly[i].x, p.mod.cap_poly[i].y); };
-                uint64_t h2 = coef(kCapTerms - 1);
-#pragma unroll
-                for (int i = kCapTerms - 2; i >= 0; --i) h2 = f2_fma(h2, z2, coef(i));
-                if (edge) add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), -m), fmaf(-slope, fabsf(off + (2 * e + 1)), -m));
-                float t0, t1;
-                f2_unpack(f2_fma(y2, h2, add2), t0, t1);
+                float e0, e1, t0, t1;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), in2), e0, e1);
+                f2_unpack(f2_add(f2_pack(ex2(e0), ex2(e1)), one2), e0, e1);
+                if (edge) add2 = f2_pack(fmaf(-slope, fabsf(off + 2 * e), top), fmaf(-slope, fabsf(off + (2 * e + 1)), top));
+                f2_unpack(f2_fma(f2_pack(rcp_approx(e0), rcp_approx(e1)), cap2, add2), t0, t1);
                 if (!edge) add2 = f2_add(add2, step2);
                 if (edge) {
                   if (2 * e < l0 || 2 * e >= h0) t0 = -INFINITY;
                   if (2 * e + 1 < l0 || 2 * e + 1 >= h0) t1 = -INFINITY;
                 }
                 const float p0 = ex2(t0), p1 = ex2(t1);
-                part2[e & 1] = f2_add(part2[e & 1], f2_pack(p0, p1));
+                sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
                 pw[at + e] = pack_bf16x2(p0, p1);
               }
             };
             tmem_ld16(col, ba);
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
-              part2[0] = part2[1] = 0;
               tc_wait_ld_regs16(ba);
               tmem_ld16(col + 32 * c + 16, bb);
               part(ba, 32 * c, 0);
               tc_wait_ld_regs16(bb);
               if (c == 0) tmem_ld16(col + 32, ba);
               part(bb, 32 * c + 16, 8);
-              if (__any_sync(0xffffffffu, !(y_max <= kCapPolyMax))) {
-                if (c == 0) tc_wait_ld_regs16(ba);  // (no load in flight when its registers are given up)
-                return c;
-              }
               tmem_st16(col + 16 * c, pw);
-              sum2[0] = f2_add(sum2[0], part2[0]);
-              sum2[1] = f2_add(sum2[1], part2[1]);
             }
-            return 2;
           };
-          const int done = __any_sync(0xffffffffu, edge_here) ? run(BoolTag<true>{}) : run(BoolTag<false>{});
-#pragma unroll 1
-          for (int q = 4 * done; q < 8; ++q) {
-            uint32_t x[8], w[4];
-            tmem_ld8(col + 8 * q, x);
-            tc_wait_ld_regs8(x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float t[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int32_t at = 8 * q + 2 * e + i;
-                t[i] = p.mod.cap_log2 * tanh_any(__uint_as_float(x[2 * e + i]) * p.mod.cap_in);
-                t[i] += fmaf(-slope, fabsf(static_cast<float>(key0 + at - pos)), -m);
-                if (at < lo || at >= hi) t[i] = -INFINITY;
-                t[i] = ex2(t[i]);
-              }
-              sum2[0] = f2_add(sum2[0], f2_pack(t[0], t[1]));
-              w[e] = pack_bf16x2(t[0], t[1]);
-            }
-            tmem_st4(col + 4 * q, w);
-          }
+          if (__any_sync(0xffffffffu, edge_here)) run(BoolTag<true>{});
+          else run(BoolTag<false>{});
           float a0, a1, a2, a3;
           f2_unpack(sum2[0], a0, a1);
           f2_unpack(sum2[1], a2, a3);

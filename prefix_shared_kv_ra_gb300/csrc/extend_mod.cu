@@ -4,9 +4,10 @@
 //
 // The masks are ranges of keys per row, so they act twice: in the work list, where an item (a query tile of a request) gets
 // only the keys that one of its rows sees -- a window of 1024 over a context of 3300 reads a third -- and in the kernel,
-// where tiles that lie inside every row's range are exponentiated without looking at it.  The cap itself is nine packed
-// instructions per pair of scores (score_mod.cuh) where the softmax warps wait on latencies most of the time: 612 us with
-// it, 603 without, 558 for the plain call (8 prompts of 700..1500 tokens over 0..2000 cached, 64/8 heads).
+// where tiles that lie inside every row's range are exponentiated without looking at it.  8 prompts of 700..1500 tokens
+// over 0..2000 cached ones, 64/8 heads (425 GFLOP, 223 us of the measured matrix rate): 435 us without a cap (the plain call
+// 559: its scores, three times as sharp as a model's at the start of training, send it back to its exact path), 602 with
+// one, where the softmax warps issue half of the time and their special function units are busy half of it.
 #include <algorithm>
 
 #include "api_common.h"

@@ -2,9 +2,12 @@
 //
 // A capped score is cap tanh(s / cap), wanted as t = cap log2(e) tanh(y) with y = s sm_scale / cap for the base-2
 // exponential.  The hardware's tanh is good to about 2^-11 only: at a score of 20 that is 1% of the weight, more than
-// the rounding of the weights to bf16.  For |y| <= 1.25 tanh(y) / y is taken as a polynomial of degree 6 in y^2 (a
-// minimax fit of the relative error, 7e-7 in fp32 arithmetic: at a score of 50, 4e-5 of the weight); it needs no special
-// function unit, which the exponential keeps busy.  Beyond, 1 - 2 / (e^2|y| + 1), whose cancellation is gone there.
+// the rounding of the weights to bf16.  Two forms of it are used:
+//  * 1 - 2 / (e^2y + 1), off by about 2^-22 everywhere: at a cap of 55 that is 2e-5 of a weight (the extend pass with a fixed
+//    reference, whose caps are that small);
+//  * for larger caps, and in decode, a polynomial of degree 6 in y^2 times y where |y| <= 1.25 (a minimax fit of the
+//    relative error, 7e-7 in fp32 arithmetic: at a score of 50, 4e-5 of the weight), and the first form beyond, where it
+//    no longer cancels.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -32,6 +35,7 @@ struct ScoreMod {
   float cap_in;              // sm_scale / cap (0: no cap)
   float cap_log2;            // cap log2(e)
   float2 in2;                  // pairs of equal values: cap_in, or sm_scale log2(e) without a cap;
+  float2 exp2y;                // 2 cap_in log2(e): 2^(s exp2y) = e^(2 y)
   float2 cap_poly[kCapTerms];  // cap log2(e) times the coefficients
 };
 

@@ -24,8 +24,9 @@ inline ra_status score_mod(ScoreMod* mod, float sm_scale, float score_cap, int32
     // beyond these the cap's products leave fp32 (and no score of one is anything but 0 or uncapped)
     RA_REQUIRE(score_cap >= 1e-6f && score_cap <= 1e12f, "score_cap must be in [1e-6, 1e12]");
     mod->cap_in = sm_scale / score_cap;
-    RA_REQUIRE(std::isfinite(mod->cap_in) && mod->cap_in > 1e-30f, "sm_scale / score_cap out of range");
+    RA_REQUIRE(mod->cap_in < 1e30f && mod->cap_in > 1e-30f, "sm_scale / score_cap out of range");
     mod->in2 = make_float2(mod->cap_in, mod->cap_in);
+    mod->exp2y = make_float2(2.f * mod->cap_in * kLog2e, 2.f * mod->cap_in * kLog2e);
     mod->cap_log2 = score_cap * kLog2e;
     for (int i = 0; i < kCapTerms; ++i) mod->cap_poly[i] = make_float2(mod->cap_log2 * cap_coef(i), mod->cap_log2 * cap_coef(i));
   }
