@@ -28,7 +28,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libra.so")
 # argument checks of the small operators (CPython API and torch's C++ tensors)
 BINDING = os.path.join(PKG, f"_ra_binding.{sysconfig.get_config_var('SOABI')}.torch{torch.__version__}.so")
-SOURCES = ["api_common.cu", "kv_store.cu", "decode.cu", "extend.cu", "extend_mod.cu", "decode_static.cu",
+SOURCES = ["api_common.cu", "kv_store.cu", "decode.cu", "decode_mod.cu", "extend.cu", "extend_mod.cu", "decode_static.cu",
            "kv8_store.cu", "decode_kv8.cu", "qk_norm_rope.cu", "tree.cu", "tree_narrow.cu", "tree_verify.cu",
            "step_slots.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

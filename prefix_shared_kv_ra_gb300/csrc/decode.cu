@@ -33,7 +33,6 @@
 #include "decode_internal.h"
 #include "decode_item.cuh"
 #include "ra_ptx.cuh"
-#include "score_mod_host.h"
 
 namespace ra {
 
@@ -61,9 +60,7 @@ constexpr float kDecodeRescale = 8.0f;  // log2 units: the decode softmax's refe
 // consumer warp is done with an item whose request goes through the combine, it makes the partials
 // visible device-wide (a gpu-scope fence) and adds one to the request's count, so the combine can merge
 // the request as soon as its count is complete -- the fence stays off the consumer warps' path.
-// With MOD (ra_decode_attention_mod) a request's keys begin at its own first one, and its scores may be capped and have
-// a bias by distance.
-template <int D, bool MOD>
+template <int D>
 __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1) decode_kernel(const DecodeParams p) {
   constexpr int KT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -135,7 +132,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1) de
       if (!mbar_wait(item0 + 8 * (n % kItemRing), (n / kItemRing) & 1)) return -1;
       const int32_t idx = s_items[n % kItemRing];
       if (idx < 0) return 0;
-      decode_item<MOD>(p, idx, it);
+      decode_item(p, idx, it);
       return 1;
     };
     auto load_slot = [&](const Item& it, int32_t s) -> int32_t {  // rows past the range repeat the last key
@@ -231,8 +228,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1) de
       if (idx < 0) break;
       if (lane == 0) {
         Item it;
-        decode_item<MOD>(p, idx, it);
-        if (!(it.n_splits == 1 && (MOD || it.start == 0))) {  // partials, merged by the combine
+        decode_item(p, idx, it);
+        if (!(it.n_splits == 1 && it.start == 0)) {  // partials, merged by the combine
           __threadfence();  // the consumers' partials (ordered before this by the done barrier) first
           atomicAdd(p.req_done + it.b, 1);
         }
@@ -265,18 +262,8 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1) de
       break;
     }
     Item it;
-    decode_item<MOD>(p, idx, it);
+    decode_item(p, idx, it);
     const int kh = it.hg * p.hpc + warp;
-    [[maybe_unused]] float slope0 = 0.f, slope1 = 0.f;  // of q heads 2 tq and 2 tq + 1, in log2 units
-    [[maybe_unused]] int32_t pos = 0;                   // the query's position
-    if constexpr (MOD) {
-      pos = min(__ldg(p.seq_lens + it.b), p.max_seq_len) - 1;
-      if (p.mod.slopes) {
-        const float* sl = p.mod.slopes + kh * p.group;
-        if (2 * tq < p.group) slope0 = __ldg(sl + 2 * tq) * kLog2e;
-        if (2 * tq + 1 < p.group) slope1 = __ldg(sl + 2 * tq + 1) * kLog2e;
-      }
-    }
     // Q^T fragments (B operand): column g is q head kh*G + g
     uint32_t qf[KT][2];
     {
@@ -312,33 +299,10 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1) de
       const int32_t kbase = it.k0 + s * kSlab;
       const bool v_lo = kbase + g < it.k1;
       const bool v_hi = kbase + g + 8 < it.k1;
-      float x0, x1, x2, x3;
-      if constexpr (MOD) {
-        x0 = s1[0] + s2[0], x1 = s1[1] + s2[1], x2 = s1[2] + s2[2], x3 = s1[3] + s2[3];
-        if (p.mod.cap_in > 0.f) {
-          const float y0 = x0 * p.mod.cap_in, y1 = x1 * p.mod.cap_in, y2 = x2 * p.mod.cap_in, y3 = x3 * p.mod.cap_in;
-          // (a vote: the general form costs two special functions a score)
-          const bool far = !(fmaxf(fmaxf(fabsf(y0), fabsf(y1)), fmaxf(fabsf(y2), fabsf(y3))) <= kCapPolyMax);
-          if (__any_sync(0xffffffffu, far)) {
-            x0 = tanh_any(y0), x1 = tanh_any(y1), x2 = tanh_any(y2), x3 = tanh_any(y3);
-          } else {
-            x0 = tanh_small(y0), x1 = tanh_small(y1), x2 = tanh_small(y2), x3 = tanh_small(y3);
-          }
-          x0 *= p.mod.cap_log2, x1 *= p.mod.cap_log2, x2 *= p.mod.cap_log2, x3 *= p.mod.cap_log2;
-        } else {
-          x0 *= p.scale_log2, x1 *= p.scale_log2, x2 *= p.scale_log2, x3 *= p.scale_log2;
-        }
-        const float far_lo = static_cast<float>(pos - (kbase + g)), far_hi = far_lo - 8.f;  // distances
-        x0 = v_lo ? fmaf(-slope0, far_lo, x0) : -INFINITY;
-        x1 = v_lo ? fmaf(-slope1, far_lo, x1) : -INFINITY;
-        x2 = v_hi ? fmaf(-slope0, far_hi, x2) : -INFINITY;
-        x3 = v_hi ? fmaf(-slope1, far_hi, x3) : -INFINITY;
-      } else {
-        x0 = v_lo ? (s1[0] + s2[0]) * p.scale_log2 : -INFINITY;
-        x1 = v_lo ? (s1[1] + s2[1]) * p.scale_log2 : -INFINITY;
-        x2 = v_hi ? (s1[2] + s2[2]) * p.scale_log2 : -INFINITY;
-        x3 = v_hi ? (s1[3] + s2[3]) * p.scale_log2 : -INFINITY;
-      }
+      const float x0 = v_lo ? (s1[0] + s2[0]) * p.scale_log2 : -INFINITY;
+      const float x1 = v_lo ? (s1[1] + s2[1]) * p.scale_log2 : -INFINITY;
+      const float x2 = v_hi ? (s1[2] + s2[2]) * p.scale_log2 : -INFINITY;
+      const float x3 = v_hi ? (s1[3] + s2[3]) * p.scale_log2 : -INFINITY;
       // Lazy reference: the running maximum moves (and O and l are rescaled) only when a score of the slab
       // exceeds it by more than kDecodeRescale, which a warp vote finds; otherwise the slab is exponentiated
       // against the reference as it stands (every p <= 2^kDecodeRescale).  The first slab of an item always
@@ -392,7 +356,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1) de
     const float inv0 = 1.f / l0, inv1 = 1.f / l1;
     const bool h0 = 2 * tq < p.group, h1 = 2 * tq + 1 < p.group;
     const int64_t bh0 = static_cast<int64_t>(it.b) * p.hq + kh * p.group + 2 * tq;
-    if (it.n_splits == 1 && (MOD || it.start == 0)) {
+    if (it.n_splits == 1 && it.start == 0) {
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) {
         const int d = mt * 16 + g;
@@ -450,7 +414,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kProducers + 1), 1) de
 // ceil(key_start / cchunk) prefix slots), the weights from warp shuffles, and the other rows kRows at a
 // time -- with multi-level groups, prefix rows only where a group wrote them (a finite log-sum-exp).
 // Partials are taken private first, then prefix, in chunks of 32 folded with a running maximum.
-template <int D, bool MOD>
+template <int D>
 __device__ __forceinline__ void merge_request_head(const DecodeParams& p) {
   constexpr int V = D / 32;
   constexpr int kRows = 8;
@@ -477,15 +441,6 @@ __device__ __forceinline__ void merge_request_head(const DecodeParams& p) {
   // no group wrote hold -inf: weight 0, skipped)
   const int32_t n_pre = start > 0 ? (p.casc_one_level ? (start + p.cchunk - 1) / p.cchunk : p.casc_slots) : 0;
   if (n_splits == 1 && n_pre == 0) return;  // written directly by the decode kernel
-  if constexpr (MOD) {
-    if (n_splits == 0) {  // the request sees no key
-#pragma unroll
-      for (int v = 0; v < V; v += 2)
-        *reinterpret_cast<__nv_bfloat162*>(p.o + static_cast<int64_t>(warp_global) * D + lane * V + v) =
-            __floats2bfloat162_rn(0.f, 0.f);
-      return;
-    }
-  }
   // wait for this request's partials: lane 0 polls; then every lane reads both counts itself and fences,
   // so that each lane's own loads of the partials follow an acquire of the counts it saw complete
   const int32_t expect = n_splits * p.n_hgroups;
@@ -570,10 +525,10 @@ __device__ __forceinline__ void merge_request_head(const DecodeParams& p) {
         __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
 }
 
-template <int D, bool MOD>
+template <int D>
 __global__ void __launch_bounds__(32 * kCombineWarps) decode_combine_kernel(const DecodeParams p) {
   griddep_launch();
-  merge_request_head<D, MOD>(p);
+  merge_request_head<D>(p);
   // every CTA waits before it leaves, so that this grid's completion implies the decode kernel's (and,
   // through it, the plan kernel's and the prefix pass's): the next kernel on the stream may rely on it
   griddep_wait();
@@ -638,6 +593,7 @@ __device__ __forceinline__ void scatter_new_rows(const DecodeParams& p, int64_t 
 // so the CTAs that finish last finish on short items.  One CTA of kPlanThreads threads; each thread owns
 // a contiguous run of requests.  It also resets the work counter.  With a fused store (and no groups)
 // CTAs 1.. of the grid scatter the step's new rows instead.
+// With MOD (ra_decode_attention_mod; no groups, no store) a request's keys begin at its own first one.
 template <bool MOD>
 __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeParams p) {
   if (!MOD && blockIdx.x > 0) {  // the fused store's CTAs (only without groups; CTA 0 plans)
@@ -780,9 +736,9 @@ __global__ void cascade_setup_kernel(const DecodeParams p, int32_t* ints, int32_
   }
 }
 
-template <int D, bool MOD>
+template <int D>
 ra_status launch_decode(const DecodeParams& p, int grid, int smem, cudaStream_t stream) {
-  auto kern = decode_kernel<D, MOD>;
+  auto kern = decode_kernel<D>;
   static int configured[64] = {};
   DeviceInfo dev;
   if (ra_status st = current_device(&dev)) return st;
@@ -795,7 +751,7 @@ ra_status launch_decode(const DecodeParams& p, int grid, int smem, cudaStream_t 
   if (ra_status st = launch_pdl("decode_kernel", kern, dim3(grid), dim3(32 * (p.hpc + kProducers + 1)), smem, stream, p))
     return st;
   const int nwarps = p.batch * p.hq;
-  return launch_pdl("decode_combine_kernel", decode_combine_kernel<D, MOD>, dim3((nwarps + kCombineWarps - 1) / kCombineWarps),
+  return launch_pdl("decode_combine_kernel", decode_combine_kernel<D>, dim3((nwarps + kCombineWarps - 1) / kCombineWarps),
                     dim3(32 * kCombineWarps), 0, stream, p);
 }
 
@@ -950,8 +906,7 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
                              const int32_t* group_reqs, const int32_t* group_prefix_start,
                              const int32_t* group_prefix_len, const int32_t* group_level,
                              int32_t max_group_prefix_len, int32_t max_group_size, int32_t max_group_levels,
-                             const ra::ScoreMod* mod, void* workspace, size_t workspace_bytes, uint32_t* device_error,
-                             ra_stream_t stream) {
+                             void* workspace, size_t workspace_bytes, uint32_t* device_error, ra_stream_t stream) {
   using namespace ra;
   const bool fused = k_new != nullptr || v_new != nullptr || out_cache_loc != nullptr;
   RA_REQUIRE(batch >= 0 && batch <= 65535, "batch must be in [0, 65535] (got %d)", batch);
@@ -1064,9 +1019,7 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
     if (ra_status st = launch_cascade_prefix(p, ca, head_dim, s, &p.prefix_ctas)) return st;
   }
   // (with groups the set-up kernel did the fused store: the plan kernel runs behind the prefix pass)
-  if (mod) p.mod = *mod;
-  if (ra_status st = mod ? launch_decode_plan_mod(p, s) : launch_decode_plan(p, num_groups > 0 ? 0 : store_ctas, s))
-    return st;
+  if (ra_status st = launch_decode_plan(p, num_groups > 0 ? 0 : store_ctas, s)) return st;
   // persistent decode geometry
   p.hpc = heads_per_cta(num_kv_heads);
   p.n_hgroups = num_kv_heads / p.hpc;
@@ -1080,8 +1033,7 @@ static ra_status decode_call(const void* k_pool, const void* v_pool, int64_t num
   DeviceInfo dev;
   if (ra_status st = current_device(&dev)) return st;
   const int grid = static_cast<int>(n_items < dev.num_sms ? n_items : dev.num_sms);
-  if (mod) return head_dim == 128 ? launch_decode<128, true>(p, grid, smem, s) : launch_decode<64, true>(p, grid, smem, s);
-  return head_dim == 128 ? launch_decode<128, false>(p, grid, smem, s) : launch_decode<64, false>(p, grid, smem, s);
+  return head_dim == 128 ? launch_decode<128>(p, grid, smem, s) : launch_decode<64>(p, grid, smem, s);
 }
 
 extern "C" ra_status ra_decode_attention(const void* k_pool, const void* v_pool, int64_t num_slots,
@@ -1099,24 +1051,8 @@ extern "C" ra_status ra_decode_attention(const void* k_pool, const void* v_pool,
   return decode_call(k_pool, v_pool, num_slots, num_kv_heads, head_dim, nullptr, nullptr, nullptr, q, o,
                      num_q_heads, sm_scale, req_to_token, table_stride, table_rows, req_pool_indices, seq_lens, batch,
                      max_seq_len, num_groups, group_indptr, group_reqs, group_prefix_start, group_prefix_len,
-                     group_level, max_group_prefix_len, max_group_size, max_group_levels, nullptr, workspace,
-                     workspace_bytes, device_error, stream);
-}
-
-extern "C" ra_status ra_decode_attention_mod(const void* k_pool, const void* v_pool, int64_t num_slots,
-                                             int32_t num_kv_heads, int32_t head_dim, const void* q, void* o,
-                                             int32_t num_q_heads, float sm_scale, float score_cap, int32_t window,
-                                             const float* slopes, const int32_t* first_key, const int32_t* req_to_token,
-                                             int64_t table_stride, int64_t table_rows, const int32_t* req_pool_indices,
-                                             const int32_t* seq_lens, int32_t batch, int32_t max_seq_len, void* workspace,
-                                             size_t workspace_bytes, uint32_t* device_error, ra_stream_t stream) {
-  ra::clear_error();
-  ra::ScoreMod mod{};
-  if (ra_status st = ra::score_mod(&mod, sm_scale, score_cap, window, slopes, first_key, nullptr)) return st;
-  return decode_call(k_pool, v_pool, num_slots, num_kv_heads, head_dim, nullptr, nullptr, nullptr, q, o, num_q_heads,
-                     sm_scale, req_to_token, table_stride, table_rows, req_pool_indices, seq_lens, batch, max_seq_len, 0,
-                     nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0, 1, &mod, workspace, workspace_bytes, device_error,
-                     stream);
+                     group_level, max_group_prefix_len, max_group_size, max_group_levels, workspace, workspace_bytes,
+                     device_error, stream);
 }
 
 extern "C" ra_status ra_decode_attention_store(void* k_pool, void* v_pool, int64_t num_slots, int32_t num_kv_heads,
@@ -1137,6 +1073,6 @@ extern "C" ra_status ra_decode_attention_store(void* k_pool, void* v_pool, int64
   return decode_call(k_pool, v_pool, num_slots, num_kv_heads, head_dim, k_new, v_new, out_cache_loc, q, o,
                      num_q_heads, sm_scale, req_to_token, table_stride, table_rows, req_pool_indices, seq_lens, batch,
                      max_seq_len, num_groups, group_indptr, group_reqs, group_prefix_start, group_prefix_len,
-                     group_level, max_group_prefix_len, max_group_size, max_group_levels, nullptr, workspace,
-                     workspace_bytes, device_error, stream);
+                     group_level, max_group_prefix_len, max_group_size, max_group_levels, workspace, workspace_bytes,
+                     device_error, stream);
 }
