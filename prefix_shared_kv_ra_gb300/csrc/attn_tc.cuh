@@ -320,31 +320,64 @@ __device__ __forceinline__ float bias_bound(int32_t first, int32_t end, int32_t 
   return -slope * static_cast<float>(slope >= 0.f ? near : far);
 }
 
-// Attention of one row with changed scores, by a warp: a key per lane for the scores, D / 32 dimensions per lane for the
-// values; its log2-sum-exp in lse.  For rows whose tensor-core result is not finite although values that are not finite may lie outside what the
-// row sees (a zero weight times such a value is a NaN in the product over a whole tile); slow and rare.  Lane l's
-// dimensions l * D / 32 .. in acc.
+// The offset of the K and V rows of a key of the item.
+template <int D>
+__device__ __forceinline__ int64_t key_row(const TcParams& p, const Job& jb, int32_t key) {
+  int32_t slot = __ldg(p.table + static_cast<int64_t>(jb.table_row) * p.table_stride + key);
+  if (slot < 0 || slot >= p.num_slots) slot = 0;
+  return (static_cast<int64_t>(slot) * p.hkv + jb.kh) * D;
+}
+
+// Whether V of a key in [from, to) of the item holds a value that is not finite (by a warp, a key per lane).
+template <int D>
+__device__ __forceinline__ bool odd_values(const TcParams& p, const Job& jb, int32_t from, int32_t to) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int32_t k0 = from; k0 < to; k0 += 32) {
+    const uint4* v = reinterpret_cast<const uint4*>(
+        p.v_pool + key_row<D>(p, jb, min(k0 + static_cast<int32_t>(threadIdx.x & 31), to - 1)));
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 x = __ldg(v + i);
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+    }
+  }
+  return __any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u);
+}
+
+// A row with changed scores whose tensor-core result cannot stand, or may not: `far` says that its sum left the range of its
+// reference; otherwise its output is not finite.  That is right if only values that it sees are not finite; a value that
+// it does not see gets there as well (a zero weight times it is a NaN in the product over a whole tile), and an
+// overflow.  True if the row was computed again, by the warp: a key per lane for the scores, D / 32 dimensions per lane
+// (l * D / 32 ..) for the values, its log2-sum-exp in lse.  Rare, and slow.
 template <int D, bool CAP>
-__device__ __forceinline__ void mod_row(const TcParams& p, const Job& jb, int64_t q_row, int32_t first, int32_t end,
+__device__ __forceinline__ bool mod_row(const TcParams& p, const Job& jb, bool far, int64_t q_row, int32_t first, int32_t end,
                                         int32_t pos, float slope, float (&acc)[D / 32], float& lse) {
   constexpr int V = D / 32;
+  if (!far && !odd_values<D>(p, jb, jb.kbeg, min(first, jb.kend)) && !odd_values<D>(p, jb, max(end, jb.kbeg), jb.kend) &&
+      odd_values<D>(p, jb, first, end))
+    return false;
   const int lane = threadIdx.x & 31;
-  const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>(p.q + q_row * D);
+  const uint4* q = reinterpret_cast<const uint4*>(p.q + q_row * D);
   float m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 1
   for (int32_t k0 = first; k0 < end; k0 += 32) {
     const int32_t key = min(k0 + lane, end - 1);
-    int32_t slot = __ldg(p.table + static_cast<int64_t>(jb.table_row) * p.table_stride + key);
-    if (slot < 0 || slot >= p.num_slots) slot = 0;
-    const int64_t row = (static_cast<int64_t>(slot) * p.hkv + jb.kh) * D;
-    const __nv_bfloat162* k = reinterpret_cast<const __nv_bfloat162*>(p.k_pool + row);
+    const int64_t row = key_row<D>(p, jb, key);
+    const uint4* k = reinterpret_cast<const uint4*>(p.k_pool + row);
     float s = 0.f;
 #pragma unroll 4
-    for (int d = 0; d < D / 2; ++d) {
-      const float2 a = __bfloat1622float2(q[d]), b = __bfloat1622float2(k[d]);
-      s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
+    for (int d = 0; d < D / 8; ++d) {
+      const uint4 a = __ldg(q + d), b = __ldg(k + d);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(aw[i] << 16), __uint_as_float(bw[i] << 16), s);
+        s = fmaf(__uint_as_float(aw[i] & 0xffff0000u), __uint_as_float(bw[i] & 0xffff0000u), s);
+      }
     }
     float x = CAP ? p.mod.cap_log2 * tanh_any(s * p.mod.cap_in) : s * p.scale_log2;
     x = k0 + lane < end ? fmaf(-slope, fabsf(static_cast<float>(pos - key)), x) : -INFINITY;
@@ -357,12 +390,13 @@ __device__ __forceinline__ void mod_row(const TcParams& p, const Job& jb, int64_
     l = l * alpha + w;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= alpha;
-#pragma unroll 1
-    for (int i = 0; i < 32 && k0 + i < end; ++i) {
+    // (lanes past the end hold the last key again, with weight 0)
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      const int64_t ri = __shfl_sync(0xffffffffu, row, i);
+      const __nv_bfloat16* vr = p.v_pool + __shfl_sync(0xffffffffu, row, i) + lane * V;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(wi, __bfloat162float(p.v_pool[ri + lane * V + v]), acc[v]);
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(wi, __bfloat162float(vr[v]), acc[v]);
     }
   }
 #pragma unroll
@@ -371,6 +405,7 @@ __device__ __forceinline__ void mod_row(const TcParams& p, const Job& jb, int64_
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] *= inv;
   lse = l == 0.f ? -INFINITY : m + __log2f(l);
+  return true;
 }
 
 }  // namespace tc
@@ -905,30 +940,35 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
       for (int c = 0; c < D / 64; ++c) tmem_ld32(col_o + c * 32, oa[c]);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) tc_wait_ld_regs(oa[c]);
-      // a result that is not finite may come from a value that this row does not see: it is handed on as a sum out of range
+      // whether the result is finite (bad: 0) goes to the other half with the sum
       float bad[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
 #pragma unroll
         for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(oa[c][e]), 0.f, bad[e & 3]);
-      l += (bad[0] + bad[1]) + (bad[2] + bad[3]);
+      bad[0] = (bad[0] + bad[1]) + (bad[2] + bad[3]);
       tmem_st1(col_o, __float_as_uint(l));
+      tmem_st1(col_o + 1, __float_as_uint(bad[0]));
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_join[ti]));
       const bool stuck = !mbar_wait(smem_u32(&bar_join[ti]), n & 1);
       if (__any_sync(0xffffffffu, stuck)) { ok = false; break; }
       tc_fence_after();
-      uint32_t other;
-      tmem_ld1(half == 0 ? col_o + D / 2 : col_o - D / 2, other);
+      const uint32_t col_other = half == 0 ? col_o + D / 2 : col_o - D / 2;
+      uint32_t other, other_bad;
+      tmem_ld1(col_other, other);
+      tmem_ld1(col_other + 1, other_bad);
       l += __uint_as_float(other);
       tc_fence_before();
       mbar_arrive(smem_u32(&bar_ofree[ti]));
-      const bool redo = row_valid && !(l >= kSumFloor && l <= kSumCeiling) && !(first >= lim && l == 0.f);
+      const bool far = first < lim && (l < kSumFloor || l > kSumCeiling);
+      // (where the sum is a NaN, from a score, so is the result)
+      const bool redo = row_valid && l == l && (far || !(bad[0] == 0.f && __uint_as_float(other_bad) == 0.f));
       const float inv_l = l == 0.f ? 0.f : 1.f / l;
       const int64_t row = (jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G);
       const int64_t part_row = (static_cast<int64_t>(jb.slot) * p.hkv + jb.kh) * p.part_rows + ti * kRows + r;
-      if (row_valid && !redo) {
+      if (row_valid) {
         if (jb.slot < 0) {
           uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + half * (D / 2));
 #pragma unroll
@@ -955,18 +995,24 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
           if (half == 0) p.part_lse[part_row] = m + __log2f(l);
         }
       }
-      for (uint32_t rows = half == 0 ? __ballot_sync(0xffffffffu, redo) : 0u; rows != 0; rows &= rows - 1) {
+      // such rows of the warp one by one, behind their own threads' stores, each half's columns by its own warp
+      for (uint32_t rows = __ballot_sync(0xffffffffu, redo); rows != 0; rows &= rows - 1) {
         const int src = __ffs(rows) - 1;
         const int64_t row1 = __shfl_sync(0xffffffffu, row, src), at = __shfl_sync(0xffffffffu, part_row, src);
         float y[D / 32], lse;
-        mod_row<D, true>(p, jb, row1, __shfl_sync(0xffffffffu, first, src), __shfl_sync(0xffffffffu, lim, src),
-                         __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, slope, src), y, lse);
+        if (!mod_row<D, true>(p, jb, __shfl_sync(0xffffffffu, far, src), row1, __shfl_sync(0xffffffffu, first, src),
+                              __shfl_sync(0xffffffffu, lim, src), __shfl_sync(0xffffffffu, pos, src),
+                              __shfl_sync(0xffffffffu, slope, src), y, lse))
+          continue;
+        __syncwarp();
+        if (lane >> 4 == half) {
 #pragma unroll
-        for (int v = 0; v < D / 32; ++v) {
-          if (jb.slot < 0) p.o[row1 * D + lane * (D / 32) + v] = __float2bfloat16_rn(y[v]);
-          else p.part_o[at * D + lane * (D / 32) + v] = y[v];
+          for (int v = 0; v < D / 32; ++v) {
+            if (jb.slot < 0) p.o[row1 * D + lane * (D / 32) + v] = __float2bfloat16_rn(y[v]);
+            else p.part_o[at * D + lane * (D / 32) + v] = y[v];
+          }
         }
-        if (jb.slot >= 0 && lane == 0) p.part_lse[at] = lse;
+        if (jb.slot >= 0 && half == 0 && lane == 0) p.part_lse[at] = lse;
       }
     }
     if (!ok) give_up();
@@ -1411,15 +1457,14 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
           }
         }
       };
-      // changed scores: a result that is not finite may come from a value that this row does not see, or from the reference
-      [[maybe_unused]] auto redo_row = [&](const uint32_t (&oa)[D / 32][32]) -> bool {
+      // changed scores: a result that is not finite (where the sum is: a NaN there comes from a score)
+      [[maybe_unused]] auto odd_row = [&](const uint32_t (&oa)[D / 32][32]) -> bool {
         float bad[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(oa[c][e]), 0.f, bad[e & 3]);
-        return row_valid && (!((bad[0] + bad[1]) + (bad[2] + bad[3]) == 0.f) ||
-                             (first < lim && !(l >= kSumFloor && l <= kSumCeiling)));
+        return row_valid && l == l && !((bad[0] + bad[1]) + (bad[2] + bad[3]) == 0.f);
       };
       [[maybe_unused]] bool redo = false;
       [[maybe_unused]] int64_t part_row = 0;
@@ -1427,7 +1472,7 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
         __nv_bfloat16* dst = p.o + ((jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G)) * static_cast<int64_t>(D);
         uint32_t oa[D / 32][32];
         load_o(oa);
-        if constexpr (MOD) redo = redo_row(oa);
+        if constexpr (MOD) redo = odd_row(oa);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t (&ov)[32] = oa[c];
@@ -1457,7 +1502,7 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
         float* dst = (TREE || MOD ? p.part_o : p.casc_o) + ps * D;
         uint32_t oa[D / 32][32];
         load_o(oa);
-        if constexpr (MOD) redo = redo_row(oa), part_row = ps;
+        if constexpr (MOD) redo = odd_row(oa), part_row = ps;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           const uint32_t (&ov)[32] = oa[c];
@@ -1474,13 +1519,16 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
         if (write) (TREE || MOD ? p.part_lse : p.casc_lse)[ps] = m_used + __log2f(l);
       }
       if constexpr (MOD) {
+        const bool far = row_valid && first < lim && (l < kSumFloor || l > kSumCeiling);
         // such rows of the warp one by one, behind their own threads' stores
-        for (uint32_t rows = __ballot_sync(0xffffffffu, redo); rows != 0; rows &= rows - 1) {
+        for (uint32_t rows = __ballot_sync(0xffffffffu, redo || far); rows != 0; rows &= rows - 1) {
           const int src = __ffs(rows) - 1;
           const int64_t row = __shfl_sync(0xffffffffu, (jb.q_tok0 + tok) * p.hq + jb.kh * G + (r % G), src);
           float y[D / 32], lse;
-          mod_row<D, CAP>(p, jb, row, __shfl_sync(0xffffffffu, first, src), __shfl_sync(0xffffffffu, lim, src),
-                          __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, slope, src), y, lse);
+          if (!mod_row<D, CAP>(p, jb, __shfl_sync(0xffffffffu, far, src), row, __shfl_sync(0xffffffffu, first, src),
+                               __shfl_sync(0xffffffffu, lim, src), __shfl_sync(0xffffffffu, pos, src),
+                               __shfl_sync(0xffffffffu, slope, src), y, lse))
+            continue;
           __syncwarp();
           const int64_t at = __shfl_sync(0xffffffffu, part_row, src);
 #pragma unroll

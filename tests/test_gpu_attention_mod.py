@@ -345,3 +345,39 @@ def test_pools_past_32_bits():
     one.k, one.v, one.table, one.rpi = c.k, c.v, c.table, c.rpi
     one.check(o)
     assert int(c.err) == 0 and int(one.err) == 0
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0, 200.0])
+@pytest.mark.parametrize("split", [False, True])
+def test_finite_dimensions_beside_values_that_are_not(cap, split):
+    """A visible V value that is not finite: its dimension is not finite, every other one within the bound; a row that sees
+    nothing gives 0 beside NaN; values whose products overflow behind capped weights do not."""
+    rng = np.random.default_rng(13)
+    n = 64 if split else 3000                               # few rows: split key ranges; many: whole ones
+    c = Case(rng, [500], [n], 8, 2, 128, cap=cap, sharp=2.0)
+    c.first = np.zeros(n, np.int64)
+    c.first[5:9] = 10 ** 6                                  # rows that see nothing
+    slots = torch.from_numpy(c.table[c.rpi[0]].astype(np.int64)).to(DEV)
+    clean = c.v.clone()
+    for value in (float("nan"), float("inf")):
+        c.v = clean.clone()
+        c.v[slots[7], 0, 11] = value                        # seen by all other rows
+        c.v[slots[500 + n - 1], 1, 64] = value              # seen by the last row only
+        o = f64(c.extend())
+        k, v = f64(c.k)[c.table[c.rpi[0], :500 + n]], f64(clean)[c.table[c.rpi[0], :500 + n]]
+        some = np.r_[0:40, n - 24:n]
+        ref, bound = M.attend(f64(c.q)[some], k, v, c.scale, 500 + some, cap, None, 0, c.first[some], 0)
+        hit = np.zeros(ref.shape, bool)
+        hit[:, :4, 11] = (c.first[some] == 0)[:, None]
+        hit[-1, 4:, 64] = True
+        assert not np.isfinite(o[some][hit]).any()
+        assert (np.abs(o[some] - ref) <= bound)[~hit].all()
+        assert not o[5:9].any()
+    c.v = clean.clone()
+    c.v[slots[:500], 1] = 2.0 ** 100                        # times weights of up to 2^43: past fp32
+    c.k[slots[:500], 1] = c.q[20, 4].sign() * 8.0
+    o = f64(c.extend())
+    k, v = f64(c.k)[c.table[c.rpi[0], :500 + n]], f64(c.v)[c.table[c.rpi[0], :500 + n]]
+    some = np.r_[0:5, 18:24]
+    ref, bound = M.attend(f64(c.q)[some], k, v, c.scale, 500 + some, cap)
+    assert np.isfinite(o[some]).all() and (np.abs(o[some] - ref) <= bound).all()
