@@ -22,6 +22,8 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanRun = 4;      // query tiles whose first keys a warp reads at once
+constexpr int kPlanLows = 4096;  // query tiles whose first key is kept
 constexpr int kPlanBins = 4096;  // key-tile counts above kPlanBins - 1 share the first bin
 constexpr int kModSms = 152;     // GB300; a constant, so that the workspace does not depend on the device
 constexpr int kSplitItems = 2 * kModSms;  // calls of fewer items (query tiles x kv heads) may split their key ranges, into
@@ -80,10 +82,17 @@ struct PlanArgs {
   uint32_t* err;
 };
 
-// One CTA lists the (request, query tile) pairs with their key ranges, most key tiles first (a counting sort).  A warp per
-// request: without first_key a lane per query tile, with it the lanes share a tile's tokens.
+// One CTA lists the (request, query tile) pairs with their key ranges, most key tiles first (a counting sort), in two
+// passes: the lengths of the ranges, then the list.  Without first_key a warp takes a request and its lanes the query tiles.
+// With it (DOCS) a lane takes a query tile, too, its warp reads the tiles' tokens together, four tiles in flight, and the
+// second pass finds the first pass's answers in shared memory.  (A warp per request there too, tile after tile, was 70 us of
+// an 81 us call of 7 requests of up to 1,749 tokens in documents of 129, 8/1 heads: now 13 of 31; 4 prompts of 2,000..4,095
+// tokens in documents of 611, 16/16 heads of 64, 96 -> 74.)  Two kernels: one for both cost the calls without first_key 1 to
+// 2 us of instruction fetches.
+template <bool DOCS>
 __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const PlanArgs a) {
   __shared__ int32_t s_bin[kPlanBins];
+  __shared__ int32_t s_low[DOCS ? kPlanLows : 1];  // the first keys of query tiles
   __shared__ int32_t s_warp[kPlanWarps], s_cost[kPlanWarps], s_chunk[kPlanWarps], s_nt[kSplitItems];
   __shared__ int32_t s_entries, s_longest, s_parts, s_merges;
   griddep_launch();  // the attention kernel may start its launch; it waits for this grid before reading the list
@@ -92,48 +101,110 @@ __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const Pla
   for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) s_bin[i] = 0;
   if (threadIdx.x == 0) s_entries = s_longest = s_parts = s_merges = 0;
   __syncthreads();
-  // f(b, tile, first key, end of keys) for every query tile of this warp's requests, called by one lane
-  auto for_tiles = [&](bool report, auto f) {
-    for (int b = warp; b < a.batch; b += kPlanWarps) {
-      int32_t E = __ldg(a.extend_lens + b);
-      const int32_t P = __ldg(a.prefix_lens + b);
-      if (E < 0 || E > a.max_extend_len || P < 0 || P > a.max_prefix_len) {
-        if (report && lane == 0) flag_error(a.err, RA_DEVERR_LENGTH);
-        E = min(max(E, 0), a.max_extend_len);  // the rows within the bound are still computed
-        if (P < 0 || P > a.max_prefix_len) continue;
-      }
-      if (static_cast<int64_t>(P) + E > a.table_stride) {
-        if (report && lane == 0) flag_error(a.err, RA_DEVERR_LENGTH);
-        continue;
-      }
-      const int32_t tiles = (E + a.tokens_per_cta - 1) / a.tokens_per_cta;
-      const int32_t full = a.full_lens ? min(__ldg(a.full_lens + b), P + E) : 0;
-      const int64_t q0 = __ldg(a.qo_indptr + b);
-      // (a request whose rows are not inside o is refused when its items are claimed; its keys are not looked up here)
-      const bool look = a.first_key != nullptr && q0 >= 0 && q0 + E <= a.total_q;
-      for (int32_t t0 = 0; t0 < tiles; t0 += look ? 1 : 32) {
-        const int32_t t = look ? t0 : t0 + lane;
-        const int32_t tok0 = t * a.tokens_per_cta, tok1 = min(E, tok0 + a.tokens_per_cta);
-        int32_t first = a.window > 0 ? max(P + tok0 - a.window + 1, 0) : 0;
-        if (look) {
-          int32_t low = INT32_MAX;
-          for (int32_t i = tok0 + lane; i < tok1; i += 32) {
-            const int32_t w = a.window > 0 ? P + i - a.window + 1 : 0;
-            low = min(low, max(w, __ldg(a.first_key + q0 + i)));
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, off));
-          first = max(low, 0);
+  // the lengths of request b; false: nothing of it can be listed
+  auto lengths = [&](int32_t b, bool report, int32_t& E, int32_t& P, int32_t& full) -> bool {
+    E = __ldg(a.extend_lens + b);
+    P = __ldg(a.prefix_lens + b);
+    full = a.full_lens ? __ldg(a.full_lens + b) : 0;
+    bool bad = E < 0 || E > a.max_extend_len, skip = P < 0 || P > a.max_prefix_len;
+    E = min(max(E, 0), a.max_extend_len);  // the rows within the bound are still computed
+    if (!skip && static_cast<int64_t>(P) + E > a.table_stride) skip = true;
+    if ((bad || skip) && report) flag_error(a.err, RA_DEVERR_LENGTH);
+    full = min(full, P + E);
+    return !skip;
+  };
+  // f(b, tile, first key, end of keys) for every query tile of this warp, called by one lane; at least one key, also where no
+  // row sees any: their rows are written
+  auto for_tiles = [&](bool list, auto f) {
+    if constexpr (!DOCS) {
+      for (int32_t b = warp; b < a.batch; b += kPlanWarps) {
+        int32_t E, P, full;
+        if (!lengths(b, !list && lane == 0, E, P, full)) continue;
+        const int32_t tiles = (E + a.tokens_per_cta - 1) / a.tokens_per_cta;
+        for (int32_t t = lane; t < tiles; t += 32) {
+          const int32_t tok0 = t * a.tokens_per_cta, end = max(P + min(E, tok0 + a.tokens_per_cta), full);
+          const int32_t first = a.window > 0 ? max(P + tok0 - a.window + 1, 0) : 0;
+          f(b, t, min(first, end - 1), end);
         }
-        const int32_t end = max(P + tok1, full);
-        // (at least one key, also where no row sees any: their rows are written)
-        if (t < tiles && (!look || lane == 0)) f(b, t, min(first, end - 1), end);
+      }
+    } else {
+      // 32 requests at a time, a lane reading each one's lengths, their query tiles numbered by a scan.  The groups of
+      // requests have equal shares of the warps and of s_low.
+      const int32_t groups = (a.batch + 31) / 32, share = max(1, kPlanWarps / groups), lows = kPlanLows / groups;
+      for (int32_t gr = warp / share; gr < groups; gr += kPlanWarps / share) {
+        const int32_t b0 = gr * 32;
+        int32_t E = 0, P = 0, full = 0, tiles = 0;
+        int64_t q0 = -1;
+        if (b0 + lane < a.batch) {
+          q0 = __ldg(a.qo_indptr + b0 + lane);
+          const bool listed = lengths(b0 + lane, !list && warp % share == 0, E, P, full);
+          // (a request of more rows than o has is refused when its items are claimed)
+          E = listed ? static_cast<int32_t>(min(static_cast<int64_t>(E), a.total_q)) : 0;
+          tiles = (E + a.tokens_per_cta - 1) / a.tokens_per_cta;
+        }
+        int32_t incl = tiles;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += y;
+        }
+        const int32_t count = __shfl_sync(0xffffffffu, incl, 31);
+        for (int32_t v = warp % share; v < count; v += share * 32) {
+          const int32_t u = v + lane * share;  // this lane's query tile
+          int32_t at = 0;  // its request's lane: those before it end at or before u
+#pragma unroll
+          for (int step = 16; step > 0; step >>= 1)
+            if (__shfl_sync(0xffffffffu, incl, at + step - 1) <= u) at += step;
+          const int32_t Eb = __shfl_sync(0xffffffffu, E, at), Pb = __shfl_sync(0xffffffffu, P, at);
+          const int64_t qb = __shfl_sync(0xffffffffu, q0, at);
+          const int32_t end_all = __shfl_sync(0xffffffffu, full, at);
+          const int32_t t = u - __shfl_sync(0xffffffffu, incl - tiles, at);
+          const bool live = u < count;
+          const int32_t tok0 = live ? t * a.tokens_per_cta : 0, tok1 = live ? min(Eb, tok0 + a.tokens_per_cta) : 0;
+          const bool known = list && u < lows;
+          int32_t low = live && known ? s_low[gr * lows + u] : 0;
+          if (__any_sync(0xffffffffu, live && !known)) {  // (for the whole warp: its lanes work together)
+            // (rows not inside o: the request is refused when its items are claimed, its keys are not looked up)
+            const int32_t n = live && !known && qb >= 0 && qb + Eb <= a.total_q ? tok1 - tok0 : 0;
+            // the tile's tokens, a lane each, their first keys of kPlanRun tiles in flight at once
+            for (int32_t i0 = 0; i0 < 32 && v + i0 * share < count; i0 += kPlanRun) {
+              int32_t first[kPlanRun];
+#pragma unroll
+              for (int e = 0; e < kPlanRun; ++e) first[e] = INT32_MAX;
+              const int32_t most = __reduce_max_sync(0xffffffffu, lane >= i0 && lane < i0 + kPlanRun ? n : 0);
+              for (int32_t i = lane; i < most + lane; i += 32) {
+                int32_t x[kPlanRun];
+#pragma unroll
+                for (int e = 0; e < kPlanRun; ++e) {
+                  const int32_t ne = __shfl_sync(0xffffffffu, n, i0 + e);
+                  const int64_t row = __shfl_sync(0xffffffffu, qb + tok0, i0 + e);
+                  x[e] = i < ne ? __ldg(a.first_key + row + i) : INT32_MAX;
+                }
+#pragma unroll
+                for (int e = 0; e < kPlanRun; ++e) {
+                  const int32_t p0 = __shfl_sync(0xffffffffu, Pb + tok0, i0 + e);
+                  if (a.window > 0 && x[e] < INT32_MAX) x[e] = max(x[e], p0 + i - a.window + 1);
+                  first[e] = min(first[e], x[e]);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < kPlanRun; ++e) {
+                const int32_t y = __reduce_min_sync(0xffffffffu, first[e]);
+                if (lane == i0 + e && n > 0) low = y;
+              }
+            }
+            low = max(low, 0);
+            if (live && !known && u < lows) s_low[gr * lows + u] = low;
+          }
+          const int32_t end = max(Pb + tok1, end_all);
+          if (live) f(b0 + at, t, min(low, end - 1), end);
+        }
       }
     }
   };
   auto tiles_of = [](int32_t first, int32_t end) { return (end - first + tc::kKeys - 1) / tc::kKeys; };
   auto bin_of = [](int32_t tiles) { return kPlanBins - 1 - min(tiles, kPlanBins - 1); };  // bin 0 = longest
-  for_tiles(true, [&](int32_t, int32_t, int32_t first, int32_t end) {
+  for_tiles(false, [&](int32_t, int32_t, int32_t first, int32_t end) {
     const int32_t nt = tiles_of(first, end), at = atomicAdd(&s_entries, 1);
     if (at < kSplitItems) s_nt[at] = nt;
     atomicMax(&s_longest, nt);
@@ -203,7 +274,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const Pla
   for (int e = 0; e < kPer; ++e) s_bin[threadIdx.x * kPer + e] = base + v[e];
   __syncthreads();
   griddep_wait();  // the previous kernel may be the previous call's, still claiming from this list and counter
-  for_tiles(false, [&](int32_t b, int32_t t, int32_t first, int32_t end) {
+  for_tiles(true, [&](int32_t b, int32_t t, int32_t first, int32_t end) {
     const int32_t nt = tiles_of(first, end), pieces = (nt + chunk - 1) / chunk;
     int32_t slot = -1;
     if (pieces > 1) {
@@ -367,7 +438,9 @@ extern "C" ra_status ra_extend_attention_mod(
   const PlanArgs a{extend_lens, prefix_lens, qo_indptr, batch,  max_extend_len, max_prefix_len, table_stride, total_q,
                    tokens_per_cta, first_key, full_lens, window, num_kv_heads,   ws,             device_error};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (ra_status st = launch_pdl("extend_mod_plan_kernel", extend_mod_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a))
+  if (ra_status st = launch_pdl("extend_mod_plan_kernel",
+                                first_key ? extend_mod_plan_kernel<true> : extend_mod_plan_kernel<false>, dim3(1),
+                                dim3(kPlanThreads), 0, s, a))
     return st;
   // at most sum_b ceil(E_b / tokens_per_cta) entries; CTAs past the listed count return at once
   const int64_t entries = std::min<int64_t>(

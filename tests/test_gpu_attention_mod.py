@@ -381,3 +381,28 @@ def test_finite_dimensions_beside_values_that_are_not(cap, split):
     some = np.r_[0:5, 18:24]
     ref, bound = M.attend(f64(c.q)[some], k, v, c.scale, 500 + some, cap)
     assert np.isfinite(o[some]).all() and (np.abs(o[some] - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("batch,longest", [(1, 8300), (70, 2870), (70, 301)])
+def test_documents_over_many_query_tiles(batch, longest):
+    """Two tokens a query tile: more tiles than the plan keeps first keys for, more requests than a warp has lanes, and
+    requests without new tokens among them."""
+    rng = np.random.default_rng(batch + longest)
+    E = rng.integers(0, 9, batch)
+    E[batch // 2] = longest
+    P = rng.integers(0, 20, batch)
+    c = Case(rng, P, E, 128, 1, 64, cap=20.0, doc=7, slopes=True)
+    o = c.extend()
+    assert c.err.item() == 0
+    k, v, q, o = f64(c.k), f64(c.v), f64(c.q), f64(o)
+    for b in range(batch):
+        slots = c.table[c.rpi[b], :P[b] + E[b]]
+        for at in range(0, P[b] + E[b], 70):  # whole documents: no row sees outside
+            pos = np.arange(max(at, P[b]), min(at + 70, P[b] + E[b]))
+            if len(pos) == 0:
+                continue
+            rows = c.qo[b] + pos - P[b]
+            keys = slots[at:at + 70]
+            ref, bound = M.attend(q[rows], k[keys], v[keys], c.scale, pos - at, c.cap, c.slopes, 0, c.first[rows] - at, 0)
+            bad = ~(np.abs(o[rows] - ref) <= bound)
+            assert not bad.any(), (b, at, np.argwhere(bad)[:4])
