@@ -16,6 +16,8 @@ explainer, §04; anrans handbook "v0.2：不到四千行的调度核心跑出 3.
   with kv_dtype="e4m3" the cache is a quantised pool: ra_kv8_store and ra_kv8_decode_attention, and for the
   extend call the slots of the admitted requests' contexts read back, each once, into bf16 rows of the step
   (ra_kv8_load);
+  with device_slots=True the slot ids reach the GPU once, as the step's free pages: ra_step_slots makes the table
+  entries, out_cache_loc, row starts and lengths from them, in the decode graph too;
 * completion: a finished turn is inserted into the tree (slots of positions another request
   inserted meanwhile are freed), unlocked, and its row released.
 
@@ -33,7 +35,7 @@ import numpy as np
 import torch
 
 from . import (ra_decode_attention, ra_decode_workspace_bytes, ra_extend_attention, ra_extend_workspace_bytes,
-               ra_kv8_decode_attention, ra_kv8_load, ra_kv8_slot_bytes, ra_kv8_store, ra_kv_store)
+               ra_kv8_decode_attention, ra_kv8_load, ra_kv8_slot_bytes, ra_kv8_store, ra_kv_store, ra_step_slots)
 from .radix import RadixCache, SlotPool
 
 __all__ = ["ServingReplay", "Request", "multiturn_chat", "run_chat"]
@@ -54,7 +56,7 @@ class Request:
 class ServingReplay:
     def __init__(self, *, num_slots: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_len: int,
                  max_running: int, device, seed: int = 0, graph_sizes: Sequence[int] = (8, 16, 32, 64, 128, 256),
-                 use_graphs: bool = True, kv_dtype: str = "bf16"):
+                 use_graphs: bool = True, kv_dtype: str = "bf16", device_slots: bool = False):
         if kv_dtype not in ("bf16", "e4m3"):
             raise ValueError(f"kv_dtype must be 'bf16' or 'e4m3' (got {kv_dtype!r})")
         self.dev = torch.device(device)
@@ -82,6 +84,7 @@ class ServingReplay:
         self.prefilled: List[int] = []   # rids past their prefill, in admission order
         self.finished: List[Request] = []
         self.use_graphs = use_graphs
+        self.device_slots = device_slots
         self.graph_sizes = sorted(graph_sizes)
         self._graphs: Dict[int, tuple] = {}
         self.stats = dict(steps=0, extend_tokens=0, decode_tokens=0, prompt_tokens=0, cached_tokens=0,
@@ -145,24 +148,35 @@ class ServingReplay:
                    loc=torch.zeros(bs, dtype=torch.int32, device=self.dev),
                    rpi=torch.full((bs,), self.pad_row, dtype=torch.int32, device=self.dev),
                    lens=torch.ones(bs, dtype=torch.int32, device=self.dev))
+        if self.device_slots:
+            for name, n in (("new", bs), ("pages", bs), ("count", 1), ("positions", bs), ("qo", bs + 1)):
+                buf[name] = torch.zeros(n, dtype=torch.int32, device=self.dev)
         buf["o"] = torch.empty_like(buf["q"])
         buf["ws"] = torch.empty(ra_decode_workspace_bytes(bs, self.hq, self.hkv, self.d, self.max_len),
                                 dtype=torch.uint8, device=self.dev)
 
         # `run` holds the tensors, not this object: a replay that goes out of use frees its graphs at once, and not
         # when the garbage collector finds a cycle (destroying a graph invalidates a capture under way)
-        table, hkv = self.table, self.hkv
+        table, hkv, device_slots = self.table, self.hkv, self.device_slots
         args = dict(max_seq_len=self.max_len, sm_scale=self.scale, workspace=buf["ws"], device_error=self.err)
+
+        def slots():
+            if device_slots:
+                ra_step_slots(table, buf["rpi"], buf["lens"], buf["new"], buf["pages"], buf["count"], buf["loc"],
+                              buf["positions"], buf["qo"], buf["lens"], device_error=args["device_error"])
+
         if self.kv8_pool is not None:
             pool = self.kv8_pool
 
             def run():
+                slots()
                 ra_kv8_store(pool, buf["k_new"], buf["v_new"], buf["loc"], device_error=args["device_error"])
                 ra_kv8_decode_attention(pool, buf["q"], buf["o"], table, buf["rpi"], buf["lens"], num_kv_heads=hkv, **args)
         else:
             k_pool, v_pool = self.k_pool, self.v_pool
 
             def run():
+                slots()
                 ra_kv_store(k_pool, v_pool, buf["k_new"], buf["v_new"], buf["loc"], device_error=args["device_error"])
                 ra_decode_attention(k_pool, v_pool, buf["q"], buf["o"], table, buf["rpi"], buf["lens"], **args)
         g = None
@@ -221,7 +235,8 @@ class ServingReplay:
             reserved += out_len
             slots = np.concatenate([hit, self._alloc(len(prompt) - hit.size)]).astype(np.int32)
             row = self.free_rows.pop()
-            self.table[row, :slots.size] = self._i32(slots)
+            held = hit.size if self.device_slots else slots.size  # (the rest: ra_step_slots)
+            self.table[row, :held] = self._i32(slots[:held])
             req = Request(rid, prompt, out_len, slots, row, node, int(hit.size))
             self.running[rid] = req
             admitted.append(req)
@@ -234,16 +249,23 @@ class ServingReplay:
             pre = np.array([r.cached for r in admitted], np.int32)
             total = int(ext.sum())
             loc = np.concatenate([r.slots[r.cached:] for r in admitted])
+            rows, pre_d, ext_d = self._i32([r.row for r in admitted]), self._i32(pre), self._i32(ext)
+            if self.device_slots:
+                loc_d, positions, lens = (torch.empty(k, dtype=torch.int32, device=self.dev)
+                                          for k in (total, total, len(admitted)))
+                qo = torch.empty(len(admitted) + 1, dtype=torch.int32, device=self.dev)
+                ra_step_slots(self.table, rows, pre_d, ext_d, self._i32(loc[::-1].copy()), self._i32([total]), loc_d,
+                              positions, qo, lens, device_error=self.err)
+            else:
+                loc_d, qo = self._i32(loc), self._i32(np.concatenate([[0], np.cumsum(ext)]))
             q = self._randn((total, self.hq, self.d))
-            self._store(self._randn((total, self.hkv, self.d)), self._randn((total, self.hkv, self.d)),
-                        self._i32(loc))
-            k_pool, v_pool, table, rows = self._extend_pool(admitted, self._i32([r.row for r in admitted]))
+            self._store(self._randn((total, self.hkv, self.d)), self._randn((total, self.hkv, self.d)), loc_d)
+            k_pool, v_pool, table, rows = self._extend_pool(admitted, rows)
             ws = torch.empty(ra_extend_workspace_bytes(len(admitted), total, self.hq, self.hkv), dtype=torch.uint8,
                              device=self.dev)
-            ra_extend_attention(k_pool, v_pool, q, torch.empty_like(q), table, rows, self._i32(pre), self._i32(ext),
-                                self._i32(np.concatenate([[0], np.cumsum(ext)])), max_extend_len=int(ext.max()),
-                                max_prefix_len=int(pre.max()), sm_scale=self.scale, workspace=ws,
-                                device_error=self.err)
+            ra_extend_attention(k_pool, v_pool, q, torch.empty_like(q), table, rows, pre_d, ext_d, qo,
+                                max_extend_len=int(ext.max()), max_prefix_len=int(pre.max()), sm_scale=self.scale,
+                                workspace=ws, device_error=self.err)
             self.stats["extend_tokens"] += total
         # ---- one decode token for every request past its prefill
         dec = [self.running[rid] for rid in self.prefilled]
@@ -257,12 +279,19 @@ class ServingReplay:
                 r.slots = np.concatenate([r.slots, new[k:k + 1]])
                 lens[k] = r.slots.size
             rows = self._i32([r.row for r in dec])
-            self.table[rows.long(), self._i32(lens - 1).long()] = self._i32(new)
+            if self.device_slots:
+                buf["pages"][:n] = self._i32(new[::-1].copy())  # taken from the end
+                buf["count"].fill_(n)
+                buf["new"].zero_()
+                buf["new"][:n] = 1
+                lens -= 1  # (of the tokens before: the call adds the new ones)
+            else:
+                self.table[rows.long(), self._i32(lens - 1).long()] = self._i32(new)
+                buf["loc"][:n] = self._i32(new)
+                buf["loc"][n:] = 0
             buf["q"][:n] = self._randn((n, self.hq, self.d))
             buf["k_new"][:n] = self._randn((n, self.hkv, self.d))
             buf["v_new"][:n] = self._randn((n, self.hkv, self.d))
-            buf["loc"][:n] = self._i32(new)
-            buf["loc"][n:] = 0
             buf["rpi"][:n] = rows
             buf["rpi"][n:] = self.pad_row
             buf["lens"][:n] = self._i32(lens)
