@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
       if (P < 0 || T < 0 || kept < 0 || kept > T || T > p.path_stride || static_cast<int64_t>(P) + T > p.table_stride ||
           first < 0 || static_cast<int64_t>(first) + T > p.total_q)
         bad |= RA_DEVERR_LENGTH;
+      // ra_step_slots gave a request that it had no pages for the dummy slot: that one must not reach the free list
+      if (!bad && T > 0 && __ldg(p.loc + first) <= 0) bad = RA_DEVERR_SLOT;
       if (bad) {
         if (first_cta) flag_error(p.err, bad);
         T = kept = 0;

@@ -243,3 +243,30 @@ def test_step_and_commit_in_a_graph():
     assert np.array_equal(host(table), t) and int(count) == c and np.array_equal(host(cur), lens)
     assert np.array_equal(host(free), f)
     assert sorted(set(host(free)[:c]) | set(t[t >= 0])) == list(range(1, 2001))   # no slot lost or doubled
+
+
+@pytest.mark.parametrize("pages", [0, 3, 9])
+def test_requests_without_slots_are_not_committed(pages):
+    """Too few free pages: the requests that got the dummy slot keep their lengths and rows, and it is not freed."""
+    B, T = 4, 3
+    table = i32(np.arange(B * 30).reshape(B, 30) + 100)
+    before = host(table)
+    rpi, cur, new = i32([2, 0, 3, 1]), i32([5, 0, 7, 20]), i32([T] * B)
+    free, count = i32(list(range(1, pages + 1)) + [-9] * (B * T - pages)), i32([pages])
+    loc, pos = (torch.full((B * T,), -7, dtype=torch.int32, device=DEV) for _ in range(2))
+    qo, seq = torch.zeros(B + 1, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ra.ra_step_slots(table, rpi, cur, new, free, count, loc, pos, qo, seq, device_error=err)
+    assert int(err) == ra.DEVERR_FULL
+    err.zero_()
+    ra.ra_tree_commit(table, rpi, cur, new, qo, loc, i32([[0, 2, -1]] * B), i32([2] * B), seq, free, count, device_error=err)
+    assert int(err) == ra.DEVERR_SLOT
+    placed = pages // T
+    assert int(count) == pages - 2 * placed
+    row = host(table)
+    held = [row[r, p:p + 2] for r, p in zip([2, 0, 3, 1][:placed], [5, 0, 7, 20])]
+    slots = np.concatenate(held + [host(free)[:int(count)]])
+    assert sorted(slots.tolist()) == list(range(1, pages + 1))
+    assert host(seq).tolist() == [n + (2 if b < placed else 0) for b, n in enumerate([5, 0, 7, 20])]
+    for b in range(placed, B):
+        assert np.array_equal(row[[2, 0, 3, 1][b]], before[[2, 0, 3, 1][b]])
