@@ -406,3 +406,16 @@ def test_documents_over_many_query_tiles(batch, longest):
             ref, bound = M.attend(q[rows], k[keys], v[keys], c.scale, pos - at, c.cap, c.slopes, 0, c.first[rows] - at, 0)
             bad = ~(np.abs(o[rows] - ref) <= bound)
             assert not bad.any(), (b, at, np.argwhere(bad)[:4])
+
+
+@pytest.mark.parametrize("shift", [16, 48])
+def test_workspaces_at_16_byte_boundaries(shift):
+    """Split ranges, so that partial rows are written; old bytes around the workspace stay."""
+    kw = dict(cap=30.0, slopes=True)
+    e, c = (Case(np.random.default_rng(shift), [900, 20], E, 16, 4, 128, **kw) for E in ([40, 3], [1, 1]))
+    for call, size in ((e.extend, ra.ra_extend_mod_workspace_bytes(2, e.total, 16, 4)),
+                       (c.decode, ra.ra_decode_workspace_bytes(2, 16, 4, 128, 901))):
+        big = torch.full((size + 128,), 0xA5, dtype=torch.uint8, device=DEV)
+        assert big.data_ptr() % 64 == 0
+        assert torch.equal(call(workspace=big[shift:shift + size]), call())
+        assert (big[:shift] == 0xA5).all() and (big[shift + size:] == 0xA5).all()
