@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
       }
     }
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float ref0 = 0.f, ref1 = 0.f;  // what is subtracted: m0 and m1, or 0 while every score is minus infinity
     float acc[KT][4];
 #pragma unroll
     for (int mt = 0; mt < KT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
                 x[b][3] > m1 + kRescale;
       }
       // Lazy reference: it moves, and O and l are rescaled, only when a score of the slab exceeds it by more than kRescale;
-      // an item's first slab always moves it (its first key is in range, so the maxima are finite).
+      // an item's first slab moves it (its first key is in range) unless every score there is minus infinity.
       if (__any_sync(0xffffffffu, above)) {
         float mx0 = m0, mx1 = m1;
 #pragma unroll
@@ -278,7 +279,9 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
         }
-        const float al0 = ex2(m0 - mx0), al1 = ex2(m1 - mx1);
+        ref0 = mx0 == -INFINITY ? 0.f : mx0;
+        ref1 = mx1 == -INFINITY ? 0.f : mx1;
+        const float al0 = ex2(m0 - ref0), al1 = ex2(m1 - ref1);
         m0 = mx0;
         m1 = mx1;
         l0 *= al0;
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float p0 = ex2(x[b][0] - m0), p1 = ex2(x[b][1] - m1), p2 = ex2(x[b][2] - m0), p3 = ex2(x[b][3] - m1);
+        const float p0 = ex2(x[b][0] - ref0), p1 = ex2(x[b][1] - ref1), p2 = ex2(x[b][2] - ref0), p3 = ex2(x[b][3] - ref1);
         l0 += p0 + p2;
         l1 += p1 + p3;
         // P^T as the B operand: transpose the two 8x8 key blocks
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(32 * (kMaxHeadsPerCta + kRingProducers + 1), 1
       l1 += __shfl_xor_sync(0xffffffffu, l1, off);
     }
     // outputs: thread holds (d = mt*16 + g [+8], q head 2*tq [+1]) of this kv head
-    const float inv0 = 1.f / l0, inv1 = 1.f / l1;
+    const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
     const bool direct = it.n_splits == 1;
     const int64_t r0 = (direct ? static_cast<int64_t>(it.b) : static_cast<int64_t>(it.d)) * p.hq + kh * p.group + 2 * tq;
 #pragma unroll

@@ -419,3 +419,24 @@ def test_workspaces_at_16_byte_boundaries(shift):
         assert big.data_ptr() % 64 == 0
         assert torch.equal(call(workspace=big[shift:shift + size]), call())
         assert (big[:shift] == 0xA5).all() and (big[shift + size:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("hidden", [1, 70, 600])
+def test_scores_of_minus_infinity(hidden, slopes):
+    """Keys that rows see with a score of minus infinity weigh nothing, also where a whole tile, slab or piece has no other."""
+    rng = np.random.default_rng(hidden)
+    e, c = (Case(rng, [700, 640], E, 8, 2, 64, slopes=slopes) for E in ([40, 3], [1, 1]))
+    for case, call in ((e, e.extend), (c, c.decode)):
+        case.q = (case.q.abs() + 0.125).to(BF)
+        for b in range(2):
+            case.k[torch.from_numpy(case.table[case.rpi[b], :hidden]).long().to(DEV)] = -float("inf")
+        o = f64(call())
+        assert int(case.err) == 0
+        k, v, q = f64(case.k), f64(case.v), f64(case.q)
+        for b in range(2):
+            P, E, q0 = int(case.P[b]), int(case.E[b]), int(case.qo[b])
+            slots = case.table[case.rpi[b], hidden:P + E]
+            ref, bound = M.attend(q[q0:q0 + E], k[slots], v[slots], case.scale, P + np.arange(E) - hidden, 0.0, case.slopes)
+            bad = ~(np.abs(o[q0:q0 + E] - ref) <= bound)
+            assert not bad.any(), (b, np.argwhere(bad)[:4])
