@@ -577,13 +577,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_greedy_kernel(const G
   launch_behind_writes();
 }
 
-// CTAs per request: 8 (the most that any GPU of the architecture runs as one cluster) unless a slice would be less than a
-// load or two per thread, or the requests then no longer run all at once, two CTAs an SM (64 trees of 16 drafts, drawn /
+// CTAs per request: 8 (the most that any GPU of the architecture runs as one cluster) unless a slice would be less than four
+// values per thread (64 trees of 16 drafts over 8,000 tokens, drawn / given / greedy: 12.3 / 8.6 / 14.7 us with 2 CTAs, 13.4 /
+// 9.5 / 15.0 with 4), or the requests then no longer run all at once, two CTAs an SM (64 trees of 16 drafts, drawn /
 // given / greedy, over 32,000 tokens: 12.5 / 9.9 / 17.7 us with 4 CTAs, 18.5 / 16.0 / 24.4 with 8 in two waves; over
 // 128,000: 34.2 / 14.1 / 25.4 and 31.7 / 19.5 / 25.9).
 int cluster_ctas(int32_t vocab, int32_t batch, int sms) {
   int c = kMaxCluster;
-  while (c > 1 && static_cast<int64_t>(vocab) < static_cast<int64_t>(c) * kThreads) c /= 2;
+  while (c > 1 && static_cast<int64_t>(vocab) < static_cast<int64_t>(c) * kThreads * 4) c /= 2;
   while (c > 1 && static_cast<int64_t>(batch) * c > 2 * sms) c /= 2;
   return c;
 }
