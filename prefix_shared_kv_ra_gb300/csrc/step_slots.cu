@@ -5,10 +5,11 @@
 // Both are exclusive sums over the requests followed by one store per token and array: 12 bytes a token, some hundred
 // kilobytes at most, so launches and latencies bound them, not HBM.  One launch each: a cluster of CTAs in which every
 // CTA scans all requests by itself (512 at a time; a request is four words) and then takes its share of the tokens,
-// finding a token's request by a binary search in the scanned starts.  Nothing is exchanged between the CTAs; the cluster
-// barrier only keeps the outputs that may be the inputs' own buffers (the lengths, the free list's count) from being
-// written before every CTA has read them, which a grid of independent CTAs could not do without a second launch.  Slots of
-// 65,000 new tokens of 32 requests in pages of 16: 9.9 us (0.8 MB, 0.1 us of HBM); 224 trees of 32..64 tokens committed: 6.2.
+// finding a token's request by a binary search in the scanned starts.  The cluster barrier keeps the outputs that may be the
+// inputs' own buffers (the lengths, the free list's count) from being written before every CTA has read them, which a grid
+// of independent CTAs could not do without a second launch; and the commit's CTAs share out the check of the paths.  Slots
+// of 65,000 new tokens of 32 requests in pages of 16: 9.9 us (0.8 MB, 0.1 us of HBM); 224 trees of 32..64 tokens committed:
+// 6.9, of which 0.7 are the check of the paths.
 #include "api_common.h"
 #include "ra_ptx.cuh"
 
@@ -19,15 +20,6 @@ namespace {
 constexpr int kThreads = 512;  // also the requests of one round of the scan
 constexpr int kMaxCluster = 8;
 constexpr int kRun = 4;        // consecutive tokens of a thread
-
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 
 // Let the next kernel launch, every write of this CTA visible to it: the attention calls' planning kernels read lengths,
 // which these kernels write, before they wait for the kernel before them.
@@ -274,37 +266,60 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
   __shared__ int32_t s_start[kThreads], s_prefix[kThreads], s_row[kThreads], s_kept[kThreads], s_len[kThreads],
       s_first[kThreads];
   __shared__ int64_t s_free[kThreads];
+  __shared__ uint32_t s_wrong[2][kThreads];  // flags of the requests whose paths are wrong, by the round's parity
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t rank = cluster_rank(), ctas = gridDim.x;
+  const bool first_cta = rank == 0;
+  s_wrong[0][t] = s_wrong[1][t] = 0;
+  cluster_arrive();  // (before the CTAs store into each other's shared memory)
   griddep_wait();
-  const int t = threadIdx.x;
-  const bool first_cta = cluster_rank() == 0;
   const int64_t worker = static_cast<int64_t>(blockIdx.x) * kThreads + t, workers = static_cast<int64_t>(gridDim.x) * kThreads;
   int64_t count = __ldg(p.free_count);
   if (count < 0 || count > p.free_capacity) {
     if (first_cta && t == 0) flag_error(p.err, RA_DEVERR_LENGTH);
     count = count < 0 ? 0 : p.free_capacity;
   }
+  cluster_wait();
   int64_t freed = 0;  // slots freed by the rounds before
   for (int32_t r0 = 0; r0 < p.batch; r0 += kThreads) {
     const int32_t b = r0 + t;
     const int n = min(kThreads, p.batch - r0);
+    uint32_t* wrong = s_wrong[r0 / kThreads & 1];
     int32_t P = 0, T = 0, kept = 0, row = 0, first = 0;
+    uint32_t bad = 0;
     if (b < p.batch) {
       P = p.prefix_lens[b];
       T = __ldg(p.draft_lens + b);
       kept = __ldg(p.accept_lens + b);
       row = __ldg(p.rpi + b);
       first = __ldg(p.qo_indptr + b);
-      uint32_t bad = 0;
       if (row < 0 || row >= p.table_rows) bad = RA_DEVERR_TABLE;
       if (P < 0 || T < 0 || kept < 0 || kept > T || T > p.path_stride || static_cast<int64_t>(P) + T > p.table_stride ||
           first < 0 || static_cast<int64_t>(first) + T > p.total_q)
         bad |= RA_DEVERR_LENGTH;
       // ra_step_slots gave a request that it had no pages for the dummy slot: that one must not reach the free list
       if (!bad && T > 0 && __ldg(p.loc + first) <= 0) bad = RA_DEVERR_SLOT;
-      if (bad) {
-        if (first_cta) flag_error(p.err, bad);
-        T = kept = 0;
+      if (bad) T = kept = 0;
+    }
+    s_kept[t] = kept;
+    s_len[t] = T;
+    __syncthreads();
+    // The paths, which what follows takes to ascend within the tree: each request's by a warp of one CTA, for all of them.
+    for (int r = static_cast<int>(rank + ctas * warp); r < n; r += static_cast<int>(ctas) * (kThreads / 32)) {
+      const int32_t* path = p.path + static_cast<int64_t>(r0 + r) * p.path_stride;
+      bool ascends = true;
+      for (int k = lane; k < s_kept[r]; k += 32) {
+        const int32_t node = __ldg(path + k), before = k > 0 ? __ldg(path + k - 1) : -1;
+        ascends = ascends && before < node && node < s_len[r];
       }
+      if (!__all_sync(0xffffffffu, ascends) && lane < ctas) st_cluster_b32(smem_u32(wrong + r), lane, RA_DEVERR_LENGTH);
+    }
+    cluster_sync_all();  // every CTA has read this round's lengths, and has the answers
+    bad |= wrong[t];
+    wrong[t] = 0;  // (for the round after the next)
+    if (bad) {
+      if (first_cta) flag_error(p.err, bad);
+      T = kept = 0;
     }
     int64_t end = T, gone = T - kept, all, all_gone;
     scan2(end, gone, all, all_gone);
@@ -312,15 +327,14 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
     s_prefix[t] = P;
     s_row[t] = row;
     s_kept[t] = kept;
-    s_len[t] = T;
     s_first[t] = first;
     s_free[t] = count + freed + gone - (T - kept);
-    cluster_sync_all();  // every CTA has read this round's lengths (and wrote its shared arrays)
+    __syncthreads();
     if (first_cta && b < p.batch) p.seq_out[b] = P + kept;
     for (int64_t i = worker; i < all; i += workers) {
       const int r = request_of(s_start, n, static_cast<int32_t>(i));
       const int32_t node = static_cast<int32_t>(i) - s_start[r];
-      // accepted nodes before this one: the path ascends, as a node's parent is before it
+      // accepted nodes before this one
       const int32_t* path = p.path + static_cast<int64_t>(r0 + r) * p.path_stride;
       int lo = 0, hi = s_kept[r];
       while (lo < hi) {
@@ -332,11 +346,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
       if (lo < s_kept[r] && __ldg(path + lo) == node) {
         out[lo] = slot;
       } else {
-        const int32_t nth = node - lo;
-        if (nth >= s_len[r] - s_kept[r]) {  // a path that does not ascend or leaves the tree
-          flag_error(p.err, RA_DEVERR_LENGTH);
-          continue;
-        }
+        const int32_t nth = node - lo;  // of the refused ones
         out[s_kept[r] + nth] = -1;
         const int64_t at = s_free[r] + nth;
         if (at < p.free_capacity) p.free_list[at] = slot;

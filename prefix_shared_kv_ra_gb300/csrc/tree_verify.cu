@@ -35,26 +35,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxTree = 1024;  // drafted tokens of a request
 
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // Let the next kernel launch, every write of this CTA visible to it (the planning kernels of the attention calls read
 // lengths before they wait for the kernel before them).
 __device__ __forceinline__ void launch_behind_writes() {
   __threadfence();
   __syncthreads();
   griddep_launch();
-}
-// Store 64 bits at this CTA's shared address `addr` of CTA `rank` of the cluster.
-__device__ __forceinline__ void st_cluster_b64(uint32_t addr, uint32_t rank, uint64_t v) {
-  uint32_t remote;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
 }
 
 // ---- unevaluated sums of two floats, |lo| at most half a last place of hi where they are results (error-free
