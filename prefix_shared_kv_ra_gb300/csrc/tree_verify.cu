@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
   __shared__ int32_t s_command, s_node, s_more, s_owner, s_who;
   __shared__ Pair s_part[kWarps];
   __shared__ Pair s_t, s_total, s_before, s_goal;
+  cluster_arrive();  // (waited for before the first store into another CTA's shared memory: it has to have started)
   griddep_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int32_t b = blockIdx.x / ctas;
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
   const int32_t T = request_rows(p.draft_lens, p.qo_indptr, b, p.max_draft, p.total_q, &first, p.err, rank == 0 && t == 0);
   if (T == 0) {  // (the whole cluster)
     if (rank == 0) nothing_verified(p.path, p.accept_lens, p.next_tokens, b, p.max_draft);
+    cluster_wait();
     launch_behind_writes();
     return;
   }
@@ -209,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const VerifyPa
   const int32_t v0 = static_cast<int32_t>(begin < p.vocab ? begin : p.vocab);
   const int32_t v1 = static_cast<int32_t>(begin + slice < p.vocab ? begin + slice : p.vocab);
   __syncthreads();
+  cluster_wait();
 
   const Pair kNone{0.f, 0.f}, kOne{1.f, 0.f};
   // The walk's state, in every lane of warp 0.
@@ -503,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_greedy_kernel(const G
   __shared__ uint64_t s_warp[kWarps];
   __shared__ uint64_t s_rank[2][kMaxCluster];
   __shared__ int32_t s_next, s_token;
+  cluster_arrive();  // (waited for before the first store into another CTA's shared memory: it has to have started)
   griddep_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int32_t b = blockIdx.x / ctas;
@@ -511,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_greedy_kernel(const G
   const int32_t T = request_rows(p.draft_lens, p.qo_indptr, b, p.max_draft, p.total_q, &first, p.err, rank == 0 && t == 0);
   if (T == 0) {  // (the whole cluster)
     if (rank == 0) nothing_verified(p.path, p.accept_lens, p.next_tokens, b, p.max_draft);
+    cluster_wait();
     launch_behind_writes();
     return;
   }
@@ -521,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_greedy_kernel(const G
     s_tree.parent[i] = child ? parent : -1;
     if (child && (x < 0 || x >= p.vocab) && rank == 0) flag_error(p.err, RA_DEVERR_VALUE);
   }
+  cluster_wait();
   int32_t node = 0, count = 0;
   for (int32_t pass = 0;; ++pass) {
     if (t == 0) s_path[count] = node;
