@@ -1254,6 +1254,7 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
                     alpha *= down;
                     sum2[0] = f2_mul(sum2[0], f2_pack(down, down));
                     sum2[1] = f2_mul(sum2[1], f2_pack(down, down));
+                    tc_wait_st();  // (what follows reads this tile's stores)
 #pragma unroll 1
                     for (int k = 0; k < 2 * c; ++k) {
                       uint32_t y[8];

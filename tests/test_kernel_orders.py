@@ -36,3 +36,12 @@ def test_stores_into_other_ctas_come_behind_a_cluster_barrier():
         # one wait on the way to the store, and one on every way out before it
         before = before.split("cluster_arrive();")[1]
         assert before.count("cluster_wait();") == before.count("return;") + 1, k
+
+
+def test_stored_weights_are_complete_before_they_are_read_back():
+    """Loads and stores of tensor memory are asynchronous: a raised reference scales weights that the same tile has stored."""
+    body = kernels()["attn_tc_kernel"]
+    loop = body.index("for (int k = 0; k < 2 * c; ++k)")
+    stores = [m.start() for m in re.finditer(r"tmem_st\d+\(", body) if m.start() < loop]
+    assert "tmem_ld8(" in body[loop:loop + 300]
+    assert "tc_wait_st();" in body[stores[-1]:loop]
