@@ -607,9 +607,12 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
   __shared__ int32_t s_hist[kRemBuckets];
   __shared__ unsigned long long s_total;
   // Without groups this is the call's first kernel: it lets the decode kernel launch at once (the decode
-  // kernel waits for this grid before its first claim) and plans from the call's inputs, which no kernel
-  // of this library writes, while the kernel before it finishes; it waits for that kernel only before its
-  // first write to the workspace (the kernel may be the previous call's combine, still reading it).
+  // kernel waits for this grid before its first claim) and plans from the call's lengths while the kernel before it
+  // finishes; it waits for that kernel only before its first write to the workspace (the kernel may be the previous call's
+  // combine, still reading it).  The lengths are there: of this library's kernels, those that write lengths (ra_step_slots,
+  // ra_tree_commit, ra_tree_verify) let the next kernel launch only behind fenced writes, and the first kernel of every other
+  // call either waits before it lets one launch or, as this one, is followed by a kernel of its own that does.  They are
+  // read through L2, where those writes are, and not through the read-only path.
   // With groups it runs behind the prefix pass, which let it launch only after the key starts were
   // complete; it does not wait for the pass, so that the decode kernel can run beside it.
   const bool behind_pass = !MOD && p.key_start != nullptr;
@@ -618,8 +621,8 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
   const int32_t per = (p.batch + kPlanThreads - 1) / kPlanThreads;
   const int32_t r0 = min(p.batch, t * per), r1 = min(p.batch, r0 + per);
   auto len_of = [&](int32_t b, bool report) -> int32_t {
-    const int32_t row = __ldg(p.rpi + b);
-    int32_t L = __ldg(p.seq_lens + b);
+    const int32_t row = __ldcg(p.rpi + b);
+    int32_t L = __ldcg(p.seq_lens + b);
     if (row < 0 || row >= p.table_rows || L < 1) {
       if (report) flag_error(p.err, (row < 0 || row >= p.table_rows) ? RA_DEVERR_TABLE : RA_DEVERR_LENGTH);
       return 0;

@@ -115,10 +115,10 @@ DecodeWorkspace layout_decode_workspace(int32_t batch, int32_t num_q_heads, int3
 
 // Point p's scratch members into a workspace of layout wl (p.batch set before).
 void bind_decode_workspace(DecodeParams& p, const DecodeWorkspace& wl, const DecodePlan& pl, void* workspace);
-// Changed scores: the first key that request b of L tokens sees, in [0, L].
+// Changed scores: the first key that request b of L tokens sees, in [0, L].  (Through L2: the plan reads it as it does the lengths.)
 __device__ __forceinline__ int32_t mod_start(const DecodeParams& p, int32_t b, int32_t L) {
   int32_t first = p.mod.window > 0 ? L - p.mod.window : 0;
-  if (p.mod.first_key) first = max(first, __ldg(p.mod.first_key + b));
+  if (p.mod.first_key) first = max(first, __ldcg(p.mod.first_key + b));
   return min(max(first, 0), L);
 }
 

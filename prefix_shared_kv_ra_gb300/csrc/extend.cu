@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int32_t
   __syncthreads();
   // a request's tiles, or 0 if its lengths are invalid (flagged here, once)
   auto tiles_of = [&](int b, int32_t& P, int32_t& E, bool report) -> int32_t {
-    E = __ldg(extend_lens + b);
-    P = __ldg(prefix_lens + b);
+    E = __ldcg(extend_lens + b);  // (through L2: see below)
+    P = __ldcg(prefix_lens + b);
     if (E < 0 || E > max_extend_len || P < 0 || P > max_prefix_len) {
       if (report) flag_error(err, RA_DEVERR_LENGTH);
       E = min(max(E, 0), max_extend_len);  // the rows within the bound are still computed
@@ -121,8 +121,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int32_t
 #pragma unroll
   for (int e = 0; e < kPer; ++e) s_bin[threadIdx.x * kPer + e] = base + v[e];
   __syncthreads();
-  // Everything above read only the call's inputs.  The writes below wait for the previous kernel: it may
-  // be the previous call's extend kernel on this workspace, still claiming from its list and counter.
+  // Everything above read only the call's lengths, which are there although the previous kernel may still run: kernels of
+  // this library that write lengths let the next one launch only behind fenced writes, and they are read through L2, where
+  // those are.  The writes below wait for the previous kernel: it may be the previous call's extend kernel on this
+  // workspace, still claiming from its list and counter.
   griddep_wait();
   for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
     int32_t P, E;

@@ -97,16 +97,17 @@ __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const Pla
   __shared__ int32_t s_warp[kPlanWarps], s_cost[kPlanWarps], s_chunk[kPlanWarps], s_nt[kSplitItems];
   __shared__ int32_t s_entries, s_longest, s_parts, s_merges;
   griddep_launch();  // the attention kernel may start its launch; it waits for this grid before reading the list
-  // (this grid waits for the previous one before its first write, so its completion implies that one's)
+  // (this grid waits for the previous one before its first write, so its completion implies that one's; the call's inputs
+  // that it reads before, it reads through L2: kernels that write lengths let this one launch behind their fenced writes)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) s_bin[i] = 0;
   if (threadIdx.x == 0) s_entries = s_longest = s_parts = s_merges = 0;
   __syncthreads();
   // the lengths of request b; false: nothing of it can be listed
   auto lengths = [&](int32_t b, bool report, int32_t& E, int32_t& P, int32_t& full) -> bool {
-    E = __ldg(a.extend_lens + b);
-    P = __ldg(a.prefix_lens + b);
-    full = a.full_lens ? __ldg(a.full_lens + b) : 0;
+    E = __ldcg(a.extend_lens + b);
+    P = __ldcg(a.prefix_lens + b);
+    full = a.full_lens ? __ldcg(a.full_lens + b) : 0;
     bool bad = E < 0 || E > a.max_extend_len, skip = P < 0 || P > a.max_prefix_len;
     E = min(max(E, 0), a.max_extend_len);  // the rows within the bound are still computed
     if (!skip && static_cast<int64_t>(P) + E > a.table_stride) skip = true;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const Pla
         int32_t E = 0, P = 0, full = 0, tiles = 0;
         int64_t q0 = -1;
         if (b0 + lane < a.batch) {
-          q0 = __ldg(a.qo_indptr + b0 + lane);
+          q0 = __ldcg(a.qo_indptr + b0 + lane);
           const bool listed = lengths(b0 + lane, !list && warp % share == 0, E, P, full);
           // (a request of more rows than o has is refused when its items are claimed)
           E = listed ? static_cast<int32_t>(min(static_cast<int64_t>(E), a.total_q)) : 0;
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_mod_plan_kernel(const Pla
                 for (int e = 0; e < kPlanRun; ++e) {
                   const int32_t ne = __shfl_sync(0xffffffffu, n, i0 + e);
                   const int64_t row = __shfl_sync(0xffffffffu, qb + tok0, i0 + e);
-                  x[e] = i < ne ? __ldg(a.first_key + row + i) : INT32_MAX;
+                  x[e] = i < ne ? __ldcg(a.first_key + row + i) : INT32_MAX;
                 }
 #pragma unroll
                 for (int e = 0; e < kPlanRun; ++e) {

@@ -45,3 +45,17 @@ def test_stored_weights_are_complete_before_they_are_read_back():
     stores = [m.start() for m in re.finditer(r"tmem_st\d+\(", body) if m.start() < loop]
     assert "tmem_ld8(" in body[loop:loop + 300]
     assert "tc_wait_st();" in body[stores[-1]:loop]
+
+
+def test_planning_kernels_read_lengths_through_l2():
+    """They read lengths before they wait for the kernel before them, which may have written them and still run."""
+    found = kernels()
+    for k in ("decode_plan_kernel", "extend_plan_kernel", "extend_mod_plan_kernel"):
+        assert "__ldcg(" in found[k] and "__ldg(" not in found[k], k
+    with open(os.path.join(CSRC, "decode_internal.h")) as f:
+        text = f.read()
+    start = text[text.index("int32_t mod_start("):]
+    assert "__ldg(" not in start[:start.index("}")]
+    # and those that write lengths let the next kernel launch behind a fence only
+    for k in ("step_slots_kernel", "tree_commit_kernel", "tree_verify_kernel", "tree_verify_greedy_kernel"):
+        assert "griddep_launch();" not in found[k] and "launch_behind_writes();" in found[k], k
