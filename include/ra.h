@@ -507,9 +507,9 @@ ra_status ra_tree_verify_greedy(const void* target_logits, int32_t logits_fp32, 
  *   that was returned (may be free_count itself).
  * No K/V row moves.  A request whose lengths are negative, beyond the table or path_stride (1 .. 1024), or with n > T,
  * whose rows are outside [0, total_q), or whose first n path entries do not ascend within 0 .. T - 1, is flagged
- * RA_DEVERR_LENGTH, one with a table row out of range RA_DEVERR_TABLE, one whose first drafted token has no slot (0, as
- * ra_step_slots gives where the free list is short) RA_DEVERR_SLOT, and all are skipped (seq_lens_out[b] = P, nothing
- * freed).  Slots that free_list (free_capacity entries) has no room for are flagged RA_DEVERR_FULL and lost.
+ * RA_DEVERR_LENGTH, one with a table row out of range RA_DEVERR_TABLE, one with a drafted token that has no slot
+ * (0, as ra_step_slots gives where the free list is short or holds a wrong page id, or below) RA_DEVERR_SLOT, and all are
+ * skipped (seq_lens_out[b] = P, nothing freed).  Slots that free_list (free_capacity entries) has no room for are flagged RA_DEVERR_FULL and lost.
  */
 ra_status ra_tree_commit(int32_t* req_to_token, int64_t table_stride, int64_t table_rows,
                          const int32_t* req_pool_indices, const int32_t* prefix_lens, const int32_t* draft_lens,

@@ -7,9 +7,9 @@
 // CTA scans all requests by itself (512 at a time; a request is four words) and then takes its share of the tokens,
 // finding a token's request by a binary search in the scanned starts.  The cluster barrier keeps the outputs that may be the
 // inputs' own buffers (the lengths, the free list's count) from being written before every CTA has read them, which a grid
-// of independent CTAs could not do without a second launch; and the commit's CTAs share out the check of the paths.  Slots
-// of 65,000 new tokens of 32 requests in pages of 16: 9.9 us (0.8 MB, 0.1 us of HBM); 224 trees of 32..64 tokens committed:
-// 6.9, of which 0.7 are the check of the paths.
+// of independent CTAs could not do without a second launch; and the commit's CTAs share out the check of the paths and
+// slots.  Slots of 65,000 new tokens of 32 requests in pages of 16: 9.9 us (0.8 MB, 0.1 us of HBM); 224 trees of
+// 32..64 tokens committed: 7.2, of which 1 is the check.
 #include "api_common.h"
 #include "ra_ptx.cuh"
 
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
   __shared__ int32_t s_start[kThreads], s_prefix[kThreads], s_row[kThreads], s_kept[kThreads], s_len[kThreads],
       s_first[kThreads];
   __shared__ int64_t s_free[kThreads];
-  __shared__ uint32_t s_wrong[2][kThreads];  // flags of the requests whose paths are wrong, by the round's parity
+  __shared__ uint32_t s_wrong[2][kThreads];  // flags of the requests whose paths or slots are wrong, by the round's parity
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint32_t rank = cluster_rank(), ctas = gridDim.x;
   const bool first_cta = rank == 0;
@@ -297,22 +297,29 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
       if (P < 0 || T < 0 || kept < 0 || kept > T || T > p.path_stride || static_cast<int64_t>(P) + T > p.table_stride ||
           first < 0 || static_cast<int64_t>(first) + T > p.total_q)
         bad |= RA_DEVERR_LENGTH;
-      // ra_step_slots gave a request that it had no pages for the dummy slot: that one must not reach the free list
-      if (!bad && T > 0 && __ldg(p.loc + first) <= 0) bad = RA_DEVERR_SLOT;
       if (bad) T = kept = 0;
     }
     s_kept[t] = kept;
     s_len[t] = T;
+    s_first[t] = first;
     __syncthreads();
-    // The paths, which what follows takes to ascend within the tree: each request's by a warp of one CTA, for all of them.
+    // The paths, which what follows takes to ascend within the tree, and the slots: ra_step_slots gives a request that it has no
+    // pages for, and a token whose page id is wrong, the dummy slot, which must not reach the free list.  Each request's by a
+    // warp of one CTA, for all of them.
     for (int r = static_cast<int>(rank + ctas * warp); r < n; r += static_cast<int>(ctas) * (kThreads / 32)) {
-      const int32_t* path = p.path + static_cast<int64_t>(r0 + r) * p.path_stride;
-      bool ascends = true;
-      for (int k = lane; k < s_kept[r]; k += 32) {
-        const int32_t node = __ldg(path + k), before = k > 0 ? __ldg(path + k - 1) : -1;
-        ascends = ascends && before < node && node < s_len[r];
+      const int32_t *path = p.path + static_cast<int64_t>(r0 + r) * p.path_stride, *loc = p.loc + s_first[r];
+      bool ascends = true, placed = true;
+      const int32_t len = s_len[r], kept = s_kept[r];
+#pragma unroll 2
+      for (int k = lane; k < len; k += 32) {
+        const int32_t slot = __ldg(loc + k);
+        const int32_t node = k < kept ? __ldg(path + k) : k, before = k < kept && k > 0 ? __ldg(path + k - 1) : -1;
+        placed &= slot > 0;
+        ascends &= before < node && node < len;
       }
-      if (!__all_sync(0xffffffffu, ascends) && lane < ctas) st_cluster_b32(smem_u32(wrong + r), lane, RA_DEVERR_LENGTH);
+      const uint32_t flags = (__all_sync(0xffffffffu, ascends) ? 0u : RA_DEVERR_LENGTH) |
+                             (__all_sync(0xffffffffu, placed) ? 0u : RA_DEVERR_SLOT);
+      if (flags && lane < ctas) st_cluster_b32(smem_u32(wrong + r), lane, flags);
     }
     cluster_sync_all();  // every CTA has read this round's lengths, and has the answers
     bad |= wrong[t];
@@ -327,7 +334,6 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
     s_prefix[t] = P;
     s_row[t] = row;
     s_kept[t] = kept;
-    s_first[t] = first;
     s_free[t] = count + freed + gone - (T - kept);
     __syncthreads();
     if (first_cta && b < p.batch) p.seq_out[b] = P + kept;

@@ -37,7 +37,7 @@ class Trees:
         self.held = held  # entries in the list before the call
         self.err = torch.zeros(1, dtype=torch.int32, device=DEV)
 
-    def check(self, wrong):
+    def check(self, wrong, flags=ra.DEVERR_LENGTH):
         """Requests `wrong` are flagged and skipped, the others committed."""
         big = np.full(2 * GUARD + self.held + self.total, -5, np.int32)
         big[GUARD:GUARD + self.held] = 1 + np.arange(self.held)
@@ -51,7 +51,7 @@ class Trees:
         good = [b for b in range(self.B) if b not in wrong]
         ref = R.commit(self.table, self.rpi[good], self.prefix[good], self.drafts[good], self.qo[good], self.loc,
                        self.path[good], self.accepted[good], big[GUARD:GUARD + self.held + self.total], self.held)
-        assert int(self.err) == (ra.DEVERR_LENGTH if wrong else 0)
+        assert int(self.err) == (flags if wrong else 0)
         assert np.array_equal(host(table), ref[0])
         big[GUARD:GUARD + self.held + self.total] = ref[1]
         assert np.array_equal(host(words), big)
