@@ -392,8 +392,9 @@ size_t ra_tree_workspace_bytes(int32_t batch, int64_t total_q, int32_t num_q_hea
  *   with slopes: s <- s - slopes[h] * |p - j|;
  *   j is seen when j >= first and (j <= p or j < full), where first = max(first_key, p - window + 1, 0) (without the terms
  *   that are not given) and full = min(full_lens[b], prefix_lens[b] + extend_lens[b]) (0 if not given).
- * A row that sees no key gives 0.  What a row does not see has no influence on it, whatever it is (also infinities and
- * NaN); an infinity or NaN in V of a key that it sees makes that dimension infinite or NaN.
+ * A row that sees no key, or none with a score above minus infinity, gives 0.  What a row does not see has no influence
+ * on it, whatever it is (also infinities and NaN); an infinity or NaN in V of a key that it sees makes that dimension
+ * infinite or NaN.
  *   score_cap:  0 (none), or 1e-6 .. 1e12.
  *   window:     0 (none), or the number of keys up to its own that a row sees at most.
  *   slopes:     fp32 [num_q_heads], or NULL.

@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) decode_mod_combine_kernel(
         load_row_part<kRowLanes, V>(p.part_o + (static_cast<int64_t>(i0 + s) * p.hq + h) * D, sub, x);
       },
       acc, wsum);
-  if (n != 0) store_row_part<kRowLanes, V>(p.o + static_cast<int64_t>(bh) * D, sub, acc, n < 0 ? 0.f : 1.f / wsum);
+  // (no weight: no key, or none with a score above minus infinity)
+  if (n != 0) store_row_part<kRowLanes, V>(p.o + static_cast<int64_t>(bh) * D, sub, acc, wsum == 0.f ? 0.f : 1.f / wsum);
   griddep_wait();  // this grid's completion implies the decode kernel's
 }
 
@@ -427,12 +428,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
   __syncthreads();
   if (n != 0 && share == 0) {
     join_shares<V>(per_row, warp, s_acc, s_m, s_w, acc, wsum);
-    const float inv = n < 0 ? 0.f : 1.f / wsum;
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;  // (no key, or none with a score above minus infinity)
     __nv_bfloat16* dst = p.o + static_cast<int64_t>(bh) * D + lane * V;
 #pragma unroll
     for (int v = 0; v < V; v += 2)
-      *reinterpret_cast<__nv_bfloat162*>(dst + v) =
-          n < 0 ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+      *reinterpret_cast<__nv_bfloat162*>(dst + v) = __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
   }
   griddep_wait();  // this grid's completion implies the decode kernel's
 }
