@@ -173,11 +173,11 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(const StepParams p
       int32_t prev = 0;
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
-        const int32_t i = static_cast<int32_t>(i0) + k;
         slot[k] = 0;
         id[k] = INT32_MIN;
         row[k] = nullptr;
-        if (i >= stop) continue;
+        if (i0 + k >= stop) continue;  // (in 64 bits: the last run may end behind 2^31)
+        const int32_t i = static_cast<int32_t>(i0 + k);
         while (i >= next) {  // (over requests without new tokens)
           ++r;
           next = r + 1 < n ? s_start[r + 1] : INT32_MAX;
