@@ -1120,8 +1120,8 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
           //   t = cap log2(e) tanh(y) - slope |pos - key| - reference, y = s sm_scale / cap; or s sm_scale log2(e) - ...
           // Up to the row's position the bias is linear in the key: it and the reference are one addend, stepped along the
           // columns.  The reference only has to keep weights and sums in range (2^60 weighs as exactly as 1 in bf16 and
-          // fp32): it is the largest of the row's first 16 scores with the largest bias that any of its keys has (with the
-          // first keys' bias, far away, it would have to move in every tile).  It is raised by whole powers of two: between
+          // fp32): it is the largest of the row's first scores, up to 16, with the largest bias that any of its keys has (with
+          // the first keys' bias, far away, it would have to move in every tile).  It is raised by whole powers of two: between
           // tiles when the sum has grown, and within one when a chunk's sum leaves the range, which scales what the tile has
           // stored so far.  That and scores beyond the polynomial's range take a chunk through a loop of its own, from S, 8
           // columns at a time.  A row whose whole sum is too small for its reference is done again in the epilogue.
@@ -1133,15 +1133,22 @@ __global__ void __launch_bounds__(tc::Roles<PASS>::kThreads, 1)
           } else {
             const int32_t lo = first - key0, hi = lim - key0;  // this row's columns: [lo, hi)
             if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-              uint32_t x[16];
-              tmem_ld16(tmem + lane_addr + col_s, x);
-              tc_wait_ld_regs16(x);
+              // 16 columns at a time, those in which a row without a reference begins
+              const bool wants = m_used == -INFINITY && sees;
               float top = -INFINITY;
+              int c = __reduce_min_sync(0xffffffffu, wants ? max(lo, 0) & ~15 : kKeys);
+#pragma unroll 1
+              while (c < kKeys) {
+                uint32_t x[16];
+                tmem_ld16(tmem + lane_addr + col_s + c, x);
+                tc_wait_ld_regs16(x);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) top = fmaxf(top, e >= lo && e < hi ? __uint_as_float(x[e]) : -INFINITY);
-              if (top == -INFINITY) top = 0.f;  // (the row's keys begin behind these columns)
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, c + e >= lo && c + e < hi ? __uint_as_float(x[e]) : -INFINITY);
+                c = __reduce_min_sync(0xffffffffu, wants && lo >= c + 16 ? lo & ~15 : kKeys);
+              }
+              if (top == -INFINITY) top = 0.f;  // (so are the scores that were looked at)
               else top = CAP ? p.mod.cap_log2 * tanh_any(top * p.mod.cap_in) : top * p.scale_log2;
-              if (m_used == -INFINITY && sees) m_ref = top + bias_bound(first, lim, pos, slope);
+              if (wants) m_ref = top + bias_bound(first, lim, pos, slope);
             }
             if (__any_sync(0xffffffffu, l > kRaiseSum)) {
               const float up = l > kRaiseSum ? static_cast<float>(static_cast<int32_t>(__float_as_uint(l) >> 23) - 127) : 0.f;
