@@ -467,7 +467,8 @@ ra_status ra_step_slots(int32_t* req_to_token, int64_t table_stride, int64_t tab
  * From the node where every child was refused (or that has none), next_tokens[b] is drawn from the residual
  * r(v) = max(p(v) - t q(v), 0), or r: the smallest v with sum_{j <= v} r(j) > final_uniforms[b] sum_j r(j) (from p
  * where nothing is left of r).  Rows of p and q are taken as normalised; negative values and NaN count as 0.  Sums
- * and comparisons are held to about 2^-45.
+ * and comparisons are held to about 2^-45 of 1, the size of a row's sum: S, a difference of such sums, to about 2^-45 / S of
+ * itself, and what is compared with it or drawn from the residual likewise.
  *   target_probs, draft_probs: fp32 [total_q, vocab], rows at target_stride / draft_stride values (>= vocab).
  *   accept_uniforms: fp32 [total_q]; final_uniforms: fp32 [batch]; in [0, 1).
  *   path:        int32 [batch, max_draft_len]: the accepted nodes, ascending from node 0; -1 behind them.

@@ -6,8 +6,8 @@
 // kilobytes at most, so launches and latencies bound them, not HBM.  One launch each: a cluster of CTAs in which every
 // CTA scans all requests by itself (512 at a time; a request is four words) and then takes its share of the tokens,
 // finding a token's request by a binary search in the scanned starts.  The cluster barrier keeps the outputs that may be the
-// inputs' own buffers (the lengths, the free list's count) from being written before every CTA has read them, which a grid
-// of independent CTAs could not do without a second launch; and the commit's CTAs share out the check of the paths and
+// inputs' own buffers (the lengths, the free list's count) from being written before every CTA has read them, for which a
+// grid of independent CTAs would need a second launch; and the commit's CTAs share out the check of the paths and
 // slots.  Slots of 65,000 new tokens of 32 requests in pages of 16: 9.9 us (0.8 MB, 0.1 us of HBM); 224 trees of
 // 32..64 tokens committed: 7.2, of which 1 is the check.
 #include "api_common.h"

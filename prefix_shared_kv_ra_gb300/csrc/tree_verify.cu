@@ -14,13 +14,13 @@
 //
 // Precision: the drawn token is a whole number that depends on where u S falls between neighbouring prefix sums, as little
 // as 1e-9 apart at a vocabulary of 100,000; fp32 sums would move one draw in hundreds.  p - t q, the sums and what they are
-// compared with are held as pairs of floats (unevaluated sums, about 2^-45 relative) in the fp32 pipe: this GPU's 64-bit
+// compared with are held as pairs of floats (unevaluated sums, about 2^-45 of a whole row's) in the fp32 pipe: this GPU's 64-bit
 // rate is two values a clock and SM, and even the few scans and comparisons of a draw took 5 us of a call in it.
 //
 // Bound: the rows read, once each (a pass over 64 pairs of rows of 128,000 is 66 MB, 10 us of HBM), and for few requests
-// the chain of gather, pass and search, about 1.5 us each.  64 trees of 8..16 drafts drawn from q over 128,000 tokens: 34 us,
-// the time of the requests with the most refusals; 64 greedy trees of 32..64: 38, that of the longest accepted paths (11
-// rows one after another, 3.4 us each); 4 trees of given drafts: 7.
+// the chain of gather, pass and search, about 1.5 us each.  64 trees of 8..16 drafts drawn from q over 128,000 tokens: 33 to
+// 38 us by the draw, the time of the requests with the most refusals; 64 greedy trees of 32..64: 40 to 46 (logits in fp32
+// 50), that of the longest accepted paths (11 rows one after another, 3.4 us each); 4 trees of given drafts: 7.
 #include <cuda_bf16.h>
 
 #include "api_common.h"
