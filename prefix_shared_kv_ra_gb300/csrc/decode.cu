@@ -640,7 +640,11 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
   if (t < kRemBuckets) s_hist[t] = 0;
   __syncthreads();
   unsigned long long tot = 0;
-  for (int32_t b = r0; b < r1; ++b) tot += static_cast<unsigned long long>(len_of(b, true));
+  // (the length of the thread's first request stays in a register: with up to kPlanThreads requests, all are read once)
+  const int32_t first_len = r0 < r1 ? len_of(r0, true) : 0;
+  auto len_again = [&](int32_t b) { return b == r0 ? first_len : len_of(b, false); };
+  tot += static_cast<unsigned long long>(first_len);
+  for (int32_t b = r0 + 1; b < r1; ++b) tot += static_cast<unsigned long long>(len_of(b, true));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, off);
   if ((t & 31) == 0) atomicAdd(&s_total, tot);
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
   // item counts (all, full-chunk) of this thread's requests, scanned over the block
   int32_t cnt = 0, full = 0;
   for (int32_t b = r0; b < r1; ++b) {
-    const int32_t len = len_of(b, false);
+    const int32_t len = len_again(b);
     cnt += (len + chunk - 1) / chunk;
     full += len / chunk;
     const int32_t rem = len % chunk;
@@ -676,7 +680,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const DecodeP
   __syncthreads();
   if (!behind_pass) griddep_wait();  // the workspace is free
   for (int32_t b = r0; b < r1; ++b) {
-    const int32_t len = len_of(b, false);
+    const int32_t len = len_again(b);
     const int32_t c = (len + chunk - 1) / chunk, f = len / chunk, rem = len % chunk;
     p.req_item0[b] = cnt;
     p.req_done[b] = 0;

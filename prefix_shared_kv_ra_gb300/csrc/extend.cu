@@ -83,9 +83,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int32_t
     }
     return (E + tokens_per_cta - 1) / tokens_per_cta;
   };
+  // (the lengths of the thread's first request stay in registers: with up to kPlanThreads requests, all are read once)
+  int32_t P0 = 0, E0 = 0, n0 = 0;
   for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
     int32_t P, E;
     const int32_t n = tiles_of(b, P, E, true);
+    if (b < kPlanThreads) P0 = P, E0 = E, n0 = n;
     for (int32_t t = 0; t < n; ++t) atomicAdd(&s_bin[plan_bin(P, E, t, tokens_per_cta)], 1);
   }
   __syncthreads();
@@ -127,8 +130,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int32_t
   // workspace, still claiming from its list and counter.
   griddep_wait();
   for (int b = threadIdx.x; b < batch; b += kPlanThreads) {
-    int32_t P, E;
-    const int32_t n = tiles_of(b, P, E, false);
+    int32_t P = P0, E = E0;
+    const int32_t n = b < kPlanThreads ? n0 : tiles_of(b, P, E, false);
     for (int32_t t = 0; t < n; ++t) {
       const int32_t pos = atomicAdd(&s_bin[plan_bin(P, E, t, tokens_per_cta)], 1);
       if (pos < cap) {
