@@ -496,7 +496,8 @@ def ra_tree_commit(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor, p
                    device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """The accepted path of each verified tree into req_to_token behind the prefix, the new lengths into seq_lens_out,
     the refused tokens' slots to the end of free_list (free_count [1] written in place unless free_count_out is
-    given).  All int32."""
+    given).  A request whose path does not ascend within its tree, or of which a token has no slot (0), is flagged and
+    skipped.  All int32."""
     status = (_binding or _native()).tree_commit(req_to_token, req_pool_indices, prefix_lens, draft_lens, qo_indptr,
                                                  out_cache_loc, path, accept_lens, seq_lens_out, free_list, free_count,
                                                  free_count_out, device_error, stream)
