@@ -18,7 +18,7 @@
 // rate is two values a clock and SM, and even the few scans and comparisons of a draw took 5 us of a call in it.
 //
 // Bound: the rows read, once each (a pass over 64 pairs of rows of 128,000 is 66 MB, 10 us of HBM), and for few requests
-// the chain of gather, pass and search, about 1.5 us each.  64 trees of 8..16 drafts drawn from q over 128,000 tokens: 33 to
+// the chain of gather, pass and search, about 1.5 us each.  64 trees of 8..16 drafts drawn from q over 128,000 tokens: 28 to
 // 38 us by the draw, the time of the requests with the most refusals; 64 greedy trees of 32..64: 40 to 46 (logits in fp32
 // 50), that of the longest accepted paths (11 rows one after another, 3.4 us each); 4 trees of given drafts: 7.
 #include <cuda_bf16.h>
